@@ -208,9 +208,87 @@ LA2_API la2_status la2_backward_decay(const void *q, const void *k, const void *
                                       la2_stream_t stream);
 
 /*
+ * Gated form: the decayed recurrence with a gate of its own for every token and
+ * head (gated linear attention; youleyou.com article, its one line on
+ * data-dependent gating gives no formula, so this is a reading):
+ *   KV_t = exp(gate_t) KV_{t-1} + k_t^T v_t,   o_t = q_t KV_t,
+ * i.e. o = ((q k^T) ⊙ D) v with D[t][s] = exp(gate_{s+1} + ... + gate_t) for
+ * s <= t, 0 above. `gate` [B,H,N] holds LOG gates in `dt`: 0 is la2_forward's
+ * causal op, a constant log(lambda) is la2_forward_decay's. A gate below -1e4,
+ * -infinity included, is exactly 0: the state restarts at that token (packed
+ * documents), whatever was before it as long as that is finite. Gates above 0
+ * follow the same formula. One K/V head per query head; q, k, v, o, dout, dq, dk,
+ * dvv as for la2_forward / la2_backward. dgate [B,H,N] receives the gradient by
+ * the log gate,
+ *   dgate_t = sum over i >= t > j of D[i][j] (q_i . k_j) (dout_i . v_j),
+ * and 0 at a restart. Outputs hold the same bits on every call.
+ * LA2_BF16: d, dv in {64, 128}; LA2_F32: any 1 <= d, dv <= 128; the block size is
+ * the library's. fp32 accumulation and states, gate sums in fp32 or wider.
+ * Workspace: la2_workspace_size_gated bytes, 256-byte aligned; it must not overlap
+ * the inputs or outputs. Other conventions and errors as for la2_forward; `gate`
+ * and dgate are 16-byte aligned too.
+ */
+LA2_API size_t la2_workspace_size_gated(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv,
+                                        la2_dtype dt, int is_backward);
+LA2_API la2_status la2_forward_gated(const void *q, const void *k, const void *v, const void *gate,
+                                     void *o, int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv,
+                                     la2_dtype dt, void *workspace, size_t workspace_bytes,
+                                     la2_stream_t stream);
+LA2_API la2_status la2_backward_gated(const void *q, const void *k, const void *v, const void *gate,
+                                      const void *dout, void *dq, void *dk, void *dvv, void *dgate,
+                                      int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv,
+                                      la2_dtype dt, void *workspace, size_t workspace_bytes,
+                                      la2_stream_t stream);
+
+/*
+ * Queries and keys of an attention call from the layer's projections: RMS norm of
+ * every head's row, its weight, and the rotation of the row's pairs by the token's
+ * position (cccbook long-context chapter, section on RoPE), in one pass:
+ *   y = w x / sqrt(mean(x^2) + eps)
+ *   (z_i, z_{i+rot/2}) = (y_i cos a_i - y_{i+rot/2} sin a_i, y_i sin a_i + y_{i+rot/2} cos a_i)
+ * for i < rot/2, z_i = y_i for i >= rot, and out = scale z, with the angle
+ * a_i = pos * base^(-2i/rot). q [B,N,H,d] and k [B,N,Hkv,d] are read through
+ * strides in elements {batch, token, head} (host memory; the last dimension is
+ * dense), e.g. slices of one fused projection; q_out [B,H,N,d] and k_out
+ * [B,Hkv,N,d] are dense, what la2_forward and the other calls take.
+ * positions: device int32 [n_axes][B][N], or NULL for 0..N-1 on every axis. With
+ * n_axes > 1 (time, height, width; at most 4) sections[axis] pairs in a row turn by
+ * that axis' position (host memory; they add up to rot/2; NULL for one axis). wq, wk:
+ * [d] in `dt`, or NULL for ones. 0 <= rot <= d <= 256, rot even; base > 0, eps >= 0;
+ * both dtypes. Pointers are aligned to their element size (16-byte pieces are used
+ * where pointers, strides, d and rot/2 allow). H or Hkv = 0 skips that input, with
+ * NULL pointers allowed. fp32 arithmetic, angles reduced in fp64. Outputs must not
+ * overlap inputs or each other.
+ *
+ * Backward: dq [B,N,H,d], dk [B,N,Hkv,d] (dense), and dwq, dwk [d], the sums over all
+ * rows (fp32 partial sums per CTA, then fp64 in a fixed order), from the gradients
+ * dq_out, dk_out of the outputs and the forward's inputs. dwq is NULL exactly where wq is, dwk where wk is.
+ * Workspace: la2_qk_norm_rope_backward_workspace_size bytes, 256-byte aligned.
+ */
+LA2_API la2_status la2_qk_norm_rope(const void *q, const void *k, const int64_t *q_strides,
+                                    const int64_t *k_strides, const void *wq, const void *wk,
+                                    const int32_t *positions, void *q_out, void *k_out, int64_t B,
+                                    int64_t N, int64_t H, int64_t Hkv, int64_t d, int64_t rot,
+                                    int64_t n_axes, const int64_t *sections, double base, double eps,
+                                    double q_scale, double k_scale, la2_dtype dt, la2_stream_t stream);
+LA2_API size_t la2_qk_norm_rope_backward_workspace_size(int64_t B, int64_t N, int64_t H, int64_t Hkv,
+                                                        int64_t d);
+LA2_API la2_status la2_qk_norm_rope_backward(const void *dq_out, const void *dk_out, const void *q,
+                                             const void *k, const int64_t *q_strides,
+                                             const int64_t *k_strides, const void *wq, const void *wk,
+                                             const int32_t *positions, void *dq, void *dk, void *dwq,
+                                             void *dwk, int64_t B, int64_t N, int64_t H, int64_t Hkv,
+                                             int64_t d, int64_t rot, int64_t n_axes,
+                                             const int64_t *sections, double base, double eps,
+                                             double q_scale, double k_scale, la2_dtype dt,
+                                             void *workspace, size_t workspace_bytes,
+                                             la2_stream_t stream);
+
+/*
  * Synchronises `stream`, then reports and clears the device-side error word
- * that kernels set when a bounded wait gives up (LA2_ERR_TIMEOUT), or
- * LA2_ERR_CUDA if the stream holds a CUDA error. LA2_OK otherwise.
+ * that kernels set when a bounded wait gives up (LA2_ERR_TIMEOUT) or a slot
+ * index read on the device is refused (LA2_ERR_INVALID_ARG), or LA2_ERR_CUDA if
+ * the stream holds a CUDA error. LA2_OK otherwise.
  */
 LA2_API la2_status la2_check(la2_stream_t stream);
 
@@ -277,6 +355,62 @@ LA2_API la2_status la2_kv_state(const void *k, const void *v, float *state, int6
 LA2_API la2_status la2_decode_step(const void *q, const void *k, const void *v, void *o,
                                    float *state, int64_t B, int64_t H, int64_t d, int64_t dv,
                                    la2_dtype dt, la2_stream_t stream);
+
+/*
+ * Inference form of the gated recurrence, on a pool of state slots: `state` is
+ * [n_slots, H, d, dv] fp32, and batch row b works on slot slots[b] (device int32
+ * [B]; NULL: slot b, n_slots >= B). A row whose slot is -1 (a padded batch; any
+ * negative index) is skipped. An index >= n_slots, or one that an earlier row of the
+ * call names already, is skipped too and reported by la2_check as
+ * LA2_ERR_INVALID_ARG. Skipped rows leave the pool and their output as they were.
+ *
+ * la2_kv_state_gated: the state a prefill leaves,
+ *   S <- exp(gate_0 + ... + gate_{N-1}) S + sum_t exp(gate_{t+1} + ... + gate_{N-1}) k_t^T v_t,
+ * so a later call continues an earlier one, and a zeroed slot (or a first gate of
+ * -infinity) starts afresh. k, v, gate as for la2_forward_gated; state 16-byte
+ * aligned; summation order fixed. Workspace: la2_kv_state_gated_workspace_size.
+ *
+ * la2_decode_step_gated: one new token per row, S <- exp(gate) S + k^T v, o = q S.
+ * q, k [B,H,d], v, o [B,H,dv], gate [B,H] in `dt` (aligned to their element size).
+ * Any d, dv >= 1 and both dtypes; fp32 arithmetic. Continuing from
+ * la2_kv_state_gated, step t gives row t of la2_forward_gated's output.
+ */
+LA2_API size_t la2_kv_state_gated_workspace_size(int64_t B, int64_t H, int64_t N, int64_t d,
+                                                 int64_t dv, la2_dtype dt);
+LA2_API la2_status la2_kv_state_gated(const void *k, const void *v, const void *gate, float *state,
+                                      const int32_t *slots, int64_t n_slots, int64_t B, int64_t H,
+                                      int64_t N, int64_t d, int64_t dv, la2_dtype dt, void *workspace,
+                                      size_t workspace_bytes, la2_stream_t stream);
+LA2_API la2_status la2_decode_step_gated(const void *q, const void *k, const void *v, const void *gate,
+                                         void *o, float *state, const int32_t *slots, int64_t n_slots,
+                                         int64_t B, int64_t H, int64_t d, int64_t dv, la2_dtype dt,
+                                         la2_stream_t stream);
+
+/*
+ * Slots of a pool [n_slots, H, d, dv] fp32 (the states of any of the inference
+ * calls above; 4-byte aligned, moved in 16-byte pieces where address and slot size
+ * allow). Index lists are device int32.
+ *
+ * la2_state_copy: for every i < n, slot dst[i] <- slot src[i], or zeros where
+ * src[i] = -1 (a fresh or freed slot); dst[i] = -1 or dst[i] = src[i] does nothing.
+ * One source may serve many destinations (a prompt forked into its continuations).
+ * Sources are read as they were before the call. An entry that cannot keep that -
+ * its destination is another entry's source, or an earlier entry's destination - and
+ * one with an index outside [-1, n_slots) are skipped and reported by la2_check as
+ * LA2_ERR_INVALID_ARG.
+ *
+ * la2_state_compact: moves the live slots (live[s] != 0) into the first
+ * n_live = number of live slots: those below n_live stay, the others, in ascending
+ * order, fill the holes there, in ascending order. moved[s] receives the new slot of
+ * a live slot, -1 for the others; slots from n_live on keep what they held. At most
+ * 32768 slots (LA2_ERR_UNSUPPORTED above). live and moved must not overlap.
+ */
+LA2_API la2_status la2_state_copy(float *state, const int32_t *src, const int32_t *dst, int64_t n,
+                                  int64_t n_slots, int64_t H, int64_t d, int64_t dv,
+                                  la2_stream_t stream);
+LA2_API la2_status la2_state_compact(float *state, const int32_t *live, int32_t *moved,
+                                     int64_t n_slots, int64_t H, int64_t d, int64_t dv,
+                                     la2_stream_t stream);
 
 /*
  * Upper bound, in spin iterations, of every device-side wait (mbarrier or

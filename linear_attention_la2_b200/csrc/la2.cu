@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -15,6 +16,7 @@
 
 #include "la2.h"
 #include "la2_common.cuh"
+#include "la2_gated_simt.cuh"
 #include "la2_decode.cuh"
 #include "la2_simt.cuh"
 #include "la2_sm100.cuh"
@@ -38,6 +40,18 @@ enum KernelId : int {
   K_DECODE,
   K_STATE_ACC,
   K_REVERSE,
+  K_GATED_STATE,
+  K_GATED_SCAN,
+  K_GATED_FWD,
+  K_GATED_DQ,
+  K_GATED_DKDV,
+  K_GATED_GATE,
+  K_GATED_POOL,
+  K_GATED_DECODE,
+  K_STATE_COPY,
+  K_STATE_COMPACT,
+  K_QK_ROPE,
+  K_QK_ROPE_BWD,
   K_COUNT
 };
 
@@ -45,7 +59,11 @@ static const char* kKernelNames[K_COUNT] = {
     "la2_chunk_state_simt", "la2_chunk_scan",      "la2_fwd_simt",
     "la2_bwd_dq_simt",      "la2_bwd_dkdv_simt",   "la2_fwd_sm100",
     "la2_chunk_state_sm100", "la2_bwd_dq_sm100",   "la2_bwd_dkdv_sm100",
-    "la2_decode_step",      "la2_state_accumulate", "la2_reverse_rows"};
+    "la2_decode_step",      "la2_state_accumulate", "la2_reverse_rows",
+    "la2_gated_state",      "la2_gated_scan",      "la2_gated_fwd",
+    "la2_gated_bwd_dq",     "la2_gated_bwd_dkdv",  "la2_gated_gate_grad",
+    "la2_gated_pool_update", "la2_gated_decode_step", "la2_state_copy",
+    "la2_state_compact",    "la2_qk_norm_rope",    "la2_qk_norm_rope_bwd"};
 
 struct EventRecord {
   int kernel;
@@ -1360,6 +1378,7 @@ la2_status la2_check(la2_stream_t stream) {
   if (cudaMemcpyFromSymbol(&code, g_error_code, sizeof(int)) != cudaSuccess) return LA2_ERR_CUDA;
   if (code != 0) {
     if (cudaMemcpyToSymbol(g_error_code, &zero, sizeof(int)) != cudaSuccess) return LA2_ERR_CUDA;
+    if (code == DEV_ERR_INDEX) return LA2_ERR_INVALID_ARG;
     return code == DEV_ERR_TIMEOUT ? LA2_ERR_TIMEOUT : LA2_ERR_CUDA;
   }
   return LA2_OK;
@@ -1471,3 +1490,9 @@ extern "C" la2_status la2_forward_noalloc(const void* q, const void* k, const vo
   return la2_forward(q, k, v, o, B, H, N, d, dv, causal, block, dt, ws,
                      static_cast<size_t>(LA2_NOALLOC_SCRATCH_BYTES), stream);
 }
+
+// ==================================== gated recurrence, q/k preparation, slots
+
+#include "la2_gated.cuh"
+#include "la2_rope.cuh"
+#include "la2_slots.cuh"

@@ -14,6 +14,7 @@ __device__ int g_error_where = 0;
 
 enum DeviceError : int {
   DEV_ERR_NONE = 0,
+  DEV_ERR_INDEX = 1,  // an index read on the device is out of range or not allowed
   DEV_ERR_TIMEOUT = 5,
 };
 

@@ -136,6 +136,112 @@ decode_step_v4_kernel(const T* __restrict__ q, const T* __restrict__ k, const T*
   }
 }
 
+// The gated step on a pool of slots: S <- e^gate S + k^T v, o = q S, with the
+// state of batch row b in pool slot slots[b] (b itself without `slots`). Rows that
+// checked_slot refuses leave their output and the pool as they were. The same two
+// layouts as the step above.
+template <typename T>
+__global__ void __launch_bounds__(32 * kDecodeWarps)
+decode_gated_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+                    const T* __restrict__ gate, T* __restrict__ o, float* __restrict__ pool,
+                    const int32_t* __restrict__ slots, int64_t n_slots, int H, int d, int dv) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ float part[kDecodeWarps][32];
+  const int64_t bh = blockIdx.x, b = bh / H;
+  const int64_t slot = gated::checked_slot(slots, b, n_slots);
+  if (slot < 0) return;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int j = blockIdx.y * 32 + lane;
+  const T* qb = q + bh * d;
+  const T* kb = k + bh * d;
+  const float g = expf(to_f32(gate[bh]));
+  float acc = 0.f;
+  if (j < dv) {
+    const float vj = to_f32(v[bh * dv + j]);
+    float* col = pool + (slot * H + (bh - b * H)) * static_cast<int64_t>(d) * dv + j;
+#pragma unroll 8
+    for (int i = w; i < d; i += kDecodeWarps) {
+      const float s = fmaf(g, col[static_cast<int64_t>(i) * dv], to_f32(kb[i]) * vj);
+      col[static_cast<int64_t>(i) * dv] = s;
+      acc += to_f32(qb[i]) * s;
+    }
+  }
+  part[w][lane] = acc;
+  __syncthreads();
+  if (w == 0 && j < dv) {
+    float sum = 0.f;
+#pragma unroll
+    for (int x = 0; x < kDecodeWarps; ++x) sum += part[x][lane];
+    o[bh * dv + j] = from_f32<T>(sum);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kDecodeWarps, 3)
+decode_gated_v4_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+                       const T* __restrict__ gate, T* __restrict__ o, float* __restrict__ pool,
+                       const int32_t* __restrict__ slots, int64_t n_slots, int H, int d, int dv) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ float4 part[kDecodeWarps][32];
+  const int64_t bh = blockIdx.x, b = bh / H;
+  const int64_t slot = gated::checked_slot(slots, b, n_slots);
+  if (slot < 0) return;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int j = blockIdx.y * 128 + 4 * lane;  // first of this lane's four columns
+  const T* qb = q + bh * d;
+  const T* kb = k + bh * d;
+  const float g = expf(to_f32(gate[bh]));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (j < dv) {
+    const float4 vj = load4<T>(v + bh * dv + j);
+    float* col = pool + (slot * H + (bh - b * H)) * static_cast<int64_t>(d) * dv + j;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float4 x[kRows / 2];
+#pragma unroll
+      for (int t = 0; t < kRows / 2; ++t) {
+        const int i = w + (h * kRows / 2 + t) * kDecodeWarps;
+        if (i < d) x[t] = *reinterpret_cast<const float4*>(col + static_cast<int64_t>(i) * dv);
+      }
+#pragma unroll
+      for (int t = 0; t < kRows / 2; ++t) {
+        const int i = w + (h * kRows / 2 + t) * kDecodeWarps;
+        if (i < d) {
+          const float ki = to_f32(kb[i]), qi = to_f32(qb[i]);
+          x[t].x = fmaf(g, x[t].x, ki * vj.x);
+          x[t].y = fmaf(g, x[t].y, ki * vj.y);
+          x[t].z = fmaf(g, x[t].z, ki * vj.z);
+          x[t].w = fmaf(g, x[t].w, ki * vj.w);
+          *reinterpret_cast<float4*>(col + static_cast<int64_t>(i) * dv) = x[t];
+          acc.x += qi * x[t].x;
+          acc.y += qi * x[t].y;
+          acc.z += qi * x[t].z;
+          acc.w += qi * x[t].w;
+        }
+      }
+    }
+  }
+  part[w][lane] = acc;
+  __syncthreads();
+  if (w == 0 && j < dv) {
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int x = 0; x < kDecodeWarps; ++x) {
+      sum.x += part[x][lane].x;
+      sum.y += part[x][lane].y;
+      sum.z += part[x][lane].z;
+      sum.w += part[x][lane].w;
+    }
+    T* ob = o + bh * dv + j;
+    ob[0] = from_f32<T>(sum.x);
+    ob[1] = from_f32<T>(sum.y);
+    ob[2] = from_f32<T>(sum.z);
+    ob[3] = from_f32<T>(sum.w);
+  }
+}
+
 // state[bh] (row-major d x dv) += sum over the C chunk states of sequence bh,
 // added in chunk order. `chunk_major`: the chunk states use the tensor-core
 // layout (float4 j of row r at float4 index j*d + r), else row-major.

@@ -1,0 +1,329 @@
+// Host side of the gated recurrence: shapes, plan, launches and the C entry
+// points la2_forward_gated, la2_backward_gated, la2_kv_state_gated and
+// la2_decode_step_gated. Included at the end of la2.cu.
+#pragma once
+
+namespace la2 {
+namespace gated {
+
+struct Plan {
+  int64_t L = 0, C = 1;
+  size_t off_suffix = 0, off_tot = 0, off_qdq = 0, off_kdk = 0;  // prefix states at 0
+  size_t bytes = 0;
+};
+
+enum Need { NEED_FWD, NEED_BWD, NEED_STATE };
+
+static size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+static la2_status check(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, la2_dtype dt) {
+  if (B < 0 || H < 0 || N < 0 || d < 1 || dv < 1) return LA2_ERR_INVALID_ARG;
+  if (dt != LA2_F32 && dt != LA2_BF16) return LA2_ERR_INVALID_ARG;
+  if (double(B) * double(H) * double(N) * double(std::max(d, dv)) > 9.0e18) return LA2_ERR_INVALID_ARG;
+  if (d > 128 || dv > 128) return LA2_ERR_UNSUPPORTED;
+  if (dt == LA2_BF16 && ((d != 64 && d != 128) || (dv != 64 && dv != 128))) return LA2_ERR_UNSUPPORTED;
+  // one CTA a (sequence, chunk of at least a block), 256 elements of a state a CTA
+  const double nb = std::ceil(double(d) * double(dv) / kThreads);
+  if (double(B) * double(H) * std::max(std::ceil(double(N) / kRows), nb) > 2147483647.0)
+    return LA2_ERR_UNSUPPORTED;
+  return LA2_OK;
+}
+
+// Chunks of a sequence run in parallel: about two CTAs an SM, at least two blocks
+// each. In the backward at most 512 rows, over which the gates' gradient is a
+// running difference of row dots (see la2_gated_simt.cuh).
+static Plan make_plan(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, la2_dtype dt, Need need,
+                      int sms) {
+  Plan p;
+  const int64_t BH = B * H, T = (N + kRows - 1) / kRows;
+  if (g_chunk_len > 0) {
+    p.L = (g_chunk_len + kRows - 1) / kRows * kRows;
+  } else {
+    const int64_t want = (2 * (int64_t)std::max(sms, 1) + BH - 1) / BH;
+    const int64_t C = std::min<int64_t>(want, std::max<int64_t>(1, T / 2));
+    p.L = (T + C - 1) / C * kRows;
+    if (need == NEED_BWD) p.L = std::min<int64_t>(p.L, 512);
+  }
+  p.L = std::max<int64_t>(p.L, kRows);
+  p.C = std::max<int64_t>(1, (N + p.L - 1) / p.L);
+  const bool states = p.C > 1 || need == NEED_STATE;
+  const size_t one = states ? round256((size_t)BH * p.C * d * dv * sizeof(float)) : 0;
+  size_t at = one;
+  p.off_suffix = at;
+  if (need == NEED_BWD) at += one;
+  p.off_tot = at;
+  if (states) at += round256((size_t)BH * p.C * sizeof(double));
+  p.off_qdq = at;
+  if (need == NEED_BWD) at += round256((size_t)BH * N * sizeof(float));
+  p.off_kdk = at;
+  if (need == NEED_BWD) at += round256((size_t)BH * N * sizeof(float));
+  p.bytes = at;
+  return p;
+}
+
+template <typename Kernel>
+static bool raise_smem(Kernel kern, size_t bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+}
+
+template <typename T, bool SUFFIX>
+static la2_status chunk_states(const void* a, const void* b, const void* gate, float* out, double* tot,
+                               int64_t BH, const Shape& sh, cudaStream_t st) {
+  const size_t smem = smem_bytes(sh.d, sh.dv, 1, 1, 0);
+  if (!raise_smem(chunk_state_kernel<T, SUFFIX>, smem)) return LA2_ERR_CUDA;
+  LaunchTimer t(K_GATED_STATE, st);
+  chunk_state_kernel<T, SUFFIX><<<(unsigned)(BH * sh.C), kThreads, smem, st>>>(
+      static_cast<const T*>(a), static_cast<const T*>(b), static_cast<const T*>(gate), out, tot, sh);
+  return launch_status();
+}
+
+static la2_status scan(float* s, const double* tot, int64_t BH, const Shape& sh, int mode, cudaStream_t st) {
+  const int nel = sh.d * sh.dv, nb = (nel + kThreads - 1) / kThreads;
+  LaunchTimer t(K_GATED_SCAN, st);
+  if (launch_pdl(scan_kernel, dim3((unsigned)(BH * nb)), dim3(kThreads), 0, st, s, tot, sh.C, nel, mode) !=
+      cudaSuccess)
+    return LA2_ERR_CUDA;
+  return launch_status();
+}
+
+template <typename T>
+static la2_status forward(const void* q, const void* k, const void* v, const void* gate, void* o, char* ws,
+                          const Plan& p, int64_t BH, const Shape& sh, cudaStream_t st) {
+  float* states = p.C > 1 ? reinterpret_cast<float*>(ws) : nullptr;
+  la2_status s = LA2_OK;
+  if (states) {
+    double* tot = reinterpret_cast<double*>(ws + p.off_tot);
+    if ((s = chunk_states<T, false>(k, v, gate, states, tot, BH, sh, st)) != LA2_OK) return s;
+    if ((s = scan(states, tot, BH, sh, 0, st)) != LA2_OK) return s;
+  }
+  const size_t smem = smem_bytes(sh.d, sh.dv, 2, 1, 1);
+  if (!raise_smem(fwd_kernel<T>, smem)) return LA2_ERR_CUDA;
+  LaunchTimer t(K_GATED_FWD, st);
+  fwd_kernel<T><<<(unsigned)(BH * sh.C), kThreads, smem, st>>>(
+      static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
+      static_cast<const T*>(gate), static_cast<T*>(o), states, sh);
+  return launch_status();
+}
+
+template <typename T>
+static la2_status gate_grad(const void* gate, const float* qdq, const float* kdk, const float* prefix,
+                            const float* suffix, void* dgate, int64_t BH, const Shape& sh, cudaStream_t st) {
+  LaunchTimer t(K_GATED_GATE, st);
+  if (launch_pdl(gate_grad_kernel<T>, dim3((unsigned)(BH * sh.C)), dim3(kThreads), 0, st,
+                 static_cast<const T*>(gate), qdq, kdk, prefix, suffix, static_cast<T*>(dgate), sh.N, sh.L,
+                 sh.C, sh.d * sh.dv) != cudaSuccess)
+    return LA2_ERR_CUDA;
+  return launch_status();
+}
+
+template <typename T>
+static la2_status backward(const void* q, const void* k, const void* v, const void* gate, const void* dout,
+                           void* dq, void* dk, void* dvv, void* dgate, char* ws, const Plan& p, int64_t BH,
+                           const Shape& sh, cudaStream_t st) {
+  float* prefix = p.C > 1 ? reinterpret_cast<float*>(ws) : nullptr;
+  float* suffix = p.C > 1 ? reinterpret_cast<float*>(ws + p.off_suffix) : nullptr;
+  float* qdq = reinterpret_cast<float*>(ws + p.off_qdq);
+  float* kdk = reinterpret_cast<float*>(ws + p.off_kdk);
+  la2_status s = LA2_OK;
+  if (prefix) {
+    double* tot = reinterpret_cast<double*>(ws + p.off_tot);
+    if ((s = chunk_states<T, false>(k, v, gate, prefix, tot, BH, sh, st)) != LA2_OK) return s;
+    if ((s = scan(prefix, tot, BH, sh, 0, st)) != LA2_OK) return s;
+    if ((s = chunk_states<T, true>(q, dout, gate, suffix, tot, BH, sh, st)) != LA2_OK) return s;
+    if ((s = scan(suffix, tot, BH, sh, 1, st)) != LA2_OK) return s;
+  }
+  const T *tq = static_cast<const T*>(q), *tk = static_cast<const T*>(k), *tv = static_cast<const T*>(v),
+          *tg = static_cast<const T*>(gate), *td = static_cast<const T*>(dout);
+  const unsigned grid = (unsigned)(BH * sh.C);
+  {
+    const size_t smem = smem_bytes(sh.d, sh.dv, 1, 2, 1);
+    if (!raise_smem(bwd_dq_kernel<T>, smem)) return LA2_ERR_CUDA;
+    LaunchTimer t(K_GATED_DQ, st);
+    bwd_dq_kernel<T><<<grid, kThreads, smem, st>>>(tq, tk, tv, tg, td, static_cast<T*>(dq), qdq, prefix, sh);
+  }
+  if ((s = launch_status()) != LA2_OK) return s;
+  {
+    const size_t smem = smem_bytes(sh.d, sh.dv, 2, 2, 1);
+    if (!raise_smem(bwd_dkdv_kernel<T>, smem)) return LA2_ERR_CUDA;
+    LaunchTimer t(K_GATED_DKDV, st);
+    bwd_dkdv_kernel<T><<<grid, kThreads, smem, st>>>(tq, tk, tv, tg, td, static_cast<T*>(dk),
+                                                     static_cast<T*>(dvv), kdk, suffix, sh);
+  }
+  if ((s = launch_status()) != LA2_OK) return s;
+  return gate_grad<T>(gate, qdq, kdk, prefix, suffix, dgate, BH, sh, st);
+}
+
+// Pointers of a call: every one non-null and aligned, no output over an input,
+// another output or the workspace.
+struct Span {
+  const void* p;
+  size_t n;
+};
+static bool spans_ok(const Span* in, int n_in, const Span* out, int n_out) {
+  for (int i = 0; i < n_in; ++i)
+    if (!in[i].p || !is_aligned(in[i].p, 16)) return false;
+  for (int i = 0; i < n_out; ++i) {
+    if (!out[i].p || !is_aligned(out[i].p, 16)) return false;
+    for (int j = 0; j < n_in; ++j)
+      if (overlaps(out[i].p, out[i].n, in[j].p, in[j].n)) return false;
+    for (int j = i + 1; j < n_out; ++j)
+      if (overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return false;
+  }
+  return true;
+}
+static la2_status workspace_ok(const void* ws, size_t have, size_t need, const Span* in, int n_in,
+                               const Span* out, int n_out) {
+  if (need == 0) return LA2_OK;
+  if (!ws || have < need) return LA2_ERR_WORKSPACE;
+  if (!is_aligned(ws, 256)) return LA2_ERR_INVALID_ARG;
+  for (int i = 0; i < n_in; ++i)
+    if (overlaps(ws, need, in[i].p, in[i].n)) return LA2_ERR_INVALID_ARG;
+  for (int i = 0; i < n_out; ++i)
+    if (overlaps(ws, need, out[i].p, out[i].n)) return LA2_ERR_INVALID_ARG;
+  return LA2_OK;
+}
+
+static size_t workspace_size(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, la2_dtype dt, Need need) {
+  if (check(B, H, N, d, dv, dt) != LA2_OK) return (size_t)-1;
+  if (B == 0 || H == 0 || N == 0) return 0;
+  const int sms = device_sm_count();
+  if (sms <= 0) return (size_t)-1;
+  return make_plan(B, H, N, d, dv, dt, need, sms).bytes;
+}
+
+}  // namespace gated
+}  // namespace la2
+
+extern "C" {
+
+size_t la2_workspace_size_gated(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, la2_dtype dt,
+                                int is_backward) {
+  return gated::workspace_size(B, H, N, d, dv, dt, is_backward ? gated::NEED_BWD : gated::NEED_FWD);
+}
+
+la2_status la2_forward_gated(const void* q, const void* k, const void* v, const void* gate, void* o,
+                             int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, la2_dtype dt,
+                             void* workspace, size_t workspace_bytes, la2_stream_t stream) {
+  la2_status s = gated::check(B, H, N, d, dv, dt);
+  if (s != LA2_OK) return s;
+  if (B == 0 || H == 0 || N == 0) return LA2_OK;
+  const size_t es = dt == LA2_BF16 ? 2 : 4, rows = (size_t)B * H * N;
+  const gated::Span in[4] = {{q, rows * d * es}, {k, rows * d * es}, {v, rows * dv * es}, {gate, rows * es}};
+  const gated::Span out[1] = {{o, rows * dv * es}};
+  if (!gated::spans_ok(in, 4, out, 1)) return LA2_ERR_INVALID_ARG;
+  const int sms = device_sm_count();
+  if (sms <= 0) return LA2_ERR_CUDA;
+  const gated::Plan p = gated::make_plan(B, H, N, d, dv, dt, gated::NEED_FWD, sms);
+  s = gated::workspace_ok(workspace, workspace_bytes, p.bytes, in, 4, out, 1);
+  if (s != LA2_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const gated::Shape sh{N, p.L, p.C, (int)d, (int)dv};
+  char* ws = static_cast<char*>(workspace);
+  return dt == LA2_BF16 ? gated::forward<__nv_bfloat16>(q, k, v, gate, o, ws, p, B * H, sh, st)
+                        : gated::forward<float>(q, k, v, gate, o, ws, p, B * H, sh, st);
+}
+
+la2_status la2_backward_gated(const void* q, const void* k, const void* v, const void* gate,
+                              const void* dout, void* dq, void* dk, void* dvv, void* dgate, int64_t B,
+                              int64_t H, int64_t N, int64_t d, int64_t dv, la2_dtype dt, void* workspace,
+                              size_t workspace_bytes, la2_stream_t stream) {
+  la2_status s = gated::check(B, H, N, d, dv, dt);
+  if (s != LA2_OK) return s;
+  if (B == 0 || H == 0 || N == 0) return LA2_OK;
+  const size_t es = dt == LA2_BF16 ? 2 : 4, rows = (size_t)B * H * N;
+  const gated::Span in[5] = {{q, rows * d * es}, {k, rows * d * es}, {v, rows * dv * es},
+                             {gate, rows * es},  {dout, rows * dv * es}};
+  const gated::Span out[4] = {{dq, rows * d * es}, {dk, rows * d * es}, {dvv, rows * dv * es}, {dgate, rows * es}};
+  if (!gated::spans_ok(in, 5, out, 4)) return LA2_ERR_INVALID_ARG;
+  const int sms = device_sm_count();
+  if (sms <= 0) return LA2_ERR_CUDA;
+  const gated::Plan p = gated::make_plan(B, H, N, d, dv, dt, gated::NEED_BWD, sms);
+  s = gated::workspace_ok(workspace, workspace_bytes, p.bytes, in, 5, out, 4);
+  if (s != LA2_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const gated::Shape sh{N, p.L, p.C, (int)d, (int)dv};
+  char* ws = static_cast<char*>(workspace);
+  return dt == LA2_BF16
+             ? gated::backward<__nv_bfloat16>(q, k, v, gate, dout, dq, dk, dvv, dgate, ws, p, B * H, sh, st)
+             : gated::backward<float>(q, k, v, gate, dout, dq, dk, dvv, dgate, ws, p, B * H, sh, st);
+}
+
+size_t la2_kv_state_gated_workspace_size(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, la2_dtype dt) {
+  return gated::workspace_size(B, H, N, d, dv, dt, gated::NEED_STATE);
+}
+
+la2_status la2_kv_state_gated(const void* k, const void* v, const void* gate, float* state,
+                              const int32_t* slots, int64_t n_slots, int64_t B, int64_t H, int64_t N,
+                              int64_t d, int64_t dv, la2_dtype dt, void* workspace, size_t workspace_bytes,
+                              la2_stream_t stream) {
+  la2_status s = gated::check(B, H, N, d, dv, dt);
+  if (s != LA2_OK) return s;
+  if (n_slots < 0 || n_slots > 0x7fffffff || (!slots && n_slots < B)) return LA2_ERR_INVALID_ARG;
+  if (B == 0 || H == 0 || N == 0) return LA2_OK;
+  const size_t es = dt == LA2_BF16 ? 2 : 4, rows = (size_t)B * H * N;
+  const gated::Span in[4] = {{k, rows * d * es}, {v, rows * dv * es}, {gate, rows * es},
+                             {slots, (size_t)B * sizeof(int32_t)}};
+  const gated::Span out[1] = {{state, (size_t)n_slots * H * d * dv * sizeof(float)}};
+  const int n_in = slots ? 4 : 3;
+  if (slots && !is_aligned(slots, 4)) return LA2_ERR_INVALID_ARG;
+  if (!gated::spans_ok(in, 3, out, 1)) return LA2_ERR_INVALID_ARG;
+  if (slots && overlaps(in[3].p, in[3].n, out[0].p, out[0].n)) return LA2_ERR_INVALID_ARG;
+  const int sms = device_sm_count();
+  if (sms <= 0) return LA2_ERR_CUDA;
+  const gated::Plan p = gated::make_plan(B, H, N, d, dv, dt, gated::NEED_STATE, sms);
+  s = gated::workspace_ok(workspace, workspace_bytes, p.bytes, in, n_in, out, 1);
+  if (s != LA2_OK) return s;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const gated::Shape sh{N, p.L, p.C, (int)d, (int)dv};
+  float* chunks = static_cast<float*>(workspace);
+  double* tot = reinterpret_cast<double*>(static_cast<char*>(workspace) + p.off_tot);
+  s = dt == LA2_BF16 ? gated::chunk_states<__nv_bfloat16, false>(k, v, gate, chunks, tot, B * H, sh, st)
+                     : gated::chunk_states<float, false>(k, v, gate, chunks, tot, B * H, sh, st);
+  if (s != LA2_OK) return s;
+  const int64_t nb = (d * dv + gated::kThreads - 1) / gated::kThreads;
+  LaunchTimer t(K_GATED_POOL, st);
+  if (launch_pdl(gated::pool_update_kernel, dim3((unsigned)(B * H * nb)), dim3(gated::kThreads), 0, st,
+                 static_cast<const float*>(chunks), static_cast<const double*>(tot), state, slots, n_slots,
+                 p.C, (int)H, (int)d, (int)dv, 0) != cudaSuccess)
+    return LA2_ERR_CUDA;
+  return launch_status();
+}
+
+la2_status la2_decode_step_gated(const void* q, const void* k, const void* v, const void* gate, void* o,
+                                 float* state, const int32_t* slots, int64_t n_slots, int64_t B, int64_t H,
+                                 int64_t d, int64_t dv, la2_dtype dt, la2_stream_t stream) {
+  if (B < 0 || H < 0 || d < 1 || dv < 1) return LA2_ERR_INVALID_ARG;
+  if (dt != LA2_F32 && dt != LA2_BF16) return LA2_ERR_INVALID_ARG;
+  if (n_slots < 0 || n_slots > 0x7fffffff || (!slots && n_slots < B)) return LA2_ERR_INVALID_ARG;
+  if (double(std::max(B, n_slots)) * double(H) * double(d) * double(dv) > 2.0e18) return LA2_ERR_INVALID_ARG;
+  if (B == 0 || H == 0) return LA2_OK;
+  const size_t es = dt == LA2_BF16 ? 2 : 4, BH = (size_t)B * H;
+  if (!q || !k || !v || !gate || !o || !state) return LA2_ERR_INVALID_ARG;
+  if (!is_aligned(q, es) || !is_aligned(k, es) || !is_aligned(v, es) || !is_aligned(gate, es) ||
+      !is_aligned(o, es) || !is_aligned(state, 4) || !is_aligned(slots, 4))
+    return LA2_ERR_INVALID_ARG;
+  if (BH > 0x7fffffff || (dv + 31) / 32 > 65535) return LA2_ERR_UNSUPPORTED;
+  const gated::Span in[5] = {{q, BH * d * es}, {k, BH * d * es}, {v, BH * dv * es}, {gate, BH * es},
+                             {slots, slots ? (size_t)B * sizeof(int32_t) : 0}};
+  const size_t no = BH * dv * es, ns = (size_t)n_slots * H * d * dv * sizeof(float);
+  for (const gated::Span& x : in)
+    if (x.p && (overlaps(o, no, x.p, x.n) || overlaps(state, ns, x.p, x.n))) return LA2_ERR_INVALID_ARG;
+  if (overlaps(o, no, state, ns)) return LA2_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  LaunchTimer t(K_GATED_DECODE, st);
+  // Four columns per lane under the conditions of la2_decode_step's.
+  const bool v4 = dv % 4 == 0 && d <= kDecodeWarps * kRows && is_aligned(state, 16) && is_aligned(v, 4 * es) &&
+                  is_aligned(o, es);
+  const dim3 grid((unsigned)BH, (unsigned)(v4 ? (dv + 127) / 128 : (dv + 31) / 32)), block(32 * kDecodeWarps);
+  auto launch = [&](auto tag) {
+    using T = decltype(tag);
+    auto kern = v4 ? decode_gated_v4_kernel<T> : decode_gated_kernel<T>;
+    return launch_pdl(kern, grid, block, 0, st, static_cast<const T*>(q), static_cast<const T*>(k),
+                      static_cast<const T*>(v), static_cast<const T*>(gate), static_cast<T*>(o), state, slots,
+                      n_slots, (int)H, (int)d, (int)dv);
+  };
+  if ((dt == LA2_BF16 ? launch(__nv_bfloat16()) : launch(0.f)) != cudaSuccess) return LA2_ERR_CUDA;
+  return launch_status();
+}
+
+}  // extern "C"

@@ -1,0 +1,716 @@
+// RMS norm of every query and key head with the position rotation in the same
+// pass, and its gradients. Included at the end of la2.cu.
+//
+// A row x of d values (one token, one head), weight w, position angles a_i:
+//
+//   r = 1 / sqrt(mean(x^2) + eps),  y = w (r x),
+//   (z_i, z_(i+h)) = (y_i cos a_i - y_(i+h) sin a_i, y_i sin a_i + y_(i+h) cos a_i),  i < h = rot / 2,
+//   z_i = y_i for i >= rot;  out = scale z.
+//
+// Pair i turns by a_i = pos[axis(i)][token] base^(-2i/rot): with several axes
+// (time, height, width) each takes a run of pairs. Backwards, with g the
+// gradient turned back by -a and scaled (the rotation is orthogonal):
+//
+//   dw = sum over rows of g (r x),   u = w g,   dx = r (u - (r x) mean(u (r x))).
+//
+// The input rows are slices of the [B, N, heads, d] projections (any batch,
+// token and head strides), the output the dense [B, H, N, d] tensors that the
+// attention entry points read, so the transposition costs no pass of its own.
+//
+// Bound by HBM: each row is read once and written once (backwards: two reads).
+// A CTA takes a tile of consecutive tokens and all their heads: the angles are
+// computed once a token and kept in shared memory (the turns in fp64 - at
+// position 2^20 an fp32 product is 0.06 rad off - and only their fraction goes
+// on to fp32), and the rows of one head in the tile are consecutive in the output.
+#pragma once
+
+namespace la2 {
+namespace rope {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxD = 256;
+constexpr int kMaxAxes = 4;
+constexpr int kMaxTokens = 8;  // tokens of a tile
+
+struct Params {
+  const void* x[2];        // queries, keys (backward: the forward's inputs)
+  const void* w[2];        // weights, or null for ones
+  void* out[2];            // forward: [B,H,N,d]; backward: dx [B,N,H,d]
+  const void* dy[2];       // backward: [B,H,N,d]
+  float* dw_part;          // backward: [grid][2][d]
+  const int32_t* pos;      // [axes][B*N], or null: 0..N-1
+  int64_t sb[2], sn[2], sh[2];  // input strides in elements
+  int64_t N, tokens;       // tokens = B * N
+  int32_t heads[2];
+  int32_t d, half, tile, splits;
+  float eps, scale[2];
+  double turn[kMaxD / 2];  // base^(-2i/rot) / (2 pi)
+  uint8_t axis[kMaxD / 2];
+};
+
+// cos and sin of every angle of the tile's tokens.
+__device__ __forceinline__ void fill_angles(const Params& p, int64_t tok0, int ntok, float2* cs) {
+  for (int i = threadIdx.x; i < ntok * p.half; i += kThreads) {
+    const int t = i / p.half, j = i - t * p.half;
+    const int64_t tok = tok0 + t;
+    const int64_t at = p.pos ? p.pos[p.axis[j] * p.tokens + tok]
+                             : static_cast<uint32_t>(tok) % static_cast<uint32_t>(p.N);
+    const double a = static_cast<double>(at) * p.turn[j];
+    float s, c;
+    sincospif(2.f * static_cast<float>(a - rint(a)), &s, &c);
+    cs[i] = make_float2(c, s);
+  }
+}
+
+struct Row {
+  int which;               // 0 query, 1 key
+  int64_t in, out;         // element offsets (out: [B,H,N,d]); flat: [B,N,H,d]
+  int64_t flat;
+  int t;                   // token within the tile
+};
+// Row r of the tile: heads outermost, so that neighbouring rows are neighbouring
+// tokens of one head.
+__device__ __forceinline__ Row row_of(const Params& p, int64_t tok0, int ntok, int r) {
+  Row x;
+  int h = r / ntok;
+  x.t = r - h * ntok;
+  x.which = h >= p.heads[0];
+  if (x.which) h -= p.heads[0];
+  const int64_t tok = tok0 + x.t;  // below 2^31
+  const int64_t b = static_cast<uint32_t>(tok) / static_cast<uint32_t>(p.N), n = tok - b * p.N;
+  x.in = b * p.sb[x.which] + n * p.sn[x.which] + h * p.sh[x.which];
+  x.out = ((b * p.heads[x.which] + h) * p.N + n) * p.d;
+  x.flat = (tok * p.heads[x.which] + h) * p.d;
+  return x;
+}
+
+template <int G>
+__device__ __forceinline__ float group_sum(float x) {
+#pragma unroll
+  for (int m = G / 2; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+  return x;
+}
+
+// One row as a thread sees it. VEC > 1: a group of G lanes holds a row, lane l
+// the VEC values from VEC l on, and the partner of a pair sits h / VEC lanes
+// away. VEC = 1: a warp holds a row, lane l the pairs l, l + 32, ... and the
+// values behind the rotated ones alike (any even rot, any alignment).
+template <typename T, int VEC>
+__device__ __forceinline__ void load_vec(const T* p, float (&x)[VEC]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (VEC == 8) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    } else {
+      x[i] = __uint_as_float(w[i]);
+    }
+  }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_vec(T* p, const float (&x)[VEC]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (VEC == 8) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&v);
+    } else {
+      w[i] = __float_as_uint(x[i]);
+    }
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Turns the pairs of a row spread over a group: x <- R(sign * angle) x.
+template <int VEC>
+__device__ __forceinline__ void turn_vec(float (&x)[VEC], const float2* cs, int l, int half, float sign) {
+  const int hl = half / VEC;
+  const bool lo = l < hl, hi = l >= hl && l < 2 * hl;
+  const int src = (threadIdx.x & 31) + (lo ? hl : (hi ? -hl : 0));
+  const int j0 = VEC * (hi ? l - hl : l);
+  const float f = lo ? -sign : sign;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    const float o = __shfl_sync(0xffffffffu, x[e], src);
+    if (lo || hi) {
+      const float2 a = cs[j0 + e];
+      x[e] = fmaf(x[e], a.x, f * a.y * o);
+    }
+  }
+}
+
+template <typename T, int VEC, int G>
+__global__ void __launch_bounds__(kThreads)
+rope_fwd_vec_kernel(const __grid_constant__ Params p) {
+  extern __shared__ float2 cs[];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tile;
+  const int ntok = static_cast<int>(imin64(p.tile, p.tokens - tok0));
+  const int l = threadIdx.x % G, d = p.d;
+  const bool on = l * VEC < d;
+  const float inv_d = 1.f / static_cast<float>(d);
+  const int rows = ntok * (p.heads[0] + p.heads[1]);
+  constexpr int GROUPS = kThreads / G, U = 2;  // U rows a thread in flight
+  const int step = GROUPS * p.splits;
+  fill_angles(p, tok0, ntok, cs);
+  __syncthreads();
+  for (int r0 = threadIdx.x / G + GROUPS * blockIdx.y; r0 < (rows + 3) / 4 * 4; r0 += step * U) {
+    // (a multiple of the 32 / G rows of a warp: whole warps stay for the shuffles)
+    float x[U][VEC];
+    Row row[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * step;
+      row[u] = row_of(p, tok0, ntok, min(r, rows - 1));
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[u][e] = 0.f;
+      if (on && r < rows) load_vec<T, VEC>(static_cast<const T*>(p.x[row[u].which]) + row[u].in + l * VEC, x[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int which = row[u].which;
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s = fmaf(x[u][e], x[u][e], s);
+      s = group_sum<G>(s);
+      const float r = rsqrtf(fmaf(s, inv_d, p.eps));
+      if (p.w[which] && on) {
+        float w[VEC];
+        load_vec<T, VEC>(static_cast<const T*>(p.w[which]) + l * VEC, w);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[u][e] = x[u][e] * r * w[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[u][e] *= r;
+      }
+      turn_vec<VEC>(x[u], cs + row[u].t * p.half, l, p.half, 1.f);
+      const float f = p.scale[which];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[u][e] *= f;
+      if (on && r0 + u * step < rows) store_vec<T, VEC>(static_cast<T*>(p.out[which]) + row[u].out + l * VEC, x[u]);
+    }
+  }
+}
+
+// Adds a CTA's per-thread sums of dw up in a fixed order: dw[2][d] of the CTA.
+__device__ __forceinline__ void store_dw(const Params& p, const float* smem_dw) {
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * p.d; i += kThreads) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s += smem_dw[w * 2 * p.d + i];
+    p.dw_part[static_cast<int64_t>(blockIdx.x) * 2 * p.d + i] = s;
+  }
+}
+
+template <typename T, int VEC, int G>
+__global__ void __launch_bounds__(kThreads)
+rope_bwd_vec_kernel(const __grid_constant__ Params p) {
+  extern __shared__ float2 cs[];
+  float* sdw = reinterpret_cast<float*>(cs + p.tile * p.half);  // [kWarps][2][d]
+  pdl_launch_dependents();
+  pdl_wait();
+  const int l = threadIdx.x % G, d = p.d;
+  const bool on = l * VEC < d;
+  const float inv_d = 1.f / static_cast<float>(d);
+  constexpr int GROUPS = kThreads / G;
+  float dw[2][VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) dw[0][e] = dw[1][e] = 0.f;
+  for (int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tile; tok0 < p.tokens;
+       tok0 += static_cast<int64_t>(gridDim.x) * p.tile) {
+    const int ntok = static_cast<int>(imin64(p.tile, p.tokens - tok0));
+    const int rows = ntok * (p.heads[0] + p.heads[1]);
+    __syncthreads();
+    fill_angles(p, tok0, ntok, cs);
+    __syncthreads();
+    for (int r0 = threadIdx.x / G; r0 < (rows + GROUPS - 1) / GROUPS * GROUPS; r0 += GROUPS) {
+      const bool ok = on && r0 < rows;
+      const Row row = row_of(p, tok0, ntok, min(r0, rows - 1));
+      float x[VEC], g[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[e] = g[e] = 0.f;
+      if (ok) {
+        load_vec<T, VEC>(static_cast<const T*>(p.x[row.which]) + row.in + l * VEC, x);
+        load_vec<T, VEC>(static_cast<const T*>(p.dy[row.which]) + row.out + l * VEC, g);
+      }
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s = fmaf(x[e], x[e], s);
+      s = group_sum<G>(s);
+      const float r = rsqrtf(fmaf(s, inv_d, p.eps));
+      turn_vec<VEC>(g, cs + row.t * p.half, l, p.half, -1.f);
+      const float f = p.scale[row.which];
+      float w[VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) w[e] = 1.f;
+      if (p.w[row.which] && on) load_vec<T, VEC>(static_cast<const T*>(p.w[row.which]) + l * VEC, w);
+      float dot = 0.f;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        g[e] *= f;
+        x[e] *= r;
+        const float c = g[e] * x[e];
+        if (row.which) dw[1][e] += c; else dw[0][e] += c;
+        g[e] *= w[e];
+        dot = fmaf(g[e], x[e], dot);
+      }
+      dot = group_sum<G>(dot) * inv_d;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) g[e] = r * fmaf(-x[e], dot, g[e]);
+      if (ok) store_vec<T, VEC>(static_cast<T*>(p.out[row.which]) + row.flat + l * VEC, g);
+    }
+  }
+#pragma unroll
+  for (int m = G; m < 32; m <<= 1)  // the groups of a warp
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      dw[0][e] += __shfl_xor_sync(0xffffffffu, dw[0][e], m);
+      dw[1][e] += __shfl_xor_sync(0xffffffffu, dw[1][e], m);
+    }
+  if ((threadIdx.x & 31) < G && on) {
+    float* o = sdw + (threadIdx.x >> 5) * 2 * d + l * VEC;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      o[e] = dw[0][e];
+      o[d + e] = dw[1][e];
+    }
+  }
+  store_dw(p, sdw);
+}
+
+// A warp a row. Value slots of a lane: M pairs (a, b), then 2M single values.
+template <typename T, int M>
+struct WarpRow {
+  float a[M], b[M], c[2 * M];
+  __device__ __forceinline__ void load(const T* p, int lane, int half, int d) {
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const int j = lane + 32 * m;
+      a[m] = j < half ? to_f32(p[j]) : 0.f;
+      b[m] = j < half ? to_f32(p[half + j]) : 0.f;
+    }
+#pragma unroll
+    for (int m = 0; m < 2 * M; ++m) {
+      const int j = 2 * half + lane + 32 * m;
+      c[m] = j < d ? to_f32(p[j]) : 0.f;
+    }
+  }
+  __device__ __forceinline__ void store(T* p, int lane, int half, int d) const {
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const int j = lane + 32 * m;
+      if (j < half) {
+        p[j] = from_f32<T>(a[m]);
+        p[half + j] = from_f32<T>(b[m]);
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < 2 * M; ++m) {
+      const int j = 2 * half + lane + 32 * m;
+      if (j < d) p[j] = from_f32<T>(c[m]);
+    }
+  }
+  __device__ __forceinline__ void turn(const float2* cs, int lane, int half, float sign) {
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const int j = lane + 32 * m;
+      if (j < half) {
+        const float2 t = cs[j];
+        const float x = a[m], y = b[m];
+        a[m] = fmaf(x, t.x, -sign * t.y * y);
+        b[m] = fmaf(y, t.x, sign * t.y * x);
+      }
+    }
+  }
+  template <class F>
+  __device__ __forceinline__ void each(F f) {  // f(slot)
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      f(a[m], m);
+      f(b[m], M + m);
+    }
+#pragma unroll
+    for (int m = 0; m < 2 * M; ++m) f(c[m], 2 * M + m);
+  }
+  __device__ __forceinline__ float at(int s) const { return s < M ? a[s] : (s < 2 * M ? b[s - M] : c[s - 2 * M]); }
+};
+
+template <typename T, int M>
+__global__ void __launch_bounds__(kThreads)
+rope_fwd_row_kernel(const __grid_constant__ Params p) {
+  extern __shared__ float2 cs[];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tile;
+  const int ntok = static_cast<int>(imin64(p.tile, p.tokens - tok0));
+  const int lane = threadIdx.x & 31, d = p.d, half = p.half;
+  const float inv_d = 1.f / static_cast<float>(d);
+  const int rows = ntok * (p.heads[0] + p.heads[1]);
+  fill_angles(p, tok0, ntok, cs);
+  __syncthreads();
+  const int step = kWarps * p.splits;
+  for (int r0 = (threadIdx.x >> 5) + kWarps * blockIdx.y; r0 < rows; r0 += 2 * step) {
+    WarpRow<T, M> x[2];
+    Row row[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      row[u] = row_of(p, tok0, ntok, min(r0 + u * step, rows - 1));
+      x[u].load(static_cast<const T*>(p.x[row[u].which]) + row[u].in, lane, half, d);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (r0 + u * step >= rows) break;
+      const int which = row[u].which;
+      float s = 0.f;
+      x[u].each([&](float& v, int) { s = fmaf(v, v, s); });
+      s = group_sum<32>(s);
+      const float r = rsqrtf(fmaf(s, inv_d, p.eps));
+      x[u].each([&](float& v, int) { v *= r; });
+      if (p.w[which]) {
+        WarpRow<T, M> w;
+        w.load(static_cast<const T*>(p.w[which]), lane, half, d);
+        x[u].each([&](float& v, int i) { v *= w.at(i); });
+      }
+      x[u].turn(cs + row[u].t * half, lane, half, 1.f);
+      const float f = p.scale[which];
+      x[u].each([&](float& v, int) { v *= f; });
+      x[u].store(static_cast<T*>(p.out[which]) + row[u].out, lane, half, d);
+    }
+  }
+}
+
+template <typename T, int M>
+__global__ void __launch_bounds__(kThreads)
+rope_bwd_row_kernel(const __grid_constant__ Params p) {
+  extern __shared__ float2 cs[];
+  float* sdw = reinterpret_cast<float*>(cs + p.tile * p.half);  // [kWarps][2][d]
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, d = p.d, half = p.half;
+  const float inv_d = 1.f / static_cast<float>(d);
+  float dw[2][4 * M];
+#pragma unroll
+  for (int i = 0; i < 4 * M; ++i) dw[0][i] = dw[1][i] = 0.f;
+  for (int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tile; tok0 < p.tokens;
+       tok0 += static_cast<int64_t>(gridDim.x) * p.tile) {
+    const int ntok = static_cast<int>(imin64(p.tile, p.tokens - tok0));
+    const int rows = ntok * (p.heads[0] + p.heads[1]);
+    __syncthreads();
+    fill_angles(p, tok0, ntok, cs);
+    __syncthreads();
+    for (int r0 = threadIdx.x >> 5; r0 < rows; r0 += kWarps) {
+      const Row row = row_of(p, tok0, ntok, r0);
+      WarpRow<T, M> x, g;
+      x.load(static_cast<const T*>(p.x[row.which]) + row.in, lane, half, d);
+      g.load(static_cast<const T*>(p.dy[row.which]) + row.out, lane, half, d);
+      float s = 0.f;
+      x.each([&](float& v, int) { s = fmaf(v, v, s); });
+      s = group_sum<32>(s);
+      const float r = rsqrtf(fmaf(s, inv_d, p.eps));
+      x.each([&](float& v, int) { v *= r; });
+      g.turn(cs + row.t * half, lane, half, -1.f);
+      const float f = p.scale[row.which];
+      g.each([&](float& v, int i) {
+        v *= f;
+        if (row.which) dw[1][i] += v * x.at(i); else dw[0][i] += v * x.at(i);
+      });
+      if (p.w[row.which]) {
+        WarpRow<T, M> w;
+        w.load(static_cast<const T*>(p.w[row.which]), lane, half, d);
+        g.each([&](float& v, int i) { v *= w.at(i); });
+      }
+      float dot = 0.f;
+      g.each([&](float& v, int i) { dot = fmaf(v, x.at(i), dot); });
+      dot = group_sum<32>(dot) * inv_d;
+      g.each([&](float& v, int i) { v = r * fmaf(-x.at(i), dot, v); });
+      g.store(static_cast<T*>(p.out[row.which]) + row.flat, lane, half, d);
+    }
+  }
+  WarpRow<float, M> o;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    o.each([&](float& v, int i) { v = dw[which][i]; });
+    o.store(sdw + ((threadIdx.x >> 5) * 2 + which) * d, lane, half, d);
+  }
+  store_dw(p, sdw);
+}
+
+// dw of the queries' and keys' weights from the CTAs' sums, in fp64 and a fixed order.
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+dw_kernel(const float* __restrict__ part, int n, int d, T* __restrict__ dwq, T* __restrict__ dwk) {
+  pdl_launch_dependents();
+  pdl_wait();
+  __shared__ double sum[kWarps][32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
+  double s = 0.0;
+  if (i < 2 * d) {
+#pragma unroll 8
+    for (int c = w; c < n; c += kWarps) s += part[static_cast<int64_t>(c) * 2 * d + i];
+  }
+  sum[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && i < 2 * d) {
+    for (int x = 1; x < kWarps; ++x) s += sum[x][lane];
+    T* o = i < d ? dwq : dwk;
+    if (o) o[i < d ? i : i - d] = from_f32<T>(static_cast<float>(s));
+  }
+}
+
+// ---------------------------------------------------------------------- host
+
+struct Args {
+  const void *q, *k, *wq, *wk;
+  int64_t qs[3], ks[3];
+  const int32_t* pos;
+  int64_t B, N, H, Hkv, d, rot, axes;
+  const int64_t* sections;
+  double base, eps, q_scale, k_scale;
+  la2_dtype dt;
+};
+
+static la2_status check(const Args& a) {
+  if (a.B < 0 || a.N < 0 || a.H < 0 || a.Hkv < 0 || a.d < 1 || a.rot < 0 || a.rot > a.d || a.rot % 2)
+    return LA2_ERR_INVALID_ARG;
+  if (a.dt != LA2_F32 && a.dt != LA2_BF16) return LA2_ERR_INVALID_ARG;
+  if (a.axes < 1 || !(a.base > 0.0) || !(a.eps >= 0.0) || !std::isfinite(a.base) || !std::isfinite(a.eps) ||
+      !std::isfinite(a.q_scale) || !std::isfinite(a.k_scale))
+    return LA2_ERR_INVALID_ARG;
+  if (a.d > kMaxD || a.axes > kMaxAxes) return LA2_ERR_UNSUPPORTED;
+  if (!a.sections && a.axes != 1) return LA2_ERR_INVALID_ARG;
+  if (a.sections) {
+    int64_t sum = 0;
+    for (int i = 0; i < a.axes; ++i) {
+      if (a.sections[i] < 0 || a.sections[i] > a.rot) return LA2_ERR_INVALID_ARG;
+      sum += a.sections[i];
+    }
+    if (sum != a.rot / 2) return LA2_ERR_INVALID_ARG;
+  }
+  for (int i = 0; i < 3; ++i)
+    if (a.qs[i] < 0 || a.ks[i] < 0 || a.qs[i] > (int64_t(1) << 48) || a.ks[i] > (int64_t(1) << 48))
+      return LA2_ERR_INVALID_ARG;
+  if (double(a.B) * double(a.N) * (double(a.H) + double(a.Hkv)) * double(a.d) > 9.0e17) return LA2_ERR_INVALID_ARG;
+  if (a.B > 0x7fffffff || a.N > 0x7fffffff || a.H + a.Hkv > (1 << 20)) return LA2_ERR_UNSUPPORTED;
+  if (double(a.B) * double(a.N) > 2147483647.0) return LA2_ERR_UNSUPPORTED;
+  return LA2_OK;
+}
+
+// Bytes from the first to behind the last element of a strided [B, N, heads, d] slice.
+static size_t extent(const Args& a, const int64_t* s, int64_t heads, size_t es) {
+  if (a.B == 0 || a.N == 0 || heads == 0) return 0;
+  return ((size_t)((a.B - 1) * s[0] + (a.N - 1) * s[1] + (heads - 1) * s[2] + a.d)) * es;
+}
+
+static int bwd_grid(const Args& a, int tile, int sms) {
+  const int64_t tiles = (a.B * a.N + tile - 1) / tile;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tiles, 4 * (int64_t)sms)));
+}
+
+// Tokens of a tile: eight where that still gives every SM four CTAs, else fewer.
+static int tile_of(const Args& a, int sms) {
+  const int64_t t = a.B * a.N / (4 * (int64_t)sms);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(t, kMaxTokens)));
+}
+
+static Params params(const Args& a, int tile) {
+  Params p{};
+  p.x[0] = a.q;
+  p.x[1] = a.k;
+  p.w[0] = a.wq;
+  p.w[1] = a.wk;
+  p.pos = a.pos;
+  p.sb[0] = a.qs[0]; p.sn[0] = a.qs[1]; p.sh[0] = a.qs[2];
+  p.sb[1] = a.ks[0]; p.sn[1] = a.ks[1]; p.sh[1] = a.ks[2];
+  p.N = a.N;
+  p.tokens = a.B * a.N;
+  p.heads[0] = (int)a.H;
+  p.heads[1] = (int)a.Hkv;
+  p.d = (int)a.d;
+  p.half = (int)a.rot / 2;
+  p.tile = tile;
+  p.splits = 1;
+  p.eps = (float)a.eps;
+  p.scale[0] = (float)a.q_scale;
+  p.scale[1] = (float)a.k_scale;
+  int i = 0;
+  for (int ax = 0; ax < a.axes; ++ax)
+    for (int64_t n = a.sections ? a.sections[ax] : a.rot / 2; n > 0; --n, ++i) p.axis[i] = (uint8_t)ax;
+  for (i = 0; i < p.half; ++i)
+    p.turn[i] = std::pow(a.base, -2.0 * i / (double)a.rot) / 6.283185307179586476925286766559;
+  return p;
+}
+
+// Whether rows can be taken in 16-byte pieces whose pair partners are whole pieces.
+static bool vec_ok(const Args& a, const void* const* more, int n) {
+  const int64_t es = a.dt == LA2_BF16 ? 2 : 4, vec = 16 / es;
+  if (a.d % vec || (a.rot / 2) % vec || a.d / vec > 32) return false;
+  for (int i = 0; i < 3; ++i)
+    if (a.qs[i] % vec || a.ks[i] % vec) return false;
+  if (!is_aligned(a.q, 16) || !is_aligned(a.k, 16) || !is_aligned(a.wq, 16) || !is_aligned(a.wk, 16)) return false;
+  for (int i = 0; i < n; ++i)
+    if (!is_aligned(more[i], 16)) return false;
+  return true;
+}
+
+template <typename T>
+static la2_status launch_fwd(const Args& a, Params p, bool vec, int sms, cudaStream_t st) {
+  const int64_t tiles = (p.tokens + p.tile - 1) / p.tile;
+  // few tokens (a decode batch): their heads over several CTAs
+  const int64_t rows = (int64_t)p.tile * (a.H + a.Hkv);
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(2 * sms / tiles, (rows + 15) / 16));
+  const size_t smem = (size_t)p.tile * p.half * sizeof(float2);
+  const dim3 grid((unsigned)tiles, (unsigned)p.splits), block(kThreads);
+  constexpr int VEC = 16 / sizeof(T);
+  void (*kern)(const Params);
+  if (vec)
+    kern = a.d / VEC <= 8 ? rope_fwd_vec_kernel<T, VEC, 8>
+                          : (a.d / VEC <= 16 ? rope_fwd_vec_kernel<T, VEC, 16> : rope_fwd_vec_kernel<T, VEC, 32>);
+  else
+    kern = a.d <= 128 ? rope_fwd_row_kernel<T, 2> : rope_fwd_row_kernel<T, 4>;
+  LaunchTimer t(K_QK_ROPE, st);
+  if (launch_pdl(kern, grid, block, smem, st, p) != cudaSuccess) return LA2_ERR_CUDA;
+  return launch_status();
+}
+
+template <typename T>
+static la2_status launch_bwd(const Args& a, const Params& p, bool vec, int grid, void* dwq, void* dwk,
+                             cudaStream_t st) {
+  const size_t smem = (size_t)p.tile * p.half * sizeof(float2) + (size_t)kWarps * 2 * p.d * sizeof(float);
+  constexpr int VEC = 16 / sizeof(T);
+  void (*kern)(const Params);
+  if (vec)
+    kern = a.d / VEC <= 8 ? rope_bwd_vec_kernel<T, VEC, 8>
+                          : (a.d / VEC <= 16 ? rope_bwd_vec_kernel<T, VEC, 16> : rope_bwd_vec_kernel<T, VEC, 32>);
+  else
+    kern = a.d <= 128 ? rope_bwd_row_kernel<T, 2> : rope_bwd_row_kernel<T, 4>;
+  {
+    LaunchTimer t(K_QK_ROPE_BWD, st);
+    if (launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, p) != cudaSuccess) return LA2_ERR_CUDA;
+    if (dwq || dwk)
+      if (launch_pdl(dw_kernel<T>, dim3((2 * p.d + 31) / 32), dim3(kThreads), 0, st,
+                     static_cast<const float*>(p.dw_part), grid, p.d, static_cast<T*>(dwq),
+                     static_cast<T*>(dwk)) != cudaSuccess)
+        return LA2_ERR_CUDA;
+  }
+  return launch_status();
+}
+
+}  // namespace rope
+}  // namespace la2
+
+extern "C" {
+
+la2_status la2_qk_norm_rope(const void* q, const void* k, const int64_t* q_strides, const int64_t* k_strides,
+                            const void* wq, const void* wk, const int32_t* positions, void* q_out,
+                            void* k_out, int64_t B, int64_t N, int64_t H, int64_t Hkv, int64_t d,
+                            int64_t rot, int64_t n_axes, const int64_t* sections, double base, double eps,
+                            double q_scale, double k_scale, la2_dtype dt, la2_stream_t stream) {
+  if (!q_strides || !k_strides) return LA2_ERR_INVALID_ARG;
+  rope::Args a{q, k, wq, wk, {q_strides[0], q_strides[1], q_strides[2]},
+               {k_strides[0], k_strides[1], k_strides[2]}, positions, B, N, H, Hkv, d, rot, n_axes, sections,
+               base, eps, q_scale, k_scale, dt};
+  la2_status s = rope::check(a);
+  if (s != LA2_OK) return s;
+  if (B == 0 || N == 0 || H + Hkv == 0) return LA2_OK;
+  const size_t es = dt == LA2_BF16 ? 2 : 4;
+  if ((H > 0 && (!q || !q_out)) || (Hkv > 0 && (!k || !k_out))) return LA2_ERR_INVALID_ARG;
+  const void* ptr[6] = {q, k, wq, wk, q_out, k_out};
+  for (const void* x : ptr)
+    if (!is_aligned(x, es)) return LA2_ERR_INVALID_ARG;
+  if (!is_aligned(positions, 4)) return LA2_ERR_INVALID_ARG;
+  const size_t nq = (size_t)B * N * H * d * es, nk = (size_t)B * N * Hkv * d * es;
+  const gated::Span in[5] = {{q, rope::extent(a, a.qs, H, es)}, {k, rope::extent(a, a.ks, Hkv, es)},
+                             {wq, wq ? (size_t)d * es : 0}, {wk, wk ? (size_t)d * es : 0},
+                             {positions, positions ? (size_t)n_axes * B * N * 4 : 0}};
+  for (const gated::Span& x : in)
+    if (x.n && (overlaps(q_out, nq, x.p, x.n) || overlaps(k_out, nk, x.p, x.n))) return LA2_ERR_INVALID_ARG;
+  if (nq && nk && overlaps(q_out, nq, k_out, nk)) return LA2_ERR_INVALID_ARG;
+  const int sms = device_sm_count();
+  if (sms <= 0) return LA2_ERR_CUDA;
+  rope::Params p = rope::params(a, rope::tile_of(a, sms));
+  p.out[0] = q_out;
+  p.out[1] = k_out;
+  const void* outs[2] = {q_out, k_out};
+  const bool vec = rope::vec_ok(a, outs, 2);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return dt == LA2_BF16 ? rope::launch_fwd<__nv_bfloat16>(a, p, vec, sms, st)
+                        : rope::launch_fwd<float>(a, p, vec, sms, st);
+}
+
+size_t la2_qk_norm_rope_backward_workspace_size(int64_t B, int64_t N, int64_t H, int64_t Hkv, int64_t d) {
+  if (B < 0 || N < 0 || H < 0 || Hkv < 0 || d < 1 || d > rope::kMaxD) return (size_t)-1;
+  if (double(B) * double(N) > 2147483647.0) return (size_t)-1;
+  if (B == 0 || N == 0 || H + Hkv == 0) return 0;
+  const int sms = device_sm_count();
+  if (sms <= 0) return (size_t)-1;
+  rope::Args a{};
+  a.B = B;
+  a.N = N;
+  return (size_t)rope::bwd_grid(a, rope::tile_of(a, sms), sms) * 2 * d * sizeof(float);
+}
+
+la2_status la2_qk_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q, const void* k,
+                                     const int64_t* q_strides, const int64_t* k_strides, const void* wq,
+                                     const void* wk, const int32_t* positions, void* dq, void* dk, void* dwq,
+                                     void* dwk, int64_t B, int64_t N, int64_t H, int64_t Hkv, int64_t d,
+                                     int64_t rot, int64_t n_axes, const int64_t* sections, double base,
+                                     double eps, double q_scale, double k_scale, la2_dtype dt,
+                                     void* workspace, size_t workspace_bytes, la2_stream_t stream) {
+  if (!q_strides || !k_strides) return LA2_ERR_INVALID_ARG;
+  rope::Args a{q, k, wq, wk, {q_strides[0], q_strides[1], q_strides[2]},
+               {k_strides[0], k_strides[1], k_strides[2]}, positions, B, N, H, Hkv, d, rot, n_axes, sections,
+               base, eps, q_scale, k_scale, dt};
+  la2_status s = rope::check(a);
+  if (s != LA2_OK) return s;
+  // a weight and its gradient come together
+  if ((wq == nullptr) != (dwq == nullptr) || (wk == nullptr) != (dwk == nullptr)) return LA2_ERR_INVALID_ARG;
+  const size_t es = dt == LA2_BF16 ? 2 : 4;
+  const void* ptr[10] = {dq_out, dk_out, q, k, wq, wk, dq, dk, dwq, dwk};
+  for (const void* x : ptr)
+    if (!is_aligned(x, es)) return LA2_ERR_INVALID_ARG;
+  if (!is_aligned(positions, 4)) return LA2_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (B == 0 || N == 0 || H + Hkv == 0) {  // sums over no rows
+    if (dwq && cudaMemsetAsync(dwq, 0, d * es, st) != cudaSuccess) return LA2_ERR_CUDA;
+    if (dwk && cudaMemsetAsync(dwk, 0, d * es, st) != cudaSuccess) return LA2_ERR_CUDA;
+    return LA2_OK;
+  }
+  if ((H > 0 && (!q || !dq || !dq_out)) || (Hkv > 0 && (!k || !dk || !dk_out))) return LA2_ERR_INVALID_ARG;
+  const int sms = device_sm_count();
+  if (sms <= 0) return LA2_ERR_CUDA;
+  const int tile = rope::tile_of(a, sms), grid = rope::bwd_grid(a, tile, sms);
+  const size_t need = (size_t)grid * 2 * d * sizeof(float);
+  if (!workspace || workspace_bytes < need) return LA2_ERR_WORKSPACE;
+  if (!is_aligned(workspace, 256)) return LA2_ERR_INVALID_ARG;
+  const size_t nq = (size_t)B * N * H * d * es, nk = (size_t)B * N * Hkv * d * es;
+  const gated::Span in[7] = {{q, rope::extent(a, a.qs, H, es)}, {k, rope::extent(a, a.ks, Hkv, es)},
+                             {wq, wq ? (size_t)d * es : 0}, {wk, wk ? (size_t)d * es : 0},
+                             {positions, positions ? (size_t)n_axes * B * N * 4 : 0}, {dq_out, nq}, {dk_out, nk}};
+  const gated::Span out[5] = {{dq, nq}, {dk, nk}, {dwq, dwq ? (size_t)d * es : 0},
+                              {dwk, dwk ? (size_t)d * es : 0}, {workspace, need}};
+  for (int i = 0; i < 5; ++i) {
+    if (!out[i].n) continue;
+    for (const gated::Span& x : in)
+      if (x.n && overlaps(out[i].p, out[i].n, x.p, x.n)) return LA2_ERR_INVALID_ARG;
+    for (int j = i + 1; j < 5; ++j)
+      if (out[j].n && overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return LA2_ERR_INVALID_ARG;
+  }
+  rope::Params p = rope::params(a, tile);
+  p.out[0] = dq;
+  p.out[1] = dk;
+  p.dy[0] = dq_out;
+  p.dy[1] = dk_out;
+  p.dw_part = static_cast<float*>(workspace);
+  const void* more[4] = {dq, dk, dq_out, dk_out};
+  const bool vec = rope::vec_ok(a, more, 4);
+  return dt == LA2_BF16 ? rope::launch_bwd<__nv_bfloat16>(a, p, vec, grid, dwq, dwk, st)
+                        : rope::launch_bwd<float>(a, p, vec, grid, dwq, dwk, st);
+}
+
+}  // extern "C"

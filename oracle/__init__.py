@@ -18,3 +18,12 @@ from .la2_oracle import (  # noqa: F401
     recurrent_forward_decay,
     relative_frobenius,
 )
+from .gated_oracle import (  # noqa: E402,F401
+    backward_gated,
+    forward_gated,
+    kv_state_gated,
+    qk_norm_rope,
+    qk_norm_rope_backward,
+    state_compact,
+    state_copy,
+)
