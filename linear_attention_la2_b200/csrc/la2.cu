@@ -22,6 +22,7 @@
 #include "la2_sm100.cuh"
 #include "la2_sm100_causal.cuh"
 #include "la2_sm100_bwd.cuh"
+#include "la2_gated_sm100.cuh"
 
 namespace la2 {
 

@@ -8,6 +8,7 @@ namespace gated {
 
 struct Plan {
   int64_t L = 0, C = 1;
+  bool tc = false;
   size_t off_suffix = 0, off_tot = 0, off_qdq = 0, off_kdk = 0;  // prefix states at 0
   size_t bytes = 0;
 };
@@ -22,6 +23,7 @@ static la2_status check(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, 
   if (double(B) * double(H) * double(N) * double(std::max(d, dv)) > 9.0e18) return LA2_ERR_INVALID_ARG;
   if (d > 128 || dv > 128) return LA2_ERR_UNSUPPORTED;
   if (dt == LA2_BF16 && ((d != 64 && d != 128) || (dv != 64 && dv != 128))) return LA2_ERR_UNSUPPORTED;
+  if (N > 0x7fffffff - kRows) return LA2_ERR_UNSUPPORTED;  // rows are TMA coordinates
   // one CTA a (sequence, chunk of at least a block), 256 elements of a state a CTA
   const double nb = std::ceil(double(d) * double(dv) / kThreads);
   if (double(B) * double(H) * std::max(std::ceil(double(N) / kRows), nb) > 2147483647.0)
@@ -29,15 +31,35 @@ static la2_status check(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, 
   return LA2_OK;
 }
 
-// Chunks of a sequence run in parallel: about two CTAs an SM, at least two blocks
-// each. In the backward at most 512 rows, over which the gates' gradient is a
-// running difference of row dots (see la2_gated_simt.cuh).
+// Chunks of a sequence run in parallel. CUDA cores: about two CTAs an SM, at least
+// two blocks each; in the backward at most 512 rows, over which the gates' gradient
+// is a running difference of row dots (see la2_gated_simt.cuh). Tensor cores: one CTA
+// an SM, so the count is the one whose waves of CTAs, times blocks a chunk and a fixed
+// cost, are shortest; more than one chunk adds the pass over the chunks' own states.
 static Plan make_plan(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, la2_dtype dt, Need need,
                       int sms) {
   Plan p;
   const int64_t BH = B * H, T = (N + kRows - 1) / kRows;
+  p.tc = dt == LA2_BF16 && d == 128 && dv == 128;
   if (g_chunk_len > 0) {
     p.L = (g_chunk_len + kRows - 1) / kRows * kRows;
+  } else if (p.tc) {
+    constexpr double kFixed = 4.0, kStateFixed = 5.0, kStateBlock = 0.5;  // in blocks of the main pass
+    const int64_t G = std::max(sms, 1), most = std::max<int64_t>(1, T / 2);
+    int64_t best_c = 1;
+    double best = 0.0;
+    for (int64_t c = 1; c <= most && (c == 1 || BH * (c - 1) < 8 * G); ++c) {
+      const double waves = static_cast<double>((BH * c + G - 1) / G), per = static_cast<double>((T + c - 1) / c);
+      double cost = waves * (per + kFixed);
+      if (need == NEED_STATE) cost = waves * (per * kStateBlock + kStateFixed);
+      else if (c > 1)
+        cost += static_cast<double>((BH * (c - 1) + G - 1) / G) * (per * kStateBlock + kStateFixed);
+      if (c == 1 || cost < best) {
+        best = cost;
+        best_c = c;
+      }
+    }
+    p.L = (T + best_c - 1) / best_c * kRows;
   } else {
     const int64_t want = (2 * (int64_t)std::max(sms, 1) + BH - 1) / BH;
     const int64_t C = std::min<int64_t>(want, std::max<int64_t>(1, T / 2));
@@ -103,6 +125,88 @@ static la2_status forward(const void* q, const void* k, const void* v, const voi
       static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
       static_cast<const T*>(gate), static_cast<T*>(o), states, sh);
   return launch_status();
+}
+
+// Tensor cores: chunk states of the chunks that another one starts from (all of them
+// after a prefill), then their scan.
+static la2_status states_tc(const void* y, const void* z, const void* gate, float* out, double* tot, int64_t BH,
+                            const Shape& sh, bool suffix, bool all, cudaStream_t st) {
+  TcStateParams p{};
+  p.gate = static_cast<const __nv_bfloat16*>(gate);
+  p.out = out;
+  p.tot = tot;
+  p.N = sh.N;
+  p.L = sh.L;
+  p.C = sh.C;
+  p.first = suffix ? 1 : 0;
+  p.count = all ? sh.C : sh.C - 1;
+  p.spin_limit = spin_limit();
+  {
+    LaunchTimer t(K_GATED_STATE, st);
+    if ((suffix ? launch_state_sm100<true>(y, z, p, BH, st) : launch_state_sm100<false>(y, z, p, BH, st)) != cudaSuccess)
+      return LA2_ERR_CUDA;
+  }
+  const la2_status s = launch_status();
+  return s != LA2_OK || all ? s : scan(out, tot, BH, sh, suffix ? 1 : 0, st);
+}
+
+static TcParams tc_params(const void* gate, const float* init, const Shape& sh) {
+  TcParams p{};
+  p.gate = static_cast<const __nv_bfloat16*>(gate);
+  p.init = init;
+  p.N = sh.N;
+  p.L = sh.L;
+  p.C = sh.C;
+  p.spin_limit = spin_limit();
+  return p;
+}
+
+static la2_status forward_tc(const void* q, const void* k, const void* v, const void* gate, void* o, char* ws,
+                             const Plan& p, int64_t BH, const Shape& sh, cudaStream_t st) {
+  float* states = p.C > 1 ? reinterpret_cast<float*>(ws) : nullptr;
+  if (states) {
+    const la2_status s = states_tc(k, v, gate, states, reinterpret_cast<double*>(ws + p.off_tot), BH, sh, false, false, st);
+    if (s != LA2_OK) return s;
+  }
+  LaunchTimer t(K_GATED_FWD, st);
+  if (launch_sm100<false, false>(q, k, v, o, tc_params(gate, states, sh), BH, st) != cudaSuccess) return LA2_ERR_CUDA;
+  return launch_status();
+}
+
+template <typename T>
+static la2_status gate_grad(const void* gate, const float* qdq, const float* kdk, const float* prefix,
+                            const float* suffix, void* dgate, int64_t BH, const Shape& sh, cudaStream_t st);
+
+static la2_status backward_tc(const void* q, const void* k, const void* v, const void* gate, const void* dout,
+                              void* dq, void* dk, void* dvv, void* dgate, char* ws, const Plan& p, int64_t BH,
+                              const Shape& sh, cudaStream_t st) {
+  float* prefix = p.C > 1 ? reinterpret_cast<float*>(ws) : nullptr;
+  float* suffix = p.C > 1 ? reinterpret_cast<float*>(ws + p.off_suffix) : nullptr;
+  float* qdq = reinterpret_cast<float*>(ws + p.off_qdq);
+  float* kdk = reinterpret_cast<float*>(ws + p.off_kdk);
+  la2_status s = LA2_OK;
+  if (prefix) {
+    double* tot = reinterpret_cast<double*>(ws + p.off_tot);
+    if ((s = states_tc(k, v, gate, prefix, tot, BH, sh, false, false, st)) != LA2_OK) return s;
+    if ((s = states_tc(q, dout, gate, suffix, tot, BH, sh, true, false, st)) != LA2_OK) return s;
+  }
+  {
+    TcParams t = tc_params(gate, prefix, sh);
+    t.dot_x = static_cast<const __nv_bfloat16*>(q);
+    t.dots = qdq;
+    LaunchTimer lt(K_GATED_DQ, st);
+    if (launch_sm100<false, true>(dout, v, k, dq, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
+  }
+  {
+    TcParams t = tc_params(gate, suffix, sh);
+    LaunchTimer lt(K_GATED_DKDV, st);
+    if (launch_sm100<true, false>(k, q, dout, dvv, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
+    t.dot_x = static_cast<const __nv_bfloat16*>(k);
+    t.dots = kdk;
+    if (launch_sm100<true, true>(v, dout, q, dk, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
+  }
+  if ((s = launch_status()) != LA2_OK) return s;
+  return gate_grad<__nv_bfloat16>(gate, qdq, kdk, prefix, suffix, dgate, BH, sh, st);
 }
 
 template <typename T>
@@ -219,6 +323,7 @@ la2_status la2_forward_gated(const void* q, const void* k, const void* v, const 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const gated::Shape sh{N, p.L, p.C, (int)d, (int)dv};
   char* ws = static_cast<char*>(workspace);
+  if (p.tc) return gated::forward_tc(q, k, v, gate, o, ws, p, B * H, sh, st);
   return dt == LA2_BF16 ? gated::forward<__nv_bfloat16>(q, k, v, gate, o, ws, p, B * H, sh, st)
                         : gated::forward<float>(q, k, v, gate, o, ws, p, B * H, sh, st);
 }
@@ -243,6 +348,7 @@ la2_status la2_backward_gated(const void* q, const void* k, const void* v, const
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const gated::Shape sh{N, p.L, p.C, (int)d, (int)dv};
   char* ws = static_cast<char*>(workspace);
+  if (p.tc) return gated::backward_tc(q, k, v, gate, dout, dq, dk, dvv, dgate, ws, p, B * H, sh, st);
   return dt == LA2_BF16
              ? gated::backward<__nv_bfloat16>(q, k, v, gate, dout, dq, dk, dvv, dgate, ws, p, B * H, sh, st)
              : gated::backward<float>(q, k, v, gate, dout, dq, dk, dvv, dgate, ws, p, B * H, sh, st);
@@ -277,14 +383,17 @@ la2_status la2_kv_state_gated(const void* k, const void* v, const void* gate, fl
   const gated::Shape sh{N, p.L, p.C, (int)d, (int)dv};
   float* chunks = static_cast<float*>(workspace);
   double* tot = reinterpret_cast<double*>(static_cast<char*>(workspace) + p.off_tot);
-  s = dt == LA2_BF16 ? gated::chunk_states<__nv_bfloat16, false>(k, v, gate, chunks, tot, B * H, sh, st)
-                     : gated::chunk_states<float, false>(k, v, gate, chunks, tot, B * H, sh, st);
+  if (p.tc)
+    s = gated::states_tc(k, v, gate, chunks, tot, B * H, sh, false, true, st);
+  else
+    s = dt == LA2_BF16 ? gated::chunk_states<__nv_bfloat16, false>(k, v, gate, chunks, tot, B * H, sh, st)
+                       : gated::chunk_states<float, false>(k, v, gate, chunks, tot, B * H, sh, st);
   if (s != LA2_OK) return s;
   const int64_t nb = (d * dv + gated::kThreads - 1) / gated::kThreads;
   LaunchTimer t(K_GATED_POOL, st);
   if (launch_pdl(gated::pool_update_kernel, dim3((unsigned)(B * H * nb)), dim3(gated::kThreads), 0, st,
                  static_cast<const float*>(chunks), static_cast<const double*>(tot), state, slots, n_slots,
-                 p.C, (int)H, (int)d, (int)dv, 0) != cudaSuccess)
+                 p.C, (int)H, (int)d, (int)dv, p.tc ? 1 : 0) != cudaSuccess)
     return LA2_ERR_CUDA;
   return launch_status();
 }
