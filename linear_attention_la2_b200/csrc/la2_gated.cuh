@@ -9,9 +9,14 @@ namespace gated {
 struct Plan {
   int64_t L = 0, C = 1;
   bool tc = false;
+  // Tensor cores: the pieces whose own states are computed (Ls rows, K a sequence,
+  // `per` a chunk); per = 0 (and K = C): a scan turns them into the chunks' states.
+  int64_t Ls = 0, K = 1, per = 0;
   size_t off_suffix = 0, off_tot = 0, off_qdq = 0, off_kdk = 0;  // prefix states at 0
   size_t bytes = 0;
 };
+
+constexpr int64_t kSumPieces = 8;  // pieces a chunk adds up itself; more are scanned
 
 enum Need { NEED_FWD, NEED_BWD, NEED_STATE };
 
@@ -41,25 +46,35 @@ static Plan make_plan(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, la
   Plan p;
   const int64_t BH = B * H, T = (N + kRows - 1) / kRows;
   p.tc = dt == LA2_BF16 && d == 128 && dv == 128;
+  int64_t per = 1;
   if (g_chunk_len > 0) {
     p.L = (g_chunk_len + kRows - 1) / kRows * kRows;
   } else if (p.tc) {
-    constexpr double kFixed = 4.0, kStateFixed = 5.0, kStateBlock = 0.5;  // in blocks of the main pass
+    // in blocks of the main pass: what a launch of it and of the state pass costs
+    // beside its blocks, a block of the state pass, and the scan
+    constexpr double kFixed = 5.0, kStateFixed = 5.0, kStateBlock = 0.5, kScan = 5.0;
     const int64_t G = std::max(sms, 1), most = std::max<int64_t>(1, T / 2);
+    auto waves = [&](int64_t units) { return static_cast<double>((units + G - 1) / G); };
+    auto blocks = [&](int64_t parts) { return static_cast<double>((T + parts - 1) / parts); };
     int64_t best_c = 1;
     double best = 0.0;
     for (int64_t c = 1; c <= most && (c == 1 || BH * (c - 1) < 8 * G); ++c) {
-      const double waves = static_cast<double>((BH * c + G - 1) / G), per = static_cast<double>((T + c - 1) / c);
-      double cost = waves * (per + kFixed);
-      if (need == NEED_STATE) cost = waves * (per * kStateBlock + kStateFixed);
-      else if (c > 1)
-        cost += static_cast<double>((BH * (c - 1) + G - 1) / G) * (per * kStateBlock + kStateFixed);
+      double cost = need == NEED_STATE ? 0.0 : waves(BH * c) * (blocks(c) + kFixed);
+      int64_t m = 1;
+      if (need == NEED_STATE) {
+        cost = waves(BH * c) * (blocks(c) * kStateBlock + kStateFixed);
+      } else if (c > 1) {
+        m = std::max<int64_t>(1, std::min<int64_t>(G / (BH * (c - 1)), std::min<int64_t>(kSumPieces, T) / c));
+        cost += waves(BH * (c - 1) * m) * (blocks(c * m) * kStateBlock + kStateFixed) + (c > kSumPieces ? kScan : 0.0);
+      }
       if (c == 1 || cost < best) {
         best = cost;
         best_c = c;
+        per = m;
       }
     }
-    p.L = (T + best_c - 1) / best_c * kRows;
+    p.Ls = (T + best_c * per - 1) / (best_c * per) * kRows;
+    p.L = p.Ls * per;
   } else {
     const int64_t want = (2 * (int64_t)std::max(sms, 1) + BH - 1) / BH;
     const int64_t C = std::min<int64_t>(want, std::max<int64_t>(1, T / 2));
@@ -68,13 +83,19 @@ static Plan make_plan(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, la
   }
   p.L = std::max<int64_t>(p.L, kRows);
   p.C = std::max<int64_t>(1, (N + p.L - 1) / p.L);
+  p.K = p.C;
+  if (p.tc && p.Ls == 0) p.Ls = p.L;
+  if (p.tc && need != NEED_STATE) {
+    p.K = std::max<int64_t>(1, (N + p.Ls - 1) / p.Ls);
+    p.per = p.K <= kSumPieces ? p.L / p.Ls : 0;
+  }
   const bool states = p.C > 1 || need == NEED_STATE;
-  const size_t one = states ? round256((size_t)BH * p.C * d * dv * sizeof(float)) : 0;
+  const size_t one = states ? round256((size_t)BH * p.K * d * dv * sizeof(float)) : 0;
   size_t at = one;
   p.off_suffix = at;
   if (need == NEED_BWD) at += one;
   p.off_tot = at;
-  if (states) at += round256((size_t)BH * p.C * sizeof(double));
+  if (states) at += round256((size_t)BH * p.K * sizeof(double));
   p.off_qdq = at;
   if (need == NEED_BWD) at += round256((size_t)BH * N * sizeof(float));
   p.off_kdk = at;
@@ -127,19 +148,20 @@ static la2_status forward(const void* q, const void* k, const void* v, const voi
   return launch_status();
 }
 
-// Tensor cores: chunk states of the chunks that another one starts from (all of them
-// after a prefill), then their scan.
+// Tensor cores: states of the pieces that a chunk starts from (all of them after a
+// prefill), and their scan where the chunks do not add them up.
 static la2_status states_tc(const void* y, const void* z, const void* gate, float* out, double* tot, int64_t BH,
-                            const Shape& sh, bool suffix, bool all, cudaStream_t st) {
+                            const Shape& sh, const Plan& pl, bool suffix, bool all, cudaStream_t st) {
+  const int64_t per = std::max<int64_t>(1, pl.per);
   TcStateParams p{};
   p.gate = static_cast<const __nv_bfloat16*>(gate);
   p.out = out;
   p.tot = tot;
   p.N = sh.N;
-  p.L = sh.L;
-  p.C = sh.C;
-  p.first = suffix ? 1 : 0;
-  p.count = all ? sh.C : sh.C - 1;
+  p.L = pl.Ls;
+  p.K = pl.K;
+  p.first = suffix ? per : 0;
+  p.count = all ? pl.K : suffix ? pl.K - per : (pl.C - 1) * per;
   p.spin_limit = spin_limit();
   {
     LaunchTimer t(K_GATED_STATE, st);
@@ -147,35 +169,41 @@ static la2_status states_tc(const void* y, const void* z, const void* gate, floa
       return LA2_ERR_CUDA;
   }
   const la2_status s = launch_status();
-  return s != LA2_OK || all ? s : scan(out, tot, BH, sh, suffix ? 1 : 0, st);
+  return s != LA2_OK || all || pl.per > 0 ? s : scan(out, tot, BH, sh, suffix ? 1 : 0, st);
 }
 
-static TcParams tc_params(const void* gate, const float* init, const Shape& sh) {
+static TcParams tc_params(const void* gate, const float* init, const double* tot, const Shape& sh, const Plan& pl) {
   TcParams p{};
   p.gate = static_cast<const __nv_bfloat16*>(gate);
   p.init = init;
+  p.tot = tot;
   p.N = sh.N;
   p.L = sh.L;
   p.C = sh.C;
   p.spin_limit = spin_limit();
+  p.K = static_cast<int32_t>(pl.K);
+  p.per = static_cast<int32_t>(pl.per);
   return p;
 }
 
 static la2_status forward_tc(const void* q, const void* k, const void* v, const void* gate, void* o, char* ws,
                              const Plan& p, int64_t BH, const Shape& sh, cudaStream_t st) {
   float* states = p.C > 1 ? reinterpret_cast<float*>(ws) : nullptr;
+  double* tot = reinterpret_cast<double*>(ws + p.off_tot);
   if (states) {
-    const la2_status s = states_tc(k, v, gate, states, reinterpret_cast<double*>(ws + p.off_tot), BH, sh, false, false, st);
+    const la2_status s = states_tc(k, v, gate, states, tot, BH, sh, p, false, false, st);
     if (s != LA2_OK) return s;
   }
   LaunchTimer t(K_GATED_FWD, st);
-  if (launch_sm100<false, false>(q, k, v, o, tc_params(gate, states, sh), BH, st) != cudaSuccess) return LA2_ERR_CUDA;
+  if (launch_sm100<false, false>(q, k, v, o, nullptr, tc_params(gate, states, tot, sh, p), BH, st) != cudaSuccess)
+    return LA2_ERR_CUDA;
   return launch_status();
 }
 
 template <typename T>
 static la2_status gate_grad(const void* gate, const float* qdq, const float* kdk, const float* prefix,
-                            const float* suffix, void* dgate, int64_t BH, const Shape& sh, cudaStream_t st);
+                            const float* suffix, const double* tot, void* dgate, int64_t BH, const Shape& sh,
+                            const Plan& p, cudaStream_t st);
 
 static la2_status backward_tc(const void* q, const void* k, const void* v, const void* gate, const void* dout,
                               void* dq, void* dk, void* dvv, void* dgate, char* ws, const Plan& p, int64_t BH,
@@ -184,38 +212,37 @@ static la2_status backward_tc(const void* q, const void* k, const void* v, const
   float* suffix = p.C > 1 ? reinterpret_cast<float*>(ws + p.off_suffix) : nullptr;
   float* qdq = reinterpret_cast<float*>(ws + p.off_qdq);
   float* kdk = reinterpret_cast<float*>(ws + p.off_kdk);
+  double* tot = reinterpret_cast<double*>(ws + p.off_tot);
   la2_status s = LA2_OK;
   if (prefix) {
-    double* tot = reinterpret_cast<double*>(ws + p.off_tot);
-    if ((s = states_tc(k, v, gate, prefix, tot, BH, sh, false, false, st)) != LA2_OK) return s;
-    if ((s = states_tc(q, dout, gate, suffix, tot, BH, sh, true, false, st)) != LA2_OK) return s;
+    if ((s = states_tc(k, v, gate, prefix, tot, BH, sh, p, false, false, st)) != LA2_OK) return s;
+    if ((s = states_tc(q, dout, gate, suffix, tot, BH, sh, p, true, false, st)) != LA2_OK) return s;
   }
   {
-    TcParams t = tc_params(gate, prefix, sh);
-    t.dot_x = static_cast<const __nv_bfloat16*>(q);
+    TcParams t = tc_params(gate, prefix, tot, sh, p);
     t.dots = qdq;
     LaunchTimer lt(K_GATED_DQ, st);
-    if (launch_sm100<false, true>(dout, v, k, dq, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
+    if (launch_sm100<false, true>(dout, v, k, dq, q, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
   }
   {
-    TcParams t = tc_params(gate, suffix, sh);
+    TcParams t = tc_params(gate, suffix, tot, sh, p);
     LaunchTimer lt(K_GATED_DKDV, st);
-    if (launch_sm100<true, false>(k, q, dout, dvv, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
-    t.dot_x = static_cast<const __nv_bfloat16*>(k);
+    if (launch_sm100<true, false>(k, q, dout, dvv, nullptr, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
     t.dots = kdk;
-    if (launch_sm100<true, true>(v, dout, q, dk, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
+    if (launch_sm100<true, true>(v, dout, q, dk, k, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
   }
   if ((s = launch_status()) != LA2_OK) return s;
-  return gate_grad<__nv_bfloat16>(gate, qdq, kdk, prefix, suffix, dgate, BH, sh, st);
+  return gate_grad<__nv_bfloat16>(gate, qdq, kdk, prefix, suffix, tot, dgate, BH, sh, p, st);
 }
 
 template <typename T>
 static la2_status gate_grad(const void* gate, const float* qdq, const float* kdk, const float* prefix,
-                            const float* suffix, void* dgate, int64_t BH, const Shape& sh, cudaStream_t st) {
+                            const float* suffix, const double* tot, void* dgate, int64_t BH, const Shape& sh,
+                            const Plan& p, cudaStream_t st) {
   LaunchTimer t(K_GATED_GATE, st);
   if (launch_pdl(gate_grad_kernel<T>, dim3((unsigned)(BH * sh.C)), dim3(kThreads), 0, st,
-                 static_cast<const T*>(gate), qdq, kdk, prefix, suffix, static_cast<T*>(dgate), sh.N, sh.L,
-                 sh.C, sh.d * sh.dv) != cudaSuccess)
+                 static_cast<const T*>(gate), qdq, kdk, prefix, suffix, tot, static_cast<T*>(dgate), sh.N,
+                 sh.L, sh.C, sh.d * sh.dv, p.K, p.per) != cudaSuccess)
     return LA2_ERR_CUDA;
   return launch_status();
 }
@@ -228,9 +255,9 @@ static la2_status backward(const void* q, const void* k, const void* v, const vo
   float* suffix = p.C > 1 ? reinterpret_cast<float*>(ws + p.off_suffix) : nullptr;
   float* qdq = reinterpret_cast<float*>(ws + p.off_qdq);
   float* kdk = reinterpret_cast<float*>(ws + p.off_kdk);
+  double* tot = reinterpret_cast<double*>(ws + p.off_tot);
   la2_status s = LA2_OK;
   if (prefix) {
-    double* tot = reinterpret_cast<double*>(ws + p.off_tot);
     if ((s = chunk_states<T, false>(k, v, gate, prefix, tot, BH, sh, st)) != LA2_OK) return s;
     if ((s = scan(prefix, tot, BH, sh, 0, st)) != LA2_OK) return s;
     if ((s = chunk_states<T, true>(q, dout, gate, suffix, tot, BH, sh, st)) != LA2_OK) return s;
@@ -254,7 +281,7 @@ static la2_status backward(const void* q, const void* k, const void* v, const vo
                                                      static_cast<T*>(dvv), kdk, suffix, sh);
   }
   if ((s = launch_status()) != LA2_OK) return s;
-  return gate_grad<T>(gate, qdq, kdk, prefix, suffix, dgate, BH, sh, st);
+  return gate_grad<T>(gate, qdq, kdk, prefix, suffix, tot, dgate, BH, sh, p, st);
 }
 
 // Pointers of a call: every one non-null and aligned, no output over an input,
@@ -384,7 +411,7 @@ la2_status la2_kv_state_gated(const void* k, const void* v, const void* gate, fl
   float* chunks = static_cast<float*>(workspace);
   double* tot = reinterpret_cast<double*>(static_cast<char*>(workspace) + p.off_tot);
   if (p.tc)
-    s = gated::states_tc(k, v, gate, chunks, tot, B * H, sh, false, true, st);
+    s = gated::states_tc(k, v, gate, chunks, tot, B * H, sh, p, false, true, st);
   else
     s = dt == LA2_BF16 ? gated::chunk_states<__nv_bfloat16, false>(k, v, gate, chunks, tot, B * H, sh, st)
                        : gated::chunk_states<float, false>(k, v, gate, chunks, tot, B * H, sh, st);

@@ -134,13 +134,16 @@ __device__ __forceinline__ void load_rows(float* dst, const T* __restrict__ src,
 }
 
 // The block's gate sums: c[t] for t < kRows (rows behind the last one repeat it)
-// and the weights e^(c_t) and e^(c_R - c_t). Ends with a barrier.
+// and the weights e^(c_t) and e^(c_R - c_t). `start`: the block opens its sequence,
+// where nothing comes before the first token for its gate to pass on (0, unless NaN).
+// Ends with a barrier.
 template <typename T>
-__device__ __forceinline__ void gate_tables(const T* __restrict__ gate, int rows, double* c, float* head,
-                                            float* tail) {
+__device__ __forceinline__ void gate_tables(const T* __restrict__ gate, int rows, bool start, double* c,
+                                            float* head, float* tail) {
   if (threadIdx.x < 32) {
     const int i = 2 * threadIdx.x;
-    const double x = i < rows ? gate_log(to_f32(gate[i])) : 0.0;
+    double x = i < rows ? gate_log(to_f32(gate[i])) : 0.0;
+    if (start && i == 0 && x == x) x = 0.0;
     const double y = i + 1 < rows ? gate_log(to_f32(gate[i + 1])) : 0.0;
     double s = x + y;
 #pragma unroll
@@ -222,7 +225,7 @@ chunk_state_kernel(const T* __restrict__ a, const T* __restrict__ b, const T* __
     __syncthreads();
     load_rows(As, a + (bh * sh.N + i0) * sh.d, rows, sh.d);
     load_rows(Bs, b + (bh * sh.N + i0) * sh.dv, rows, sh.dv);
-    gate_tables(gate + bh * sh.N + i0, rows, c, head, tail);
+    gate_tables(gate + bh * sh.N + i0, rows, false, c, head, tail);
     sum += c[kRows - 1];
     const float whole = head[kRows - 1];
     const float* w = SUFFIX ? head : tail;
@@ -257,7 +260,7 @@ fwd_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict
     load_rows(Qs, q + row * d, rows, d);
     load_rows(Ks, k + row * d, rows, d);
     load_rows(Vs, v + row * dv, rows, dv);
-    gate_tables(gate + row, rows, c, head, tail);
+    gate_tables(gate + row, rows, i0 == 0, c, head, tail);
     tile_product(
         rows, rows, d, [&](int r, int x) { return Qs[r * ld + x]; }, [&](int x, int j) { return Ks[j * ld + x]; },
         One1{}, 0, Zero2{}, Zero2{},
@@ -308,7 +311,7 @@ bwd_dq_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restr
     load_rows(Vs, v + row * dv, rows, dv);
     load_rows(Gs, dout + row * dv, rows, dv);
     if (threadIdx.x < kRows) dots[threadIdx.x] = 0.f;
-    gate_tables(gate + row, rows, c, head, tail);
+    gate_tables(gate + row, rows, i0 == 0, c, head, tail);
     tile_product(
         rows, rows, dv, [&](int r, int x) { return Gs[r * lv + x]; }, [&](int x, int j) { return Vs[j * lv + x]; },
         One1{}, 0, Zero2{}, Zero2{},
@@ -369,7 +372,7 @@ bwd_dkdv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __res
     load_rows(Vs, v + row * dv, rows, dv);
     load_rows(Gs, dout + row * dv, rows, dv);
     if (threadIdx.x < kRows) dots[threadIdx.x] = 0.f;
-    gate_tables(gate + row, rows, c, head, tail);
+    gate_tables(gate + row, rows, i0 == 0, c, head, tail);
     // P[t][j] = D (q_t . k_j), then dV; the same tile then holds D (dO_t . v_j) for dK
     tile_product(
         rows, rows, d, [&](int r, int x) { return Qs[r * ld + x]; }, [&](int x, int j) { return Ks[j * ld + x]; },
@@ -495,14 +498,16 @@ pool_update_kernel(const float* __restrict__ chunks, const double* __restrict__ 
 }
 
 // dl_t = flow at the chunk's end + sum over the chunk's rows from t on of
-// (q . dq - k . dk). The flow at the end of chunk c is <state before chunk c + 1,
-// U behind chunk c> (0 for the last chunk); elements in any common order. One CTA
-// a (sequence, chunk).
+// (q . dq - k . dk). The flow at the end of chunk c is <state before chunk c + 1, U
+// behind chunk c> (0 for the last chunk); elements in any common order. One CTA a
+// (sequence, chunk). `per` = 0: prefix and suffix hold those states, scanned;
+// otherwise they hold K pieces' own states, `per` a chunk, and are summed here.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 gate_grad_kernel(const T* __restrict__ gate, const float* __restrict__ qdq, const float* __restrict__ kdk,
-                 const float* __restrict__ prefix, const float* __restrict__ suffix, T* __restrict__ dgate,
-                 int64_t N, int64_t L, int64_t C, int nel) {
+                 const float* __restrict__ prefix, const float* __restrict__ suffix,
+                 const double* __restrict__ tot, T* __restrict__ dgate, int64_t N, int64_t L, int64_t C, int nel,
+                 int64_t K, int64_t per) {
   pdl_launch_dependents();
   pdl_wait();
   __shared__ double part[kThreads / 32];
@@ -511,10 +516,24 @@ gate_grad_kernel(const T* __restrict__ gate, const float* __restrict__ qdq, cons
   const int64_t t0 = ch * L, t1 = imin64(N, t0 + L);
   double carry = 0.0;
   if (ch + 1 < C) {
-    const float* a = prefix + (bh * C + ch + 1) * nel;
-    const float* b = suffix + (bh * C + ch) * nel;
+    const int64_t edge = (ch + 1) * per;  // first piece behind the chunk
+    const int64_t n_pre = per ? edge : 1, n_suf = per ? K - edge : 1;
+    const float* a = prefix + (bh * K + (per ? edge - 1 : ch + 1)) * nel;
+    const float* b = suffix + (bh * K + (per ? edge : ch)) * nel;
     double x = 0.0;
-    for (int i = threadIdx.x; i < nel; i += kThreads) x += static_cast<double>(a[i]) * b[i];
+    for (int i = threadIdx.x; i < nel; i += kThreads) {
+      float u = 0.f, v = 0.f, f = 1.f;
+      for (int64_t j = 0; j < n_pre; ++j) {  // nearest first, each decayed over the nearer ones
+        u = fmaf(f, a[i - j * nel], u);
+        if (j + 1 < n_pre) f *= expf(static_cast<float>(tot[bh * K + edge - 1 - j]));
+      }
+      f = 1.f;
+      for (int64_t j = 0; j < n_suf; ++j) {
+        v = fmaf(f, b[i + j * nel], v);
+        if (j + 1 < n_suf) f *= expf(static_cast<float>(tot[bh * K + edge + j]));
+      }
+      x += static_cast<double>(u) * v;
+    }
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
     if (lane == 0) part[w] = x;

@@ -12,20 +12,21 @@
 //   dK        v   dO  q    back      s >= t   e^(c_s - c_t)      U, read transposed
 //
 // Per block of 64 rows, walking a chunk of one (b, h) sequence in one CTA:
-//   S     = X Y^T                      tcgen05 -> TMEM
+//   S     = X Y^T                      tcgen05 -> TMEM (two buffers)
 //   P     = bf16(S w)                  mask warps, TMEM -> shared memory
-//   near  = P Z                        tcgen05 -> TMEM
-//   far   = X state                    tcgen05 -> TMEM, from a bf16 copy of the state
+//   near  = Z^T P^T                    tcgen05 -> TMEM, transposed: M = 128 lanes,
+//   far   = state^T X^T                64 columns each, so two buffers of both fit
 //   out   = head far + near            epilogue warps: the row's e^(c_t) (walking
 //                                      back e^(c_R - c_t)) is applied in fp32
-//   state <- e^(c_R) state + Y~^T Z    tcgen05, Y~ = bf16 rows scaled by e^(c_R - c_s)
+//   state <- e^(c_R) state + Y~^T Z    tcgen05, Y~ = rows scaled by e^(c_R - c_s)
 //                                      (walking back e^(c_s))
-// X and Y stay unscaled in shared memory: Y~ is a copy that two warps make as soon
-// as the tile has landed, off the path S -> P -> near, and X needs no scaling since
-// far and near are separate accumulators. The state stays in TMEM: the state warps
-// read it once a block, write its bf16 copy and put e^(c_R) times it back, which the
-// block's update adds onto. S of the next block is issued before P of this one is
-// waited for.
+// far and near are separate accumulators, so X needs no scaling. Y~ is made in place
+// once S has read Y, as a bf16 value there and its bf16 remainder beside it (two
+// MMAs): one rounding fewer in the outputs, and states good to 2^-17. The state stays
+// in TMEM: the state warps read it once a block, write its bf16 copy for far, and put
+// e^(c_R) times it back, which the block's update adds onto. The loop-carried path is
+// update -> copy -> update; S of the next block is issued before P of this one is
+// waited for, and the accumulators' second buffer lets the epilogue trail a block.
 //
 // Gate sums: c in base 2, fp32, at most 64 terms; a log gate under kLog2Zero (in
 // base 2) counts as that, its exponential is 0, so a restart cuts exactly and costs
@@ -35,8 +36,8 @@
 // unrounded rows) for the gates' gradient, a running difference of them: their
 // errors have to cancel over a chunk. P is rounded alike in both passes (the same
 // products, the same weights), so the near parts agree; for the far parts the state's
-// copy and Y~ are kept as two bf16 tiles, value and remainder (2^-17 instead of 2^-9;
-// a second MMA each, into the same accumulator).
+// copy is kept as value and remainder too (2^-17 instead of 2^-9). The dots' rows are
+// loaded into the output's staging tile, read there and overwritten by the output.
 #pragma once
 
 #include "la2_gated_simt.cuh"
@@ -51,7 +52,7 @@ constexpr int kTile = 64 * 128 * 2;       // one 64 x 128 bf16 tile
 constexpr int kCopy = 128 * 128 * 2;      // the state's bf16 copy
 constexpr float kLog2Zero = -160.f;
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kTabs = 4;                  // gate tables in flight (see the table warp)
+constexpr int kTabs = 8;                  // gate tables in flight (see the table warp)
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -80,54 +81,73 @@ __device__ __forceinline__ void warp_sums(float x, float y, int lane, float& a, 
 
 struct TcParams {
   const __nv_bfloat16* gate;   // [BH][N]
-  const float* init;           // [BH][C][128*128] (state_f4): state next to each chunk, or null
-  const __nv_bfloat16* dot_x;  // GRAD: [BH][N][128], the rows of the dots
+  const float* init;           // [BH][K][128*128] (state_f4): states of the sequence's pieces, or null
+  const double* tot;           // [BH][K]: sums of their gates
   float* dots;                 // GRAD: [BH][N]
   int64_t N, L, C, spin_limit;
+  // Pieces: `per` a chunk; a chunk starts from all pieces before it (walking back:
+  // behind it), each decayed over those between. per = 0: init holds one state a
+  // chunk, scanned already.
+  int32_t K, per;
 };
 
 template <bool GRAD>
 struct TcCfg {
   static constexpr int KS = GRAD ? 2 : 3;          // stages of X, Y, Z
-  static constexpr int PARTS = GRAD ? 2 : 1;       // bf16 tiles of Y~ and of the state's copy
-  static constexpr int OFF_Y2 = KS * 3 * kTile;
-  static constexpr int OFF_P = OFF_Y2 + PARTS * kTile;
+  static constexpr int PARTS = GRAD ? 2 : 1;       // bf16 tiles of the state's copy
+  static constexpr int OB = GRAD ? 2 : 1;          // staging tiles of the output
+  static constexpr int OFF_LO = KS * 3 * kTile;    // remainder of Y~
+  static constexpr int OFF_P = OFF_LO + kTile;
   static constexpr int OFF_COPY = OFF_P + 64 * 64 * 2;
   static constexpr int OFF_OUT = OFF_COPY + PARTS * kCopy;
-  static constexpr int OFF_TAB = OFF_OUT + kTile;
-  static constexpr int OFF_BAR = OFF_TAB + kTabs * 64 * 4;
-  static constexpr int NBAR = 2 * KS + 2 + 2 + 2 + 2 + 2 + 2 + kTabs + 1;
+  static constexpr int OFF_TAB = OFF_OUT + OB * kTile;
+  static constexpr int OFF_DOT = OFF_TAB + kTabs * 64 * 4;
+  static constexpr int OFF_BAR = OFF_DOT + (GRAD ? 2 * 4 * 64 * 4 : 0);
+  static constexpr int NBAR = 2 * KS + 4 + 2 + 2 + 3 + 4 + 2 + 2 + kTabs + 1;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
-// TMEM columns
-constexpr uint32_t kColState = 0, kColFar = 128, kColNear = 256, kColS = 384;  // S: two buffers of 64
+// TMEM columns: the state; two buffers of S (64); two of far and near (64 each)
+constexpr uint32_t kColState = 0, kColS = 128, kColOut = 256;
 
-// Row r of a [64 x 128] swizzled tile times f: the value, and with two parts its remainder.
-template <int PARTS>
-__device__ __forceinline__ void scaled_copy(uint32_t src, uint32_t dst, int r, float f, int ch0, int n) {
+// Row r of a [64 x 128] swizzled tile times f, chunks [ch0, ch0 + n) of 8 columns:
+// the value to `hi`, its remainder to `lo` (tiles of the same layout).
+__device__ __forceinline__ void scale_row(uint32_t src, uint32_t hi_t, uint32_t lo_t, int r, float f, int ch0, int n) {
 #pragma unroll 4
   for (int ch = ch0; ch < ch0 + n; ++ch) {
-    const uint32_t off = (ch >> 3) * 64 * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+    const uint32_t off = (ch >> 3) * 8192 + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
     uint32_t x[4], hi[4], lo[4];
     s::ld_shared_v4(src + off, x[0], x[1], x[2], x[3]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float a = __uint_as_float(x[e] << 16) * f, b = __uint_as_float(x[e] & 0xffff0000u) * f;
       hi[e] = s::pack_bf16x2(a, b);
-      if (PARTS == 2)
-        lo[e] = s::pack_bf16x2(a - __uint_as_float(hi[e] << 16), b - __uint_as_float(hi[e] & 0xffff0000u));
+      lo[e] = s::pack_bf16x2(a - __uint_as_float(hi[e] << 16), b - __uint_as_float(hi[e] & 0xffff0000u));
     }
-    s::st_shared_v4(dst + off, hi[0], hi[1], hi[2], hi[3]);
-    if (PARTS == 2) s::st_shared_v4(dst + kTile + off, lo[0], lo[1], lo[2], lo[3]);
+    s::st_shared_v4(hi_t + off, hi[0], hi[1], hi[2], hi[3]);
+    s::st_shared_v4(lo_t + off, lo[0], lo[1], lo[2], lo[3]);
   }
+}
+
+// Sums v[i] over the warp's lanes for all 32 i: lane l returns the sum of v[l].
+__device__ __forceinline__ float transposed_sum(float (&v)[32], int lane) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) {
+    const bool up = lane & m;
+#pragma unroll
+    for (int i = 0; i < m; ++i) {
+      const float keep = up ? v[i + m] : v[i], send = up ? v[i] : v[i + m];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
+    }
+  }
+  return v[0];
 }
 
 template <bool BACK, bool GRAD>
 __global__ void __launch_bounds__(512, 1)
 gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_y,
                    const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_o,
-                   const TcParams prm) {
+                   const __grid_constant__ CUtensorMap tm_dot, const TcParams prm) {
   using CF = TcCfg<GRAD>;
   constexpr int KS = CF::KS, PARTS = CF::PARTS;
   extern __shared__ uint8_t smem_raw[];
@@ -141,10 +161,13 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
   uint64_t* s_full = in_empty + KS;
   uint64_t* s_empty = s_full + 2;
   uint64_t *p_full = s_empty + 2, *p_empty = p_full + 1;
-  uint64_t *y2_full = p_empty + 1, *y2_empty = y2_full + 1;
-  uint64_t *copy_full = y2_empty + 1, *updated = copy_full + 1;
-  uint64_t *o_full = updated + 1, *o_empty = o_full + 1;
-  uint64_t* tab_full = o_empty + 1;
+  uint64_t *y_full = p_empty + 1, *y_empty = y_full + 1;
+  uint64_t *copy_full = y_empty + 1, *copy_empty = copy_full + 1, *updated = copy_empty + 1;
+  uint64_t* o_full = updated + 1;
+  uint64_t* o_empty = o_full + 2;
+  uint64_t *staged = o_empty + 2, *out_free = staged + 1;
+  uint64_t* dot_full = out_free + 1;
+  uint64_t* tab_full = dot_full + 2;
   uint64_t* drain = tab_full + kTabs;
   uint32_t* tmem_base = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base + 1);
@@ -154,19 +177,27 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
   const int64_t t0 = ch * prm.L, t1 = min(prm.N, t0 + prm.L);
   const int n = static_cast<int>((t1 - t0 + 63) / 64);
   const bool has_init = prm.init && (BACK ? ch + 1 < prm.C : ch > 0);
+  const int first_copy = has_init ? 0 : 1;  // the first block that has a far part
   auto row_of = [&](int i) { return t0 + static_cast<int64_t>(BACK ? n - 1 - i : i) * 64; };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < KS; ++i) { s::mbar_init(&in_full[i], 1); s::mbar_init(&in_empty[i], 1); }
-    for (int i = 0; i < 2; ++i) { s::mbar_init(&s_full[i], 1); s::mbar_init(&s_empty[i], 128); }
+    for (int i = 0; i < 2; ++i) {
+      s::mbar_init(&s_full[i], 1);
+      s::mbar_init(&s_empty[i], 128);
+      s::mbar_init(&o_full[i], 1);
+      s::mbar_init(&o_empty[i], 128);
+      s::mbar_init(&dot_full[i], 1);
+    }
     s::mbar_init(p_full, 128);
     s::mbar_init(p_empty, 1);
-    s::mbar_init(y2_full, 64);
-    s::mbar_init(y2_empty, 1);
+    s::mbar_init(y_full, 64);
+    s::mbar_init(y_empty, 1);
     s::mbar_init(copy_full, 128);
+    s::mbar_init(copy_empty, 1);
     s::mbar_init(updated, 1);
-    s::mbar_init(o_full, 1);
-    s::mbar_init(o_empty, 128);
+    s::mbar_init(staged, 128);
+    s::mbar_init(out_free, 1);
     for (int i = 0; i < kTabs; ++i) s::mbar_init(&tab_full[i], 32);
     s::mbar_init(drain, 1);
     *abort_flag = 0;
@@ -177,6 +208,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     s::tma_prefetch(&tm_y);
     s::tma_prefetch(&tm_z);
     s::tma_prefetch(&tm_o);
+    if (GRAD) s::tma_prefetch(&tm_dot);
   }
   if (warp == 1) {
     s::tmem_alloc(tmem_base, 512);
@@ -220,11 +252,11 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
   } else if (warp == 1) {
     // ================================================================== MMA
     constexpr uint32_t ID_S = s::make_idesc(64, 64, false, false);
-    constexpr uint32_t ID_FAR = s::make_idesc(64, 128, false, !GRAD);  // GRAD: the state read transposed
+    constexpr uint32_t ID_FAR = s::make_idesc(128, 64, !GRAD, false);  // GRAD: the state read transposed
     constexpr uint32_t ID_UPD = s::make_idesc(128, 128, true, true);
-    constexpr uint32_t ID_NEAR = s::make_idesc(64, 128, false, true);
+    constexpr uint32_t ID_NEAR = s::make_idesc(128, 64, true, false);
     const uint32_t base = s::smem_u32(smem);
-    const uint32_t y2 = base + CF::OFF_Y2, pa = base + CF::OFF_P, cp = base + CF::OFF_COPY;
+    const uint32_t ylo = base + CF::OFF_LO, pa = base + CF::OFF_P, cp = base + CF::OFF_COPY;
     auto scores = [&](int i) -> bool {  // S of block i
       if (!wait(&in_full[i % KS], (i / KS) & 1, 71)) return false;
       if (!wait(&s_empty[i & 1], ((i >> 1) & 1) ^ 1, 72)) return false;
@@ -239,46 +271,46 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       s::mma_commit_warp(&s_full[i & 1]);
       return true;
     };
-    int copies = 0;
     bool ok = scores(0);
     for (int i = 0; i < n && ok; ++i) {
-      const uint32_t xa = base + (i % KS) * 3 * kTile, za = xa + 2 * kTile;
-      const bool far = i > 0 || has_init;
+      const uint32_t xa = base + (i % KS) * 3 * kTile, ya = xa + kTile, za = ya + kTile;
+      const bool far = i >= first_copy;
+      const uint32_t t_far = tmem + kColOut + 128 * (i & 1), t_near = t_far + 64;
       ok = false;
-      if (!wait(o_empty, (i & 1) ^ 1, 73)) break;
-      if (far) {
-        if (!wait(copy_full, copies & 1, 74)) break;
-        ++copies;
-        s::tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < 8 * PARTS; ++k) {
-          const uint32_t a = xa + ((k & 7) >> 2) * 8192 + (k & 3) * 32;
-          const uint32_t b = cp + (k >> 3) * kCopy;
-          const uint64_t bd = GRAD ? s::make_desc(b + ((k & 7) >> 2) * 16384 + (k & 3) * 32, 16, 1024)
-                                   : s::make_desc(b + (k & 7) * 2048, 16384, 1024);
-          s::mma_bf16_ss_warp(tmem + kColFar, s::make_desc(a, 16, 1024), bd, ID_FAR, k > 0);
-        }
-      }
+      if (far && !wait(copy_full, (i - first_copy) & 1, 74)) break;
       if (i + 1 < n) {  // the state past the chunk's last block is not needed
-        if (!wait(y2_full, i & 1, 75)) break;
+        if (!wait(y_full, i & 1, 75)) break;
         s::tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 4 * PARTS; ++k) {
-          const uint64_t yd = s::make_desc(y2 + (k >> 2) * kTile + (k & 3) * 2048, 8192, 1024);
+        for (int k = 0; k < 8; ++k) {
+          const uint64_t yd = s::make_desc((k < 4 ? ya : ylo) + (k & 3) * 2048, 8192, 1024);
           const uint64_t zd = s::make_desc(za + (k & 3) * 2048, 8192, 1024);
           s::mma_bf16_ss_warp(tmem + kColState, GRAD ? zd : yd, GRAD ? yd : zd, ID_UPD, far || k > 0);
         }
         s::mma_commit_warp(updated);
-        s::mma_commit_warp(y2_empty);
-        if (!scores(i + 1)) break;
+        s::mma_commit_warp(y_empty);
       }
+      if (!wait(&o_empty[i & 1], ((i >> 1) & 1) ^ 1, 73)) break;
+      s::tc_fence_after();
+      if (far) {
+#pragma unroll
+        for (int k = 0; k < 8 * PARTS; ++k) {
+          const uint32_t c = cp + (k >> 3) * kCopy;
+          const uint64_t ad = GRAD ? s::make_desc(c + ((k & 7) >> 2) * 16384 + (k & 3) * 32, 16, 1024)
+                                   : s::make_desc(c + (k & 7) * 2048, 16384, 1024);
+          s::mma_bf16_ss_warp(t_far, ad, s::make_desc(xa + ((k & 7) >> 2) * 8192 + (k & 3) * 32, 16, 1024), ID_FAR,
+                              k > 0);
+        }
+        s::mma_commit_warp(copy_empty);
+      }
+      if (i + 1 < n && !scores(i + 1)) break;
       if (!wait(p_full, i & 1, 76)) break;
       s::tc_fence_after();
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        s::mma_bf16_ss_warp(tmem + kColNear, s::make_desc(pa + k * 32, 16, 1024),
-                            s::make_desc(za + k * 2048, 8192, 1024), ID_NEAR, k > 0);
-      s::mma_commit_warp(o_full);
+        s::mma_bf16_ss_warp(t_near, s::make_desc(za + k * 2048, 8192, 1024), s::make_desc(pa + k * 32, 16, 1024),
+                            ID_NEAR, k > 0);
+      s::mma_commit_warp(&o_full[i & 1]);
       s::mma_commit_warp(p_empty);
       s::mma_commit_warp(&in_empty[i % KS]);
       ok = true;
@@ -287,13 +319,17 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     s::drain_wait(drain, 0);
   } else if (warp < 4) {
     // ============================================ gate tables (warp 2) and Y~
-    // Table i goes into slot i % 4. Warp 2 writes it after its Y~ of block i - 1,
-    // which waited for the update of block i - 2, which is issued after everything
-    // of block i - 3 but its epilogue's reads, and after those (o_empty): the slot's
-    // last readers, of block i - 4, are done.
+    // Table i is written after Y~ of block i - 1, which waited for the update of
+    // block i - 2 (y_empty). That update is issued after far and near of block i - 3,
+    // and those wait for the epilogue's reads of block i - 5 (o_empty): readers of
+    // blocks i - 5 and before are done, so five slots would do without a wait.
     const int r = threadIdx.x - 64;
     const __nv_bfloat16* g = prm.gate + bh * prm.N;
-    auto gate_at = [&](int64_t t) { return t < t1 ? g[t] : __float2bfloat16(0.f); };
+    // (nothing comes before the first token for its gate to pass on: 0, unless NaN)
+    auto gate_at = [&](int64_t t) {
+      const __nv_bfloat16 x = t < t1 ? g[t] : __float2bfloat16(0.f);
+      return t > 0 || __hisnan(x) ? x : __float2bfloat16(0.f);
+    };
     __nv_bfloat16 gx = gate_at(row_of(0) + 2 * lane), gy = gate_at(row_of(0) + 2 * lane + 1);
     for (int i = 0; i < n; ++i) {
       if (warp == 2) {
@@ -309,17 +345,20 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       if (i + 1 == n) break;
       const float* c = tab_of(i, 77);
       if (!c) break;
-      if (!wait(&in_full[i % KS], (i / KS) & 1, 78)) break;
-      if (!wait(y2_empty, (i & 1) ^ 1, 79)) break;
       const float f = ex2(BACK ? c[r] : c[63] - c[r]);
-      scaled_copy<PARTS>(s::smem_u32(smem + (i % KS) * 3 * kTile + kTile), s::smem_u32(smem + CF::OFF_Y2), r, f, 0, 16);
+      if (!wait(&s_full[i & 1], (i >> 1) & 1, 78)) break;  // S has read Y
+      if (!wait(y_empty, (i & 1) ^ 1, 79)) break;
+      const uint32_t ya = s::smem_u32(smem + (i % KS) * 3 * kTile + kTile);
+      scale_row(ya, ya, s::smem_u32(smem + CF::OFF_LO), r, f, 0, 16);
       s::fence_proxy_async();
-      s::mbar_arrive(y2_full);
+      s::mbar_arrive(y_full);
     }
   } else if (wg == 1) {
     // ======================================================== S -> P, weighted
     const int r = s::acc_row<64>(w4, lane);
     const uint32_t pbase = s::smem_u32(smem + CF::OFF_P);
+    // the half of the columns that this warp's 16 rows do not keep at all
+    const int dropped = BACK ? (w4 >= 2 ? 0 : -1) : (w4 < 2 ? 1 : -1);
     for (int i = 0; i < n; ++i) {
       const float* c = tab_of(i, 80);
       if (!c) break;
@@ -329,19 +368,22 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       uint32_t w[32];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        if (h == dropped) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[16 * h + e] = 0u;
+          continue;
+        }
         uint32_t v[32];
         s::tmem_ld32(tmem + kColS + 64 * (i & 1) + 32 * h + lane_off, v);
         s::tmem_ld_wait();
-        if (r >= 0) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int col = 32 * h + 2 * e;
-            const float2 cc = *reinterpret_cast<const float2*>(c + col);
-            const float wa = ex2(BACK ? cc.x - cr : cr - cc.x), wb = ex2(BACK ? cc.y - cr : cr - cc.y);
-            const float a = (BACK ? col >= r : col <= r) ? __uint_as_float(v[2 * e]) * wa : 0.f;
-            const float b = (BACK ? col + 1 >= r : col + 1 <= r) ? __uint_as_float(v[2 * e + 1]) * wb : 0.f;
-            w[16 * h + e] = s::pack_bf16x2(a, b);
-          }
+        for (int e = 0; e < 16; ++e) {
+          const int col = 32 * h + 2 * e;
+          const float2 cc = *reinterpret_cast<const float2*>(c + col);
+          const float wa = ex2(BACK ? cc.x - cr : cr - cc.x), wb = ex2(BACK ? cc.y - cr : cr - cc.y);
+          const float a = (BACK ? col >= r : col <= r) ? __uint_as_float(v[2 * e]) * wa : 0.f;
+          const float b = (BACK ? col + 1 >= r : col + 1 <= r) ? __uint_as_float(v[2 * e + 1]) * wb : 0.f;
+          w[16 * h + e] = s::pack_bf16x2(a, b);
         }
       }
       s::tc_fence_before();
@@ -359,9 +401,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     const int r = 32 * w4 + lane;  // state row
     const uint32_t ts = tmem + kColState + lane_off;
     const uint32_t cbase = s::smem_u32(smem + CF::OFF_COPY);
-    const float4* init =
-        has_init ? reinterpret_cast<const float4*>(prm.init + static_cast<int64_t>(blockIdx.x) * 128 * 128) : nullptr;
-    for (int i = has_init ? 0 : 1; i < n; ++i) {
+    for (int i = first_copy; i < n; ++i) {
       const float* c = tab_of(i, 83);
       if (!c) break;
       const float whole = ex2(c[63]);
@@ -369,22 +409,40 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         if (!wait(updated, (i - 1) & 1, 84)) break;
         s::tc_fence_after();
       }
+      bool ok = true;
 #pragma unroll
       for (int c32 = 0; c32 < 4; ++c32) {
         uint32_t v[32];
         if (i == 0) {
+          // the pieces between this chunk and the sequence's start (walking back:
+          // its end), nearest first, each decayed over the nearer ones
+          float x[32];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 x = init[s::state_f4<128>(r, c32 * 8 + q)];
-            v[4 * q] = __float_as_uint(x.x);
-            v[4 * q + 1] = __float_as_uint(x.y);
-            v[4 * q + 2] = __float_as_uint(x.z);
-            v[4 * q + 3] = __float_as_uint(x.w);
+          for (int e = 0; e < 32; ++e) x[e] = 0.f;
+          const int pieces = prm.per == 0 ? 1 : static_cast<int>(BACK ? prm.K - (ch + 1) * prm.per : ch * prm.per);
+          float f = 1.f;
+          for (int j = 0; j < pieces; ++j) {
+            const int64_t at = bh * prm.K + (prm.per == 0 ? ch : BACK ? (ch + 1) * prm.per + j : ch * prm.per - 1 - j);
+            const float4* src = reinterpret_cast<const float4*>(prm.init + at * 128 * 128);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float4 y = src[s::state_f4<128>(r, c32 * 8 + q)];
+              x[4 * q] = fmaf(f, y.x, x[4 * q]);
+              x[4 * q + 1] = fmaf(f, y.y, x[4 * q + 1]);
+              x[4 * q + 2] = fmaf(f, y.z, x[4 * q + 2]);
+              x[4 * q + 3] = fmaf(f, y.w, x[4 * q + 3]);
+            }
+            if (j + 1 < pieces) f *= expf(static_cast<float>(prm.tot[at]));
           }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(x[e]);
         } else {
           s::tmem_ld32(ts + c32 * 32, v);
           s::tmem_ld_wait();
         }
+        // far of the block before has read the copy
+        if (c32 == 0 && i > first_copy) ok = wait(copy_empty, (i - 1 - first_copy) & 1, 88);
+        if (!ok) break;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const uint32_t off = (c32 >> 1) * 16384 + r * 128 + ((((c32 & 1) * 4 + q) ^ (r & 7)) << 4);
@@ -405,6 +463,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
           s::tmem_st32(ts + c32 * 32, v);
         }
       }
+      if (!ok) break;
       s::tmem_st_wait();
       s::fence_proxy_async();
       s::tc_fence_before();
@@ -412,72 +471,108 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     }
   } else {
     // =========================================== out = head far + near -> HBM
-    const int r = s::acc_row<64>(w4, lane);
-    const int rl = lane & 15;
-    uint8_t* stage = smem + CF::OFF_OUT + w4 * 16 * 128;
-    for (int i = 0; i < n; ++i) {
-      const bool far = i > 0 || has_init;
-      const int64_t row = row_of(i) + r;
-      const bool valid = r >= 0 && row < t1;
-      const uint4* xr = GRAD ? reinterpret_cast<const uint4*>(prm.dot_x + (bh * prm.N + (valid ? row : t0)) * 128) : nullptr;
-      uint4 x[4];
-      if (GRAD && valid)
+    // Thread e holds column e of the 64 rows; the staging tile is [row][column].
+    const int e = 32 * w4 + lane;
+    const uint32_t obase = s::smem_u32(smem + CF::OFF_OUT) + (e >> 6) * 8192 + (e & 7) * 2;
+    const int cj = (e & 63) >> 3;
+    uint32_t sw[8];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) x[q] = xr[q];
+    for (int m = 0; m < 8; ++m) sw[m] = static_cast<uint32_t>((cj ^ m) << 4);
+    float* dotbuf = reinterpret_cast<float*>(smem + CF::OFF_DOT);
+    const bool lead = w4 == 0 && lane == 0;
+    int dots_issued = 0;
+    auto load_dot_rows = [&](int i) {  // by the lead thread, into the block's staging tile
+      uint8_t* dst = smem + CF::OFF_OUT + (i & 1) * kTile;
+      s::mbar_expect_tx(&dot_full[i & 1], kTile);
+      for (int p = 0; p < 2; ++p)
+        s::tma_load_3d(dst + p * 8192, &tm_dot, &dot_full[i & 1], 64 * p, static_cast<int>(row_of(i)), static_cast<int>(bh));
+      ++dots_issued;
+    };
+    if (GRAD && lead)
+      for (int i = 0; i < min(n, 2); ++i) load_dot_rows(i);
+    int i = 0;
+    for (; i < n; ++i) {
+      const bool far = i >= first_copy;
       const float* c = tab_of(i, 85);
       if (!c) break;
-      const float head = r >= 0 && far ? ex2(BACK ? c[63] - c[r] : c[r]) : 0.f;
-      if (!wait(o_full, i & 1, 86)) break;
-      s::tc_fence_after();
-      if (lane == 0) s::bulk_wait_group_read<0>();  // the store of the block before has read the stage
-      __syncwarp();
-      float dot = 0.f;
-#pragma unroll
-      for (int c32 = 0; c32 < 4; ++c32) {
-        uint32_t near[32], v[32];
-        s::tmem_ld32(tmem + kColNear + c32 * 32 + lane_off, near);
-        if (far) s::tmem_ld32(tmem + kColFar + c32 * 32 + lane_off, v);
-        s::tmem_ld_wait();
-        if (r >= 0) {
-          float o[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            o[e] = far ? fmaf(head, __uint_as_float(v[e]), __uint_as_float(near[e])) : __uint_as_float(near[e]);
-          if (GRAD) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t u[4] = {x[q].x, x[q].y, x[q].z, x[q].w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                dot = fmaf(o[8 * q + 2 * e], __uint_as_float(u[e] << 16), dot);
-                dot = fmaf(o[8 * q + 2 * e + 1], __uint_as_float(u[e] & 0xffff0000u), dot);
-              }
-              if (valid && c32 < 3) x[q] = xr[4 * (c32 + 1) + q];
-            }
-          }
-          const uint32_t base = s::smem_u32(stage + (c32 >> 1) * 8192) + rl * 128;
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            s::st_shared_v4(base + ((((c32 & 1) * 4 + q) ^ (rl & 7)) << 4), s::pack_bf16x2(o[8 * q], o[8 * q + 1]),
-                            s::pack_bf16x2(o[8 * q + 2], o[8 * q + 3]), s::pack_bf16x2(o[8 * q + 4], o[8 * q + 5]),
-                            s::pack_bf16x2(o[8 * q + 6], o[8 * q + 7]));
-        }
+      const float call = c[63];
+      if (GRAD) {
+        if (!wait(&dot_full[i & 1], (i >> 1) & 1, 89)) break;
+      } else if (i > 0) {
+        if (!wait(out_free, (i - 1) & 1, 89)) break;
       }
-      s::tc_fence_before();
-      s::mbar_arrive(o_empty);
-      if (GRAD && valid) prm.dots[bh * prm.N + row] = dot;
+      if (!wait(&o_full[i & 1], (i >> 1) & 1, 86)) break;
+      s::tc_fence_after();
+      const uint32_t t_far = tmem + kColOut + 128 * (i & 1) + lane_off, t_near = t_far + 64;
+      const uint32_t ob = obase + (GRAD ? (i & 1) * kTile : 0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t near[32], v[32];
+        s::tmem_ld32(t_near + 32 * h, near);
+        if (far) s::tmem_ld32(t_far + 32 * h, v);
+        s::tmem_ld_wait();
+        float o[32];
+#pragma unroll
+        for (int t = 0; t < 32; t += 4) {
+          const float4 ct = *reinterpret_cast<const float4*>(c + 32 * h + t);
+          const float cc[4] = {ct.x, ct.y, ct.z, ct.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const float hd = ex2(BACK ? call - cc[u] : cc[u]);
+            o[t + u] = far ? fmaf(hd, __uint_as_float(v[t + u]), __uint_as_float(near[t + u]))
+                           : __uint_as_float(near[t + u]);
+          }
+        }
+        if (h == 1) {
+          s::tc_fence_before();
+          s::mbar_arrive(&o_empty[i & 1]);
+        }
+#pragma unroll
+        for (int t = 0; t < 32; t += 2) {
+          const uint32_t pk = s::pack_bf16x2(o[t], o[t + 1]);
+          const uint32_t a0 = ob + (32 * h + t) * 128 + sw[t & 7], a1 = ob + (32 * h + t + 1) * 128 + sw[(t + 1) & 7];
+          if (GRAD) {  // the dots' rows, then their place takes the output
+            uint16_t x0, x1;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x0) : "r"(a0) : "memory");
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x1) : "r"(a1) : "memory");
+            o[t] *= __uint_as_float(static_cast<uint32_t>(x0) << 16);
+            o[t + 1] *= __uint_as_float(static_cast<uint32_t>(x1) << 16);
+          }
+          s::st_shared_u16(a0, static_cast<uint16_t>(pk));
+          s::st_shared_u16(a1, static_cast<uint16_t>(pk >> 16));
+        }
+        if (GRAD) dotbuf[(i & 1) * 256 + w4 * 64 + 32 * h + lane] = transposed_sum(o, lane);
+      }
       s::fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) {
+      s::mbar_arrive(staged);
+      // (All four warps meet here: whoever goes on to block i + 2, whose dots use the
+      // same buffer, has met the readers of this block's at block i + 1.)
+      if (!wait(staged, i & 1, 89)) break;
+      if (lead) {
         // A chunk ends on a block boundary or at N, where the tensor map clips.
-        const int64_t y = row_of(i) + 16 * w4;
-        if (y < t1)
-          for (int p = 0; p < 2; ++p)
-            s::tma_store_3d(&tm_o, stage + p * 8192, 64 * p, static_cast<int>(y), static_cast<int>(bh));
+        for (int p = 0; p < 2; ++p)
+          s::tma_store_3d(&tm_o, smem + CF::OFF_OUT + (GRAD ? (i & 1) * kTile : 0) + p * 8192, 64 * p,
+                          static_cast<int>(row_of(i)), static_cast<int>(bh));
         s::bulk_commit_group();
       }
+      if (GRAD && w4 < 2) {  // the dots of 64 rows
+        const int t = 32 * w4 + lane;
+        const float* db = dotbuf + (i & 1) * 256 + t;
+        if (row_of(i) + t < t1) prm.dots[bh * prm.N + row_of(i) + t] = (db[0] + db[64]) + (db[128] + db[192]);
+      }
+      if (lead) {
+        s::bulk_wait_group_read<0>();  // the store has read the tile
+        if (!GRAD) s::mbar_arrive(out_free);
+        else if (i + 2 < n) load_dot_rows(i + 2);
+      }
+      __syncwarp();
     }
-    if (lane == 0) s::bulk_wait_group<0>();  // stores done before exit
+    if (lead) {
+      // loads still in flight after an abort, and the stores, are done before exit
+      if (GRAD)
+        for (int j = max(0, dots_issued - 2); j < dots_issued; ++j) s::drain_wait(&dot_full[j & 1], (j >> 1) & 1);
+      s::bulk_wait_group<0>();
+    }
   }
 
   s::tc_fence_before();
@@ -490,8 +585,8 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 
 // ---------------------------------------------------------------- chunk states
 //
-// Own state of every chunk (see chunk_state_kernel), SUFFIX false from (k, v), true
-// from (q, dO): sum of w_t y_t^T z_t with the weight taken to the chunk's end (its
+// Own state of every piece of L rows (see chunk_state_kernel), SUFFIX false from (k, v), true
+// from (q, dO): sum of w_t y_t^T z_t with the weight taken to the piece's end (its
 // start), so the accumulator is never decayed: the blocks are walked from that edge,
 // and the sum of the gates walked so far goes into the scale of the rows. Y~ is value
 // and remainder, so the fp32 state is good to 2^-17: it is what the caller's pool
@@ -508,9 +603,9 @@ struct StateCfg {
 
 struct TcStateParams {
   const __nv_bfloat16* gate;
-  float* out;      // [BH][C][128*128] (state_f4)
-  double* tot;     // [BH][C]
-  int64_t N, L, C, first, count, spin_limit;  // chunks [first, first + count) of every sequence
+  float* out;      // [BH][K][128*128] (state_f4)
+  double* tot;     // [BH][K]
+  int64_t N, L, K, first, count, spin_limit;  // pieces [first, first + count) of the K of every sequence
 };
 
 template <bool SUFFIX>
@@ -619,16 +714,16 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
       }
       ok = wait(&in_full[i % KS], (i / KS) & 1, 93) && wait(&y2_empty[i & 1], ((i >> 1) & 1) ^ 1, 94);
       if (!ok) break;
-      scaled_copy<2>(s::smem_u32(smem + (i % KS) * 2 * kTile), s::smem_u32(smem + CF::OFF_Y2 + (i & 1) * 2 * kTile), r,
-                     f, ch0, 4);
+      const uint32_t y2 = s::smem_u32(smem + CF::OFF_Y2 + (i & 1) * 2 * kTile);
+      scale_row(s::smem_u32(smem + (i % KS) * 2 * kTile), y2, y2 + kTile, r, f, ch0, 4);
       s::fence_proxy_async();
       s::mbar_arrive(&y2_full[i & 1]);
     }
-    if (warp == 4 && lane == 0) prm.tot[bh * prm.C + ch] = run * 0.693147180559945309417;  // natural log
+    if (warp == 4 && lane == 0) prm.tot[bh * prm.K + ch] = run * 0.693147180559945309417;  // natural log
     if (ok && warp < 8 && wait(done, 0, 95)) {
       s::tc_fence_after();
       const int row = 32 * (warp & 3) + lane;
-      float4* dst = reinterpret_cast<float4*>(prm.out + (bh * prm.C + ch) * 128 * 128);
+      float4* dst = reinterpret_cast<float4*>(prm.out + (bh * prm.K + ch) * 128 * 128);
 #pragma unroll
       for (int c32 = 0; c32 < 4; ++c32) {
         uint32_t v[32];
@@ -664,16 +759,17 @@ inline cudaError_t launch_state_sm100(const void* y, const void* z, const TcStat
 }
 
 template <bool BACK, bool GRAD>
-inline cudaError_t launch_sm100(const void* x, const void* y, const void* z, void* o, const TcParams& p, int64_t BH,
-                                cudaStream_t st) {
-  CUtensorMap tx, ty, tz, to;
+inline cudaError_t launch_sm100(const void* x, const void* y, const void* z, void* o, const void* dot_rows,
+                                const TcParams& p, int64_t BH, cudaStream_t st) {
+  CUtensorMap tx, ty, tz, to, td;
   if (!make_tmap_3d(&tx, x, BH, p.N, 128, 64) || !make_tmap_3d(&ty, y, BH, p.N, 128, 64) ||
-      !make_tmap_3d(&tz, z, BH, p.N, 128, 64) || !make_tmap_3d(&to, o, BH, p.N, 128, 16))
+      !make_tmap_3d(&tz, z, BH, p.N, 128, 64) || !make_tmap_3d(&to, o, BH, p.N, 128, 64) ||
+      !make_tmap_3d(&td, GRAD ? dot_rows : x, BH, p.N, 128, 64))
     return cudaErrorInvalidValue;
   auto kern = gated_sm100_kernel<BACK, GRAD>;
   static bool done[128];
   if (!smem_attribute_set(kern, TcCfg<GRAD>::SMEM, done)) return cudaErrorInvalidValue;
-  return launch_pdl(kern, dim3((unsigned)(BH * p.C)), dim3(512), TcCfg<GRAD>::SMEM, st, tx, ty, tz, to, p);
+  return launch_pdl(kern, dim3((unsigned)(BH * p.C)), dim3(512), TcCfg<GRAD>::SMEM, st, tx, ty, tz, to, td, p);
 }
 
 }  // namespace gated
