@@ -38,6 +38,9 @@
 // products, the same weights), so the near parts agree; for the far parts the state's
 // copy is kept as value and remainder too (2^-17 instead of 2^-9). The dots' rows are
 // loaded into the output's staging tile, read there and overwritten by the output.
+//
+// The roles' inner loops stay rolled: five roles share each scheduler, and unrolled
+// over a block their instructions came from beyond its instruction cache.
 #pragma once
 
 #include "la2_gated_simt.cuh"
@@ -50,6 +53,7 @@ namespace s = sm100;
 
 constexpr int kTile = 64 * 128 * 2;       // one 64 x 128 bf16 tile
 constexpr int kCopy = 128 * 128 * 2;      // the state's bf16 copy
+constexpr int kMainThreads = 640;
 constexpr float kLog2Zero = -160.f;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kTabs = 8;                  // gate tables in flight (see the table warp)
@@ -79,6 +83,31 @@ __device__ __forceinline__ void warp_sums(float x, float y, int lane, float& a, 
   a = (lane ? before : 0.f) + x;
 }
 
+// One lane of the warp, the same for every MMA and commit of the issuing loop.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e;
+}
+// n MMAs of 16 k each by the elected lane; the operands' descriptors step by da and
+// db (bytes / 16) from MMA to MMA, and from the fourth to the fifth (and so on) by
+// da4, db4 instead.
+template <int N>
+__device__ __forceinline__ void mma_run(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t da, uint32_t db,
+                                        uint32_t da4, uint32_t db4, uint32_t idesc, uint32_t accumulate) {
+  if (lead) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      s::mma_bf16_ss(d, a + (k >> 2) * da4 + (k & 3) * da, b + (k >> 2) * db4 + (k & 3) * db, idesc,
+                     k > 0 ? 1u : accumulate);
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
+  if (lead) s::mma_commit(bar);
+  __syncwarp();
+}
+
 struct TcParams {
   const __nv_bfloat16* gate;   // [BH][N]
   const float* init;           // [BH][K][128*128] (state_f4): states of the sequence's pieces, or null
@@ -101,7 +130,7 @@ struct TcCfg {
   static constexpr int OFF_COPY = OFF_P + 64 * 64 * 2;
   static constexpr int OFF_OUT = OFF_COPY + PARTS * kCopy;
   static constexpr int OFF_TAB = OFF_OUT + OB * kTile;
-  static constexpr int OFF_DOT = OFF_TAB + kTabs * 64 * 4;
+  static constexpr int OFF_DOT = OFF_TAB + kTabs * 128 * 4;
   static constexpr int OFF_BAR = OFF_DOT + (GRAD ? 2 * 4 * 64 * 4 : 0);
   static constexpr int NBAR = 2 * KS + 4 + 2 + 2 + 3 + 4 + 2 + 2 + kTabs + 1;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
@@ -110,29 +139,17 @@ struct TcCfg {
 // TMEM columns: the state; two buffers of S (64); two of far and near (64 each)
 constexpr uint32_t kColState = 0, kColS = 128, kColOut = 256;
 
-// Row r of a [64 x 128] swizzled tile times f, chunks [ch0, ch0 + n) of 8 columns:
-// the value to `hi`, its remainder to `lo` (tiles of the same layout).
-__device__ __forceinline__ void scale_row(uint32_t src, uint32_t hi_t, uint32_t lo_t, int r, float f, int ch0, int n) {
-#pragma unroll 4
-  for (int ch = ch0; ch < ch0 + n; ++ch) {
-    const uint32_t off = (ch >> 3) * 8192 + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
-    uint32_t x[4], hi[4], lo[4];
-    s::ld_shared_v4(src + off, x[0], x[1], x[2], x[3]);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float a = __uint_as_float(x[e] << 16) * f, b = __uint_as_float(x[e] & 0xffff0000u) * f;
-      hi[e] = s::pack_bf16x2(a, b);
-      lo[e] = s::pack_bf16x2(a - __uint_as_float(hi[e] << 16), b - __uint_as_float(hi[e] & 0xffff0000u));
-    }
-    s::st_shared_v4(hi_t + off, hi[0], hi[1], hi[2], hi[3]);
-    s::st_shared_v4(lo_t + off, lo[0], lo[1], lo[2], lo[3]);
-  }
+// Two bf16 values times f: the rounded products, and what they are off, rounded.
+__device__ __forceinline__ void split_scaled(uint32_t x, float f, uint32_t& hi, uint32_t& lo) {
+  const float a = __uint_as_float(x << 16) * f, b = __uint_as_float(x & 0xffff0000u) * f;
+  hi = s::pack_bf16x2(a, b);
+  lo = s::pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
 }
 
-// Sums v[i] over the warp's lanes for all 32 i: lane l returns the sum of v[l].
-__device__ __forceinline__ float transposed_sum(float (&v)[32], int lane) {
+// Sums v[i] over the warp's lanes for all 16 i: lane l returns the sum of v[l % 16].
+__device__ __forceinline__ float transposed_sum(float (&v)[16], int lane) {
 #pragma unroll
-  for (int m = 16; m > 0; m >>= 1) {
+  for (int m = 8; m > 0; m >>= 1) {
     const bool up = lane & m;
 #pragma unroll
     for (int i = 0; i < m; ++i) {
@@ -140,11 +157,20 @@ __device__ __forceinline__ float transposed_sum(float (&v)[32], int lane) {
       v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
     }
   }
-  return v[0];
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+}
+
+// Thread t of the warp reads 16 consecutive columns of TMEM lane (lane field) + t.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 
 template <bool BACK, bool GRAD>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __launch_bounds__(kMainThreads, 1)
 gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_y,
                    const __grid_constant__ CUtensorMap tm_z, const __grid_constant__ CUtensorMap tm_o,
                    const __grid_constant__ CUtensorMap tm_dot, const TcParams prm) {
@@ -153,7 +179,8 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (from lane 0, so that the compiler takes what depends on it as warp-uniform)
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int wg = warp >> 2, w4 = warp & 3;
 
   uint64_t* in_full = reinterpret_cast<uint64_t*>(smem + CF::OFF_BAR);
@@ -191,7 +218,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     }
     s::mbar_init(p_full, 128);
     s::mbar_init(p_empty, 1);
-    s::mbar_init(y_full, 64);
+    s::mbar_init(y_full, 128);
     s::mbar_init(y_empty, 1);
     s::mbar_init(copy_full, 128);
     s::mbar_init(copy_empty, 1);
@@ -226,7 +253,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     return __all_sync(0xffffffffu, s::wait_bar(bar, parity, lim, abort_flag, where));
   };
   auto tab_of = [&](int i, int where) -> const float* {  // the block's gate sums, or null after an abort
-    return wait(&tab_full[i % kTabs], (i / kTabs) & 1, where) ? tab + (i % kTabs) * 64 : nullptr;
+    return wait(&tab_full[i % kTabs], (i / kTabs) & 1, where) ? tab + (i % kTabs) * 128 : nullptr;
   };
   const uint32_t lane_off = static_cast<uint32_t>(32 * w4) << 16;
 
@@ -255,75 +282,69 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     constexpr uint32_t ID_FAR = s::make_idesc(128, 64, !GRAD, false);  // GRAD: the state read transposed
     constexpr uint32_t ID_UPD = s::make_idesc(128, 128, true, true);
     constexpr uint32_t ID_NEAR = s::make_idesc(128, 64, true, false);
+    const uint32_t lead = elect_one();
     const uint32_t base = s::smem_u32(smem);
-    const uint32_t ylo = base + CF::OFF_LO, pa = base + CF::OFF_P, cp = base + CF::OFF_COPY;
+    // Operand descriptors at their first 16 k: X and Y by rows (S, far), Y~ and Z by
+    // columns (update, near) of stage 0; a stage further on is 3 kTile.
+    constexpr uint32_t kStage = 3 * kTile / 16, kY = kTile / 16, kZ = 2 * kTile / 16;
+    const uint64_t row_d = s::make_desc(base, 16, 1024), col_d = s::make_desc(base, 8192, 1024);
+    const uint64_t lo_d = s::make_desc(base + CF::OFF_LO, 8192, 1024), p_d = s::make_desc(base + CF::OFF_P, 16, 1024);
+    const uint64_t copy_d = GRAD ? s::make_desc(base + CF::OFF_COPY, 16, 1024)
+                                 : s::make_desc(base + CF::OFF_COPY, 16384, 1024);
+    constexpr uint32_t kCopyStep = GRAD ? 2 : 128, kCopyStep4 = GRAD ? 1024 : 512;
     auto scores = [&](int i) -> bool {  // S of block i
       if (!wait(&in_full[i % KS], (i / KS) & 1, 71)) return false;
       if (!wait(&s_empty[i & 1], ((i >> 1) & 1) ^ 1, 72)) return false;
       s::tc_fence_after();
-      const uint32_t xa = base + (i % KS) * 3 * kTile, ya = xa + kTile;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t off = (k >> 2) * 8192 + (k & 3) * 32;
-        s::mma_bf16_ss_warp(tmem + kColS + 64 * (i & 1), s::make_desc(xa + off, 16, 1024),
-                            s::make_desc(ya + off, 16, 1024), ID_S, k > 0);
-      }
-      s::mma_commit_warp(&s_full[i & 1]);
+      const uint32_t st = (i % KS) * kStage;
+      mma_run<8>(lead, tmem + kColS + 64 * (i & 1), row_d + st, row_d + st + kY, 2, 2, 512, 512, ID_S, 0);
+      commit(lead, &s_full[i & 1]);
       return true;
     };
     bool ok = scores(0);
     for (int i = 0; i < n && ok; ++i) {
-      const uint32_t xa = base + (i % KS) * 3 * kTile, ya = xa + kTile, za = ya + kTile;
+      const uint32_t st = (i % KS) * kStage;
       const bool far = i >= first_copy;
       const uint32_t t_far = tmem + kColOut + 128 * (i & 1), t_near = t_far + 64;
       ok = false;
+      // With three stages the next block has landed by now; with two its load began
+      // when the block before this one was done, so its S waits until after far.
+      if (KS > 2 && i + 1 < n && !scores(i + 1)) break;
       if (far && !wait(copy_full, (i - first_copy) & 1, 74)) break;
       if (i + 1 < n) {  // the state past the chunk's last block is not needed
         if (!wait(y_full, i & 1, 75)) break;
         s::tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint64_t yd = s::make_desc((k < 4 ? ya : ylo) + (k & 3) * 2048, 8192, 1024);
-          const uint64_t zd = s::make_desc(za + (k & 3) * 2048, 8192, 1024);
-          s::mma_bf16_ss_warp(tmem + kColState, GRAD ? zd : yd, GRAD ? yd : zd, ID_UPD, far || k > 0);
-        }
-        s::mma_commit_warp(updated);
-        s::mma_commit_warp(y_empty);
+        const uint64_t y1 = col_d + st + kY, z = col_d + st + kZ;
+        mma_run<4>(lead, tmem + kColState, GRAD ? z : y1, GRAD ? y1 : z, 128, 128, 0, 0, ID_UPD, far);
+        mma_run<4>(lead, tmem + kColState, GRAD ? z : lo_d, GRAD ? lo_d : z, 128, 128, 0, 0, ID_UPD, 1);
+        commit(lead, updated);
+        commit(lead, y_empty);
       }
       if (!wait(&o_empty[i & 1], ((i >> 1) & 1) ^ 1, 73)) break;
       s::tc_fence_after();
       if (far) {
-#pragma unroll
-        for (int k = 0; k < 8 * PARTS; ++k) {
-          const uint32_t c = cp + (k >> 3) * kCopy;
-          const uint64_t ad = GRAD ? s::make_desc(c + ((k & 7) >> 2) * 16384 + (k & 3) * 32, 16, 1024)
-                                   : s::make_desc(c + (k & 7) * 2048, 16384, 1024);
-          s::mma_bf16_ss_warp(t_far, ad, s::make_desc(xa + ((k & 7) >> 2) * 8192 + (k & 3) * 32, 16, 1024), ID_FAR,
-                              k > 0);
-        }
-        s::mma_commit_warp(copy_empty);
+        mma_run<8>(lead, t_far, copy_d, row_d + st, kCopyStep, 2, kCopyStep4, 512, ID_FAR, 0);
+        if (PARTS == 2)
+          mma_run<8>(lead, t_far, copy_d + kCopy / 16, row_d + st, kCopyStep, 2, kCopyStep4, 512, ID_FAR, 1);
+        commit(lead, copy_empty);
       }
-      if (i + 1 < n && !scores(i + 1)) break;
+      if (KS == 2 && i + 1 < n && !scores(i + 1)) break;
       if (!wait(p_full, i & 1, 76)) break;
       s::tc_fence_after();
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        s::mma_bf16_ss_warp(t_near, s::make_desc(za + k * 2048, 8192, 1024), s::make_desc(pa + k * 32, 16, 1024),
-                            ID_NEAR, k > 0);
-      s::mma_commit_warp(&o_full[i & 1]);
-      s::mma_commit_warp(p_empty);
-      s::mma_commit_warp(&in_empty[i % KS]);
+      mma_run<4>(lead, t_near, col_d + st + kZ, p_d, 128, 2, 0, 0, ID_NEAR, 0);
+      commit(lead, &o_full[i & 1]);
+      commit(lead, p_empty);
+      commit(lead, &in_empty[i % KS]);
       ok = true;
     }
-    s::mma_commit_warp(drain);  // every MMA issued must finish before TMEM is released
+    commit(lead, drain);  // every MMA issued must finish before TMEM is released
     s::drain_wait(drain, 0);
-  } else if (warp < 4) {
-    // ============================================ gate tables (warp 2) and Y~
-    // Table i is written after Y~ of block i - 1, which waited for the update of
-    // block i - 2 (y_empty). That update is issued after far and near of block i - 3,
-    // and those wait for the epilogue's reads of block i - 5 (o_empty): readers of
-    // blocks i - 5 and before are done, so five slots would do without a wait.
-    const int r = threadIdx.x - 64;
+  } else if (warp == 2) {
+    // =========================================================== gate tables
+    // Per block: the running sums c, then the epilogue's factors of far. Table i goes
+    // into slot i % 8 when block i - KS has released its stage (in_empty): everything
+    // of it is done but its epilogue, and before its far was issued the epilogue had
+    // read block i - KS - 2 (o_empty), so readers of block i - 8 are long done.
     const __nv_bfloat16* g = prm.gate + bh * prm.N;
     // (nothing comes before the first token for its gate to pass on: 0, unless NaN)
     auto gate_at = [&](int64_t t) {
@@ -332,24 +353,42 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     };
     __nv_bfloat16 gx = gate_at(row_of(0) + 2 * lane), gy = gate_at(row_of(0) + 2 * lane + 1);
     for (int i = 0; i < n; ++i) {
-      if (warp == 2) {
-        float a, b;
-        warp_sums(gate_log2(gx), gate_log2(gy), lane, a, b);
-        reinterpret_cast<float2*>(tab + (i % kTabs) * 64)[lane] = make_float2(a, b);
-        s::mbar_arrive(&tab_full[i % kTabs]);
-        if (i + 1 < n) {
-          gx = gate_at(row_of(i + 1) + 2 * lane);
-          gy = gate_at(row_of(i + 1) + 2 * lane + 1);
-        }
+      if (i >= KS && !wait(&in_empty[i % KS], (i / KS - 1) & 1, 77)) break;
+      float a, b;
+      warp_sums(gate_log2(gx), gate_log2(gy), lane, a, b);
+      const float all = __shfl_sync(0xffffffffu, b, 31);
+      float2* t = reinterpret_cast<float2*>(tab + (i % kTabs) * 128);
+      t[lane] = make_float2(a, b);
+      t[32 + lane] = BACK ? make_float2(ex2(all - a), ex2(all - b)) : make_float2(ex2(a), ex2(b));
+      s::mbar_arrive(&tab_full[i % kTabs]);
+      if (i + 1 < n) {
+        gx = gate_at(row_of(i + 1) + 2 * lane);
+        gy = gate_at(row_of(i + 1) + 2 * lane + 1);
       }
-      if (i + 1 == n) break;
-      const float* c = tab_of(i, 77);
+    }
+  } else if (wg == 4) {
+    // ===================================================================== Y~
+    // Two threads a row: the value over Y once S has read it, the remainder into its
+    // tile once the update of the block before has read that.
+    const int r = threadIdx.x & 63, half = (threadIdx.x >> 6) & 1;
+    const uint32_t lo_t = s::smem_u32(smem + CF::OFF_LO) + half * 8192 + r * 128;
+    for (int i = 0; i + 1 < n; ++i) {
+      const float* c = tab_of(i, 78);
       if (!c) break;
       const float f = ex2(BACK ? c[r] : c[63] - c[r]);
-      if (!wait(&s_full[i & 1], (i >> 1) & 1, 78)) break;  // S has read Y
-      if (!wait(y_empty, (i & 1) ^ 1, 79)) break;
-      const uint32_t ya = s::smem_u32(smem + (i % KS) * 3 * kTile + kTile);
-      scale_row(ya, ya, s::smem_u32(smem + CF::OFF_LO), r, f, 0, 16);
+      if (!wait(&s_full[i & 1], (i >> 1) & 1, 79)) break;
+      if (!wait(y_empty, (i & 1) ^ 1, 90)) break;
+      const uint32_t ya = s::smem_u32(smem + (i % KS) * 3 * kTile + kTile) + half * 8192 + r * 128;
+#pragma unroll 2
+      for (int ch = 0; ch < 8; ++ch) {
+        const uint32_t off = (ch ^ (r & 7)) << 4;
+        uint32_t x[4], hi[4], lo[4];
+        s::ld_shared_v4(ya + off, x[0], x[1], x[2], x[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split_scaled(x[e], f, hi[e], lo[e]);
+        s::st_shared_v4(ya + off, hi[0], hi[1], hi[2], hi[3]);
+        s::st_shared_v4(lo_t + off, lo[0], lo[1], lo[2], lo[3]);
+      }
       s::fence_proxy_async();
       s::mbar_arrive(y_full);
     }
@@ -365,34 +404,34 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       const float cr = r >= 0 ? c[r] : 0.f;
       if (!wait(&s_full[i & 1], (i >> 1) & 1, 81)) break;
       s::tc_fence_after();
-      uint32_t w[32];
+      if (!wait(p_empty, (i & 1) ^ 1, 82)) break;  // near of the block before has read P
+#pragma unroll 1
+      for (int h = 0; h < 4; ++h) {
+        uint32_t w[8];
+        if (h >> 1 == dropped) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (h == dropped) {
+          for (int e = 0; e < 8; ++e) w[e] = 0u;
+        } else {
+          uint32_t v[16];
+          tmem_ld16(tmem + kColS + 64 * (i & 1) + 16 * h + lane_off, v);
+          s::tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) w[16 * h + e] = 0u;
-          continue;
+          for (int e = 0; e < 8; ++e) {
+            const int col = 16 * h + 2 * e;
+            const float2 cc = *reinterpret_cast<const float2*>(c + col);
+            const float wa = ex2(BACK ? cc.x - cr : cr - cc.x), wb = ex2(BACK ? cc.y - cr : cr - cc.y);
+            const float a = (BACK ? col >= r : col <= r) ? __uint_as_float(v[2 * e]) * wa : 0.f;
+            const float b = (BACK ? col + 1 >= r : col + 1 <= r) ? __uint_as_float(v[2 * e + 1]) * wb : 0.f;
+            w[e] = s::pack_bf16x2(a, b);
+          }
         }
-        uint32_t v[32];
-        s::tmem_ld32(tmem + kColS + 64 * (i & 1) + 32 * h + lane_off, v);
-        s::tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int col = 32 * h + 2 * e;
-          const float2 cc = *reinterpret_cast<const float2*>(c + col);
-          const float wa = ex2(BACK ? cc.x - cr : cr - cc.x), wb = ex2(BACK ? cc.y - cr : cr - cc.y);
-          const float a = (BACK ? col >= r : col <= r) ? __uint_as_float(v[2 * e]) * wa : 0.f;
-          const float b = (BACK ? col + 1 >= r : col + 1 <= r) ? __uint_as_float(v[2 * e + 1]) * wb : 0.f;
-          w[16 * h + e] = s::pack_bf16x2(a, b);
+        if (r >= 0) {
+          s::st_shared_v4(pbase + r * 128 + (((2 * h) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
+          s::st_shared_v4(pbase + r * 128 + (((2 * h + 1) ^ (r & 7)) << 4), w[4], w[5], w[6], w[7]);
         }
       }
       s::tc_fence_before();
       s::mbar_arrive(&s_empty[i & 1]);
-      if (!wait(p_empty, (i & 1) ^ 1, 82)) break;  // near of the block before has read P
-      if (r >= 0)
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          s::st_shared_v4(pbase + r * 128 + ((q ^ (r & 7)) << 4), w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
       s::fence_proxy_async();
       s::mbar_arrive(p_full);
     }
@@ -401,26 +440,51 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     const int r = 32 * w4 + lane;  // state row
     const uint32_t ts = tmem + kColState + lane_off;
     const uint32_t cbase = s::smem_u32(smem + CF::OFF_COPY);
-    for (int i = first_copy; i < n; ++i) {
-      const float* c = tab_of(i, 83);
-      if (!c) break;
-      const float whole = ex2(c[63]);
-      if (i > 0) {
-        if (!wait(updated, (i - 1) & 1, 84)) break;
-        s::tc_fence_after();
-      }
-      bool ok = true;
+    // 32 columns of row r into the copy, and times f into the state
+    auto put = [&](uint32_t (&v)[32], int c32, float f, bool keep) {
 #pragma unroll
-      for (int c32 = 0; c32 < 4; ++c32) {
-        uint32_t v[32];
-        if (i == 0) {
-          // the pieces between this chunk and the sequence's start (walking back:
-          // its end), nearest first, each decayed over the nearer ones
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t off = (c32 >> 1) * 16384 + r * 128 + ((((c32 & 1) * 4 + q) ^ (r & 7)) << 4);
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float a = __uint_as_float(v[8 * q + 2 * e]), b = __uint_as_float(v[8 * q + 2 * e + 1]);
+          hi[e] = s::pack_bf16x2(a, b);
+          if (PARTS == 2)
+            lo[e] = s::pack_bf16x2(a - __uint_as_float(hi[e] << 16), b - __uint_as_float(hi[e] & 0xffff0000u));
+        }
+        s::st_shared_v4(cbase + off, hi[0], hi[1], hi[2], hi[3]);
+        if (PARTS == 2) s::st_shared_v4(cbase + kCopy + off, lo[0], lo[1], lo[2], lo[3]);
+      }
+      if (keep) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(f * __uint_as_float(v[e]));
+        s::tmem_st32(ts + c32 * 32, v);
+      }
+    };
+    auto done = [&]() {
+      s::tmem_st_wait();
+      s::fence_proxy_async();
+      s::tc_fence_before();
+      s::mbar_arrive(copy_full);
+    };
+    bool ok = true;
+    if (has_init) {
+      const float* c = tab_of(0, 83);
+      ok = c != nullptr;
+      if (ok) {
+        // the pieces between this chunk and the sequence's start (walking back: its
+        // end), nearest first, each decayed over the nearer ones
+        const int pieces = prm.per == 0 ? 1 : static_cast<int>(BACK ? prm.K - (ch + 1) * prm.per : ch * prm.per);
+        const float whole = ex2(c[63]);
+#pragma unroll 1
+        for (int c32 = 0; c32 < 4; ++c32) {
           float x[32];
+          uint32_t v[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) x[e] = 0.f;
-          const int pieces = prm.per == 0 ? 1 : static_cast<int>(BACK ? prm.K - (ch + 1) * prm.per : ch * prm.per);
           float f = 1.f;
+#pragma unroll 1
           for (int j = 0; j < pieces; ++j) {
             const int64_t at = bh * prm.K + (prm.per == 0 ? ch : BACK ? (ch + 1) * prm.per + j : ch * prm.per - 1 - j);
             const float4* src = reinterpret_cast<const float4*>(prm.init + at * 128 * 128);
@@ -436,40 +500,29 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(x[e]);
-        } else {
-          s::tmem_ld32(ts + c32 * 32, v);
-          s::tmem_ld_wait();
+          put(v, c32, whole, n > 1);
         }
-        // far of the block before has read the copy
-        if (c32 == 0 && i > first_copy) ok = wait(copy_empty, (i - 1 - first_copy) & 1, 88);
-        if (!ok) break;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t off = (c32 >> 1) * 16384 + r * 128 + ((((c32 & 1) * 4 + q) ^ (r & 7)) << 4);
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float a = __uint_as_float(v[8 * q + 2 * e]), b = __uint_as_float(v[8 * q + 2 * e + 1]);
-            hi[e] = s::pack_bf16x2(a, b);
-            if (PARTS == 2)
-              lo[e] = s::pack_bf16x2(a - __uint_as_float(hi[e] << 16), b - __uint_as_float(hi[e] & 0xffff0000u));
-          }
-          s::st_shared_v4(cbase + off, hi[0], hi[1], hi[2], hi[3]);
-          if (PARTS == 2) s::st_shared_v4(cbase + kCopy + off, lo[0], lo[1], lo[2], lo[3]);
-        }
-        if (i + 1 < n) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(whole * __uint_as_float(v[e]));
-          s::tmem_st32(ts + c32 * 32, v);
-        }
+        done();
       }
-      if (!ok) break;
-      s::tmem_st_wait();
-      s::fence_proxy_async();
-      s::tc_fence_before();
-      s::mbar_arrive(copy_full);
     }
-  } else {
+    for (int i = 1; i < n && ok; ++i) {
+      const float* c = tab_of(i, 83);
+      if (!c) break;
+      const float whole = ex2(c[63]);
+      if (!wait(updated, (i - 1) & 1, 84)) break;
+      // far of the block before has read the copy
+      if (i > first_copy && !wait(copy_empty, (i - 1 - first_copy) & 1, 88)) break;
+      s::tc_fence_after();
+#pragma unroll 1
+      for (int c32 = 0; c32 < 4; ++c32) {
+        uint32_t v[32];
+        s::tmem_ld32(ts + c32 * 32, v);
+        s::tmem_ld_wait();
+        put(v, c32, whole, i + 1 < n);
+      }
+      done();
+    }
+  } else if (wg == 3) {
     // =========================================== out = head far + near -> HBM
     // Thread e holds column e of the 64 rows; the staging tile is [row][column].
     const int e = 32 * w4 + lane;
@@ -493,9 +546,9 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     int i = 0;
     for (; i < n; ++i) {
       const bool far = i >= first_copy;
-      const float* c = tab_of(i, 85);
-      if (!c) break;
-      const float call = c[63];
+      const float* head = tab_of(i, 85);
+      if (!head) break;
+      head += 64;
       if (GRAD) {
         if (!wait(&dot_full[i & 1], (i >> 1) & 1, 89)) break;
       } else if (i > 0) {
@@ -505,32 +558,27 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       s::tc_fence_after();
       const uint32_t t_far = tmem + kColOut + 128 * (i & 1) + lane_off, t_near = t_far + 64;
       const uint32_t ob = obase + (GRAD ? (i & 1) * kTile : 0);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t near[32], v[32];
-        s::tmem_ld32(t_near + 32 * h, near);
-        if (far) s::tmem_ld32(t_far + 32 * h, v);
+#pragma unroll 1
+      for (int h = 0; h < 4; ++h) {
+        uint32_t near[16], v[16];
+        tmem_ld16(t_near + 16 * h, near);
+        if (far) tmem_ld16(t_far + 16 * h, v);
         s::tmem_ld_wait();
-        float o[32];
+        float o[16];
 #pragma unroll
-        for (int t = 0; t < 32; t += 4) {
-          const float4 ct = *reinterpret_cast<const float4*>(c + 32 * h + t);
-          const float cc[4] = {ct.x, ct.y, ct.z, ct.w};
+        for (int t = 0; t < 16; t += 4) {
+          const float4 h4 = *reinterpret_cast<const float4*>(head + 16 * h + t);
+          const float hd[4] = {h4.x, h4.y, h4.z, h4.w};
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const float hd = ex2(BACK ? call - cc[u] : cc[u]);
-            o[t + u] = far ? fmaf(hd, __uint_as_float(v[t + u]), __uint_as_float(near[t + u]))
+          for (int u = 0; u < 4; ++u)
+            o[t + u] = far ? fmaf(hd[u], __uint_as_float(v[t + u]), __uint_as_float(near[t + u]))
                            : __uint_as_float(near[t + u]);
-          }
         }
-        if (h == 1) {
-          s::tc_fence_before();
-          s::mbar_arrive(&o_empty[i & 1]);
-        }
+        const uint32_t oh = ob + h * 16 * 128;
 #pragma unroll
-        for (int t = 0; t < 32; t += 2) {
+        for (int t = 0; t < 16; t += 2) {
           const uint32_t pk = s::pack_bf16x2(o[t], o[t + 1]);
-          const uint32_t a0 = ob + (32 * h + t) * 128 + sw[t & 7], a1 = ob + (32 * h + t + 1) * 128 + sw[(t + 1) & 7];
+          const uint32_t a0 = oh + t * 128 + sw[t & 7], a1 = oh + (t + 1) * 128 + sw[(t + 1) & 7];
           if (GRAD) {  // the dots' rows, then their place takes the output
             uint16_t x0, x1;
             asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x0) : "r"(a0) : "memory");
@@ -541,8 +589,13 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
           s::st_shared_u16(a0, static_cast<uint16_t>(pk));
           s::st_shared_u16(a1, static_cast<uint16_t>(pk >> 16));
         }
-        if (GRAD) dotbuf[(i & 1) * 256 + w4 * 64 + 32 * h + lane] = transposed_sum(o, lane);
+        if (GRAD) {
+          const float dot = transposed_sum(o, lane);
+          if (lane < 16) dotbuf[(i & 1) * 256 + w4 * 64 + 16 * h + lane] = dot;
+        }
       }
+      s::tc_fence_before();
+      s::mbar_arrive(&o_empty[i & 1]);
       s::fence_proxy_async();
       s::mbar_arrive(staged);
       // (All four warps meet here: whoever goes on to block i + 2, whose dots use the
@@ -617,7 +670,8 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (from lane 0, so that the compiler takes what depends on it as warp-uniform)
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   uint64_t* in_full = reinterpret_cast<uint64_t*>(smem + CF::OFF_BAR);
   uint64_t* in_empty = in_full + KS;
   uint64_t* y2_full = in_empty + KS;
@@ -677,22 +731,21 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
     }
   } else if (warp == 1) {
     constexpr uint32_t ID_UPD = s::make_idesc(128, 128, true, true);
-    const uint32_t base = s::smem_u32(smem);
+    const uint32_t lead = elect_one();
+    const uint64_t in_d = s::make_desc(s::smem_u32(smem), 8192, 1024);
     bool ok = true;
     for (int i = 0; i < n && ok; ++i) {
       ok = wait(&in_full[i % KS], (i / KS) & 1, 91) && wait(&y2_full[i & 1], (i >> 1) & 1, 92);
       if (!ok) break;
       s::tc_fence_after();
-      const uint32_t y2 = base + CF::OFF_Y2 + (i & 1) * 2 * kTile, za = base + (i % KS) * 2 * kTile + kTile;
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        s::mma_bf16_ss_warp(tmem, s::make_desc(y2 + (k >> 2) * kTile + (k & 3) * 2048, 8192, 1024),
-                            s::make_desc(za + (k & 3) * 2048, 8192, 1024), ID_UPD, i > 0 || k > 0);
-      s::mma_commit_warp(&y2_empty[i & 1]);
-      s::mma_commit_warp(&in_empty[i % KS]);
+      const uint64_t y2 = in_d + (CF::OFF_Y2 + (i & 1) * 2 * kTile) / 16, z = in_d + ((i % KS) * 2 * kTile + kTile) / 16;
+      mma_run<4>(lead, tmem, y2, z, 128, 128, 0, 0, ID_UPD, i > 0);
+      mma_run<4>(lead, tmem, y2 + kTile / 16, z, 128, 128, 0, 0, ID_UPD, 1);
+      commit(lead, &y2_empty[i & 1]);
+      commit(lead, &in_empty[i % KS]);
     }
-    if (ok) s::mma_commit_warp(done);
-    s::mma_commit_warp(drain);
+    if (ok) commit(lead, done);
+    commit(lead, drain);
     s::drain_wait(drain, 0);
   } else if (warp >= 4) {
     const int r = (warp - 4) * 8 + (lane >> 2), ch0 = (lane & 3) * 4;
@@ -715,7 +768,17 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
       ok = wait(&in_full[i % KS], (i / KS) & 1, 93) && wait(&y2_empty[i & 1], ((i >> 1) & 1) ^ 1, 94);
       if (!ok) break;
       const uint32_t y2 = s::smem_u32(smem + CF::OFF_Y2 + (i & 1) * 2 * kTile);
-      scale_row(s::smem_u32(smem + (i % KS) * 2 * kTile), y2, y2 + kTile, r, f, ch0, 4);
+      const uint32_t ya = s::smem_u32(smem + (i % KS) * 2 * kTile);
+#pragma unroll
+      for (int ch = ch0; ch < ch0 + 4; ++ch) {
+        const uint32_t off = (ch >> 3) * 8192 + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+        uint32_t x[4], hi[4], lo[4];
+        s::ld_shared_v4(ya + off, x[0], x[1], x[2], x[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split_scaled(x[e], f, hi[e], lo[e]);
+        s::st_shared_v4(y2 + off, hi[0], hi[1], hi[2], hi[3]);
+        s::st_shared_v4(y2 + kTile + off, lo[0], lo[1], lo[2], lo[3]);
+      }
       s::fence_proxy_async();
       s::mbar_arrive(&y2_full[i & 1]);
     }
@@ -769,7 +832,7 @@ inline cudaError_t launch_sm100(const void* x, const void* y, const void* z, voi
   auto kern = gated_sm100_kernel<BACK, GRAD>;
   static bool done[128];
   if (!smem_attribute_set(kern, TcCfg<GRAD>::SMEM, done)) return cudaErrorInvalidValue;
-  return launch_pdl(kern, dim3((unsigned)(BH * p.C)), dim3(512), TcCfg<GRAD>::SMEM, st, tx, ty, tz, to, td, p);
+  return launch_pdl(kern, dim3((unsigned)(BH * p.C)), dim3(kMainThreads), TcCfg<GRAD>::SMEM, st, tx, ty, tz, to, td, p);
 }
 
 }  // namespace gated
