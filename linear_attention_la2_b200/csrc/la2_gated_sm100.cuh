@@ -308,7 +308,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       const uint32_t t_far = tmem + kColOut + 128 * (i & 1), t_near = t_far + 64;
       ok = false;
       // With three stages the next block has landed by now; with two its load began
-      // when the block before this one was done, so its S waits until after far.
+      // when the block before this one was done, so its S comes after the update.
       if (KS > 2 && i + 1 < n && !scores(i + 1)) break;
       if (far && !wait(copy_full, (i - first_copy) & 1, 74)) break;
       if (i + 1 < n) {  // the state past the chunk's last block is not needed
@@ -319,6 +319,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         mma_run<4>(lead, tmem + kColState, GRAD ? z : lo_d, GRAD ? lo_d : z, 128, 128, 0, 0, ID_UPD, 1);
         commit(lead, updated);
         commit(lead, y_empty);
+        if (KS == 2 && !scores(i + 1)) break;
       }
       if (!wait(&o_empty[i & 1], ((i >> 1) & 1) ^ 1, 73)) break;
       s::tc_fence_after();
@@ -328,7 +329,6 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
           mma_run<8>(lead, t_far, copy_d + kCopy / 16, row_d + st, kCopyStep, 2, kCopyStep4, 512, ID_FAR, 1);
         commit(lead, copy_empty);
       }
-      if (KS == 2 && i + 1 < n && !scores(i + 1)) break;
       if (!wait(p_full, i & 1, 76)) break;
       s::tc_fence_after();
       mma_run<4>(lead, t_near, col_d + st + kZ, p_d, 128, 2, 0, 0, ID_NEAR, 0);
@@ -440,11 +440,11 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     const int r = 32 * w4 + lane;  // state row
     const uint32_t ts = tmem + kColState + lane_off;
     const uint32_t cbase = s::smem_u32(smem + CF::OFF_COPY);
-    // 32 columns of row r into the copy, and times f into the state
-    auto put = [&](uint32_t (&v)[32], int c32, float f, bool keep) {
+    // 16 columns of row r into the copy, and times f into the state
+    auto put = [&](uint32_t (&v)[16], int h, float f, bool keep) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t off = (c32 >> 1) * 16384 + r * 128 + ((((c32 & 1) * 4 + q) ^ (r & 7)) << 4);
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t off = (h >> 2) * 16384 + r * 128 + ((((h & 3) * 2 + q) ^ (r & 7)) << 4);
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -458,8 +458,8 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       }
       if (keep) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(f * __uint_as_float(v[e]));
-        s::tmem_st32(ts + c32 * 32, v);
+        for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(f * __uint_as_float(v[e]));
+        s::tmem_st16(ts + h * 16, v);
       }
     };
     auto done = [&]() {
@@ -478,19 +478,19 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         const int pieces = prm.per == 0 ? 1 : static_cast<int>(BACK ? prm.K - (ch + 1) * prm.per : ch * prm.per);
         const float whole = ex2(c[63]);
 #pragma unroll 1
-        for (int c32 = 0; c32 < 4; ++c32) {
-          float x[32];
-          uint32_t v[32];
+        for (int h = 0; h < 8; ++h) {
+          float x[16];
+          uint32_t v[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = 0.f;
+          for (int e = 0; e < 16; ++e) x[e] = 0.f;
           float f = 1.f;
 #pragma unroll 1
           for (int j = 0; j < pieces; ++j) {
             const int64_t at = bh * prm.K + (prm.per == 0 ? ch : BACK ? (ch + 1) * prm.per + j : ch * prm.per - 1 - j);
             const float4* src = reinterpret_cast<const float4*>(prm.init + at * 128 * 128);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float4 y = src[s::state_f4<128>(r, c32 * 8 + q)];
+            for (int q = 0; q < 4; ++q) {
+              const float4 y = src[s::state_f4<128>(r, h * 4 + q)];
               x[4 * q] = fmaf(f, y.x, x[4 * q]);
               x[4 * q + 1] = fmaf(f, y.y, x[4 * q + 1]);
               x[4 * q + 2] = fmaf(f, y.z, x[4 * q + 2]);
@@ -499,8 +499,8 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             if (j + 1 < pieces) f *= expf(static_cast<float>(prm.tot[at]));
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(x[e]);
-          put(v, c32, whole, n > 1);
+          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(x[e]);
+          put(v, h, whole, n > 1);
         }
         done();
       }
@@ -513,12 +513,17 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       // far of the block before has read the copy
       if (i > first_copy && !wait(copy_empty, (i - 1 - first_copy) & 1, 88)) break;
       s::tc_fence_after();
+      uint32_t v[16], w[16];  // the next load is under way while one is put
+      tmem_ld16(ts, v);
+      s::tmem_ld_wait();
 #pragma unroll 1
-      for (int c32 = 0; c32 < 4; ++c32) {
-        uint32_t v[32];
-        s::tmem_ld32(ts + c32 * 32, v);
+      for (int h = 0; h < 8; h += 2) {
+        tmem_ld16(ts + 16 * (h + 1), w);
+        put(v, h, whole, i + 1 < n);
         s::tmem_ld_wait();
-        put(v, c32, whole, i + 1 < n);
+        if (h < 6) tmem_ld16(ts + 16 * (h + 2), v);
+        put(w, h + 1, whole, i + 1 < n);
+        s::tmem_ld_wait();
       }
       done();
     }
@@ -532,19 +537,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 #pragma unroll
     for (int m = 0; m < 8; ++m) sw[m] = static_cast<uint32_t>((cj ^ m) << 4);
     float* dotbuf = reinterpret_cast<float*>(smem + CF::OFF_DOT);
-    const bool lead = w4 == 0 && lane == 0;
-    int dots_issued = 0;
-    auto load_dot_rows = [&](int i) {  // by the lead thread, into the block's staging tile
-      uint8_t* dst = smem + CF::OFF_OUT + (i & 1) * kTile;
-      s::mbar_expect_tx(&dot_full[i & 1], kTile);
-      for (int p = 0; p < 2; ++p)
-        s::tma_load_3d(dst + p * 8192, &tm_dot, &dot_full[i & 1], 64 * p, static_cast<int>(row_of(i)), static_cast<int>(bh));
-      ++dots_issued;
-    };
-    if (GRAD && lead)
-      for (int i = 0; i < min(n, 2); ++i) load_dot_rows(i);
-    int i = 0;
-    for (; i < n; ++i) {
+    for (int i = 0; i < n; ++i) {
       const bool far = i >= first_copy;
       const float* head = tab_of(i, 85);
       if (!head) break;
@@ -563,6 +556,13 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         uint32_t near[16], v[16];
         tmem_ld16(t_near + 16 * h, near);
         if (far) tmem_ld16(t_far + 16 * h, v);
+        const uint32_t oh = ob + h * 16 * 128;
+        uint16_t x[16];  // the dots' rows, before their place takes the output
+        if (GRAD) {
+#pragma unroll
+          for (int t = 0; t < 16; ++t)
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x[t]) : "r"(oh + t * 128 + sw[t & 7]) : "memory");
+        }
         s::tmem_ld_wait();
         float o[16];
 #pragma unroll
@@ -574,22 +574,15 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             o[t + u] = far ? fmaf(hd[u], __uint_as_float(v[t + u]), __uint_as_float(near[t + u]))
                            : __uint_as_float(near[t + u]);
         }
-        const uint32_t oh = ob + h * 16 * 128;
 #pragma unroll
         for (int t = 0; t < 16; t += 2) {
           const uint32_t pk = s::pack_bf16x2(o[t], o[t + 1]);
-          const uint32_t a0 = oh + t * 128 + sw[t & 7], a1 = oh + (t + 1) * 128 + sw[(t + 1) & 7];
-          if (GRAD) {  // the dots' rows, then their place takes the output
-            uint16_t x0, x1;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x0) : "r"(a0) : "memory");
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x1) : "r"(a1) : "memory");
-            o[t] *= __uint_as_float(static_cast<uint32_t>(x0) << 16);
-            o[t + 1] *= __uint_as_float(static_cast<uint32_t>(x1) << 16);
-          }
-          s::st_shared_u16(a0, static_cast<uint16_t>(pk));
-          s::st_shared_u16(a1, static_cast<uint16_t>(pk >> 16));
+          s::st_shared_u16(oh + t * 128 + sw[t & 7], static_cast<uint16_t>(pk));
+          s::st_shared_u16(oh + (t + 1) * 128 + sw[(t + 1) & 7], static_cast<uint16_t>(pk >> 16));
         }
         if (GRAD) {
+#pragma unroll
+          for (int t = 0; t < 16; ++t) o[t] *= __uint_as_float(static_cast<uint32_t>(x[t]) << 16);
           const float dot = transposed_sum(o, lane);
           if (lane < 16) dotbuf[(i & 1) * 256 + w4 * 64 + 16 * h + lane] = dot;
         }
@@ -598,32 +591,55 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       s::mbar_arrive(&o_empty[i & 1]);
       s::fence_proxy_async();
       s::mbar_arrive(staged);
-      // (All four warps meet here: whoever goes on to block i + 2, whose dots use the
-      // same buffer, has met the readers of this block's at block i + 1.)
-      if (!wait(staged, i & 1, 89)) break;
-      if (lead) {
+    }
+  } else if (warp == 3) {
+    // ==================================== stores, and the rows of the dots (GRAD)
+    // A staging tile: [dots' rows loaded ->] output written (staged) -> store has
+    // read it -> free (out_free, or the load of the dots' rows two blocks on). The
+    // dots of a block meet here, before its tile and their buffer are free again.
+    const float* dotbuf = reinterpret_cast<const float*>(smem + CF::OFF_DOT);
+    auto load_dot_rows = [&](int i) {
+      uint8_t* dst = smem + CF::OFF_OUT + (i & 1) * kTile;
+      s::mbar_expect_tx(&dot_full[i & 1], kTile);
+      for (int p = 0; p < 2; ++p)
+        s::tma_load_3d(dst + p * 8192, &tm_dot, &dot_full[i & 1], 64 * p, static_cast<int>(row_of(i)), static_cast<int>(bh));
+    };
+    int issued = 0;
+    if (GRAD)
+      for (; issued < min(n, 2); ++issued)
+        if (lane == 0) load_dot_rows(issued);
+    for (int i = 0; i < n; ++i) {
+      if (!wait(staged, i & 1, 91)) break;
+      if (lane == 0) {
         // A chunk ends on a block boundary or at N, where the tensor map clips.
         for (int p = 0; p < 2; ++p)
           s::tma_store_3d(&tm_o, smem + CF::OFF_OUT + (GRAD ? (i & 1) * kTile : 0) + p * 8192, 64 * p,
                           static_cast<int>(row_of(i)), static_cast<int>(bh));
         s::bulk_commit_group();
       }
-      if (GRAD && w4 < 2) {  // the dots of 64 rows
-        const int t = 32 * w4 + lane;
-        const float* db = dotbuf + (i & 1) * 256 + t;
-        if (row_of(i) + t < t1) prm.dots[bh * prm.N + row_of(i) + t] = (db[0] + db[64]) + (db[128] + db[192]);
+      if (GRAD) {
+        const float* db = dotbuf + (i & 1) * 256 + 2 * lane;
+        const int64_t row = row_of(i) + 2 * lane;
+        float2 a[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) a[w] = *reinterpret_cast<const float2*>(db + 64 * w);
+        float* d = prm.dots + bh * prm.N + row;
+        if (row < t1) d[0] = (a[0].x + a[1].x) + (a[2].x + a[3].x);
+        if (row + 1 < t1) d[1] = (a[0].y + a[1].y) + (a[2].y + a[3].y);
+        __syncwarp();
       }
-      if (lead) {
+      if (lane == 0) {
         s::bulk_wait_group_read<0>();  // the store has read the tile
         if (!GRAD) s::mbar_arrive(out_free);
         else if (i + 2 < n) load_dot_rows(i + 2);
       }
+      if (GRAD && i + 2 < n) ++issued;
       __syncwarp();
     }
-    if (lead) {
+    if (lane == 0) {
       // loads still in flight after an abort, and the stores, are done before exit
       if (GRAD)
-        for (int j = max(0, dots_issued - 2); j < dots_issued; ++j) s::drain_wait(&dot_full[j & 1], (j >> 1) & 1);
+        for (int j = max(0, issued - 2); j < issued; ++j) s::drain_wait(&dot_full[j & 1], (j >> 1) & 1);
       s::bulk_wait_group<0>();
     }
   }
