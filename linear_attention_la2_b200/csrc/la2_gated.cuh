@@ -12,7 +12,7 @@ struct Plan {
   // Tensor cores: the pieces whose own states are computed (Ls rows, K a sequence,
   // `per` a chunk); per = 0 (and K = C): a scan turns them into the chunks' states.
   int64_t Ls = 0, K = 1, per = 0;
-  size_t off_suffix = 0, off_tot = 0, off_qdq = 0, off_kdk = 0;  // prefix states at 0
+  size_t off_suffix = 0, off_suffix_t = 0, off_tot = 0, off_qdq = 0, off_kdk = 0;  // prefix states at 0
   size_t bytes = 0;
 };
 
@@ -94,6 +94,8 @@ static Plan make_plan(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, la
   size_t at = one;
   p.off_suffix = at;
   if (need == NEED_BWD) at += one;
+  p.off_suffix_t = at;  // tensor cores: the suffix states transposed, for dV
+  if (need == NEED_BWD && p.tc) at += one;
   p.off_tot = at;
   if (states) at += round256((size_t)BH * p.K * sizeof(double));
   p.off_qdq = at;
@@ -148,28 +150,34 @@ static la2_status forward(const void* q, const void* k, const void* v, const voi
   return launch_status();
 }
 
-// Tensor cores: states of the pieces that a chunk starts from (all of them after a
-// prefill), and their scan where the chunks do not add them up.
-static la2_status states_tc(const void* y, const void* z, const void* gate, float* out, double* tot, int64_t BH,
-                            const Shape& sh, const Plan& pl, bool suffix, bool all, cudaStream_t st) {
+// Tensor cores: states of the pieces that a chunk starts from, and their scan where
+// the chunks do not add them up themselves. kind: what they are for.
+enum States { FOR_O, FOR_DQ, FOR_DK_DV, FOR_POOL };
+static la2_status states_tc(const void* y, const void* z, const void* gate, float* out, float* out_t, double* tot,
+                            int64_t BH, const Shape& sh, const Plan& pl, States kind, cudaStream_t st) {
   const int64_t per = std::max<int64_t>(1, pl.per);
   TcStateParams p{};
   p.gate = static_cast<const __nv_bfloat16*>(gate);
   p.out = out;
+  p.out_t = out_t;
   p.tot = tot;
   p.N = sh.N;
   p.L = pl.Ls;
   p.K = pl.K;
-  p.first = suffix ? per : 0;
-  p.count = all ? pl.K : suffix ? pl.K - per : (pl.C - 1) * per;
+  p.first = kind == FOR_DK_DV ? per : 0;
+  p.count = kind == FOR_POOL ? pl.K : kind == FOR_DK_DV ? pl.K - per : (pl.C - 1) * per;
   p.spin_limit = spin_limit();
   {
     LaunchTimer t(K_GATED_STATE, st);
-    if ((suffix ? launch_state_sm100<true>(y, z, p, BH, st) : launch_state_sm100<false>(y, z, p, BH, st)) != cudaSuccess)
-      return LA2_ERR_CUDA;
+    const cudaError_t e = kind == FOR_DK_DV ? launch_state_sm100<true, false>(y, z, p, BH, st)
+                          : kind == FOR_O   ? launch_state_sm100<false, true>(y, z, p, BH, st)
+                                            : launch_state_sm100<false, false>(y, z, p, BH, st);
+    if (e != cudaSuccess) return LA2_ERR_CUDA;
   }
-  const la2_status s = launch_status();
-  return s != LA2_OK || all || pl.per > 0 ? s : scan(out, tot, BH, sh, suffix ? 1 : 0, st);
+  la2_status s = launch_status();
+  if (s != LA2_OK || kind == FOR_POOL || pl.per > 0) return s;
+  s = scan(out, tot, BH, sh, kind == FOR_DK_DV ? 1 : 0, st);
+  return s != LA2_OK || !out_t ? s : scan(out_t, tot, BH, sh, 1, st);
 }
 
 static TcParams tc_params(const void* gate, const float* init, const double* tot, const Shape& sh, const Plan& pl) {
@@ -191,7 +199,7 @@ static la2_status forward_tc(const void* q, const void* k, const void* v, const 
   float* states = p.C > 1 ? reinterpret_cast<float*>(ws) : nullptr;
   double* tot = reinterpret_cast<double*>(ws + p.off_tot);
   if (states) {
-    const la2_status s = states_tc(k, v, gate, states, tot, BH, sh, p, false, false, st);
+    const la2_status s = states_tc(k, v, gate, states, nullptr, tot, BH, sh, p, FOR_O, st);
     if (s != LA2_OK) return s;
   }
   LaunchTimer t(K_GATED_FWD, st);
@@ -210,13 +218,14 @@ static la2_status backward_tc(const void* q, const void* k, const void* v, const
                               const Shape& sh, cudaStream_t st) {
   float* prefix = p.C > 1 ? reinterpret_cast<float*>(ws) : nullptr;
   float* suffix = p.C > 1 ? reinterpret_cast<float*>(ws + p.off_suffix) : nullptr;
+  float* suffix_t = p.C > 1 ? reinterpret_cast<float*>(ws + p.off_suffix_t) : nullptr;
   float* qdq = reinterpret_cast<float*>(ws + p.off_qdq);
   float* kdk = reinterpret_cast<float*>(ws + p.off_kdk);
   double* tot = reinterpret_cast<double*>(ws + p.off_tot);
   la2_status s = LA2_OK;
   if (prefix) {
-    if ((s = states_tc(k, v, gate, prefix, tot, BH, sh, p, false, false, st)) != LA2_OK) return s;
-    if ((s = states_tc(q, dout, gate, suffix, tot, BH, sh, p, true, false, st)) != LA2_OK) return s;
+    if ((s = states_tc(k, v, gate, prefix, nullptr, tot, BH, sh, p, FOR_DQ, st)) != LA2_OK) return s;
+    if ((s = states_tc(q, dout, gate, suffix, suffix_t, tot, BH, sh, p, FOR_DK_DV, st)) != LA2_OK) return s;
   }
   {
     TcParams t = tc_params(gate, prefix, tot, sh, p);
@@ -225,9 +234,10 @@ static la2_status backward_tc(const void* q, const void* k, const void* v, const
     if (launch_sm100<false, true>(dout, v, k, dq, q, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
   }
   {
-    TcParams t = tc_params(gate, suffix, tot, sh, p);
+    TcParams t = tc_params(gate, suffix_t, tot, sh, p);
     LaunchTimer lt(K_GATED_DKDV, st);
     if (launch_sm100<true, false>(k, q, dout, dvv, nullptr, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
+    t.init = suffix;
     t.dots = kdk;
     if (launch_sm100<true, true>(v, dout, q, dk, k, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
   }
@@ -411,7 +421,7 @@ la2_status la2_kv_state_gated(const void* k, const void* v, const void* gate, fl
   float* chunks = static_cast<float*>(workspace);
   double* tot = reinterpret_cast<double*>(static_cast<char*>(workspace) + p.off_tot);
   if (p.tc)
-    s = gated::states_tc(k, v, gate, chunks, tot, B * H, sh, p, false, true, st);
+    s = gated::states_tc(k, v, gate, chunks, nullptr, tot, B * H, sh, p, gated::FOR_POOL, st);
   else
     s = dt == LA2_BF16 ? gated::chunk_states<__nv_bfloat16, false>(k, v, gate, chunks, tot, B * H, sh, st)
                        : gated::chunk_states<float, false>(k, v, gate, chunks, tot, B * H, sh, st);

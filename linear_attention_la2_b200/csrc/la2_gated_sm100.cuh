@@ -5,28 +5,34 @@
 // One kernel does all four products of a layer, as out_t = sum over the kept s of
 // w(t, s) (x_t . y_s) z_s with (x, y, z) in the query, key and value places:
 //
-//             x   y   z    walk      kept     w                  state (c x e)
-//   O         q   k   v    forward   s <= t   e^(c_t - c_s)      KV = k^T v
-//   dQ        dO  v   k    forward   s <= t   e^(c_t - c_s)      KV, read transposed
-//   dV        k   q   dO   back      s >= t   e^(c_s - c_t)      U = q^T dO
-//   dK        v   dO  q    back      s >= t   e^(c_s - c_t)      U, read transposed
+//             x   y   z    walk      kept     w                  state (z x y)
+//   O         q   k   v    forward   s <= t   e^(c_t - c_s)      KV^T = v^T k
+//   dQ        dO  v   k    forward   s <= t   e^(c_t - c_s)      KV = k^T v
+//   dV        k   q   dO   back      s >= t   e^(c_s - c_t)      U^T = dO^T q
+//   dK        v   dO  q    back      s >= t   e^(c_s - c_t)      U = q^T dO
 //
 // Per block of 64 rows, walking a chunk of one (b, h) sequence in one CTA:
-//   S     = X Y^T                      tcgen05 -> TMEM (two buffers)
+//   S     = X Y^T                      tcgen05 -> TMEM
 //   P     = bf16(S w)                  mask warps, TMEM -> shared memory
-//   near  = Z^T P^T                    tcgen05 -> TMEM, transposed: M = 128 lanes,
-//   far   = state^T X^T                64 columns each, so two buffers of both fit
+//   near  = Z^T P^T                    tcgen05 -> TMEM, transposed: M = 128 lanes, 64
+//   far   = state X^T                  columns each; the state's bf16 copy is the A
+//                                      operand, read from TMEM
 //   out   = head far + near            epilogue warps: the row's e^(c_t) (walking
 //                                      back e^(c_R - c_t)) is applied in fp32
-//   state <- e^(c_R) state + Y~^T Z    tcgen05, Y~ = rows scaled by e^(c_R - c_s)
+//   state <- e^(c_R) state + Z^T Y~    tcgen05, Y~ = rows scaled by e^(c_R - c_s)
 //                                      (walking back e^(c_s))
 // far and near are separate accumulators, so X needs no scaling. Y~ is made in place
 // once S has read Y, as a bf16 value there and its bf16 remainder beside it (two
 // MMAs): one rounding fewer in the outputs, and states good to 2^-17. The state stays
 // in TMEM: the state warps read it once a block, write its bf16 copy for far, and put
 // e^(c_R) times it back, which the block's update adds onto. The loop-carried path is
-// update -> copy -> update; S of the next block is issued before P of this one is
-// waited for, and the accumulators' second buffer lets the epilogue trail a block.
+// update -> copy -> update; S of the next block is issued before it, and the second
+// buffers of far and P let the epilogue and the mask trail.
+//
+// What bounds it: shared-memory bandwidth. Tile loads, operand reads, the scaling, P
+// and the output tile take about 2200 cycles of 128 bytes a 64-row block (GRAD 2900),
+// against 2850 cycles that a block's share of HBM takes at 148 SMs; the state's copy
+// as an operand in shared memory took 500 (GRAD 1000) more.
 //
 // Gate sums: c in base 2, fp32, at most 64 terms; a log gate under kLog2Zero (in
 // base 2) counts as that, its exponential is 0, so a restart cuts exactly and costs
@@ -52,7 +58,6 @@ namespace gated {
 namespace s = sm100;
 
 constexpr int kTile = 64 * 128 * 2;       // one 64 x 128 bf16 tile
-constexpr int kCopy = 128 * 128 * 2;      // the state's bf16 copy
 constexpr int kMainThreads = 640;
 constexpr float kLog2Zero = -160.f;
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -103,6 +108,14 @@ __device__ __forceinline__ void mma_run(uint32_t lead, uint32_t d, uint64_t a, u
   }
   __syncwarp();
 }
+// D[tmem] (+)= A[tmem] B[smem] by the calling thread (A: M lanes, two bf16 a column).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 __device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
   if (lead) s::mma_commit(bar);
   __syncwarp();
@@ -122,22 +135,20 @@ struct TcParams {
 
 template <bool GRAD>
 struct TcCfg {
-  static constexpr int KS = GRAD ? 2 : 3;          // stages of X, Y, Z
-  static constexpr int PARTS = GRAD ? 2 : 1;       // bf16 tiles of the state's copy
-  static constexpr int OB = GRAD ? 2 : 1;          // staging tiles of the output
+  static constexpr int KS = 3;                     // stages of X, Y, Z
+  static constexpr int PARTS = GRAD ? 2 : 1;       // bf16 parts of the state's copy (64 columns each)
   static constexpr int OFF_LO = KS * 3 * kTile;    // remainder of Y~
   static constexpr int OFF_P = OFF_LO + kTile;
-  static constexpr int OFF_COPY = OFF_P + 64 * 64 * 2;
-  static constexpr int OFF_OUT = OFF_COPY + PARTS * kCopy;
-  static constexpr int OFF_TAB = OFF_OUT + OB * kTile;
+  static constexpr int OFF_OUT = OFF_P + 2 * 64 * 64 * 2;
+  static constexpr int OFF_TAB = OFF_OUT + 2 * kTile;
   static constexpr int OFF_DOT = OFF_TAB + kTabs * 128 * 4;
   static constexpr int OFF_BAR = OFF_DOT + (GRAD ? 2 * 4 * 64 * 4 : 0);
-  static constexpr int NBAR = 2 * KS + 4 + 2 + 2 + 3 + 4 + 2 + 2 + kTabs + 1;
+  static constexpr int NBAR = 2 * KS + 3 + 4 + 2 + 3 + 2 + 3 + kTabs + 1;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
-// TMEM columns: the state; two buffers of S (64); two of far and near (64 each)
-constexpr uint32_t kColState = 0, kColS = 128, kColOut = 256;
+// TMEM columns: the state, its copy (value, remainder), S, two buffers of far, near
+constexpr uint32_t kColState = 0, kColCopy = 128, kColS = 256, kColFar = 320, kColNear = 448;
 
 // Two bf16 values times f: the rounded products, and what they are off, rounded.
 __device__ __forceinline__ void split_scaled(uint32_t x, float f, uint32_t& hi, uint32_t& lo) {
@@ -158,6 +169,13 @@ __device__ __forceinline__ float transposed_sum(float (&v)[16], int lane) {
     }
   }
   return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+}
+
+// Thread t of the warp writes 8 consecutive columns of TMEM lane (lane field) + t.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // Thread t of the warp reads 16 consecutive columns of TMEM lane (lane field) + t.
@@ -187,14 +205,12 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
   uint64_t* in_empty = in_full + KS;
   uint64_t* s_full = in_empty + KS;
   uint64_t* s_empty = s_full + 2;
-  uint64_t *p_full = s_empty + 2, *p_empty = p_full + 1;
-  uint64_t *y_full = p_empty + 1, *y_empty = y_full + 1;
+  uint64_t *p_full = s_empty + 1, *p_empty = p_full + 2;
+  uint64_t *y_full = p_empty + 2, *y_empty = y_full + 1;
   uint64_t *copy_full = y_empty + 1, *copy_empty = copy_full + 1, *updated = copy_empty + 1;
-  uint64_t* o_full = updated + 1;
-  uint64_t* o_empty = o_full + 2;
-  uint64_t *staged = o_empty + 2, *out_free = staged + 1;
-  uint64_t* dot_full = out_free + 1;
-  uint64_t* tab_full = dot_full + 2;
+  uint64_t *o_full = updated + 1, *o_empty = o_full + 1;
+  uint64_t *staged = o_empty + 1, *tile_free = staged + 1;
+  uint64_t* tab_full = tile_free + 2;
   uint64_t* drain = tab_full + kTabs;
   uint32_t* tmem_base = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base + 1);
@@ -211,20 +227,19 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     for (int i = 0; i < KS; ++i) { s::mbar_init(&in_full[i], 1); s::mbar_init(&in_empty[i], 1); }
     for (int i = 0; i < 2; ++i) {
       s::mbar_init(&s_full[i], 1);
-      s::mbar_init(&s_empty[i], 128);
-      s::mbar_init(&o_full[i], 1);
-      s::mbar_init(&o_empty[i], 128);
-      s::mbar_init(&dot_full[i], 1);
+      s::mbar_init(&p_full[i], 128);
+      s::mbar_init(&p_empty[i], 1);
+      s::mbar_init(&tile_free[i], 1);
     }
-    s::mbar_init(p_full, 128);
-    s::mbar_init(p_empty, 1);
+    s::mbar_init(s_empty, 128);
+    s::mbar_init(o_full, 1);
+    s::mbar_init(o_empty, 128);
     s::mbar_init(y_full, 128);
     s::mbar_init(y_empty, 1);
     s::mbar_init(copy_full, 128);
     s::mbar_init(copy_empty, 1);
     s::mbar_init(updated, 1);
     s::mbar_init(staged, 128);
-    s::mbar_init(out_free, 1);
     for (int i = 0; i < kTabs; ++i) s::mbar_init(&tab_full[i], 32);
     s::mbar_init(drain, 1);
     *abort_flag = 0;
@@ -279,7 +294,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
   } else if (warp == 1) {
     // ================================================================== MMA
     constexpr uint32_t ID_S = s::make_idesc(64, 64, false, false);
-    constexpr uint32_t ID_FAR = s::make_idesc(128, 64, !GRAD, false);  // GRAD: the state read transposed
+    constexpr uint32_t ID_FAR = s::make_idesc(128, 64, false, false);
     constexpr uint32_t ID_UPD = s::make_idesc(128, 128, true, true);
     constexpr uint32_t ID_NEAR = s::make_idesc(128, 64, true, false);
     const uint32_t lead = elect_one();
@@ -289,15 +304,12 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     constexpr uint32_t kStage = 3 * kTile / 16, kY = kTile / 16, kZ = 2 * kTile / 16;
     const uint64_t row_d = s::make_desc(base, 16, 1024), col_d = s::make_desc(base, 8192, 1024);
     const uint64_t lo_d = s::make_desc(base + CF::OFF_LO, 8192, 1024), p_d = s::make_desc(base + CF::OFF_P, 16, 1024);
-    const uint64_t copy_d = GRAD ? s::make_desc(base + CF::OFF_COPY, 16, 1024)
-                                 : s::make_desc(base + CF::OFF_COPY, 16384, 1024);
-    constexpr uint32_t kCopyStep = GRAD ? 2 : 128, kCopyStep4 = GRAD ? 1024 : 512;
     auto scores = [&](int i) -> bool {  // S of block i
       if (!wait(&in_full[i % KS], (i / KS) & 1, 71)) return false;
-      if (!wait(&s_empty[i & 1], ((i >> 1) & 1) ^ 1, 72)) return false;
+      if (!wait(s_empty, (i & 1) ^ 1, 72)) return false;
       s::tc_fence_after();
       const uint32_t st = (i % KS) * kStage;
-      mma_run<8>(lead, tmem + kColS + 64 * (i & 1), row_d + st, row_d + st + kY, 2, 2, 512, 512, ID_S, 0);
+      mma_run<8>(lead, tmem + kColS, row_d + st, row_d + st + kY, 2, 2, 512, 512, ID_S, 0);
       commit(lead, &s_full[i & 1]);
       return true;
     };
@@ -305,35 +317,34 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     for (int i = 0; i < n && ok; ++i) {
       const uint32_t st = (i % KS) * kStage;
       const bool far = i >= first_copy;
-      const uint32_t t_far = tmem + kColOut + 128 * (i & 1), t_near = t_far + 64;
       ok = false;
-      // With three stages the next block has landed by now; with two its load began
-      // when the block before this one was done, so its S comes after the update.
-      if (KS > 2 && i + 1 < n && !scores(i + 1)) break;
+      if (i + 1 < n && !scores(i + 1)) break;
       if (far && !wait(copy_full, (i - first_copy) & 1, 74)) break;
       if (i + 1 < n) {  // the state past the chunk's last block is not needed
         if (!wait(y_full, i & 1, 75)) break;
         s::tc_fence_after();
-        const uint64_t y1 = col_d + st + kY, z = col_d + st + kZ;
-        mma_run<4>(lead, tmem + kColState, GRAD ? z : y1, GRAD ? y1 : z, 128, 128, 0, 0, ID_UPD, far);
-        mma_run<4>(lead, tmem + kColState, GRAD ? z : lo_d, GRAD ? lo_d : z, 128, 128, 0, 0, ID_UPD, 1);
+        mma_run<4>(lead, tmem + kColState, col_d + st + kZ, col_d + st + kY, 128, 128, 0, 0, ID_UPD, far);
+        mma_run<4>(lead, tmem + kColState, col_d + st + kZ, lo_d, 128, 128, 0, 0, ID_UPD, 1);
         commit(lead, updated);
         commit(lead, y_empty);
-        if (KS == 2 && !scores(i + 1)) break;
       }
-      if (!wait(&o_empty[i & 1], ((i >> 1) & 1) ^ 1, 73)) break;
-      s::tc_fence_after();
-      if (far) {
-        mma_run<8>(lead, t_far, copy_d, row_d + st, kCopyStep, 2, kCopyStep4, 512, ID_FAR, 0);
-        if (PARTS == 2)
-          mma_run<8>(lead, t_far, copy_d + kCopy / 16, row_d + st, kCopyStep, 2, kCopyStep4, 512, ID_FAR, 1);
+      if (far) {  // (its buffer: the epilogue has read block i - 2, see near of i - 1)
+        s::tc_fence_after();
+        if (lead) {
+#pragma unroll
+          for (int k = 0; k < 8 * PARTS; ++k)
+            mma_ts(tmem + kColFar + 64 * (i & 1), tmem + kColCopy + 8 * k,
+                   row_d + st + ((k & 7) >> 2) * 512 + (k & 3) * 2, ID_FAR, k > 0);
+        }
+        __syncwarp();
         commit(lead, copy_empty);
       }
-      if (!wait(p_full, i & 1, 76)) break;
+      if (!wait(&p_full[i & 1], (i >> 1) & 1, 76)) break;
+      if (!wait(o_empty, (i & 1) ^ 1, 73)) break;  // the epilogue has read near of block i - 1
       s::tc_fence_after();
-      mma_run<4>(lead, t_near, col_d + st + kZ, p_d, 128, 2, 0, 0, ID_NEAR, 0);
-      commit(lead, &o_full[i & 1]);
-      commit(lead, p_empty);
+      mma_run<4>(lead, tmem + kColNear, col_d + st + kZ, p_d + (i & 1) * 512, 128, 2, 0, 0, ID_NEAR, 0);
+      commit(lead, o_full);
+      commit(lead, &p_empty[i & 1]);
       commit(lead, &in_empty[i % KS]);
       ok = true;
     }
@@ -343,8 +354,8 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     // =========================================================== gate tables
     // Per block: the running sums c, then the epilogue's factors of far. Table i goes
     // into slot i % 8 when block i - KS has released its stage (in_empty): everything
-    // of it is done but its epilogue, and before its far was issued the epilogue had
-    // read block i - KS - 2 (o_empty), so readers of block i - 8 are long done.
+    // of it is done but its epilogue, and before its near was issued the epilogue had
+    // read block i - KS - 1 (o_empty), so readers of block i - 8 are long done.
     const __nv_bfloat16* g = prm.gate + bh * prm.N;
     // (nothing comes before the first token for its gate to pass on: 0, unless NaN)
     auto gate_at = [&](int64_t t) {
@@ -402,9 +413,10 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       const float* c = tab_of(i, 80);
       if (!c) break;
       const float cr = r >= 0 ? c[r] : 0.f;
+      const uint32_t pb = pbase + (i & 1) * 8192 + r * 128;
       if (!wait(&s_full[i & 1], (i >> 1) & 1, 81)) break;
       s::tc_fence_after();
-      if (!wait(p_empty, (i & 1) ^ 1, 82)) break;  // near of the block before has read P
+      if (!wait(&p_empty[i & 1], ((i >> 1) & 1) ^ 1, 82)) break;  // near of block i - 2 has read its P
 #pragma unroll 1
       for (int h = 0; h < 4; ++h) {
         uint32_t w[8];
@@ -413,7 +425,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
           for (int e = 0; e < 8; ++e) w[e] = 0u;
         } else {
           uint32_t v[16];
-          tmem_ld16(tmem + kColS + 64 * (i & 1) + 16 * h + lane_off, v);
+          tmem_ld16(tmem + kColS + 16 * h + lane_off, v);
           s::tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -426,36 +438,31 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
           }
         }
         if (r >= 0) {
-          s::st_shared_v4(pbase + r * 128 + (((2 * h) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
-          s::st_shared_v4(pbase + r * 128 + (((2 * h + 1) ^ (r & 7)) << 4), w[4], w[5], w[6], w[7]);
+          s::st_shared_v4(pb + (((2 * h) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
+          s::st_shared_v4(pb + (((2 * h + 1) ^ (r & 7)) << 4), w[4], w[5], w[6], w[7]);
         }
       }
       s::tc_fence_before();
-      s::mbar_arrive(&s_empty[i & 1]);
+      s::mbar_arrive(s_empty);
       s::fence_proxy_async();
-      s::mbar_arrive(p_full);
+      s::mbar_arrive(&p_full[i & 1]);
     }
   } else if (wg == 2) {
     // ==================================== the state's bf16 copy, and its decay
     const int r = 32 * w4 + lane;  // state row
-    const uint32_t ts = tmem + kColState + lane_off;
-    const uint32_t cbase = s::smem_u32(smem + CF::OFF_COPY);
+    const uint32_t ts = tmem + kColState + lane_off, tc = tmem + kColCopy + lane_off;
     // 16 columns of row r into the copy, and times f into the state
     auto put = [&](uint32_t (&v)[16], int h, float f, bool keep) {
+      uint32_t hi[8], lo[8];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const uint32_t off = (h >> 2) * 16384 + r * 128 + ((((h & 3) * 2 + q) ^ (r & 7)) << 4);
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float a = __uint_as_float(v[8 * q + 2 * e]), b = __uint_as_float(v[8 * q + 2 * e + 1]);
-          hi[e] = s::pack_bf16x2(a, b);
-          if (PARTS == 2)
-            lo[e] = s::pack_bf16x2(a - __uint_as_float(hi[e] << 16), b - __uint_as_float(hi[e] & 0xffff0000u));
-        }
-        s::st_shared_v4(cbase + off, hi[0], hi[1], hi[2], hi[3]);
-        if (PARTS == 2) s::st_shared_v4(cbase + kCopy + off, lo[0], lo[1], lo[2], lo[3]);
+      for (int e = 0; e < 8; ++e) {
+        const float a = __uint_as_float(v[2 * e]), b = __uint_as_float(v[2 * e + 1]);
+        hi[e] = s::pack_bf16x2(a, b);
+        if (PARTS == 2)
+          lo[e] = s::pack_bf16x2(a - __uint_as_float(hi[e] << 16), b - __uint_as_float(hi[e] & 0xffff0000u));
       }
+      tmem_st8(tc + 8 * h, hi);
+      if (PARTS == 2) tmem_st8(tc + 64 + 8 * h, lo);
       if (keep) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(f * __uint_as_float(v[e]));
@@ -464,7 +471,6 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     };
     auto done = [&]() {
       s::tmem_st_wait();
-      s::fence_proxy_async();
       s::tc_fence_before();
       s::mbar_arrive(copy_full);
     };
@@ -542,15 +548,12 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       const float* head = tab_of(i, 85);
       if (!head) break;
       head += 64;
-      if (GRAD) {
-        if (!wait(&dot_full[i & 1], (i >> 1) & 1, 89)) break;
-      } else if (i > 0) {
-        if (!wait(out_free, (i - 1) & 1, 89)) break;
-      }
-      if (!wait(&o_full[i & 1], (i >> 1) & 1, 86)) break;
+      // the tile: the dots' rows have landed (GRAD), or the store of block i - 2 has read it
+      if (!wait(&tile_free[i & 1], ((i >> 1) & 1) ^ (GRAD ? 0 : 1), 89)) break;
+      if (!wait(o_full, i & 1, 86)) break;
       s::tc_fence_after();
-      const uint32_t t_far = tmem + kColOut + 128 * (i & 1) + lane_off, t_near = t_far + 64;
-      const uint32_t ob = obase + (GRAD ? (i & 1) * kTile : 0);
+      const uint32_t t_far = tmem + kColFar + 64 * (i & 1) + lane_off, t_near = tmem + kColNear + lane_off;
+      const uint32_t ob = obase + (i & 1) * kTile;
 #pragma unroll 1
       for (int h = 0; h < 4; ++h) {
         uint32_t near[16], v[16];
@@ -588,21 +591,21 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         }
       }
       s::tc_fence_before();
-      s::mbar_arrive(&o_empty[i & 1]);
+      s::mbar_arrive(o_empty);
       s::fence_proxy_async();
       s::mbar_arrive(staged);
     }
   } else if (warp == 3) {
     // ==================================== stores, and the rows of the dots (GRAD)
     // A staging tile: [dots' rows loaded ->] output written (staged) -> store has
-    // read it -> free (out_free, or the load of the dots' rows two blocks on). The
+    // read it -> free (tile_free: then, or when the dots' rows two blocks on have landed). The
     // dots of a block meet here, before its tile and their buffer are free again.
     const float* dotbuf = reinterpret_cast<const float*>(smem + CF::OFF_DOT);
     auto load_dot_rows = [&](int i) {
       uint8_t* dst = smem + CF::OFF_OUT + (i & 1) * kTile;
-      s::mbar_expect_tx(&dot_full[i & 1], kTile);
+      s::mbar_expect_tx(&tile_free[i & 1], kTile);
       for (int p = 0; p < 2; ++p)
-        s::tma_load_3d(dst + p * 8192, &tm_dot, &dot_full[i & 1], 64 * p, static_cast<int>(row_of(i)), static_cast<int>(bh));
+        s::tma_load_3d(dst + p * 8192, &tm_dot, &tile_free[i & 1], 64 * p, static_cast<int>(row_of(i)), static_cast<int>(bh));
     };
     int issued = 0;
     if (GRAD)
@@ -613,7 +616,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       if (lane == 0) {
         // A chunk ends on a block boundary or at N, where the tensor map clips.
         for (int p = 0; p < 2; ++p)
-          s::tma_store_3d(&tm_o, smem + CF::OFF_OUT + (GRAD ? (i & 1) * kTile : 0) + p * 8192, 64 * p,
+          s::tma_store_3d(&tm_o, smem + CF::OFF_OUT + (i & 1) * kTile + p * 8192, 64 * p,
                           static_cast<int>(row_of(i)), static_cast<int>(bh));
         s::bulk_commit_group();
       }
@@ -630,7 +633,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       }
       if (lane == 0) {
         s::bulk_wait_group_read<0>();  // the store has read the tile
-        if (!GRAD) s::mbar_arrive(out_free);
+        if (!GRAD) s::mbar_arrive(&tile_free[i & 1]);
         else if (i + 2 < n) load_dot_rows(i + 2);
       }
       if (GRAD && i + 2 < n) ++issued;
@@ -639,7 +642,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     if (lane == 0) {
       // loads still in flight after an abort, and the stores, are done before exit
       if (GRAD)
-        for (int j = max(0, issued - 2); j < issued; ++j) s::drain_wait(&dot_full[j & 1], (j >> 1) & 1);
+        for (int j = max(0, issued - 2); j < issued; ++j) s::drain_wait(&tile_free[j & 1], (j >> 1) & 1);
       s::bulk_wait_group<0>();
     }
   }
@@ -673,11 +676,13 @@ struct StateCfg {
 struct TcStateParams {
   const __nv_bfloat16* gate;
   float* out;      // [BH][K][128*128] (state_f4)
+  float* out_t;    // its transpose, or null
   double* tot;     // [BH][K]
   int64_t N, L, K, first, count, spin_limit;  // pieces [first, first + count) of the K of every sequence
 };
 
-template <bool SUFFIX>
+// ROWS_Z: the state's rows are z's columns (what O and dV start from), else y's.
+template <bool SUFFIX, bool ROWS_Z>
 __global__ void __launch_bounds__(384, 1)
 gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_z,
                          const TcStateParams prm) {
@@ -755,8 +760,9 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
       if (!ok) break;
       s::tc_fence_after();
       const uint64_t y2 = in_d + (CF::OFF_Y2 + (i & 1) * 2 * kTile) / 16, z = in_d + ((i % KS) * 2 * kTile + kTile) / 16;
-      mma_run<4>(lead, tmem, y2, z, 128, 128, 0, 0, ID_UPD, i > 0);
-      mma_run<4>(lead, tmem, y2 + kTile / 16, z, 128, 128, 0, 0, ID_UPD, 1);
+      const uint64_t lo = y2 + kTile / 16;
+      mma_run<4>(lead, tmem, ROWS_Z ? z : y2, ROWS_Z ? y2 : z, 128, 128, 0, 0, ID_UPD, i > 0);
+      mma_run<4>(lead, tmem, ROWS_Z ? z : lo, ROWS_Z ? lo : z, 128, 128, 0, 0, ID_UPD, 1);
       commit(lead, &y2_empty[i & 1]);
       commit(lead, &in_empty[i % KS]);
     }
@@ -803,7 +809,8 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
       s::tc_fence_after();
       const int row = 32 * (warp & 3) + lane;
       float4* dst = reinterpret_cast<float4*>(prm.out + (bh * prm.K + ch) * 128 * 128);
-#pragma unroll
+      float* dst_t = prm.out_t ? prm.out_t + (bh * prm.K + ch) * 128 * 128 + (row >> 2) * 512 + (row & 3) : nullptr;
+#pragma unroll 1
       for (int c32 = 0; c32 < 4; ++c32) {
         uint32_t v[32];
         s::tmem_ld32(tmem + c32 * 32 + (static_cast<uint32_t>(32 * (warp & 3)) << 16), v);
@@ -813,6 +820,9 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
           dst[s::state_f4<128>(row, c32 * 8 + q)] =
               make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]), __uint_as_float(v[4 * q + 2]),
                           __uint_as_float(v[4 * q + 3]));
+        if (dst_t)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) dst_t[(c32 * 32 + e) * 4] = __uint_as_float(v[e]);
       }
     }
   }
@@ -827,11 +837,11 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
 
 // -------------------------------------------------------------------- launches
 
-template <bool SUFFIX>
+template <bool SUFFIX, bool ROWS_Z>
 inline cudaError_t launch_state_sm100(const void* y, const void* z, const TcStateParams& p, int64_t BH, cudaStream_t st) {
   CUtensorMap ty, tz;
   if (!make_tmap_3d(&ty, y, BH, p.N, 128, 64) || !make_tmap_3d(&tz, z, BH, p.N, 128, 64)) return cudaErrorInvalidValue;
-  auto kern = gated_state_sm100_kernel<SUFFIX>;
+  auto kern = gated_state_sm100_kernel<SUFFIX, ROWS_Z>;
   static bool done[128];
   if (!smem_attribute_set(kern, StateCfg::SMEM, done)) return cudaErrorInvalidValue;
   return launch_pdl(kern, dim3((unsigned)(BH * p.count)), dim3(384), StateCfg::SMEM, st, ty, tz, p);
