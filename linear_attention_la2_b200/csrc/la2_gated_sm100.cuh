@@ -61,7 +61,7 @@ constexpr int kTile = 64 * 128 * 2;       // one 64 x 128 bf16 tile
 constexpr int kMainThreads = 640;
 constexpr float kLog2Zero = -160.f;
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kTabs = 8;                  // gate tables in flight (see the table warp)
+constexpr int kTabs = 8, kTab = 384;      // gate tables in flight, their floats (see the table warp)
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -94,17 +94,15 @@ __device__ __forceinline__ uint32_t elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
   return e;
 }
-// n MMAs of 16 k each by the elected lane; the operands' descriptors step by da and
-// db (bytes / 16) from MMA to MMA, and from the fourth to the fifth (and so on) by
-// da4, db4 instead.
+// N MMAs of 16 k each by the elected lane; the operands' descriptors step by da and db
+// (bytes / 16) from MMA to MMA, and from every fourth to the next by ja, jb more.
 template <int N>
 __device__ __forceinline__ void mma_run(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t da, uint32_t db,
-                                        uint32_t da4, uint32_t db4, uint32_t idesc, uint32_t accumulate) {
+                                        uint32_t ja, uint32_t jb, uint32_t idesc, uint32_t accumulate) {
   if (lead) {
 #pragma unroll
     for (int k = 0; k < N; ++k)
-      s::mma_bf16_ss(d, a + (k >> 2) * da4 + (k & 3) * da, b + (k >> 2) * db4 + (k & 3) * db, idesc,
-                     k > 0 ? 1u : accumulate);
+      s::mma_bf16_ss(d, a + k * da + (k >> 2) * ja, b + k * db + (k >> 2) * jb, idesc, k > 0 ? 1u : accumulate);
   }
   __syncwarp();
 }
@@ -141,7 +139,7 @@ struct TcCfg {
   static constexpr int OFF_P = OFF_LO + kTile;
   static constexpr int OFF_OUT = OFF_P + 2 * 64 * 64 * 2;
   static constexpr int OFF_TAB = OFF_OUT + 2 * kTile;
-  static constexpr int OFF_DOT = OFF_TAB + kTabs * 128 * 4;
+  static constexpr int OFF_DOT = OFF_TAB + kTabs * kTab * 4;
   static constexpr int OFF_BAR = OFF_DOT + (GRAD ? 2 * 4 * 64 * 4 : 0);
   static constexpr int NBAR = 2 * KS + 3 + 4 + 2 + 3 + 2 + 3 + kTabs + 1;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
@@ -157,18 +155,26 @@ __device__ __forceinline__ void split_scaled(uint32_t x, float f, uint32_t& hi, 
   lo = s::pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
 }
 
-// Sums v[i] over the warp's lanes for all 16 i: lane l returns the sum of v[l % 16].
-__device__ __forceinline__ float transposed_sum(float (&v)[16], int lane) {
-#pragma unroll
-  for (int m = 8; m > 0; m >>= 1) {
-    const bool up = lane & m;
-#pragma unroll
-    for (int i = 0; i < m; ++i) {
-      const float keep = up ? v[i + m] : v[i], send = up ? v[i] : v[i + m];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, m);
-    }
-  }
-  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+// Four 8-column fragments of 16 TMEM lanes: thread 4 g + j of the warp gets, of each,
+// columns 2 j and 2 j + 1 of lane g and then of lane g + 8.
+__device__ __forceinline__ void tmem_ld_frag4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// Four 8 x 8 bf16 matrices, transposed, from and to rows of 16 bytes (lane l: row l % 8 of matrix l / 8).
+__device__ __forceinline__ void ldmatrix_t4(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void stmatrix_t4(uint32_t addr, const uint32_t* r) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
 }
 
 // Thread t of the warp writes 8 consecutive columns of TMEM lane (lane field) + t.
@@ -268,7 +274,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     return __all_sync(0xffffffffu, s::wait_bar(bar, parity, lim, abort_flag, where));
   };
   auto tab_of = [&](int i, int where) -> const float* {  // the block's gate sums, or null after an abort
-    return wait(&tab_full[i % kTabs], (i / kTabs) & 1, where) ? tab + (i % kTabs) * 128 : nullptr;
+    return wait(&tab_full[i % kTabs], (i / kTabs) & 1, where) ? tab + (i % kTabs) * kTab : nullptr;
   };
   const uint32_t lane_off = static_cast<uint32_t>(32 * w4) << 16;
 
@@ -309,7 +315,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       if (!wait(s_empty, (i & 1) ^ 1, 72)) return false;
       s::tc_fence_after();
       const uint32_t st = (i % KS) * kStage;
-      mma_run<8>(lead, tmem + kColS, row_d + st, row_d + st + kY, 2, 2, 512, 512, ID_S, 0);
+      mma_run<8>(lead, tmem + kColS, row_d + st, row_d + st + kY, 2, 2, 504, 504, ID_S, 0);
       commit(lead, &s_full[i & 1]);
       return true;
     };
@@ -352,10 +358,14 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     s::drain_wait(drain, 0);
   } else if (warp == 2) {
     // =========================================================== gate tables
-    // Per block: the running sums c, then the epilogue's factors of far. Table i goes
-    // into slot i % 8 when block i - KS has released its stage (in_empty): everything
-    // of it is done but its epilogue, and before its near was issued the epilogue had
-    // read block i - KS - 1 (o_empty), so readers of block i - 8 are long done.
+    // Per block: the running sums c [64]; the epilogue's factors of far [64]; and for
+    // the mask, whose rows and columns meet in 16 x 16 squares, e^(c_E(s) - c_s) [64]
+    // with E(s) the last row of s' sixteen, and e^(c_t - c_E) for the first three E
+    // [3][64] (read for later t only): off the diagonal e^(c_t - c_s) is one of each,
+    // neither above 1 unless gates are. Table i goes into slot i % 8 when block i - KS
+    // has released its stage (in_empty): everything of it is done but its epilogue,
+    // and before its near was issued the epilogue had read block i - KS - 1 (o_empty),
+    // so readers of block i - 8 are long done.
     const __nv_bfloat16* g = prm.gate + bh * prm.N;
     // (nothing comes before the first token for its gate to pass on: 0, unless NaN)
     auto gate_at = [&](int64_t t) {
@@ -368,9 +378,16 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       float a, b;
       warp_sums(gate_log2(gx), gate_log2(gy), lane, a, b);
       const float all = __shfl_sync(0xffffffffu, b, 31);
-      float2* t = reinterpret_cast<float2*>(tab + (i % kTabs) * 128);
+      const float end = __shfl_sync(0xffffffffu, b, lane | 7);
+      float2* t = reinterpret_cast<float2*>(tab + (i % kTabs) * kTab);
       t[lane] = make_float2(a, b);
       t[32 + lane] = BACK ? make_float2(ex2(all - a), ex2(all - b)) : make_float2(ex2(a), ex2(b));
+      t[64 + lane] = make_float2(ex2(end - a), ex2(end - b));
+#pragma unroll
+      for (int h = 0; h < 3; ++h) {
+        const float e = __shfl_sync(0xffffffffu, b, 8 * h + 7);
+        t[96 + 32 * h + lane] = make_float2(ex2(a - e), ex2(b - e));
+      }
       s::mbar_arrive(&tab_full[i % kTabs]);
       if (i + 1 < n) {
         gx = gate_at(row_of(i + 1) + 2 * lane);
@@ -390,7 +407,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       if (!wait(&s_full[i & 1], (i >> 1) & 1, 79)) break;
       if (!wait(y_empty, (i & 1) ^ 1, 90)) break;
       const uint32_t ya = s::smem_u32(smem + (i % KS) * 3 * kTile + kTile) + half * 8192 + r * 128;
-#pragma unroll 2
+#pragma unroll 1
       for (int ch = 0; ch < 8; ++ch) {
         const uint32_t off = (ch ^ (r & 7)) << 4;
         uint32_t x[4], hi[4], lo[4];
@@ -405,41 +422,54 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     }
   } else if (wg == 1) {
     // ======================================================== S -> P, weighted
+    // A warp's 16 rows (lanes 0-15) against the columns in sixteens: h = w4 lies on
+    // the diagonal; those beyond it are not kept, and zero in both buffers from the
+    // start. The products of weights are taken in one order, (S e^(c_E - c_s))
+    // e^(c_t - c_E), whichever of t and s is the row: dQ and dK round alike.
     const int r = s::acc_row<64>(w4, lane);
-    const uint32_t pbase = s::smem_u32(smem + CF::OFF_P);
-    // the half of the columns that this warp's 16 rows do not keep at all
-    const int dropped = BACK ? (w4 >= 2 ? 0 : -1) : (w4 < 2 ? 1 : -1);
+    const uint32_t prow = s::smem_u32(smem + CF::OFF_P) + (r < 0 ? 0 : r) * 128;
+    auto p_at = [&](int buf, int q) { return prow + buf * 8192 + ((q ^ (r & 7)) << 4); };
+    if (r >= 0)
+      for (int q = 0; q < 16; ++q) s::st_shared_v4(p_at(q >> 3, q & 7), 0u, 0u, 0u, 0u);
+    const int h0 = BACK ? w4 : 0, h1 = BACK ? 3 : w4;
     for (int i = 0; i < n; ++i) {
       const float* c = tab_of(i, 80);
       if (!c) break;
-      const float cr = r >= 0 ? c[r] : 0.f;
-      const uint32_t pb = pbase + (i & 1) * 8192 + r * 128;
       if (!wait(&s_full[i & 1], (i >> 1) & 1, 81)) break;
       s::tc_fence_after();
       if (!wait(&p_empty[i & 1], ((i >> 1) & 1) ^ 1, 82)) break;  // near of block i - 2 has read its P
 #pragma unroll 1
-      for (int h = 0; h < 4; ++h) {
-        uint32_t w[8];
-        if (h >> 1 == dropped) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = 0u;
-        } else {
-          uint32_t v[16];
-          tmem_ld16(tmem + kColS + 16 * h + lane_off, v);
-          s::tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int col = 16 * h + 2 * e;
-            const float2 cc = *reinterpret_cast<const float2*>(c + col);
-            const float wa = ex2(BACK ? cc.x - cr : cr - cc.x), wb = ex2(BACK ? cc.y - cr : cr - cc.y);
-            const float a = (BACK ? col >= r : col <= r) ? __uint_as_float(v[2 * e]) * wa : 0.f;
-            const float b = (BACK ? col + 1 >= r : col + 1 <= r) ? __uint_as_float(v[2 * e + 1]) * wb : 0.f;
-            w[e] = s::pack_bf16x2(a, b);
-          }
-        }
+      for (int h = h0; h <= h1; ++h) {
+        uint32_t v[16], w[8];
+        tmem_ld16(tmem + kColS + 16 * h + lane_off, v);
+        s::tmem_ld_wait();
         if (r >= 0) {
-          s::st_shared_v4(pb + (((2 * h) ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
-          s::st_shared_v4(pb + (((2 * h + 1) ^ (r & 7)) << 4), w[4], w[5], w[6], w[7]);
+          if (h == w4) {
+            const float cr = c[r];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int col = 16 * h + 2 * e;
+              const float2 cc = *reinterpret_cast<const float2*>(c + col);
+              const float wa = ex2(BACK ? cc.x - cr : cr - cc.x), wb = ex2(BACK ? cc.y - cr : cr - cc.y);
+              const float a = (BACK ? col >= r : col <= r) ? __uint_as_float(v[2 * e]) * wa : 0.f;
+              const float b = (BACK ? col + 1 >= r : col + 1 <= r) ? __uint_as_float(v[2 * e + 1]) * wb : 0.f;
+              w[e] = s::pack_bf16x2(a, b);
+            }
+          } else {
+            const float* cols = c + (BACK ? 192 + 64 * w4 : 128) + 16 * h;
+            const float f = c[BACK ? 128 + r : 192 + 64 * h + r];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              const float4 x = *reinterpret_cast<const float4*>(cols + 2 * e);
+              const float s0 = __uint_as_float(v[2 * e]), s1 = __uint_as_float(v[2 * e + 1]),
+                          s2 = __uint_as_float(v[2 * e + 2]), s3 = __uint_as_float(v[2 * e + 3]);
+              w[e] = BACK ? s::pack_bf16x2((s0 * f) * x.x, (s1 * f) * x.y) : s::pack_bf16x2((s0 * x.x) * f, (s1 * x.y) * f);
+              w[e + 1] = BACK ? s::pack_bf16x2((s2 * f) * x.z, (s3 * f) * x.w)
+                              : s::pack_bf16x2((s2 * x.z) * f, (s3 * x.w) * f);
+            }
+          }
+          s::st_shared_v4(p_at(i & 1, 2 * h), w[0], w[1], w[2], w[3]);
+          s::st_shared_v4(p_at(i & 1, 2 * h + 1), w[4], w[5], w[6], w[7]);
         }
       }
       s::tc_fence_before();
@@ -519,79 +549,92 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       // far of the block before has read the copy
       if (i > first_copy && !wait(copy_empty, (i - 1 - first_copy) & 1, 88)) break;
       s::tc_fence_after();
-      uint32_t v[16], w[16];  // the next load is under way while one is put
-      tmem_ld16(ts, v);
-      s::tmem_ld_wait();
 #pragma unroll 1
-      for (int h = 0; h < 8; h += 2) {
-        tmem_ld16(ts + 16 * (h + 1), w);
+      for (int h = 0; h < 8; ++h) {
+        uint32_t v[16];
+        tmem_ld16(ts + 16 * h, v);
+        s::tmem_ld_wait();
         put(v, h, whole, i + 1 < n);
-        s::tmem_ld_wait();
-        if (h < 6) tmem_ld16(ts + 16 * (h + 2), v);
-        put(w, h + 1, whole, i + 1 < n);
-        s::tmem_ld_wait();
       }
       done();
     }
   } else if (wg == 3) {
     // =========================================== out = head far + near -> HBM
-    // Thread e holds column e of the 64 rows; the staging tile is [row][column].
-    const int e = 32 * w4 + lane;
-    const uint32_t obase = s::smem_u32(smem + CF::OFF_OUT) + (e >> 6) * 8192 + (e & 7) * 2;
-    const int cj = (e & 63) >> 3;
-    uint32_t sw[8];
-#pragma unroll
-    for (int m = 0; m < 8; ++m) sw[m] = static_cast<uint32_t>((cj ^ m) << 4);
+    // TMEM holds out transposed: lane e (column of the output), 64 columns t. Read in
+    // 16 x 8 fragments, thread 4 g + j of the warp has lanes g and g + 8, columns 2 j
+    // and 2 j + 1 of each, which is what stmatrix writes, transposed, into the staging
+    // tile's rows t (and ldmatrix reads the dots' rows from there in).
+    const uint32_t tile = s::smem_u32(smem + CF::OFF_OUT);
     float* dotbuf = reinterpret_cast<float*>(smem + CF::OFF_DOT);
+    const int m = lane >> 3, i8 = lane & 7;  // matrix of four, its row, that this lane addresses
     for (int i = 0; i < n; ++i) {
       const bool far = i >= first_copy;
       const float* head = tab_of(i, 85);
       if (!head) break;
-      head += 64;
+      head += 64 + 2 * (lane & 3);
       // the tile: the dots' rows have landed (GRAD), or the store of block i - 2 has read it
       if (!wait(&tile_free[i & 1], ((i >> 1) & 1) ^ (GRAD ? 0 : 1), 89)) break;
       if (!wait(o_full, i & 1, 86)) break;
       s::tc_fence_after();
-      const uint32_t t_far = tmem + kColFar + 64 * (i & 1) + lane_off, t_near = tmem + kColNear + lane_off;
-      const uint32_t ob = obase + (i & 1) * kTile;
+      float dot[16];  // columns 8 g + 2 j, + 1 of this thread, summed over its lanes
+#pragma unroll
+      for (int e = 0; e < 16; ++e) dot[e] = 0.f;
 #pragma unroll 1
-      for (int h = 0; h < 4; ++h) {
-        uint32_t near[16], v[16];
-        tmem_ld16(t_near + 16 * h, near);
-        if (far) tmem_ld16(t_far + 16 * h, v);
-        const uint32_t oh = ob + h * 16 * 128;
-        uint16_t x[16];  // the dots' rows, before their place takes the output
-        if (GRAD) {
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t t_lane = lane_off + (static_cast<uint32_t>(16 * half) << 16);
+        const int e8 = 4 * w4 + 2 * half + (m & 1);  // eight columns of the output
+        const uint32_t row0 = tile + (i & 1) * kTile + (e8 >> 3) * 8192 + (8 * (m >> 1) + i8) * 128 + (((e8 & 7) ^ i8) << 4);
 #pragma unroll
-          for (int t = 0; t < 16; ++t)
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x[t]) : "r"(oh + t * 128 + sw[t & 7]) : "memory");
-        }
-        s::tmem_ld_wait();
-        float o[16];
+        for (int part = 0; part < 2; ++part) {  // 32 rows of the output
+          uint32_t near[16], v[16];
+          tmem_ld_frag4(tmem + kColNear + 32 * part + t_lane, near);
+          if (far) tmem_ld_frag4(tmem + kColFar + 64 * (i & 1) + 32 * part + t_lane, v);
+          uint32_t x[8];
+          if (GRAD)
 #pragma unroll
-        for (int t = 0; t < 16; t += 4) {
-          const float4 h4 = *reinterpret_cast<const float4*>(head + 16 * h + t);
-          const float hd[4] = {h4.x, h4.y, h4.z, h4.w};
+            for (int u = 0; u < 2; ++u) ldmatrix_t4(row0 + (4 * part + 2 * u) * 1024, &x[4 * u]);
+          s::tmem_ld_wait();
+          uint32_t pk[8];
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            o[t + u] = far ? fmaf(hd[u], __uint_as_float(v[t + u]), __uint_as_float(near[t + u]))
-                           : __uint_as_float(near[t + u]);
-        }
+          for (int g = 0; g < 4; ++g) {
+            const float2 hd = *reinterpret_cast<const float2*>(head + 32 * part + 8 * g);
+            float o[4];
 #pragma unroll
-        for (int t = 0; t < 16; t += 2) {
-          const uint32_t pk = s::pack_bf16x2(o[t], o[t + 1]);
-          s::st_shared_u16(oh + t * 128 + sw[t & 7], static_cast<uint16_t>(pk));
-          s::st_shared_u16(oh + (t + 1) * 128 + sw[(t + 1) & 7], static_cast<uint16_t>(pk >> 16));
-        }
-        if (GRAD) {
+            for (int e = 0; e < 4; ++e)
+              o[e] = far ? fmaf(e & 1 ? hd.y : hd.x, __uint_as_float(v[4 * g + e]), __uint_as_float(near[4 * g + e]))
+                         : __uint_as_float(near[4 * g + e]);
+            pk[2 * g] = s::pack_bf16x2(o[0], o[1]);
+            pk[2 * g + 1] = s::pack_bf16x2(o[2], o[3]);
+            if (GRAD)
 #pragma unroll
-          for (int t = 0; t < 16; ++t) o[t] *= __uint_as_float(static_cast<uint32_t>(x[t]) << 16);
-          const float dot = transposed_sum(o, lane);
-          if (lane < 16) dotbuf[(i & 1) * 256 + w4 * 64 + 16 * h + lane] = dot;
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t xx = x[2 * g + e];
+                float* d = dot + 8 * part + 2 * g;
+                d[0] = fmaf(o[2 * e], __uint_as_float(xx << 16), d[0]);
+                d[1] = fmaf(o[2 * e + 1], __uint_as_float(xx & 0xffff0000u), d[1]);
+              }
+          }
+#pragma unroll
+          for (int u = 0; u < 2; ++u) stmatrix_t4(row0 + (4 * part + 2 * u) * 1024, &pk[4 * u]);
         }
       }
       s::tc_fence_before();
       s::mbar_arrive(o_empty);
+      if (GRAD) {
+        // over the eight threads with the same columns: each keeps half at every step
+#pragma unroll
+        for (int step = 0; step < 3; ++step) {
+          const int keep = 8 >> step, bit = 16 >> step;
+          const bool up = lane & bit;
+#pragma unroll
+          for (int e = 0; e < keep; ++e) {
+            const float a = up ? dot[e + keep] : dot[e], z = up ? dot[e] : dot[e + keep];
+            dot[e] = a + __shfl_xor_sync(0xffffffffu, z, bit);
+          }
+        }
+        const int g = (lane >> 4) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
+        *reinterpret_cast<float2*>(dotbuf + (i & 1) * 256 + w4 * 64 + 8 * g + 2 * (lane & 3)) = make_float2(dot[0], dot[1]);
+      }
       s::fence_proxy_async();
       s::mbar_arrive(staged);
     }
