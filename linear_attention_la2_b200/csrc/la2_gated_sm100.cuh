@@ -119,6 +119,11 @@ __device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
   __syncwarp();
 }
 
+// Gates are read one block ahead of their use, which covers a hit in L2 but not HBM:
+// their lines are brought into L2 this many blocks ahead.
+constexpr int kGateAhead = 8;
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 struct TcParams {
   const __nv_bfloat16* gate;   // [BH][N]
   const float* init;           // [BH][K][128*128] (state_f4): states of the sequence's pieces, or null
@@ -174,13 +179,6 @@ __device__ __forceinline__ void ldmatrix_t4(uint32_t addr, uint32_t* r) {
 __device__ __forceinline__ void stmatrix_t4(uint32_t addr, const uint32_t* r) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
                "r"(r[2]), "r"(r[3])
-               : "memory");
-}
-
-// Thread t of the warp writes 8 consecutive columns of TMEM lane (lane field) + t.
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
 
@@ -372,6 +370,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       const __nv_bfloat16 x = t < t1 ? g[t] : __float2bfloat16(0.f);
       return t > 0 || __hisnan(x) ? x : __float2bfloat16(0.f);
     };
+    if (lane < min(n, kGateAhead)) prefetch_l2(g + row_of(lane));
     __nv_bfloat16 gx = gate_at(row_of(0) + 2 * lane), gy = gate_at(row_of(0) + 2 * lane + 1);
     for (int i = 0; i < n; ++i) {
       if (i >= KS && !wait(&in_empty[i % KS], (i / KS - 1) & 1, 77)) break;
@@ -393,6 +392,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         gx = gate_at(row_of(i + 1) + 2 * lane);
         gy = gate_at(row_of(i + 1) + 2 * lane + 1);
       }
+      if (lane == 0 && i + kGateAhead < n) prefetch_l2(g + row_of(i + kGateAhead));
     }
   } else if (wg == 4) {
     // ===================================================================== Y~
@@ -481,22 +481,22 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     // ==================================== the state's bf16 copy, and its decay
     const int r = 32 * w4 + lane;  // state row
     const uint32_t ts = tmem + kColState + lane_off, tc = tmem + kColCopy + lane_off;
-    // 16 columns of row r into the copy, and times f into the state
-    auto put = [&](uint32_t (&v)[16], int h, float f, bool keep) {
-      uint32_t hi[8], lo[8];
+    // 32 columns of row r into the copy, and times f into the state
+    auto put = [&](uint32_t (&v)[32], int h, float f, bool keep) {
+      uint32_t hi[16], lo[16];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < 16; ++e) {
         const float a = __uint_as_float(v[2 * e]), b = __uint_as_float(v[2 * e + 1]);
         hi[e] = s::pack_bf16x2(a, b);
         if (PARTS == 2)
           lo[e] = s::pack_bf16x2(a - __uint_as_float(hi[e] << 16), b - __uint_as_float(hi[e] & 0xffff0000u));
       }
-      tmem_st8(tc + 8 * h, hi);
-      if (PARTS == 2) tmem_st8(tc + 64 + 8 * h, lo);
+      s::tmem_st16(tc + 16 * h, hi);
+      if (PARTS == 2) s::tmem_st16(tc + 64 + 16 * h, lo);
       if (keep) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(f * __uint_as_float(v[e]));
-        s::tmem_st16(ts + h * 16, v);
+        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(f * __uint_as_float(v[e]));
+        s::tmem_st32(ts + h * 32, v);
       }
     };
     auto done = [&]() {
@@ -514,19 +514,19 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         const int pieces = prm.per == 0 ? 1 : static_cast<int>(BACK ? prm.K - (ch + 1) * prm.per : ch * prm.per);
         const float whole = ex2(c[63]);
 #pragma unroll 1
-        for (int h = 0; h < 8; ++h) {
-          float x[16];
-          uint32_t v[16];
+        for (int h = 0; h < 4; ++h) {
+          float x[32];
+          uint32_t v[32];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = 0.f;
+          for (int e = 0; e < 32; ++e) x[e] = 0.f;
           float f = 1.f;
 #pragma unroll 1
           for (int j = 0; j < pieces; ++j) {
             const int64_t at = bh * prm.K + (prm.per == 0 ? ch : BACK ? (ch + 1) * prm.per + j : ch * prm.per - 1 - j);
             const float4* src = reinterpret_cast<const float4*>(prm.init + at * 128 * 128);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float4 y = src[s::state_f4<128>(r, h * 4 + q)];
+            for (int q = 0; q < 8; ++q) {
+              const float4 y = src[s::state_f4<128>(r, h * 8 + q)];
               x[4 * q] = fmaf(f, y.x, x[4 * q]);
               x[4 * q + 1] = fmaf(f, y.y, x[4 * q + 1]);
               x[4 * q + 2] = fmaf(f, y.z, x[4 * q + 2]);
@@ -535,7 +535,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             if (j + 1 < pieces) f *= expf(static_cast<float>(prm.tot[at]));
           }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(x[e]);
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(x[e]);
           put(v, h, whole, n > 1);
         }
         done();
@@ -550,9 +550,9 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       if (i > first_copy && !wait(copy_empty, (i - 1 - first_copy) & 1, 88)) break;
       s::tc_fence_after();
 #pragma unroll 1
-      for (int h = 0; h < 8; ++h) {
-        uint32_t v[16];
-        tmem_ld16(ts + 16 * h, v);
+      for (int h = 0; h < 4; ++h) {
+        uint32_t v[32];
+        s::tmem_ld32(ts + 32 * h, v);
         s::tmem_ld_wait();
         put(v, h, whole, i + 1 < n);
       }
@@ -817,6 +817,7 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
     const __nv_bfloat16* g = prm.gate + bh * prm.N;
     auto gate_at = [&](int64_t t) { return t < t1 ? g[t] : __float2bfloat16(0.f); };
     __nv_bfloat16 gx = gate_at(row_of(0) + 2 * lane), gy = gate_at(row_of(0) + 2 * lane + 1);
+    if (warp == 4 && lane < min(n, kGateAhead)) prefetch_l2(g + row_of(lane));
     double run = 0.0;  // sum of the gates of the blocks walked
     bool ok = true;
     for (int i = 0; i < n && ok; ++i) {
@@ -830,6 +831,7 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
         gx = gate_at(row_of(i + 1) + 2 * lane);
         gy = gate_at(row_of(i + 1) + 2 * lane + 1);
       }
+      if (warp == 4 && lane == 0 && i + kGateAhead < n) prefetch_l2(g + row_of(i + kGateAhead));
       ok = wait(&in_full[i % KS], (i / KS) & 1, 93) && wait(&y2_empty[i & 1], ((i >> 1) & 1) ^ 1, 94);
       if (!ok) break;
       const uint32_t y2 = s::smem_u32(smem + CF::OFF_Y2 + (i & 1) * 2 * kTile);
