@@ -119,10 +119,26 @@ __device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
   __syncwarp();
 }
 
-// Gates are read one block ahead of their use, which covers a hit in L2 but not HBM:
-// their lines are brought into L2 this many blocks ahead.
-constexpr int kGateAhead = 8;
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+// Calls f(i, x, y) for the blocks i < n in turn, x and y the gates of rows 2 lane and
+// 2 lane + 1 of block i (get(i, r) reads one). Loads run four blocks ahead: under load
+// one takes about as long as a block.
+template <class G, class F>
+__device__ __forceinline__ void for_gates(int n, int lane, G get, F f) {
+  __nv_bfloat16 x[4], y[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    x[u] = get(u, 2 * lane);
+    y[u] = get(u, 2 * lane + 1);
+  }
+  for (int i = 0; i < n; i += 4) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (i + u < n && !f(i + u, x[u], y[u])) return;
+      x[u] = get(i + u + 4, 2 * lane);
+      y[u] = get(i + u + 4, 2 * lane + 1);
+    }
+  }
+}
 
 struct TcParams {
   const __nv_bfloat16* gate;   // [BH][N]
@@ -365,35 +381,32 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     // and before its near was issued the epilogue had read block i - KS - 1 (o_empty),
     // so readers of block i - 8 are long done.
     const __nv_bfloat16* g = prm.gate + bh * prm.N;
-    // (nothing comes before the first token for its gate to pass on: 0, unless NaN)
-    auto gate_at = [&](int64_t t) {
-      const __nv_bfloat16 x = t < t1 ? g[t] : __float2bfloat16(0.f);
-      return t > 0 || __hisnan(x) ? x : __float2bfloat16(0.f);
-    };
-    if (lane < min(n, kGateAhead)) prefetch_l2(g + row_of(lane));
-    __nv_bfloat16 gx = gate_at(row_of(0) + 2 * lane), gy = gate_at(row_of(0) + 2 * lane + 1);
-    for (int i = 0; i < n; ++i) {
-      if (i >= KS && !wait(&in_empty[i % KS], (i / KS - 1) & 1, 77)) break;
-      float a, b;
-      warp_sums(gate_log2(gx), gate_log2(gy), lane, a, b);
-      const float all = __shfl_sync(0xffffffffu, b, 31);
-      const float end = __shfl_sync(0xffffffffu, b, lane | 7);
-      float2* t = reinterpret_cast<float2*>(tab + (i % kTabs) * kTab);
-      t[lane] = make_float2(a, b);
-      t[32 + lane] = BACK ? make_float2(ex2(all - a), ex2(all - b)) : make_float2(ex2(a), ex2(b));
-      t[64 + lane] = make_float2(ex2(end - a), ex2(end - b));
+    for_gates(
+        n, lane,
+        [&](int i, int r) {
+          const int64_t t = row_of(i) + r;
+          const __nv_bfloat16 x = i < n && t < t1 ? g[t] : __float2bfloat16(0.f);
+          // (nothing comes before the first token for its gate to pass on: 0, unless NaN)
+          return t > 0 || __hisnan(x) ? x : __float2bfloat16(0.f);
+        },
+        [&](int i, __nv_bfloat16 gx, __nv_bfloat16 gy) {
+          if (i >= KS && !wait(&in_empty[i % KS], (i / KS - 1) & 1, 77)) return false;
+          float a, b;
+          warp_sums(gate_log2(gx), gate_log2(gy), lane, a, b);
+          const float all = __shfl_sync(0xffffffffu, b, 31);
+          const float end = __shfl_sync(0xffffffffu, b, lane | 7);
+          float2* t = reinterpret_cast<float2*>(tab + (i % kTabs) * kTab);
+          t[lane] = make_float2(a, b);
+          t[32 + lane] = BACK ? make_float2(ex2(all - a), ex2(all - b)) : make_float2(ex2(a), ex2(b));
+          t[64 + lane] = make_float2(ex2(end - a), ex2(end - b));
 #pragma unroll
-      for (int h = 0; h < 3; ++h) {
-        const float e = __shfl_sync(0xffffffffu, b, 8 * h + 7);
-        t[96 + 32 * h + lane] = make_float2(ex2(a - e), ex2(b - e));
-      }
-      s::mbar_arrive(&tab_full[i % kTabs]);
-      if (i + 1 < n) {
-        gx = gate_at(row_of(i + 1) + 2 * lane);
-        gy = gate_at(row_of(i + 1) + 2 * lane + 1);
-      }
-      if (lane == 0 && i + kGateAhead < n) prefetch_l2(g + row_of(i + kGateAhead));
-    }
+          for (int h = 0; h < 3; ++h) {
+            const float e = __shfl_sync(0xffffffffu, b, 8 * h + 7);
+            t[96 + 32 * h + lane] = make_float2(ex2(a - e), ex2(b - e));
+          }
+          s::mbar_arrive(&tab_full[i % kTabs]);
+          return true;
+        });
   } else if (wg == 4) {
     // ===================================================================== Y~
     // Two threads a row: the value over Y once S has read it, the remainder into its
@@ -706,12 +719,14 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 // and the sum of the gates walked so far goes into the scale of the rows. Y~ is value
 // and remainder, so the fp32 state is good to 2^-17: it is what the caller's pool
 // receives after a prefill. Bound by HBM: K and V are read once. Warps: 0 loads,
-// 1 MMA, 4-11 scale rows (four threads a row), 4-7 write the state out.
+// 1 MMA, 2 the rows' factors, 4-11 scale rows (four threads a row), 4-7 write the
+// state out.
 struct StateCfg {
-  static constexpr int KS = 3;
+  static constexpr int KS = 4;
   static constexpr int OFF_Y2 = KS * 2 * kTile;            // two buffers of value and remainder
-  static constexpr int OFF_BAR = OFF_Y2 + 4 * kTile;
-  static constexpr int NBAR = 2 * KS + 4 + 2;
+  static constexpr int OFF_TAB = OFF_Y2 + 4 * kTile;       // rows' factors, kTabs blocks of 64
+  static constexpr int OFF_BAR = OFF_TAB + kTabs * 64 * 4;
+  static constexpr int NBAR = 2 * KS + 4 + 2 + kTabs;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
@@ -741,8 +756,10 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
   uint64_t* y2_full = in_empty + KS;
   uint64_t* y2_empty = y2_full + 2;
   uint64_t *done = y2_empty + 2, *drain = done + 1;
-  uint32_t* tmem_base = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* tab_full = drain + 1;
+  uint32_t* tmem_base = reinterpret_cast<uint32_t*>(tab_full + kTabs);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base + 1);
+  float* tab = reinterpret_cast<float*>(smem + CF::OFF_TAB);
 
   const int64_t bh = blockIdx.x / prm.count, ch = prm.first + blockIdx.x % prm.count;
   const int64_t t0 = ch * prm.L, t1 = min(prm.N, t0 + prm.L);
@@ -752,6 +769,7 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
   if (threadIdx.x == 0) {
     for (int i = 0; i < KS; ++i) { s::mbar_init(&in_full[i], 1); s::mbar_init(&in_empty[i], 1); }
     for (int i = 0; i < 2; ++i) { s::mbar_init(&y2_full[i], 256); s::mbar_init(&y2_empty[i], 1); }
+    for (int i = 0; i < kTabs; ++i) s::mbar_init(&tab_full[i], 32);
     s::mbar_init(done, 1);
     s::mbar_init(drain, 1);
     *abort_flag = 0;
@@ -812,28 +830,37 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
     if (ok) commit(lead, done);
     commit(lead, drain);
     s::drain_wait(drain, 0);
+  } else if (warp == 2) {
+    // the rows' factors, a block's when block i - KS has released its stage
+    const __nv_bfloat16* g = prm.gate + bh * prm.N;
+    double run = 0.0;  // sum of the gates of the blocks walked
+    for_gates(
+        n, lane,
+        [&](int i, int r) {
+          const int64_t t = row_of(i) + r;
+          return i < n && t < t1 ? g[t] : __float2bfloat16(0.f);
+        },
+        [&](int i, __nv_bfloat16 gx, __nv_bfloat16 gy) {
+          if (i >= KS && !wait(&in_empty[i % KS], (i / KS - 1) & 1, 96)) return false;
+          float a, b;
+          warp_sums(gate_log2(gx), gate_log2(gy), lane, a, b);
+          const float all = __shfl_sync(0xffffffffu, b, 31);
+          reinterpret_cast<float2*>(tab + (i % kTabs) * 64)[lane] =
+              make_float2(ex2(static_cast<float>(run + static_cast<double>(SUFFIX ? a : all - a))),
+                          ex2(static_cast<float>(run + static_cast<double>(SUFFIX ? b : all - b))));
+          run += static_cast<double>(all);
+          s::mbar_arrive(&tab_full[i % kTabs]);
+          return true;
+        });
+    if (lane == 0) prm.tot[bh * prm.K + ch] = run * 0.693147180559945309417;  // natural log
   } else if (warp >= 4) {
     const int r = (warp - 4) * 8 + (lane >> 2), ch0 = (lane & 3) * 4;
-    const __nv_bfloat16* g = prm.gate + bh * prm.N;
-    auto gate_at = [&](int64_t t) { return t < t1 ? g[t] : __float2bfloat16(0.f); };
-    __nv_bfloat16 gx = gate_at(row_of(0) + 2 * lane), gy = gate_at(row_of(0) + 2 * lane + 1);
-    if (warp == 4 && lane < min(n, kGateAhead)) prefetch_l2(g + row_of(lane));
-    double run = 0.0;  // sum of the gates of the blocks walked
     bool ok = true;
     for (int i = 0; i < n && ok; ++i) {
-      float a, b;
-      warp_sums(gate_log2(gx), gate_log2(gy), lane, a, b);
-      const float ca = __shfl_sync(0xffffffffu, a, r >> 1), cb = __shfl_sync(0xffffffffu, b, r >> 1);
-      const float c = (r & 1) ? cb : ca, all = __shfl_sync(0xffffffffu, b, 31);
-      const float f = ex2(static_cast<float>(run + static_cast<double>(SUFFIX ? c : all - c)));
-      run += static_cast<double>(all);
-      if (i + 1 < n) {
-        gx = gate_at(row_of(i + 1) + 2 * lane);
-        gy = gate_at(row_of(i + 1) + 2 * lane + 1);
-      }
-      if (warp == 4 && lane == 0 && i + kGateAhead < n) prefetch_l2(g + row_of(i + kGateAhead));
-      ok = wait(&in_full[i % KS], (i / KS) & 1, 93) && wait(&y2_empty[i & 1], ((i >> 1) & 1) ^ 1, 94);
+      ok = wait(&tab_full[i % kTabs], (i / kTabs) & 1, 97) && wait(&in_full[i % KS], (i / KS) & 1, 93) &&
+           wait(&y2_empty[i & 1], ((i >> 1) & 1) ^ 1, 94);
       if (!ok) break;
+      const float f = tab[(i % kTabs) * 64 + r];
       const uint32_t y2 = s::smem_u32(smem + CF::OFF_Y2 + (i & 1) * 2 * kTile);
       const uint32_t ya = s::smem_u32(smem + (i % KS) * 2 * kTile);
 #pragma unroll
@@ -849,7 +876,6 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
       s::fence_proxy_async();
       s::mbar_arrive(&y2_full[i & 1]);
     }
-    if (warp == 4 && lane == 0) prm.tot[bh * prm.K + ch] = run * 0.693147180559945309417;  // natural log
     if (ok && warp < 8 && wait(done, 0, 95)) {
       s::tc_fence_after();
       const int row = 32 * (warp & 3) + lane;
