@@ -16,7 +16,9 @@ struct Plan {
   size_t bytes = 0;
 };
 
-constexpr int64_t kSumPieces = 8;  // pieces a chunk adds up itself; more are scanned
+constexpr int64_t kSumPieces = 12;  // pieces a chunk adds up itself; more are scanned
+
+static_assert(kSumPieces <= kMaxPieces, "the gates' gradient sums as many");
 
 enum Need { NEED_FWD, NEED_BWD, NEED_STATE };
 
@@ -51,26 +53,25 @@ static Plan make_plan(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, la
     p.L = (g_chunk_len + kRows - 1) / kRows * kRows;
   } else if (p.tc) {
     // in blocks of the main pass: what a launch of it and of the state pass costs
-    // beside its blocks, a block of the state pass, and the scan
-    constexpr double kFixed = 5.0, kStateFixed = 5.0, kStateBlock = 0.5, kScan = 5.0;
+    // beside its blocks, a block of the state pass (two CTAs an SM), and the scan
+    constexpr double kFixed = 5.0, kStateFixed = 5.0, kStateBlock = 0.7, kScan = 5.0;
     const int64_t G = std::max(sms, 1), most = std::max<int64_t>(1, T / 2);
-    auto waves = [&](int64_t units) { return static_cast<double>((units + G - 1) / G); };
+    auto waves = [](int64_t units, int64_t slots) { return static_cast<double>((units + slots - 1) / slots); };
     auto blocks = [&](int64_t parts) { return static_cast<double>((T + parts - 1) / parts); };
     int64_t best_c = 1;
-    double best = 0.0;
+    double best = -1.0;
     for (int64_t c = 1; c <= most && (c == 1 || BH * (c - 1) < 8 * G); ++c) {
-      double cost = need == NEED_STATE ? 0.0 : waves(BH * c) * (blocks(c) + kFixed);
-      int64_t m = 1;
-      if (need == NEED_STATE) {
-        cost = waves(BH * c) * (blocks(c) * kStateBlock + kStateFixed);
-      } else if (c > 1) {
-        m = std::max<int64_t>(1, std::min<int64_t>(G / (BH * (c - 1)), std::min<int64_t>(kSumPieces, T) / c));
-        cost += waves(BH * (c - 1) * m) * (blocks(c * m) * kStateBlock + kStateFixed) + (c > kSumPieces ? kScan : 0.0);
-      }
-      if (c == 1 || cost < best) {
-        best = cost;
-        best_c = c;
-        per = m;
+      const int64_t mmax = need == NEED_STATE || c == 1 ? 1 : std::max<int64_t>(1, std::min(kSumPieces, T) / c);
+      for (int64_t m = 1; m <= mmax; ++m) {
+        double cost = need == NEED_STATE ? 0.0 : waves(BH * c, G) * (blocks(c * m) * m + kFixed);
+        if (need == NEED_STATE || c > 1)
+          cost += waves(BH * (need == NEED_STATE ? c : (c - 1) * m), 2 * G) * (blocks(c * m) * kStateBlock + kStateFixed);
+        if (need != NEED_STATE && c > kSumPieces) cost += kScan;
+        if (best < 0.0 || cost < best) {
+          best = cost;
+          best_c = c;
+          per = m;
+        }
       }
     }
     p.Ls = (T + best_c * per - 1) / (best_c * per) * kRows;
@@ -250,7 +251,7 @@ static la2_status gate_grad(const void* gate, const float* qdq, const float* kdk
                             const float* suffix, const double* tot, void* dgate, int64_t BH, const Shape& sh,
                             const Plan& p, cudaStream_t st) {
   LaunchTimer t(K_GATED_GATE, st);
-  if (launch_pdl(gate_grad_kernel<T>, dim3((unsigned)(BH * sh.C)), dim3(kThreads), 0, st,
+  if (launch_pdl(gate_grad_kernel<T>, dim3((unsigned)(BH * sh.C)), dim3(kGradThreads), 0, st,
                  static_cast<const T*>(gate), qdq, kdk, prefix, suffix, tot, static_cast<T*>(dgate), sh.N,
                  sh.L, sh.C, sh.d * sh.dv, p.K, p.per) != cudaSuccess)
     return LA2_ERR_CUDA;

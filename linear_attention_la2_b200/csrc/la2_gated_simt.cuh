@@ -501,48 +501,76 @@ pool_update_kernel(const float* __restrict__ chunks, const double* __restrict__ 
 // (q . dq - k . dk). The flow at the end of chunk c is <state before chunk c + 1, U
 // behind chunk c> (0 for the last chunk); elements in any common order. One CTA a
 // (sequence, chunk). `per` = 0: prefix and suffix hold those states, scanned;
-// otherwise they hold K pieces' own states, `per` a chunk, and are summed here.
+// otherwise they hold K pieces' own states, `per` a chunk, and are summed here,
+// nearest first, each decayed over the nearer ones (at most kMaxPieces).
+constexpr int kGradThreads = 1024;
+constexpr int kMaxPieces = 16;
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kGradThreads)
 gate_grad_kernel(const T* __restrict__ gate, const float* __restrict__ qdq, const float* __restrict__ kdk,
                  const float* __restrict__ prefix, const float* __restrict__ suffix,
                  const double* __restrict__ tot, T* __restrict__ dgate, int64_t N, int64_t L, int64_t C, int nel,
                  int64_t K, int64_t per) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ double part[kThreads / 32];
+  constexpr int kWarps = kGradThreads / 32;
+  __shared__ double part[kWarps];
+  __shared__ float weight[2][kMaxPieces];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t bh = blockIdx.x / C, ch = blockIdx.x % C;
   const int64_t t0 = ch * L, t1 = imin64(N, t0 + L);
   double carry = 0.0;
   if (ch + 1 < C) {
     const int64_t edge = (ch + 1) * per;  // first piece behind the chunk
-    const int64_t n_pre = per ? edge : 1, n_suf = per ? K - edge : 1;
+    const int n_pre = per ? static_cast<int>(edge) : 1, n_suf = per ? static_cast<int>(K - edge) : 1;
     const float* a = prefix + (bh * K + (per ? edge - 1 : ch + 1)) * nel;
     const float* b = suffix + (bh * K + (per ? edge : ch)) * nel;
-    double x = 0.0;
-    for (int i = threadIdx.x; i < nel; i += kThreads) {
-      float u = 0.f, v = 0.f, f = 1.f;
-      for (int64_t j = 0; j < n_pre; ++j) {  // nearest first, each decayed over the nearer ones
-        u = fmaf(f, a[i - j * nel], u);
-        if (j + 1 < n_pre) f *= expf(static_cast<float>(tot[bh * K + edge - 1 - j]));
+    if (threadIdx.x < 2) {
+      float f = 1.f;
+      const int n = threadIdx.x ? n_suf : n_pre;
+      for (int j = 0; j < n; ++j) {
+        weight[threadIdx.x][j] = f;
+        if (j + 1 < n) f *= expf(static_cast<float>(tot[bh * K + (threadIdx.x ? edge + j : edge - 1 - j)]));
       }
-      f = 1.f;
-      for (int64_t j = 0; j < n_suf; ++j) {
-        v = fmaf(f, b[i + j * nel], v);
-        if (j + 1 < n_suf) f *= expf(static_cast<float>(tot[bh * K + edge + j]));
-      }
-      x += static_cast<double>(u) * v;
     }
+    __syncthreads();
+    double x = 0.0;
+    auto term = [&](int i) {
+      float u = 0.f, v = 0.f;
+      for (int j = 0; j < n_pre; ++j) u = fmaf(weight[0][j], a[i - static_cast<int64_t>(j) * nel], u);
+      for (int j = 0; j < n_suf; ++j) v = fmaf(weight[1][j], b[i + static_cast<int64_t>(j) * nel], v);
+      x += static_cast<double>(u) * v;
+    };
+    auto term4 = [&](int i) {
+      float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+#pragma unroll 4
+      for (int j = 0; j < n_pre; ++j) {
+        const float4 y = *reinterpret_cast<const float4*>(a + i - static_cast<int64_t>(j) * nel);
+        const float f = weight[0][j];
+        u = make_float4(fmaf(f, y.x, u.x), fmaf(f, y.y, u.y), fmaf(f, y.z, u.z), fmaf(f, y.w, u.w));
+      }
+#pragma unroll 4
+      for (int j = 0; j < n_suf; ++j) {
+        const float4 y = *reinterpret_cast<const float4*>(b + i + static_cast<int64_t>(j) * nel);
+        const float f = weight[1][j];
+        v = make_float4(fmaf(f, y.x, v.x), fmaf(f, y.y, v.y), fmaf(f, y.z, v.z), fmaf(f, y.w, v.w));
+      }
+      x += (static_cast<double>(u.x) * v.x + static_cast<double>(u.y) * v.y) +
+           (static_cast<double>(u.z) * v.z + static_cast<double>(u.w) * v.w);
+    };
+    if (nel % 4 == 0)
+      for (int i = 4 * threadIdx.x; i < nel; i += 4 * kGradThreads) term4(i);
+    else
+      for (int i = threadIdx.x; i < nel; i += kGradThreads) term(i);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
     if (lane == 0) part[w] = x;
     __syncthreads();
-    for (int i = 0; i < kThreads / 32; ++i) carry += part[i];
+    for (int i = 0; i < kWarps; ++i) carry += part[i];
     __syncthreads();
   }
-  // rows of the chunk from its last, 256 at a time; thread x holds row hi - x
-  for (int64_t hi = t1 - 1; hi >= t0; hi -= kThreads) {
+  // rows of the chunk from its last; thread x holds row hi - x
+  for (int64_t hi = t1 - 1; hi >= t0; hi -= kGradThreads) {
     const int64_t t = hi - threadIdx.x, at = bh * N + t;
     double x = t >= t0 ? static_cast<double>(qdq[at]) - static_cast<double>(kdk[at]) : 0.0;
 #pragma unroll
@@ -553,8 +581,10 @@ gate_grad_kernel(const T* __restrict__ gate, const float* __restrict__ qdq, cons
     if (lane == 31) part[w] = x;
     __syncthreads();
     double before = carry;
-    for (int i = 0; i < w; ++i) before += part[i];
-    for (int i = 0; i < kThreads / 32; ++i) carry += part[i];
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < w) before += part[i];
+      carry += part[i];
+    }
     if (t >= t0) {
       const float l = to_f32(gate[at]);
       // a gate of 0 passes nothing on, and its own factor is 0; there is nothing

@@ -58,7 +58,7 @@ namespace gated {
 namespace s = sm100;
 
 constexpr int kTile = 64 * 128 * 2;       // one 64 x 128 bf16 tile
-constexpr int kMainThreads = 640;
+constexpr int kMainThreads = 768;
 constexpr float kLog2Zero = -160.f;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kTabs = 8, kTab = 384;      // gate tables in flight, their floats (see the table warp)
@@ -176,14 +176,12 @@ __device__ __forceinline__ void split_scaled(uint32_t x, float f, uint32_t& hi, 
   lo = s::pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
 }
 
-// Four 8-column fragments of 16 TMEM lanes: thread 4 g + j of the warp gets, of each,
+// Two 8-column fragments of 16 TMEM lanes: thread 4 g + j of the warp gets, of each,
 // columns 2 j and 2 j + 1 of lane g and then of lane g + 8.
-__device__ __forceinline__ void tmem_ld_frag4(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+__device__ __forceinline__ void tmem_ld_frag2(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
 }
 // Four 8 x 8 bf16 matrices, transposed, from and to rows of 16 bytes (lane l: row l % 8 of matrix l / 8).
 __device__ __forceinline__ void ldmatrix_t4(uint32_t addr, uint32_t* r) {
@@ -195,6 +193,13 @@ __device__ __forceinline__ void ldmatrix_t4(uint32_t addr, uint32_t* r) {
 __device__ __forceinline__ void stmatrix_t4(uint32_t addr, const uint32_t* r) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
                "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+
+// Thread t of the warp writes 8 consecutive columns of TMEM lane (lane field) + t.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
 
@@ -256,7 +261,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     s::mbar_init(o_empty, 128);
     s::mbar_init(y_full, 128);
     s::mbar_init(y_empty, 1);
-    s::mbar_init(copy_full, 128);
+    s::mbar_init(copy_full, 256);
     s::mbar_init(copy_empty, 1);
     s::mbar_init(updated, 1);
     s::mbar_init(staged, 128);
@@ -490,26 +495,28 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       s::fence_proxy_async();
       s::mbar_arrive(&p_full[i & 1]);
     }
-  } else if (wg == 2) {
+  } else if (wg == 2 || wg == 5) {
     // ==================================== the state's bf16 copy, and its decay
+    // One warpgroup the first 64 columns, the other the rest.
+    const int col0 = wg == 2 ? 0 : 64;
     const int r = 32 * w4 + lane;  // state row
-    const uint32_t ts = tmem + kColState + lane_off, tc = tmem + kColCopy + lane_off;
-    // 32 columns of row r into the copy, and times f into the state
-    auto put = [&](uint32_t (&v)[32], int h, float f, bool keep) {
-      uint32_t hi[16], lo[16];
+    const uint32_t ts = tmem + kColState + col0 + lane_off, tc = tmem + kColCopy + col0 / 2 + lane_off;
+    // 16 columns of row r into the copy, and times f into the state
+    auto put = [&](uint32_t (&v)[16], int h, float f, bool keep) {
+      uint32_t hi[8], lo[8];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
+      for (int e = 0; e < 8; ++e) {
         const float a = __uint_as_float(v[2 * e]), b = __uint_as_float(v[2 * e + 1]);
         hi[e] = s::pack_bf16x2(a, b);
         if (PARTS == 2)
           lo[e] = s::pack_bf16x2(a - __uint_as_float(hi[e] << 16), b - __uint_as_float(hi[e] & 0xffff0000u));
       }
-      s::tmem_st16(tc + 16 * h, hi);
-      if (PARTS == 2) s::tmem_st16(tc + 64 + 16 * h, lo);
+      tmem_st8(tc + 8 * h, hi);
+      if (PARTS == 2) tmem_st8(tc + 64 + 8 * h, lo);
       if (keep) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(f * __uint_as_float(v[e]));
-        s::tmem_st32(ts + h * 32, v);
+        for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(f * __uint_as_float(v[e]));
+        s::tmem_st16(ts + h * 16, v);
       }
     };
     auto done = [&]() {
@@ -528,18 +535,18 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         const float whole = ex2(c[63]);
 #pragma unroll 1
         for (int h = 0; h < 4; ++h) {
-          float x[32];
-          uint32_t v[32];
+          float x[16];
+          uint32_t v[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = 0.f;
+          for (int e = 0; e < 16; ++e) x[e] = 0.f;
           float f = 1.f;
 #pragma unroll 1
           for (int j = 0; j < pieces; ++j) {
             const int64_t at = bh * prm.K + (prm.per == 0 ? ch : BACK ? (ch + 1) * prm.per + j : ch * prm.per - 1 - j);
             const float4* src = reinterpret_cast<const float4*>(prm.init + at * 128 * 128);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float4 y = src[s::state_f4<128>(r, h * 8 + q)];
+            for (int q = 0; q < 4; ++q) {
+              const float4 y = src[s::state_f4<128>(r, col0 / 4 + h * 4 + q)];
               x[4 * q] = fmaf(f, y.x, x[4 * q]);
               x[4 * q + 1] = fmaf(f, y.y, x[4 * q + 1]);
               x[4 * q + 2] = fmaf(f, y.z, x[4 * q + 2]);
@@ -548,7 +555,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             if (j + 1 < pieces) f *= expf(static_cast<float>(prm.tot[at]));
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(x[e]);
+          for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(x[e]);
           put(v, h, whole, n > 1);
         }
         done();
@@ -564,8 +571,8 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       s::tc_fence_after();
 #pragma unroll 1
       for (int h = 0; h < 4; ++h) {
-        uint32_t v[32];
-        s::tmem_ld32(ts + 32 * h, v);
+        uint32_t v[16];
+        tmem_ld16(ts + 16 * h, v);
         s::tmem_ld_wait();
         put(v, h, whole, i + 1 < n);
       }
@@ -598,19 +605,15 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         const int e8 = 4 * w4 + 2 * half + (m & 1);  // eight columns of the output
         const uint32_t row0 = tile + (i & 1) * kTile + (e8 >> 3) * 8192 + (8 * (m >> 1) + i8) * 128 + (((e8 & 7) ^ i8) << 4);
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {  // 32 rows of the output
-          uint32_t near[16], v[16];
-          tmem_ld_frag4(tmem + kColNear + 32 * part + t_lane, near);
-          if (far) tmem_ld_frag4(tmem + kColFar + 64 * (i & 1) + 32 * part + t_lane, v);
-          uint32_t x[8];
-          if (GRAD)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) ldmatrix_t4(row0 + (4 * part + 2 * u) * 1024, &x[4 * u]);
+        for (int part = 0; part < 4; ++part) {  // 16 rows of the output
+          uint32_t near[8], v[8], x[4], pk[4];
+          tmem_ld_frag2(tmem + kColNear + 16 * part + t_lane, near);
+          if (far) tmem_ld_frag2(tmem + kColFar + 64 * (i & 1) + 16 * part + t_lane, v);
+          if (GRAD) ldmatrix_t4(row0 + part * 2048, x);
           s::tmem_ld_wait();
-          uint32_t pk[8];
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const float2 hd = *reinterpret_cast<const float2*>(head + 32 * part + 8 * g);
+          for (int g = 0; g < 2; ++g) {
+            const float2 hd = *reinterpret_cast<const float2*>(head + 16 * part + 8 * g);
             float o[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -622,13 +625,12 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const uint32_t xx = x[2 * g + e];
-                float* d = dot + 8 * part + 2 * g;
+                float* d = dot + 4 * part + 2 * g;
                 d[0] = fmaf(o[2 * e], __uint_as_float(xx << 16), d[0]);
                 d[1] = fmaf(o[2 * e + 1], __uint_as_float(xx & 0xffff0000u), d[1]);
               }
           }
-#pragma unroll
-          for (int u = 0; u < 2; ++u) stmatrix_t4(row0 + (4 * part + 2 * u) * 1024, &pk[4 * u]);
+          stmatrix_t4(row0 + part * 2048, pk);
         }
       }
       s::tc_fence_before();
@@ -720,15 +722,16 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 // and remainder, so the fp32 state is good to 2^-17: it is what the caller's pool
 // receives after a prefill. Bound by HBM: K and V are read once. Warps: 0 loads,
 // 1 MMA, 2 the rows' factors, 4-11 scale rows (four threads a row), 4-7 write the
-// state out.
+// state out. Two CTAs an SM: one's scaling (about 1000 cycles a block) runs beside the
+// other's waits, loads and MMAs; one CTA with twice the buffers was 1.4 times slower.
 struct StateCfg {
-  static constexpr int KS = 4;
-  static constexpr int OFF_Y2 = KS * 2 * kTile;            // two buffers of value and remainder
-  static constexpr int OFF_TAB = OFF_Y2 + 4 * kTile;       // rows' factors, kTabs blocks of 64
+  static constexpr int KS = 2;
+  static constexpr int OFF_Y2 = KS * 2 * kTile;            // value and remainder
+  static constexpr int OFF_TAB = OFF_Y2 + 2 * kTile;       // rows' factors, kTabs blocks of 64
   static constexpr int OFF_BAR = OFF_TAB + kTabs * 64 * 4;
-  static constexpr int NBAR = 2 * KS + 4 + 2 + kTabs;
+  static constexpr int NBAR = 2 * KS + 2 + 2 + kTabs;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
-  static_assert(SMEM <= 227 * 1024, "shared memory budget");
+  static_assert(SMEM <= 113 * 1024, "two CTAs an SM");
 };
 
 struct TcStateParams {
@@ -741,7 +744,7 @@ struct TcStateParams {
 
 // ROWS_Z: the state's rows are z's columns (what O and dV start from), else y's.
 template <bool SUFFIX, bool ROWS_Z>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(384, 2)
 gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_z,
                          const TcStateParams prm) {
   using CF = StateCfg;
@@ -754,8 +757,8 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
   uint64_t* in_full = reinterpret_cast<uint64_t*>(smem + CF::OFF_BAR);
   uint64_t* in_empty = in_full + KS;
   uint64_t* y2_full = in_empty + KS;
-  uint64_t* y2_empty = y2_full + 2;
-  uint64_t *done = y2_empty + 2, *drain = done + 1;
+  uint64_t* y2_empty = y2_full + 1;
+  uint64_t *done = y2_empty + 1, *drain = done + 1;
   uint64_t* tab_full = drain + 1;
   uint32_t* tmem_base = reinterpret_cast<uint32_t*>(tab_full + kTabs);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_base + 1);
@@ -768,7 +771,8 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < KS; ++i) { s::mbar_init(&in_full[i], 1); s::mbar_init(&in_empty[i], 1); }
-    for (int i = 0; i < 2; ++i) { s::mbar_init(&y2_full[i], 256); s::mbar_init(&y2_empty[i], 1); }
+    s::mbar_init(y2_full, 256);
+    s::mbar_init(y2_empty, 1);
     for (int i = 0; i < kTabs; ++i) s::mbar_init(&tab_full[i], 32);
     s::mbar_init(done, 1);
     s::mbar_init(drain, 1);
@@ -817,14 +821,14 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
     const uint64_t in_d = s::make_desc(s::smem_u32(smem), 8192, 1024);
     bool ok = true;
     for (int i = 0; i < n && ok; ++i) {
-      ok = wait(&in_full[i % KS], (i / KS) & 1, 91) && wait(&y2_full[i & 1], (i >> 1) & 1, 92);
+      ok = wait(&in_full[i % KS], (i / KS) & 1, 91) && wait(y2_full, i & 1, 92);
       if (!ok) break;
       s::tc_fence_after();
-      const uint64_t y2 = in_d + (CF::OFF_Y2 + (i & 1) * 2 * kTile) / 16, z = in_d + ((i % KS) * 2 * kTile + kTile) / 16;
+      const uint64_t y2 = in_d + CF::OFF_Y2 / 16, z = in_d + ((i % KS) * 2 * kTile + kTile) / 16;
       const uint64_t lo = y2 + kTile / 16;
       mma_run<4>(lead, tmem, ROWS_Z ? z : y2, ROWS_Z ? y2 : z, 128, 128, 0, 0, ID_UPD, i > 0);
       mma_run<4>(lead, tmem, ROWS_Z ? z : lo, ROWS_Z ? lo : z, 128, 128, 0, 0, ID_UPD, 1);
-      commit(lead, &y2_empty[i & 1]);
+      commit(lead, y2_empty);
       commit(lead, &in_empty[i % KS]);
     }
     if (ok) commit(lead, done);
@@ -858,10 +862,10 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
     bool ok = true;
     for (int i = 0; i < n && ok; ++i) {
       ok = wait(&tab_full[i % kTabs], (i / kTabs) & 1, 97) && wait(&in_full[i % KS], (i / KS) & 1, 93) &&
-           wait(&y2_empty[i & 1], ((i >> 1) & 1) ^ 1, 94);
+           wait(y2_empty, (i & 1) ^ 1, 94);
       if (!ok) break;
       const float f = tab[(i % kTabs) * 64 + r];
-      const uint32_t y2 = s::smem_u32(smem + CF::OFF_Y2 + (i & 1) * 2 * kTile);
+      const uint32_t y2 = s::smem_u32(smem + CF::OFF_Y2);
       const uint32_t ya = s::smem_u32(smem + (i % KS) * 2 * kTile);
 #pragma unroll
       for (int ch = ch0; ch < ch0 + 4; ++ch) {
@@ -874,7 +878,7 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
         s::st_shared_v4(y2 + kTile + off, lo[0], lo[1], lo[2], lo[3]);
       }
       s::fence_proxy_async();
-      s::mbar_arrive(&y2_full[i & 1]);
+      s::mbar_arrive(y2_full);
     }
     if (ok && warp < 8 && wait(done, 0, 95)) {
       s::tc_fence_after();
