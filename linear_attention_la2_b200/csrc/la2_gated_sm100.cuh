@@ -162,18 +162,67 @@ struct TcCfg {
   static constexpr int OFF_TAB = OFF_OUT + 2 * kTile;
   static constexpr int OFF_DOT = OFF_TAB + kTabs * kTab * 4;
   static constexpr int OFF_BAR = OFF_DOT + (GRAD ? 2 * 4 * 64 * 4 : 0);
-  static constexpr int NBAR = 2 * KS + 3 + 4 + 2 + 3 + 2 + 3 + kTabs + 1;
+  static constexpr int NBAR = 4 * KS + 3 + 4 + 2 + 3 + 2 + 3 + kTabs + 1;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
 // TMEM columns: the state, its copy (value, remainder), S, two buffers of far, near
 constexpr uint32_t kColState = 0, kColCopy = 128, kColS = 256, kColFar = 320, kColNear = 448;
 
-// Two bf16 values times f: the rounded products, and what they are off, rounded.
-__device__ __forceinline__ void split_scaled(uint32_t x, float f, uint32_t& hi, uint32_t& lo) {
-  const float a = __uint_as_float(x << 16) * f, b = __uint_as_float(x & 0xffff0000u) * f;
-  hi = s::pack_bf16x2(a, b);
-  lo = s::pack_bf16x2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
+// Packed fp32 pairs (two multiply-adds an instruction: the roles share the issue slots).
+__device__ __forceinline__ uint64_t f2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2(uint32_t x, uint32_t y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack(uint64_t a, uint32_t& x, uint32_t& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(x), "=r"(y) : "l"(a));
+}
+__device__ __forceinline__ void unpack(uint64_t a, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack2(uint64_t a) {  // to bf16
+  float x, y;
+  unpack(a, x, y);
+  return s::pack_bf16x2(x, y);
+}
+__device__ __forceinline__ uint32_t bfma2(uint32_t a, uint32_t b, uint32_t c) {  // bf16 pairs
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+// A factor as two bf16 values, each twice: f = h + l to 2^-17.
+struct Factor {
+  uint32_t h, l;
+};
+__device__ __forceinline__ Factor factor(float f) {
+  Factor r;
+  r.h = s::pack_bf16x2(f, f);
+  const float l = f - __uint_as_float(r.h & 0xffff0000u);
+  r.l = s::pack_bf16x2(l, l);
+  return r;
+}
+// Two bf16 values times f: the rounded products, and what they are off to 2^-17. The
+// remainder of x h against its rounding has at most 8 bits: the second product is exact.
+__device__ __forceinline__ void split_scaled(uint32_t x, const Factor& f, uint32_t& hi, uint32_t& lo) {
+  hi = bfma2(x, f.h, 0x80008000u);  // (-0: keeps the sign of a zero product)
+  lo = bfma2(x, f.l, bfma2(x, f.h, hi ^ 0x80008000u));
 }
 
 // Two 8-column fragments of 16 TMEM lanes: thread 4 g + j of the warp gets, of each,
@@ -228,7 +277,9 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 
   uint64_t* in_full = reinterpret_cast<uint64_t*>(smem + CF::OFF_BAR);
   uint64_t* in_empty = in_full + KS;
-  uint64_t* s_full = in_empty + KS;
+  uint64_t* z_full = in_empty + KS;  // (in: X and Y)
+  uint64_t* z_empty = z_full + KS;
+  uint64_t* s_full = z_empty + KS;
   uint64_t* s_empty = s_full + 2;
   uint64_t *p_full = s_empty + 1, *p_empty = p_full + 2;
   uint64_t *y_full = p_empty + 2, *y_empty = y_full + 1;
@@ -249,7 +300,12 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
   auto row_of = [&](int i) { return t0 + static_cast<int64_t>(BACK ? n - 1 - i : i) * 64; };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < KS; ++i) { s::mbar_init(&in_full[i], 1); s::mbar_init(&in_empty[i], 1); }
+    for (int i = 0; i < KS; ++i) {
+      s::mbar_init(&in_full[i], 1);
+      s::mbar_init(&in_empty[i], 1);
+      s::mbar_init(&z_full[i], 1);
+      s::mbar_init(&z_empty[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
       s::mbar_init(&s_full[i], 1);
       s::mbar_init(&p_full[i], 128);
@@ -300,21 +356,24 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
   if (warp == 0) {
     // ================================================================ loads
     if (lane == 0) {
-      int issued = 0;
-      bool ok = true;
+      int issued = 0, issued_z = 0;
       for (int i = 0; i < n; ++i) {
-        const int st = i % KS;
-        if (!s::wait_bar(&in_empty[st], ((i / KS) & 1) ^ 1, lim, abort_flag, 70)) { ok = false; break; }
-        const int row = static_cast<int>(row_of(i)), z = static_cast<int>(bh);
+        const int st = i % KS, row = static_cast<int>(row_of(i)), z = static_cast<int>(bh);
         uint8_t* dst = smem + st * 3 * kTile;
-        s::mbar_expect_tx(&in_full[st], 3 * kTile);
+        if (!s::wait_bar(&in_empty[st], ((i / KS) & 1) ^ 1, lim, abort_flag, 70)) break;
+        s::mbar_expect_tx(&in_full[st], 2 * kTile);
         for (int p = 0; p < 2; ++p) s::tma_load_3d(dst + p * 8192, &tm_x, &in_full[st], 64 * p, row, z);
         for (int p = 0; p < 2; ++p) s::tma_load_3d(dst + kTile + p * 8192, &tm_y, &in_full[st], 64 * p, row, z);
-        for (int p = 0; p < 2; ++p) s::tma_load_3d(dst + 2 * kTile + p * 8192, &tm_z, &in_full[st], 64 * p, row, z);
         ++issued;
+        if (!s::wait_bar(&z_empty[st], ((i / KS) & 1) ^ 1, lim, abort_flag, 87)) break;
+        s::mbar_expect_tx(&z_full[st], kTile);
+        for (int p = 0; p < 2; ++p) s::tma_load_3d(dst + 2 * kTile + p * 8192, &tm_z, &z_full[st], 64 * p, row, z);
+        ++issued_z;
       }
-      if (!ok)  // let every load this thread issued land before the CTA exits
+      if (issued_z < n) {  // after an abort: let every load this thread issued land before the CTA exits
         for (int j = max(0, issued - KS); j < issued; ++j) s::drain_wait(&in_full[j % KS], (j / KS) & 1);
+        for (int j = max(0, issued_z - KS); j < issued_z; ++j) s::drain_wait(&z_full[j % KS], (j / KS) & 1);
+      }
     }
   } else if (warp == 1) {
     // ================================================================== MMA
@@ -344,6 +403,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       const bool far = i >= first_copy;
       ok = false;
       if (i + 1 < n && !scores(i + 1)) break;
+      if (!wait(&z_full[i % KS], (i / KS) & 1, 87)) break;
       if (far && !wait(copy_full, (i - first_copy) & 1, 74)) break;
       if (i + 1 < n) {  // the state past the chunk's last block is not needed
         if (!wait(y_full, i & 1, 75)) break;
@@ -364,13 +424,14 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         __syncwarp();
         commit(lead, copy_empty);
       }
+      commit(lead, &in_empty[i % KS]);  // X and Y are done with, Z is not
       if (!wait(&p_full[i & 1], (i >> 1) & 1, 76)) break;
       if (!wait(o_empty, (i & 1) ^ 1, 73)) break;  // the epilogue has read near of block i - 1
       s::tc_fence_after();
       mma_run<4>(lead, tmem + kColNear, col_d + st + kZ, p_d + (i & 1) * 512, 128, 2, 0, 0, ID_NEAR, 0);
       commit(lead, o_full);
       commit(lead, &p_empty[i & 1]);
-      commit(lead, &in_empty[i % KS]);
+      commit(lead, &z_empty[i % KS]);
       ok = true;
     }
     commit(lead, drain);  // every MMA issued must finish before TMEM is released
@@ -382,7 +443,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     // with E(s) the last row of s' sixteen, and e^(c_t - c_E) for the first three E
     // [3][64] (read for later t only): off the diagonal e^(c_t - c_s) is one of each,
     // neither above 1 unless gates are. Table i goes into slot i % 8 when block i - KS
-    // has released its stage (in_empty): everything of it is done but its epilogue,
+    // has released its stage (z_empty): everything of it is done but its epilogue,
     // and before its near was issued the epilogue had read block i - KS - 1 (o_empty),
     // so readers of block i - 8 are long done.
     const __nv_bfloat16* g = prm.gate + bh * prm.N;
@@ -395,7 +456,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
           return t > 0 || __hisnan(x) ? x : __float2bfloat16(0.f);
         },
         [&](int i, __nv_bfloat16 gx, __nv_bfloat16 gy) {
-          if (i >= KS && !wait(&in_empty[i % KS], (i / KS - 1) & 1, 77)) return false;
+          if (i >= KS && !wait(&z_empty[i % KS], (i / KS - 1) & 1, 77)) return false;
           float a, b;
           warp_sums(gate_log2(gx), gate_log2(gy), lane, a, b);
           const float all = __shfl_sync(0xffffffffu, b, 31);
@@ -421,11 +482,11 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     for (int i = 0; i + 1 < n; ++i) {
       const float* c = tab_of(i, 78);
       if (!c) break;
-      const float f = ex2(BACK ? c[r] : c[63] - c[r]);
+      const Factor f = factor(ex2(BACK ? c[r] : c[63] - c[r]));
       if (!wait(&s_full[i & 1], (i >> 1) & 1, 79)) break;
       if (!wait(y_empty, (i & 1) ^ 1, 90)) break;
       const uint32_t ya = s::smem_u32(smem + (i % KS) * 3 * kTile + kTile) + half * 8192 + r * 128;
-#pragma unroll 1
+#pragma unroll 2
       for (int ch = 0; ch < 8; ++ch) {
         const uint32_t off = (ch ^ (r & 7)) << 4;
         uint32_t x[4], hi[4], lo[4];
@@ -476,14 +537,13 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
           } else {
             const float* cols = c + (BACK ? 192 + 64 * w4 : 128) + 16 * h;
             const float f = c[BACK ? 128 + r : 192 + 64 * h + r];
+            const uint64_t ff = f2(f, f);
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
-              const float4 x = *reinterpret_cast<const float4*>(cols + 2 * e);
-              const float s0 = __uint_as_float(v[2 * e]), s1 = __uint_as_float(v[2 * e + 1]),
-                          s2 = __uint_as_float(v[2 * e + 2]), s3 = __uint_as_float(v[2 * e + 3]);
-              w[e] = BACK ? s::pack_bf16x2((s0 * f) * x.x, (s1 * f) * x.y) : s::pack_bf16x2((s0 * x.x) * f, (s1 * x.y) * f);
-              w[e + 1] = BACK ? s::pack_bf16x2((s2 * f) * x.z, (s3 * f) * x.w)
-                              : s::pack_bf16x2((s2 * x.z) * f, (s3 * x.w) * f);
+              const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(cols + 2 * e);
+              const uint64_t a = f2(v[2 * e], v[2 * e + 1]), b = f2(v[2 * e + 2], v[2 * e + 3]);
+              w[e] = pack2(BACK ? mul2(mul2(a, ff), x.x) : mul2(mul2(a, x.x), ff));
+              w[e + 1] = pack2(BACK ? mul2(mul2(b, ff), x.y) : mul2(mul2(b, x.y), ff));
             }
           }
           s::st_shared_v4(p_at(i & 1, 2 * h), w[0], w[1], w[2], w[3]);
@@ -514,8 +574,9 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       tmem_st8(tc + 8 * h, hi);
       if (PARTS == 2) tmem_st8(tc + 64 + 8 * h, lo);
       if (keep) {
+        const uint64_t ff = f2(f, f);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(f * __uint_as_float(v[e]));
+        for (int e = 0; e < 16; e += 2) unpack(mul2(f2(v[e], v[e + 1]), ff), v[e], v[e + 1]);
         s::tmem_st16(ts + h * 16, v);
       }
     };
@@ -596,9 +657,9 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       if (!wait(&tile_free[i & 1], ((i >> 1) & 1) ^ (GRAD ? 0 : 1), 89)) break;
       if (!wait(o_full, i & 1, 86)) break;
       s::tc_fence_after();
-      float dot[16];  // columns 8 g + 2 j, + 1 of this thread, summed over its lanes
+      uint64_t dot[8];  // columns 8 g + 2 j, + 1 of this thread, summed over its lanes
 #pragma unroll
-      for (int e = 0; e < 16; ++e) dot[e] = 0.f;
+      for (int e = 0; e < 8; ++e) dot[e] = 0;
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         const uint32_t t_lane = lane_off + (static_cast<uint32_t>(16 * half) << 16);
@@ -613,22 +674,17 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
           s::tmem_ld_wait();
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
-            const float2 hd = *reinterpret_cast<const float2*>(head + 16 * part + 8 * g);
-            float o[4];
+            const uint64_t hd = *reinterpret_cast<const uint64_t*>(head + 16 * part + 8 * g);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              o[e] = far ? fmaf(e & 1 ? hd.y : hd.x, __uint_as_float(v[4 * g + e]), __uint_as_float(near[4 * g + e]))
-                         : __uint_as_float(near[4 * g + e]);
-            pk[2 * g] = s::pack_bf16x2(o[0], o[1]);
-            pk[2 * g + 1] = s::pack_bf16x2(o[2], o[3]);
-            if (GRAD)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < 2; ++e) {  // lane g, lane g + 8
+              uint64_t o = f2(near[4 * g + 2 * e], near[4 * g + 2 * e + 1]);
+              if (far) o = fma2(hd, f2(v[4 * g + 2 * e], v[4 * g + 2 * e + 1]), o);
+              pk[2 * g + e] = pack2(o);
+              if (GRAD) {
                 const uint32_t xx = x[2 * g + e];
-                float* d = dot + 4 * part + 2 * g;
-                d[0] = fmaf(o[2 * e], __uint_as_float(xx << 16), d[0]);
-                d[1] = fmaf(o[2 * e + 1], __uint_as_float(xx & 0xffff0000u), d[1]);
+                dot[2 * part + g] = fma2(o, f2(xx << 16, xx & 0xffff0000u), dot[2 * part + g]);
               }
+            }
           }
           stmatrix_t4(row0 + part * 2048, pk);
         }
@@ -637,18 +693,21 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       s::mbar_arrive(o_empty);
       if (GRAD) {
         // over the eight threads with the same columns: each keeps half at every step
+        float d[16];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) unpack(dot[e], d[2 * e], d[2 * e + 1]);
 #pragma unroll
         for (int step = 0; step < 3; ++step) {
           const int keep = 8 >> step, bit = 16 >> step;
           const bool up = lane & bit;
 #pragma unroll
           for (int e = 0; e < keep; ++e) {
-            const float a = up ? dot[e + keep] : dot[e], z = up ? dot[e] : dot[e + keep];
-            dot[e] = a + __shfl_xor_sync(0xffffffffu, z, bit);
+            const float a = up ? d[e + keep] : d[e], z = up ? d[e] : d[e + keep];
+            d[e] = a + __shfl_xor_sync(0xffffffffu, z, bit);
           }
         }
         const int g = (lane >> 4) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
-        *reinterpret_cast<float2*>(dotbuf + (i & 1) * 256 + w4 * 64 + 8 * g + 2 * (lane & 3)) = make_float2(dot[0], dot[1]);
+        *reinterpret_cast<float2*>(dotbuf + (i & 1) * 256 + w4 * 64 + 8 * g + 2 * (lane & 3)) = make_float2(d[0], d[1]);
       }
       s::fence_proxy_async();
       s::mbar_arrive(staged);
@@ -864,7 +923,7 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
       ok = wait(&tab_full[i % kTabs], (i / kTabs) & 1, 97) && wait(&in_full[i % KS], (i / KS) & 1, 93) &&
            wait(y2_empty, (i & 1) ^ 1, 94);
       if (!ok) break;
-      const float f = tab[(i % kTabs) * 64 + r];
+      const Factor f = factor(tab[(i % kTabs) * 64 + r]);
       const uint32_t y2 = s::smem_u32(smem + CF::OFF_Y2);
       const uint32_t ya = s::smem_u32(smem + (i % KS) * 2 * kTile);
 #pragma unroll
