@@ -18,10 +18,12 @@
 // attention entry points read, so the transposition costs no pass of its own.
 //
 // Bound by HBM: each row is read once and written once (backwards: two reads).
-// A CTA takes a tile of consecutive tokens and all their heads: the angles are
-// computed once a token and kept in shared memory (the turns in fp64 - at
-// position 2^20 an fp32 product is 0.06 rad off - and only their fraction goes
-// on to fp32), and the rows of one head in the tile are consecutive in the output.
+// A CTA takes a tile of consecutive tokens and their heads. The angles are computed
+// once a token, into shared memory: the turns in fp64 (at position 2^20 an fp32 product
+// is 0.06 rad off), and only their fraction goes on to fp32. A group of lanes, 16 bytes
+// of a row each, keeps one token's cosines and sines in registers and walks the heads,
+// several rows in flight; its neighbours hold the next tokens, so that the tile's rows
+// of a head leave as one piece of the output.
 #pragma once
 
 namespace la2 {
@@ -31,7 +33,6 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxD = 256;
 constexpr int kMaxAxes = 4;
-constexpr int kMaxTokens = 8;  // tokens of a tile
 
 struct Params {
   const void* x[2];        // queries, keys (backward: the forward's inputs)
@@ -69,8 +70,8 @@ struct Row {
   int64_t flat;
   int t;                   // token within the tile
 };
-// Row r of the tile: heads outermost, so that neighbouring rows are neighbouring
-// tokens of one head.
+// Row r of the tile (the kernels of a warp a row): heads outermost, so that
+// neighbouring rows are neighbouring tokens of one head.
 __device__ __forceinline__ Row row_of(const Params& p, int64_t tok0, int ntok, int r) {
   Row x;
   int h = r / ntok;
@@ -92,13 +93,8 @@ __device__ __forceinline__ float group_sum(float x) {
   return x;
 }
 
-// One row as a thread sees it. VEC > 1: a group of G lanes holds a row, lane l
-// the VEC values from VEC l on, and the partner of a pair sits h / VEC lanes
-// away. VEC = 1: a warp holds a row, lane l the pairs l, l + 32, ... and the
-// values behind the rotated ones alike (any even rot, any alignment).
-template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T* p, float (&x)[VEC]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
+template <int VEC>
+__device__ __forceinline__ void widen(const uint4& u, float (&x)[VEC]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -124,75 +120,131 @@ __device__ __forceinline__ void store_vec(T* p, const float (&x)[VEC]) {
   }
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
+template <typename T, int VEC>
+__device__ __forceinline__ void load_weight(const void* w, int at, bool on, float (&x)[VEC]) {
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) x[e] = 1.f;
+  if (w && on) widen(*reinterpret_cast<const uint4*>(static_cast<const T*>(w) + at), x);
+}
 
-// Turns the pairs of a row spread over a group: x <- R(sign * angle) x.
+// What a lane needs to turn its VEC values of a row: value e becomes
+// x c[e] + (its pair's other value) s[e]; c = 1, s = 0 behind the rotated ones.
 template <int VEC>
-__device__ __forceinline__ void turn_vec(float (&x)[VEC], const float2* cs, int l, int half, float sign) {
-  const int hl = half / VEC;
-  const bool lo = l < hl, hi = l >= hl && l < 2 * hl;
-  const int src = (threadIdx.x & 31) + (lo ? hl : (hi ? -hl : 0));
-  const int j0 = VEC * (hi ? l - hl : l);
-  const float f = lo ? -sign : sign;
+struct Turn {
+  float c[VEC], s[VEC];
+};
+// sign 1 turns forwards, -1 back.
+template <int VEC>
+__device__ __forceinline__ void load_turn(Turn<VEC>& t, const float2* cs, int first, int half, float sign) {
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
-    const float o = __shfl_sync(0xffffffffu, x[e], src);
-    if (lo || hi) {
-      const float2 a = cs[j0 + e];
-      x[e] = fmaf(x[e], a.x, f * a.y * o);
+    const int i = first + e;
+    const float2 a = i < 2 * half ? cs[i < half ? i : i - half] : make_float2(1.f, 0.f);
+    t.c[e] = a.x;
+    t.s[e] = i < half ? -sign * a.y : sign * a.y;
+  }
+}
+// x <- turned x. STAGE false: half is a multiple of VEC, and the other value of a pair
+// sits at the same place half / VEC lanes away. STAGE true: the group's row goes through
+// shared memory (a row of G lanes, 9 words for every 8 so that lanes meet no conflicts).
+template <int VEC, bool STAGE>
+__device__ __forceinline__ void turn_row(float (&x)[VEC], const Turn<VEC>& t, int l, int half, float* stage) {
+  if constexpr (!STAGE) {
+    const int hl = half / VEC, lane = threadIdx.x & 31;
+    const int src = l < hl ? lane + hl : (l < 2 * hl ? lane - hl : lane);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) x[e] = fmaf(x[e], t.c[e], __shfl_sync(0xffffffffu, x[e], src) * t.s[e]);
+  } else {
+    auto at = [](int i) { return i + (i >> 3); };
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) stage[at(VEC * l + e)] = x[e];
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const int i = VEC * l + e, j = i < half ? i + half : (i < 2 * half ? i - half : i);
+      x[e] = fmaf(x[e], t.c[e], stage[at(j)] * t.s[e]);
     }
   }
 }
+// Floats of a group's staging row.
+__host__ __device__ constexpr int stage_floats(int vec, int g) { return vec * g + vec * g / 8; }
 
-template <typename T, int VEC, int G>
+// The token and first head of a thread's group: groups run over the tile's tokens,
+// then over its share of the heads (`slots` heads at a time).
+struct Place {
+  int t, slot, slots;
+  bool on;          // the token exists
+  int64_t b, n, tok;
+};
+template <int G>
+__device__ __forceinline__ Place place_of(const Params& p, int64_t tok0) {
+  Place x;
+  const int g = threadIdx.x / G;
+  x.t = g % p.tile;
+  const int own = kThreads / G / p.tile;
+  x.slots = own * p.splits;
+  x.slot = g / p.tile + own * blockIdx.y;
+  x.tok = tok0 + x.t;
+  x.on = x.tok < p.tokens;
+  if (!x.on) x.tok = tok0;
+  x.b = static_cast<uint32_t>(x.tok) / static_cast<uint32_t>(p.N);
+  x.n = x.tok - x.b * p.N;
+  return x;
+}
+
+template <typename T, int VEC, int G, bool STAGE>
 __global__ void __launch_bounds__(kThreads)
 rope_fwd_vec_kernel(const __grid_constant__ Params p) {
   extern __shared__ float2 cs[];
+  __shared__ float stage_all[STAGE ? kThreads / G * stage_floats(VEC, G) : 1];
   pdl_launch_dependents();
   pdl_wait();
   const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tile;
-  const int ntok = static_cast<int>(imin64(p.tile, p.tokens - tok0));
-  const int l = threadIdx.x % G, d = p.d;
-  const bool on = l * VEC < d;
-  const float inv_d = 1.f / static_cast<float>(d);
-  const int rows = ntok * (p.heads[0] + p.heads[1]);
-  constexpr int GROUPS = kThreads / G, U = 2;  // U rows a thread in flight
-  const int step = GROUPS * p.splits;
-  fill_angles(p, tok0, ntok, cs);
+  fill_angles(p, tok0, static_cast<int>(imin64(p.tile, p.tokens - tok0)), cs);
   __syncthreads();
-  for (int r0 = threadIdx.x / G + GROUPS * blockIdx.y; r0 < (rows + 3) / 4 * 4; r0 += step * U) {
-    // (a multiple of the 32 / G rows of a warp: whole warps stay for the shuffles)
-    float x[U][VEC];
-    Row row[U];
+  const Place at = place_of<G>(p, tok0);
+  const int l = threadIdx.x % G, d = p.d;
+  const bool in_row = l * VEC < d;
+  const float inv_d = 1.f / static_cast<float>(d);
+  float* stage = stage_all + (STAGE ? threadIdx.x / G * stage_floats(VEC, G) : 0);
+  Turn<VEC> turn;
+  load_turn(turn, cs + (at.on ? at.t : 0) * p.half, l * VEC, p.half, 1.f);
+  constexpr int U = 4;  // rows in flight
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    const int heads = p.heads[which];
+    if (heads == 0) continue;
+    const T* x0 = static_cast<const T*>(p.x[which]) + at.b * p.sb[which] + at.n * p.sn[which] + l * VEC;
+    T* o0 = static_cast<T*>(p.out[which]) + (at.b * heads * p.N + at.n) * d + l * VEC;
+    float w[VEC];
+    load_weight<T, VEC>(p.w[which], l * VEC, in_row, w);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * step;
-      row[u] = row_of(p, tok0, ntok, min(r, rows - 1));
+    for (int e = 0; e < VEC; ++e) w[e] *= p.scale[which];
+#pragma unroll 1
+    for (int h0 = 0; h0 < heads; h0 += at.slots * U) {  // (the same for all lanes of a warp)
+      uint4 raw[U];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) x[u][e] = 0.f;
-      if (on && r < rows) load_vec<T, VEC>(static_cast<const T*>(p.x[row[u].which]) + row[u].in + l * VEC, x[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int which = row[u].which;
-      float s = 0.f;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) s = fmaf(x[u][e], x[u][e], s);
-      s = group_sum<G>(s);
-      const float r = rsqrtf(fmaf(s, inv_d, p.eps));
-      if (p.w[which] && on) {
-        float w[VEC];
-        load_vec<T, VEC>(static_cast<const T*>(p.w[which]) + l * VEC, w);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) x[u][e] = x[u][e] * r * w[e];
-      } else {
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) x[u][e] *= r;
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + at.slot + u * at.slots;
+        raw[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (in_row && at.on && h < heads) raw[u] = *reinterpret_cast<const uint4*>(x0 + h * p.sh[which]);
       }
-      turn_vec<VEC>(x[u], cs + row[u].t * p.half, l, p.half, 1.f);
-      const float f = p.scale[which];
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) x[u][e] *= f;
-      if (on && r0 + u * step < rows) store_vec<T, VEC>(static_cast<T*>(p.out[which]) + row[u].out + l * VEC, x[u]);
+      for (int u = 0; u < U; ++u) {
+        const int h = h0 + at.slot + u * at.slots;
+        if (h0 + u * at.slots >= heads) break;  // (uniform)
+        float x[VEC];
+        widen(raw[u], x);
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) s = fmaf(x[e], x[e], s);
+        const float r = rsqrtf(fmaf(group_sum<G>(s), inv_d, p.eps));
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) x[e] = x[e] * r * w[e];
+        turn_row<VEC, STAGE>(x, turn, l, p.half, stage);
+        if (in_row && at.on && h < heads) store_vec<T, VEC>(o0 + h * p.N * d, x);
+      }
     }
   }
 }
@@ -208,77 +260,87 @@ __device__ __forceinline__ void store_dw(const Params& p, const float* smem_dw) 
   }
 }
 
-template <typename T, int VEC, int G>
+template <typename T, int VEC, int G, bool STAGE>
 __global__ void __launch_bounds__(kThreads)
 rope_bwd_vec_kernel(const __grid_constant__ Params p) {
   extern __shared__ float2 cs[];
   float* sdw = reinterpret_cast<float*>(cs + p.tile * p.half);  // [kWarps][2][d]
+  __shared__ float stage_all[STAGE ? kThreads / G * stage_floats(VEC, G) : 1];
   pdl_launch_dependents();
   pdl_wait();
   const int l = threadIdx.x % G, d = p.d;
-  const bool on = l * VEC < d;
+  const bool in_row = l * VEC < d;
   const float inv_d = 1.f / static_cast<float>(d);
-  constexpr int GROUPS = kThreads / G;
-  float dw[2][VEC];
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) dw[0][e] = dw[1][e] = 0.f;
+  float* stage = stage_all + (STAGE ? threadIdx.x / G * stage_floats(VEC, G) : 0);
+  float* my_dw = sdw + (threadIdx.x >> 5) * 2 * d;
+  for (int i = threadIdx.x & 31; i < 2 * d; i += 32) my_dw[i] = 0.f;
   for (int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tile; tok0 < p.tokens;
        tok0 += static_cast<int64_t>(gridDim.x) * p.tile) {
-    const int ntok = static_cast<int>(imin64(p.tile, p.tokens - tok0));
-    const int rows = ntok * (p.heads[0] + p.heads[1]);
     __syncthreads();
-    fill_angles(p, tok0, ntok, cs);
+    fill_angles(p, tok0, static_cast<int>(imin64(p.tile, p.tokens - tok0)), cs);
     __syncthreads();
-    for (int r0 = threadIdx.x / G; r0 < (rows + GROUPS - 1) / GROUPS * GROUPS; r0 += GROUPS) {
-      const bool ok = on && r0 < rows;
-      const Row row = row_of(p, tok0, ntok, min(r0, rows - 1));
-      float x[VEC], g[VEC];
+    const Place at = place_of<G>(p, tok0);
+    Turn<VEC> turn;
+    load_turn(turn, cs + (at.on ? at.t : 0) * p.half, l * VEC, p.half, -1.f);
+    constexpr int U = 2;  // rows in flight, two reads each
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+      const int heads = p.heads[which];
+      if (heads == 0) continue;
+      const T* x0 = static_cast<const T*>(p.x[which]) + at.b * p.sb[which] + at.n * p.sn[which] + l * VEC;
+      const T* g0 = static_cast<const T*>(p.dy[which]) + (at.b * heads * p.N + at.n) * d + l * VEC;
+      T* o0 = static_cast<T*>(p.out[which]) + at.tok * heads * d + l * VEC;
+      float w[VEC], dw[VEC];
+      load_weight<T, VEC>(p.w[which], l * VEC, in_row, w);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) x[e] = g[e] = 0.f;
-      if (ok) {
-        load_vec<T, VEC>(static_cast<const T*>(p.x[row.which]) + row.in + l * VEC, x);
-        load_vec<T, VEC>(static_cast<const T*>(p.dy[row.which]) + row.out + l * VEC, g);
+      for (int e = 0; e < VEC; ++e) dw[e] = 0.f;
+      const float scale = p.scale[which];
+#pragma unroll 1
+      for (int h0 = 0; h0 < heads; h0 += at.slots * U) {
+        uint4 xr[U], gr[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int h = h0 + at.slot + u * at.slots;
+          xr[u] = gr[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (in_row && at.on && h < heads) {
+            xr[u] = *reinterpret_cast<const uint4*>(x0 + h * p.sh[which]);
+            gr[u] = *reinterpret_cast<const uint4*>(g0 + h * p.N * d);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int h = h0 + at.slot + u * at.slots;
+          if (h0 + u * at.slots >= heads) break;  // (uniform)
+          float x[VEC], g[VEC];
+          widen(xr[u], x);
+          widen(gr[u], g);
+          float s = 0.f;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) s = fmaf(x[e], x[e], s);
+          const float r = rsqrtf(fmaf(group_sum<G>(s), inv_d, p.eps));
+          turn_row<VEC, STAGE>(g, turn, l, p.half, stage);
+          float dot = 0.f;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            g[e] *= scale;
+            x[e] *= r;
+            dw[e] = fmaf(g[e], x[e], dw[e]);
+            g[e] *= w[e];
+            dot = fmaf(g[e], x[e], dot);
+          }
+          dot = group_sum<G>(dot) * inv_d;
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) g[e] = r * fmaf(-x[e], dot, g[e]);
+          if (in_row && at.on && h < heads) store_vec<T, VEC>(o0 + h * d, g);
+        }
       }
-      float s = 0.f;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) s = fmaf(x[e], x[e], s);
-      s = group_sum<G>(s);
-      const float r = rsqrtf(fmaf(s, inv_d, p.eps));
-      turn_vec<VEC>(g, cs + row.t * p.half, l, p.half, -1.f);
-      const float f = p.scale[row.which];
-      float w[VEC];
+      for (int m = G; m < 32; m <<= 1)  // the groups of a warp
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) w[e] = 1.f;
-      if (p.w[row.which] && on) load_vec<T, VEC>(static_cast<const T*>(p.w[row.which]) + l * VEC, w);
-      float dot = 0.f;
+        for (int e = 0; e < VEC; ++e) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], m);
+      if ((threadIdx.x & 31) < G && in_row)
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        g[e] *= f;
-        x[e] *= r;
-        const float c = g[e] * x[e];
-        if (row.which) dw[1][e] += c; else dw[0][e] += c;
-        g[e] *= w[e];
-        dot = fmaf(g[e], x[e], dot);
-      }
-      dot = group_sum<G>(dot) * inv_d;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) g[e] = r * fmaf(-x[e], dot, g[e]);
-      if (ok) store_vec<T, VEC>(static_cast<T*>(p.out[row.which]) + row.flat + l * VEC, g);
-    }
-  }
-#pragma unroll
-  for (int m = G; m < 32; m <<= 1)  // the groups of a warp
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      dw[0][e] += __shfl_xor_sync(0xffffffffu, dw[0][e], m);
-      dw[1][e] += __shfl_xor_sync(0xffffffffu, dw[1][e], m);
-    }
-  if ((threadIdx.x & 31) < G && on) {
-    float* o = sdw + (threadIdx.x >> 5) * 2 * d + l * VEC;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      o[e] = dw[0][e];
-      o[d + e] = dw[1][e];
+        for (int e = 0; e < VEC; ++e) my_dw[which * d + l * VEC + e] += dw[e];
     }
   }
   store_dw(p, sdw);
@@ -442,22 +504,23 @@ rope_bwd_row_kernel(const __grid_constant__ Params p) {
 }
 
 // dw of the queries' and keys' weights from the CTAs' sums, in fp64 and a fixed order.
+constexpr int kDwWarps = 32;
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(32 * kDwWarps)
 dw_kernel(const float* __restrict__ part, int n, int d, T* __restrict__ dwq, T* __restrict__ dwk) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ double sum[kWarps][32];
+  __shared__ double sum[kDwWarps][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
   double s = 0.0;
   if (i < 2 * d) {
 #pragma unroll 8
-    for (int c = w; c < n; c += kWarps) s += part[static_cast<int64_t>(c) * 2 * d + i];
+    for (int c = w; c < n; c += kDwWarps) s += part[static_cast<int64_t>(c) * 2 * d + i];
   }
   sum[w][lane] = s;
   __syncthreads();
   if (w == 0 && i < 2 * d) {
-    for (int x = 1; x < kWarps; ++x) s += sum[x][lane];
+    for (int x = 1; x < kDwWarps; ++x) s += sum[x][lane];
     T* o = i < d ? dwq : dwk;
     if (o) o[i < d ? i : i - d] = from_f32<T>(static_cast<float>(s));
   }
@@ -507,15 +570,18 @@ static size_t extent(const Args& a, const int64_t* s, int64_t heads, size_t es) 
   return ((size_t)((a.B - 1) * s[0] + (a.N - 1) * s[1] + (heads - 1) * s[2] + a.d)) * es;
 }
 
-static int bwd_grid(const Args& a, int tile, int sms) {
-  const int64_t tiles = (a.B * a.N + tile - 1) / tile;
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tiles, 4 * (int64_t)sms)));
+// Tokens of a tile, a power of two: at most eight, and fewer where that would leave an
+// SM less than six tiles.
+static int tile_of(const Args& a, int sms) {
+  int64_t t = 8;
+  while (t > 1 && a.B * a.N < t * 6 * sms) t /= 2;
+  return static_cast<int>(t);
 }
 
-// Tokens of a tile: eight where that still gives every SM four CTAs, else fewer.
-static int tile_of(const Args& a, int sms) {
-  const int64_t t = a.B * a.N / (4 * (int64_t)sms);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(t, kMaxTokens)));
+// CTAs of the backward: each leaves its sums of dw, so at most as many as run at once.
+static int bwd_grid(const Args& a, int tile, int sms) {
+  const int64_t tiles = (a.B * a.N + tile - 1) / tile;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tiles, 8 * (int64_t)sms)));
 }
 
 static Params params(const Args& a, int tile) {
@@ -546,16 +612,37 @@ static Params params(const Args& a, int tile) {
   return p;
 }
 
-// Whether rows can be taken in 16-byte pieces whose pair partners are whole pieces.
+// Whether rows can be taken in 16-byte pieces.
 static bool vec_ok(const Args& a, const void* const* more, int n) {
   const int64_t es = a.dt == LA2_BF16 ? 2 : 4, vec = 16 / es;
-  if (a.d % vec || (a.rot / 2) % vec || a.d / vec > 32) return false;
+  if (a.d % vec || a.d / vec > 32) return false;
   for (int i = 0; i < 3; ++i)
     if (a.qs[i] % vec || a.ks[i] % vec) return false;
   if (!is_aligned(a.q, 16) || !is_aligned(a.k, 16) || !is_aligned(a.wq, 16) || !is_aligned(a.wk, 16)) return false;
   for (int i = 0; i < n; ++i)
     if (!is_aligned(more[i], 16)) return false;
   return true;
+}
+
+using Kernel = void (*)(const Params);
+// Lanes a row (8, 16 or 32), and whether pairs are whole 16-byte pieces apart.
+template <typename T, bool BWD, int G, bool STAGE>
+static Kernel vec_kernel() {
+  if constexpr (BWD)
+    return rope_bwd_vec_kernel<T, 16 / sizeof(T), G, STAGE>;
+  else
+    return rope_fwd_vec_kernel<T, 16 / sizeof(T), G, STAGE>;
+}
+template <typename T, bool BWD, bool STAGE>
+static Kernel vec_kernel(int lanes) {
+  return lanes <= 8 ? vec_kernel<T, BWD, 8, STAGE>() : lanes <= 16 ? vec_kernel<T, BWD, 16, STAGE>()
+                                                                   : vec_kernel<T, BWD, 32, STAGE>();
+}
+template <typename T, bool BWD>
+static Kernel vec_kernel(const Args& a) {
+  constexpr int VEC = 16 / sizeof(T);
+  const int lanes = (int)a.d / VEC;
+  return (a.rot / 2) % VEC ? vec_kernel<T, BWD, true>(lanes) : vec_kernel<T, BWD, false>(lanes);
 }
 
 template <typename T>
@@ -566,13 +653,7 @@ static la2_status launch_fwd(const Args& a, Params p, bool vec, int sms, cudaStr
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(2 * sms / tiles, (rows + 15) / 16));
   const size_t smem = (size_t)p.tile * p.half * sizeof(float2);
   const dim3 grid((unsigned)tiles, (unsigned)p.splits), block(kThreads);
-  constexpr int VEC = 16 / sizeof(T);
-  void (*kern)(const Params);
-  if (vec)
-    kern = a.d / VEC <= 8 ? rope_fwd_vec_kernel<T, VEC, 8>
-                          : (a.d / VEC <= 16 ? rope_fwd_vec_kernel<T, VEC, 16> : rope_fwd_vec_kernel<T, VEC, 32>);
-  else
-    kern = a.d <= 128 ? rope_fwd_row_kernel<T, 2> : rope_fwd_row_kernel<T, 4>;
+  const Kernel kern = vec ? vec_kernel<T, false>(a) : a.d <= 128 ? rope_fwd_row_kernel<T, 2> : rope_fwd_row_kernel<T, 4>;
   LaunchTimer t(K_QK_ROPE, st);
   if (launch_pdl(kern, grid, block, smem, st, p) != cudaSuccess) return LA2_ERR_CUDA;
   return launch_status();
@@ -582,18 +663,12 @@ template <typename T>
 static la2_status launch_bwd(const Args& a, const Params& p, bool vec, int grid, void* dwq, void* dwk,
                              cudaStream_t st) {
   const size_t smem = (size_t)p.tile * p.half * sizeof(float2) + (size_t)kWarps * 2 * p.d * sizeof(float);
-  constexpr int VEC = 16 / sizeof(T);
-  void (*kern)(const Params);
-  if (vec)
-    kern = a.d / VEC <= 8 ? rope_bwd_vec_kernel<T, VEC, 8>
-                          : (a.d / VEC <= 16 ? rope_bwd_vec_kernel<T, VEC, 16> : rope_bwd_vec_kernel<T, VEC, 32>);
-  else
-    kern = a.d <= 128 ? rope_bwd_row_kernel<T, 2> : rope_bwd_row_kernel<T, 4>;
+  const Kernel kern = vec ? vec_kernel<T, true>(a) : a.d <= 128 ? rope_bwd_row_kernel<T, 2> : rope_bwd_row_kernel<T, 4>;
   {
     LaunchTimer t(K_QK_ROPE_BWD, st);
     if (launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, p) != cudaSuccess) return LA2_ERR_CUDA;
     if (dwq || dwk)
-      if (launch_pdl(dw_kernel<T>, dim3((2 * p.d + 31) / 32), dim3(kThreads), 0, st,
+      if (launch_pdl(dw_kernel<T>, dim3((2 * p.d + 31) / 32), dim3(32 * kDwWarps), 0, st,
                      static_cast<const float*>(p.dw_part), grid, p.d, static_cast<T*>(dwq),
                      static_cast<T*>(dwk)) != cudaSuccess)
         return LA2_ERR_CUDA;
