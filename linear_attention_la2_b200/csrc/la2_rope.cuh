@@ -21,9 +21,10 @@
 // A CTA takes a tile of consecutive tokens and their heads. The angles are computed
 // once a token, into shared memory: the turns in fp64 (at position 2^20 an fp32 product
 // is 0.06 rad off), and only their fraction goes on to fp32. A group of lanes, 16 bytes
-// of a row each, keeps one token's cosines and sines in registers and walks the heads,
-// several rows in flight; its neighbours hold the next tokens, so that the tile's rows
-// of a head leave as one piece of the output.
+// of a row each, keeps one token's cosines and sines in registers and walks the heads;
+// its neighbours hold the next tokens, so that the tile's rows of a head leave as one
+// piece of the output. Rows arrive by asynchronous copies into places of the loading
+// thread's own, kDepth rows ahead: in registers as many would halve the warps.
 #pragma once
 
 namespace la2 {
@@ -193,59 +194,72 @@ __device__ __forceinline__ Place place_of(const Params& p, int64_t tok0) {
   return x;
 }
 
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+constexpr int kDepth = 8;   // 16-byte pieces a thread has in flight (backwards: half as many rows)
+
 template <typename T, int VEC, int G, bool STAGE>
 __global__ void __launch_bounds__(kThreads)
 rope_fwd_vec_kernel(const __grid_constant__ Params p) {
-  extern __shared__ float2 cs[];
+  extern __shared__ uint4 ring_all[];  // [kDepth][kThreads]
+  float2* cs = reinterpret_cast<float2*>(ring_all + kDepth * kThreads);
   __shared__ float stage_all[STAGE ? kThreads / G * stage_floats(VEC, G) : 1];
   pdl_launch_dependents();
   pdl_wait();
   const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tile;
   fill_angles(p, tok0, static_cast<int>(imin64(p.tile, p.tokens - tok0)), cs);
-  __syncthreads();
   const Place at = place_of<G>(p, tok0);
   const int l = threadIdx.x % G, d = p.d;
   const bool in_row = l * VEC < d;
   const float inv_d = 1.f / static_cast<float>(d);
   float* stage = stage_all + (STAGE ? threadIdx.x / G * stage_floats(VEC, G) : 0);
+  // rows k of the thread: its share of the queries' heads, then of the keys'
+  const int nq = (p.heads[0] + at.slots - 1) / at.slots, total = nq + (p.heads[1] + at.slots - 1) / at.slots;
+  const bool live = in_row && at.on;
+  const uint32_t ring = sm100::smem_u32(ring_all + threadIdx.x);
+  auto fetch = [&](int k) {
+    if (k < total) {
+      const int which = k >= nq, h = at.slot + (which ? k - nq : k) * at.slots;
+      const T* x = static_cast<const T*>(p.x[which]);
+      const bool on = live && h < p.heads[which];
+      if (on) x += at.b * p.sb[which] + at.n * p.sn[which] + h * p.sh[which] + l * VEC;
+      copy_async16(ring + k % kDepth * (kThreads * 16), x, on);
+    }
+    copy_commit();
+  };
+#pragma unroll 1
+  for (int k = 0; k < kDepth - 1; ++k) fetch(k);
+  __syncthreads();  // the angles
   Turn<VEC> turn;
   load_turn(turn, cs + (at.on ? at.t : 0) * p.half, l * VEC, p.half, 1.f);
-  constexpr int U = 4;  // rows in flight
+  float w[VEC];
 #pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    const int heads = p.heads[which];
-    if (heads == 0) continue;
-    const T* x0 = static_cast<const T*>(p.x[which]) + at.b * p.sb[which] + at.n * p.sn[which] + l * VEC;
-    T* o0 = static_cast<T*>(p.out[which]) + (at.b * heads * p.N + at.n) * d + l * VEC;
-    float w[VEC];
-    load_weight<T, VEC>(p.w[which], l * VEC, in_row, w);
+  for (int k = 0; k < total; ++k) {  // (the same for all lanes of a warp)
+    const int which = k >= nq, h = at.slot + (which ? k - nq : k) * at.slots, heads = p.heads[which];
+    if (k == 0 || k == nq) {
+      load_weight<T, VEC>(p.w[which], l * VEC, in_row, w);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) w[e] *= p.scale[which];
-#pragma unroll 1
-    for (int h0 = 0; h0 < heads; h0 += at.slots * U) {  // (the same for all lanes of a warp)
-      uint4 raw[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + at.slot + u * at.slots;
-        raw[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (in_row && at.on && h < heads) raw[u] = *reinterpret_cast<const uint4*>(x0 + h * p.sh[which]);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int h = h0 + at.slot + u * at.slots;
-        if (h0 + u * at.slots >= heads) break;  // (uniform)
-        float x[VEC];
-        widen(raw[u], x);
-        float s = 0.f;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) s = fmaf(x[e], x[e], s);
-        const float r = rsqrtf(fmaf(group_sum<G>(s), inv_d, p.eps));
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) x[e] = x[e] * r * w[e];
-        turn_row<VEC, STAGE>(x, turn, l, p.half, stage);
-        if (in_row && at.on && h < heads) store_vec<T, VEC>(o0 + h * p.N * d, x);
-      }
+      for (int e = 0; e < VEC; ++e) w[e] *= p.scale[which];
     }
+    fetch(k + kDepth - 1);
+    copy_wait<kDepth - 1>();
+    float x[VEC];
+    widen(ring_all[k % kDepth * kThreads + threadIdx.x], x);
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) s = fmaf(x[e], x[e], s);
+    const float r = rsqrtf(fmaf(group_sum<G>(s), inv_d, p.eps));
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) x[e] = x[e] * r * w[e];
+    turn_row<VEC, STAGE>(x, turn, l, p.half, stage);
+    if (live && h < heads)
+      store_vec<T, VEC>(static_cast<T*>(p.out[which]) + ((at.b * heads + h) * p.N + at.n) * d + l * VEC, x);
   }
 }
 
@@ -261,9 +275,11 @@ __device__ __forceinline__ void store_dw(const Params& p, const float* smem_dw) 
 }
 
 template <typename T, int VEC, int G, bool STAGE>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 rope_bwd_vec_kernel(const __grid_constant__ Params p) {
-  extern __shared__ float2 cs[];
+  constexpr int D = kDepth / 2;  // rows in flight, two reads each
+  extern __shared__ uint4 ring_all[];  // [D][2][kThreads]
+  float2* cs = reinterpret_cast<float2*>(ring_all + 2 * D * kThreads);
   float* sdw = reinterpret_cast<float*>(cs + p.tile * p.half);  // [kWarps][2][d]
   __shared__ float stage_all[STAGE ? kThreads / G * stage_floats(VEC, G) : 1];
   pdl_launch_dependents();
@@ -273,67 +289,37 @@ rope_bwd_vec_kernel(const __grid_constant__ Params p) {
   const float inv_d = 1.f / static_cast<float>(d);
   float* stage = stage_all + (STAGE ? threadIdx.x / G * stage_floats(VEC, G) : 0);
   float* my_dw = sdw + (threadIdx.x >> 5) * 2 * d;
+  const uint32_t ring = sm100::smem_u32(ring_all + threadIdx.x);
   for (int i = threadIdx.x & 31; i < 2 * d; i += 32) my_dw[i] = 0.f;
   for (int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tile; tok0 < p.tokens;
        tok0 += static_cast<int64_t>(gridDim.x) * p.tile) {
-    __syncthreads();
+    const Place at = place_of<G>(p, tok0);
+    const int nq = (p.heads[0] + at.slots - 1) / at.slots, total = nq + (p.heads[1] + at.slots - 1) / at.slots;
+    const bool live = in_row && at.on;
+    auto fetch = [&](int k) {
+      if (k < total) {
+        const int which = k >= nq, h = at.slot + (which ? k - nq : k) * at.slots, heads = p.heads[which];
+        const T *x = static_cast<const T*>(p.x[which]), *g = static_cast<const T*>(p.dy[which]);
+        const bool on = live && h < heads;
+        if (on) {
+          x += at.b * p.sb[which] + at.n * p.sn[which] + h * p.sh[which] + l * VEC;
+          g += ((at.b * heads + h) * p.N + at.n) * d + l * VEC;
+        }
+        const uint32_t dst = ring + k % D * (2 * kThreads * 16);
+        copy_async16(dst, x, on);
+        copy_async16(dst + kThreads * 16, g, on);
+      }
+      copy_commit();
+    };
+#pragma unroll 1
+    for (int k = 0; k < D - 1; ++k) fetch(k);
+    __syncthreads();  // the last tile's angles are done with
     fill_angles(p, tok0, static_cast<int>(imin64(p.tile, p.tokens - tok0)), cs);
     __syncthreads();
-    const Place at = place_of<G>(p, tok0);
     Turn<VEC> turn;
     load_turn(turn, cs + (at.on ? at.t : 0) * p.half, l * VEC, p.half, -1.f);
-    constexpr int U = 2;  // rows in flight, two reads each
-#pragma unroll 1
-    for (int which = 0; which < 2; ++which) {
-      const int heads = p.heads[which];
-      if (heads == 0) continue;
-      const T* x0 = static_cast<const T*>(p.x[which]) + at.b * p.sb[which] + at.n * p.sn[which] + l * VEC;
-      const T* g0 = static_cast<const T*>(p.dy[which]) + (at.b * heads * p.N + at.n) * d + l * VEC;
-      T* o0 = static_cast<T*>(p.out[which]) + at.tok * heads * d + l * VEC;
-      float w[VEC], dw[VEC];
-      load_weight<T, VEC>(p.w[which], l * VEC, in_row, w);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) dw[e] = 0.f;
-      const float scale = p.scale[which];
-#pragma unroll 1
-      for (int h0 = 0; h0 < heads; h0 += at.slots * U) {
-        uint4 xr[U], gr[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int h = h0 + at.slot + u * at.slots;
-          xr[u] = gr[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (in_row && at.on && h < heads) {
-            xr[u] = *reinterpret_cast<const uint4*>(x0 + h * p.sh[which]);
-            gr[u] = *reinterpret_cast<const uint4*>(g0 + h * p.N * d);
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int h = h0 + at.slot + u * at.slots;
-          if (h0 + u * at.slots >= heads) break;  // (uniform)
-          float x[VEC], g[VEC];
-          widen(xr[u], x);
-          widen(gr[u], g);
-          float s = 0.f;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) s = fmaf(x[e], x[e], s);
-          const float r = rsqrtf(fmaf(group_sum<G>(s), inv_d, p.eps));
-          turn_row<VEC, STAGE>(g, turn, l, p.half, stage);
-          float dot = 0.f;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            g[e] *= scale;
-            x[e] *= r;
-            dw[e] = fmaf(g[e], x[e], dw[e]);
-            g[e] *= w[e];
-            dot = fmaf(g[e], x[e], dot);
-          }
-          dot = group_sum<G>(dot) * inv_d;
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) g[e] = r * fmaf(-x[e], dot, g[e]);
-          if (in_row && at.on && h < heads) store_vec<T, VEC>(o0 + h * d, g);
-        }
-      }
+    float w[VEC], dw[VEC];
+    auto add_dw = [&](int which) {
 #pragma unroll
       for (int m = G; m < 32; m <<= 1)  // the groups of a warp
 #pragma unroll
@@ -341,7 +327,41 @@ rope_bwd_vec_kernel(const __grid_constant__ Params p) {
       if ((threadIdx.x & 31) < G && in_row)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) my_dw[which * d + l * VEC + e] += dw[e];
+    };
+#pragma unroll 1
+    for (int k = 0; k < total; ++k) {  // (the same for all lanes of a warp)
+      const int which = k >= nq, h = at.slot + (which ? k - nq : k) * at.slots, heads = p.heads[which];
+      if (k == 0 || k == nq) {
+        if (k > 0) add_dw(0);
+        load_weight<T, VEC>(p.w[which], l * VEC, in_row, w);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) dw[e] = 0.f;
+      }
+      fetch(k + D - 1);
+      copy_wait<D - 1>();
+      float x[VEC], g[VEC];
+      widen(ring_all[k % D * 2 * kThreads + threadIdx.x], x);
+      widen(ring_all[(k % D * 2 + 1) * kThreads + threadIdx.x], g);
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) s = fmaf(x[e], x[e], s);
+      const float r = rsqrtf(fmaf(group_sum<G>(s), inv_d, p.eps));
+      turn_row<VEC, STAGE>(g, turn, l, p.half, stage);
+      float dot = 0.f;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        g[e] *= p.scale[which];
+        x[e] *= r;
+        dw[e] = fmaf(g[e], x[e], dw[e]);
+        g[e] *= w[e];
+        dot = fmaf(g[e], x[e], dot);
+      }
+      dot = group_sum<G>(dot) * inv_d;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) g[e] = r * fmaf(-x[e], dot, g[e]);
+      if (live && h < heads) store_vec<T, VEC>(static_cast<T*>(p.out[which]) + (at.tok * heads + h) * d + l * VEC, g);
     }
+    if (total > 0) add_dw(total > nq ? 1 : 0);
   }
   store_dw(p, sdw);
 }
@@ -645,15 +665,22 @@ static Kernel vec_kernel(const Args& a) {
   return (a.rot / 2) % VEC ? vec_kernel<T, BWD, true>(lanes) : vec_kernel<T, BWD, false>(lanes);
 }
 
+// Dynamic shared memory beyond the default limit (wide rows, with their static part).
+static bool allow_smem(Kernel kern, size_t bytes) {
+  return bytes <= 36 * 1024 ||
+         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+}
+
 template <typename T>
 static la2_status launch_fwd(const Args& a, Params p, bool vec, int sms, cudaStream_t st) {
   const int64_t tiles = (p.tokens + p.tile - 1) / p.tile;
   // few tokens (a decode batch): their heads over several CTAs
   const int64_t rows = (int64_t)p.tile * (a.H + a.Hkv);
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(2 * sms / tiles, (rows + 15) / 16));
-  const size_t smem = (size_t)p.tile * p.half * sizeof(float2);
+  const size_t smem = (size_t)p.tile * p.half * sizeof(float2) + (vec ? kDepth * kThreads * 16 : 0);
   const dim3 grid((unsigned)tiles, (unsigned)p.splits), block(kThreads);
   const Kernel kern = vec ? vec_kernel<T, false>(a) : a.d <= 128 ? rope_fwd_row_kernel<T, 2> : rope_fwd_row_kernel<T, 4>;
+  if (!allow_smem(kern, smem)) return LA2_ERR_CUDA;
   LaunchTimer t(K_QK_ROPE, st);
   if (launch_pdl(kern, grid, block, smem, st, p) != cudaSuccess) return LA2_ERR_CUDA;
   return launch_status();
@@ -662,8 +689,10 @@ static la2_status launch_fwd(const Args& a, Params p, bool vec, int sms, cudaStr
 template <typename T>
 static la2_status launch_bwd(const Args& a, const Params& p, bool vec, int grid, void* dwq, void* dwk,
                              cudaStream_t st) {
-  const size_t smem = (size_t)p.tile * p.half * sizeof(float2) + (size_t)kWarps * 2 * p.d * sizeof(float);
+  const size_t smem = (size_t)p.tile * p.half * sizeof(float2) + (size_t)kWarps * 2 * p.d * sizeof(float) +
+                      (vec ? kDepth * kThreads * 16 : 0);
   const Kernel kern = vec ? vec_kernel<T, true>(a) : a.d <= 128 ? rope_bwd_row_kernel<T, 2> : rope_bwd_row_kernel<T, 4>;
+  if (!allow_smem(kern, smem)) return LA2_ERR_CUDA;
   {
     LaunchTimer t(K_QK_ROPE_BWD, st);
     if (launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, p) != cudaSuccess) return LA2_ERR_CUDA;
