@@ -94,82 +94,129 @@ __device__ __forceinline__ float group_sum(float x) {
   return x;
 }
 
+// A lane's 16 bytes of a row as packed pairs of fp32 (8 bf16 or 4 fp32 values): the
+// rows' arithmetic is two values an instruction, and the shuffles and reads below move
+// the row's raw words. One value an instruction made both passes issue-bound (46 and
+// 67 us at B4 N2K, 32 heads, against 21 and 31 us of traffic).
+using gated::f2;
+using gated::fma2;
+using gated::mul2;
+using gated::unpack;
 template <int VEC>
-__device__ __forceinline__ void widen(const uint4& u, float (&x)[VEC]) {
+__device__ __forceinline__ void widen(const uint4& u, uint64_t (&x)[VEC / 2]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (VEC == 8) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    } else {
-      x[i] = __uint_as_float(w[i]);
-    }
+  for (int i = 0; i < VEC / 2; ++i) {
+    if constexpr (VEC == 8)
+      x[i] = f2(w[i] << 16, w[i] & 0xffff0000u);
+    else
+      x[i] = f2(w[2 * i], w[2 * i + 1]);
   }
 }
-template <typename T, int VEC>
-__device__ __forceinline__ void store_vec(T* p, const float (&x)[VEC]) {
+template <int VEC>
+__device__ __forceinline__ uint4 narrow(const uint64_t (&x)[VEC / 2]) {
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (VEC == 8) {
-      const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&v);
-    } else {
-      w[i] = __float_as_uint(x[i]);
-    }
+  for (int i = 0; i < VEC / 2; ++i) {
+    if constexpr (VEC == 8)
+      w[i] = gated::pack2(x[i]);
+    else
+      unpack(x[i], w[2 * i], w[2 * i + 1]);
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
-template <typename T, int VEC>
-__device__ __forceinline__ void load_weight(const void* w, int at, bool on, float (&x)[VEC]) {
+template <int N>
+__device__ __forceinline__ float sum_products(const uint64_t (&x)[N], const uint64_t (&y)[N]) {
+  uint64_t s = mul2(x[0], y[0]);
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) x[e] = 1.f;
-  if (w && on) widen(*reinterpret_cast<const uint4*>(static_cast<const T*>(w) + at), x);
+  for (int i = 1; i < N; ++i) s = fma2(x[i], y[i], s);
+  float a, b;
+  unpack(s, a, b);
+  return a + b;
+}
+template <typename T>
+__device__ __forceinline__ float weight_at(const void* w, int i) {
+  return w ? to_f32(static_cast<const T*>(w)[i]) : 1.f;
 }
 
-// What a lane needs to turn its VEC values of a row: value e becomes
-// x c[e] + (its pair's other value) s[e]; c = 1, s = 0 behind the rotated ones.
-template <int VEC>
-struct Turn {
-  float c[VEC], s[VEC];
-};
-// sign 1 turns forwards, -1 back.
-template <int VEC>
-__device__ __forceinline__ void load_turn(Turn<VEC>& t, const float2* cs, int first, int half, float sign) {
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    const int i = first + e;
-    const float2 a = i < 2 * half ? cs[i < half ? i : i - half] : make_float2(1.f, 0.f);
-    t.c[e] = a.x;
-    t.s[e] = i < half ? -sign * a.y : sign * a.y;
-  }
-}
-// x <- turned x. STAGE false: half is a multiple of VEC, and the other value of a pair
-// sits at the same place half / VEC lanes away. STAGE true: the group's row goes through
-// shared memory (a row of G lanes, 9 words for every 8 so that lanes meet no conflicts).
+// The other value of each of a lane's pairs. STAGE false: half is a multiple of VEC, and
+// it sits at the same place half / VEC lanes away. STAGE true: the group's row goes
+// through shared memory (9 words for every 8, so that lanes meet no conflicts).
 template <int VEC, bool STAGE>
-__device__ __forceinline__ void turn_row(float (&x)[VEC], const Turn<VEC>& t, int l, int half, float* stage) {
+__device__ __forceinline__ void others(const uint4& raw, const uint64_t (&x)[VEC / 2], uint64_t (&o)[VEC / 2], int l,
+                                       int half, float* stage) {
   if constexpr (!STAGE) {
     const int hl = half / VEC, lane = threadIdx.x & 31;
     const int src = l < hl ? lane + hl : (l < 2 * hl ? lane - hl : lane);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) x[e] = fmaf(x[e], t.c[e], __shfl_sync(0xffffffffu, x[e], src) * t.s[e]);
+    uint4 r;
+    r.x = __shfl_sync(0xffffffffu, raw.x, src);
+    r.y = __shfl_sync(0xffffffffu, raw.y, src);
+    r.z = __shfl_sync(0xffffffffu, raw.z, src);
+    r.w = __shfl_sync(0xffffffffu, raw.w, src);
+    widen<VEC>(r, o);
   } else {
     auto at = [](int i) { return i + (i >> 3); };
     __syncwarp();
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) stage[at(VEC * l + e)] = x[e];
+    for (int e = 0; e < VEC / 2; ++e)
+      unpack(x[e], stage[at(VEC * l + 2 * e)], stage[at(VEC * l + 2 * e + 1)]);
     __syncwarp();
+    auto other = [&](int i) { return stage[at(i < half ? i + half : (i < 2 * half ? i - half : i))]; };
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int i = VEC * l + e, j = i < half ? i + half : (i < 2 * half ? i - half : i);
-      x[e] = fmaf(x[e], t.c[e], stage[at(j)] * t.s[e]);
-    }
+    for (int e = 0; e < VEC / 2; ++e) o[e] = f2(other(VEC * l + 2 * e), other(VEC * l + 2 * e + 1));
   }
 }
 // Floats of a group's staging row.
 __host__ __device__ constexpr int stage_floats(int vec, int g) { return vec * g + vec * g / 8; }
+
+// A lane's piece of a weight (ones without one, or behind the row).
+template <typename T, int VEC>
+__device__ __forceinline__ void load_weight(const void* w, int first, int d, uint64_t (&x)[VEC / 2]) {
+  if (w && first < d)
+    widen<VEC>(*reinterpret_cast<const uint4*>(static_cast<const T*>(w) + first), x);
+  else
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) x[e] = f2(1.f, 1.f);
+}
+
+// Coefficients of a lane's turned values: own[e] times the value plus other[e] times its
+// pair's other one. `turn` is one token's cosines and sines, sign -1 turns back, f scales;
+// with a weight, which comes before the turn, each value's own.
+template <typename T, int VEC, bool STAGE>
+__device__ __forceinline__ void coefficients(uint64_t (&own)[VEC / 2], uint64_t (&other)[VEC / 2], const float2* turn,
+                                             int first, int half, int d, float sign, float f, const void* weight) {
+  if constexpr (!STAGE) {  // pieces lie on one side of half, and so do their pairs' others
+    const bool lo = first < half, on = first < 2 * half;
+    const int j = lo ? first : first - half;
+    const float so = lo ? -sign * f : sign * f;
+    uint64_t w[VEC / 2], wo[VEC / 2];
+    load_weight<T, VEC>(weight, first, d, w);
+    load_weight<T, VEC>(weight, on ? (lo ? first + half : j) : d, d, wo);
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) {
+      const float4 a = on ? *reinterpret_cast<const float4*>(turn + j + 2 * e) : make_float4(1.f, 0.f, 1.f, 0.f);
+      own[e] = mul2(w[e], f2(f * a.x, f * a.z));
+      other[e] = mul2(wo[e], f2(so * a.y, so * a.w));
+    }
+  } else {
+    float c[VEC], s[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const int i = first + e;
+      c[e] = s[e] = 0.f;
+      if (i >= d) continue;
+      const int j = i < half ? i + half : i - half;
+      const float2 a = i < 2 * half ? turn[i < half ? i : j] : make_float2(1.f, 0.f);
+      c[e] = f * weight_at<T>(weight, i) * a.x;
+      if (i < 2 * half) s[e] = (i < half ? -sign : sign) * f * weight_at<T>(weight, j) * a.y;
+    }
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) {
+      own[e] = f2(c[2 * e], c[2 * e + 1]);
+      other[e] = f2(s[2 * e], s[2 * e + 1]);
+    }
+  }
+}
 
 // The token and first head of a thread's group: groups run over the tile's tokens,
 // then over its share of the heads (`slots` heads at a time).
@@ -194,8 +241,8 @@ __device__ __forceinline__ Place place_of(const Params& p, int64_t tok0) {
   return x;
 }
 
-__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -205,7 +252,7 @@ __device__ __forceinline__ void copy_wait() {
 constexpr int kDepth = 8;   // 16-byte pieces a thread has in flight (backwards: half as many rows)
 
 template <typename T, int VEC, int G, bool STAGE>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 rope_fwd_vec_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint4 ring_all[];  // [kDepth][kThreads]
   float2* cs = reinterpret_cast<float2*>(ring_all + kDepth * kThreads);
@@ -213,53 +260,64 @@ rope_fwd_vec_kernel(const __grid_constant__ Params p) {
   pdl_launch_dependents();
   pdl_wait();
   const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tile;
-  fill_angles(p, tok0, static_cast<int>(imin64(p.tile, p.tokens - tok0)), cs);
   const Place at = place_of<G>(p, tok0);
-  const int l = threadIdx.x % G, d = p.d;
-  const bool in_row = l * VEC < d;
-  const float inv_d = 1.f / static_cast<float>(d);
+  const int l = threadIdx.x % G, d = p.d, half = p.half;
+  const float inv_d = 1.f / static_cast<float>(d), eps = p.eps;
   float* stage = stage_all + (STAGE ? threadIdx.x / G * stage_floats(VEC, G) : 0);
   // rows k of the thread: its share of the queries' heads, then of the keys'
   const int nq = (p.heads[0] + at.slots - 1) / at.slots, total = nq + (p.heads[1] + at.slots - 1) / at.slots;
-  const bool live = in_row && at.on;
-  const uint32_t ring = sm100::smem_u32(ring_all + threadIdx.x);
-  auto fetch = [&](int k) {
-    if (k < total) {
-      const int which = k >= nq, h = at.slot + (which ? k - nq : k) * at.slots;
-      const T* x = static_cast<const T*>(p.x[which]);
-      const bool on = live && h < p.heads[which];
-      if (on) x += at.b * p.sb[which] + at.n * p.sn[which] + h * p.sh[which] + l * VEC;
-      copy_async16(ring + k % kDepth * (kThreads * 16), x, on);
+  const bool live = l * VEC < d && at.on;
+  uint4* ring = ring_all + threadIdx.x;
+  // what is fetched next: the row's place, its head, and the step to the next
+  const T* src = nullptr;
+  int64_t src_step = 0;
+  int fetch_k = 0, fetch_h = 0, fetch_heads = 0;
+  auto fetch = [&]() {
+    if (fetch_k == 0 || fetch_k == nq) {
+      const int which = fetch_k >= nq;
+      src = static_cast<const T*>(p.x[which]) + at.b * p.sb[which] + at.n * p.sn[which] + at.slot * p.sh[which] + l * VEC;
+      src_step = at.slots * p.sh[which];
+      fetch_h = at.slot;
+      fetch_heads = live ? p.heads[which] : 0;
     }
+    if (fetch_h < fetch_heads) copy_async16(sm100::smem_u32(ring + fetch_k % kDepth * kThreads), src);
     copy_commit();
+    src += src_step;
+    fetch_h += at.slots;
+    ++fetch_k;
   };
 #pragma unroll 1
-  for (int k = 0; k < kDepth - 1; ++k) fetch(k);
-  __syncthreads();  // the angles
-  Turn<VEC> turn;
-  load_turn(turn, cs + (at.on ? at.t : 0) * p.half, l * VEC, p.half, 1.f);
-  float w[VEC];
+  for (int k = 0; k < kDepth - 1; ++k) fetch();
+  fill_angles(p, tok0, static_cast<int>(imin64(p.tile, p.tokens - tok0)), cs);
+  __syncthreads();
+  uint64_t own[VEC / 2], other[VEC / 2];
+  T* dst = nullptr;
+  int64_t dst_step = 0;
+  int h = 0, heads = 0;
 #pragma unroll 1
   for (int k = 0; k < total; ++k) {  // (the same for all lanes of a warp)
-    const int which = k >= nq, h = at.slot + (which ? k - nq : k) * at.slots, heads = p.heads[which];
     if (k == 0 || k == nq) {
-      load_weight<T, VEC>(p.w[which], l * VEC, in_row, w);
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) w[e] *= p.scale[which];
+      const int which = k >= nq;
+      coefficients<T, VEC, STAGE>(own, other, cs + (at.on ? at.t : 0) * half, l * VEC, half, d, 1.f, p.scale[which], p.w[which]);
+      dst = static_cast<T*>(p.out[which]) + ((at.b * p.heads[which] + at.slot) * p.N + at.n) * d + l * VEC;
+      dst_step = at.slots * p.N * d;
+      h = at.slot;
+      heads = live ? p.heads[which] : 0;
     }
-    fetch(k + kDepth - 1);
+    fetch();
     copy_wait<kDepth - 1>();
-    float x[VEC];
-    widen(ring_all[k % kDepth * kThreads + threadIdx.x], x);
-    float s = 0.f;
+    const bool on = h < heads;
+    const uint4 raw = on ? ring[k % kDepth * kThreads] : make_uint4(0u, 0u, 0u, 0u);
+    uint64_t x[VEC / 2], o[VEC / 2];
+    widen<VEC>(raw, x);
+    others<VEC, STAGE>(raw, x, o, l, half, stage);
+    const float r = rsqrtf(fmaf(group_sum<G>(sum_products(x, x)), inv_d, eps));
+    const uint64_t rr = f2(r, r);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) s = fmaf(x[e], x[e], s);
-    const float r = rsqrtf(fmaf(group_sum<G>(s), inv_d, p.eps));
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) x[e] = x[e] * r * w[e];
-    turn_row<VEC, STAGE>(x, turn, l, p.half, stage);
-    if (live && h < heads)
-      store_vec<T, VEC>(static_cast<T*>(p.out[which]) + ((at.b * heads + h) * p.N + at.n) * d + l * VEC, x);
+    for (int e = 0; e < VEC / 2; ++e) x[e] = mul2(fma2(o[e], other[e], mul2(x[e], own[e])), rr);
+    if (on) *reinterpret_cast<uint4*>(dst) = narrow<VEC>(x);
+    dst += dst_step;
+    h += at.slots;
   }
 }
 
@@ -284,82 +342,107 @@ rope_bwd_vec_kernel(const __grid_constant__ Params p) {
   __shared__ float stage_all[STAGE ? kThreads / G * stage_floats(VEC, G) : 1];
   pdl_launch_dependents();
   pdl_wait();
-  const int l = threadIdx.x % G, d = p.d;
+  const int l = threadIdx.x % G, d = p.d, half = p.half;
   const bool in_row = l * VEC < d;
-  const float inv_d = 1.f / static_cast<float>(d);
+  const float inv_d = 1.f / static_cast<float>(d), eps = p.eps;
   float* stage = stage_all + (STAGE ? threadIdx.x / G * stage_floats(VEC, G) : 0);
   float* my_dw = sdw + (threadIdx.x >> 5) * 2 * d;
-  const uint32_t ring = sm100::smem_u32(ring_all + threadIdx.x);
+  uint4* ring = ring_all + threadIdx.x;
   for (int i = threadIdx.x & 31; i < 2 * d; i += 32) my_dw[i] = 0.f;
   for (int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tile; tok0 < p.tokens;
        tok0 += static_cast<int64_t>(gridDim.x) * p.tile) {
     const Place at = place_of<G>(p, tok0);
     const int nq = (p.heads[0] + at.slots - 1) / at.slots, total = nq + (p.heads[1] + at.slots - 1) / at.slots;
     const bool live = in_row && at.on;
-    auto fetch = [&](int k) {
-      if (k < total) {
-        const int which = k >= nq, h = at.slot + (which ? k - nq : k) * at.slots, heads = p.heads[which];
-        const T *x = static_cast<const T*>(p.x[which]), *g = static_cast<const T*>(p.dy[which]);
-        const bool on = live && h < heads;
-        if (on) {
-          x += at.b * p.sb[which] + at.n * p.sn[which] + h * p.sh[which] + l * VEC;
-          g += ((at.b * heads + h) * p.N + at.n) * d + l * VEC;
-        }
-        const uint32_t dst = ring + k % D * (2 * kThreads * 16);
-        copy_async16(dst, x, on);
-        copy_async16(dst + kThreads * 16, g, on);
+    const T *xs = nullptr, *gs = nullptr;  // fetched next
+    int64_t x_step = 0, g_step = 0;
+    int fetch_k = 0, fetch_h = 0, fetch_heads = 0;
+    auto fetch = [&]() {
+      if (fetch_k == 0 || fetch_k == nq) {
+        const int which = fetch_k >= nq;
+        xs = static_cast<const T*>(p.x[which]) + at.b * p.sb[which] + at.n * p.sn[which] + at.slot * p.sh[which] + l * VEC;
+        gs = static_cast<const T*>(p.dy[which]) + ((at.b * p.heads[which] + at.slot) * p.N + at.n) * d + l * VEC;
+        x_step = at.slots * p.sh[which];
+        g_step = at.slots * p.N * d;
+        fetch_h = at.slot;
+        fetch_heads = live ? p.heads[which] : 0;
+      }
+      if (fetch_h < fetch_heads) {
+        const uint32_t to = sm100::smem_u32(ring + fetch_k % D * (2 * kThreads));
+        copy_async16(to, xs);
+        copy_async16(to + kThreads * 16, gs);
       }
       copy_commit();
+      xs += x_step;
+      gs += g_step;
+      fetch_h += at.slots;
+      ++fetch_k;
     };
 #pragma unroll 1
-    for (int k = 0; k < D - 1; ++k) fetch(k);
+    for (int k = 0; k < D - 1; ++k) fetch();
     __syncthreads();  // the last tile's angles are done with
     fill_angles(p, tok0, static_cast<int>(imin64(p.tile, p.tokens - tok0)), cs);
     __syncthreads();
-    Turn<VEC> turn;
-    load_turn(turn, cs + (at.on ? at.t : 0) * p.half, l * VEC, p.half, -1.f);
-    float w[VEC], dw[VEC];
+    uint64_t own[VEC / 2], other[VEC / 2], w[VEC / 2], dw[VEC / 2];
+    T* dst = nullptr;
+    int64_t dst_step = 0;
+    int h = 0, heads = 0;
     auto add_dw = [&](int which) {
 #pragma unroll
-      for (int m = G; m < 32; m <<= 1)  // the groups of a warp
+      for (int e = 0; e < VEC / 2; ++e) {
+        float a, b;
+        unpack(dw[e], a, b);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], m);
-      if ((threadIdx.x & 31) < G && in_row)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) my_dw[which * d + l * VEC + e] += dw[e];
+        for (int m = G; m < 32; m <<= 1) {  // the groups of a warp
+          a += __shfl_xor_sync(0xffffffffu, a, m);
+          b += __shfl_xor_sync(0xffffffffu, b, m);
+        }
+        if ((threadIdx.x & 31) < G && in_row) {
+          my_dw[which * d + l * VEC + 2 * e] += a;
+          my_dw[which * d + l * VEC + 2 * e + 1] += b;
+        }
+      }
     };
 #pragma unroll 1
     for (int k = 0; k < total; ++k) {  // (the same for all lanes of a warp)
-      const int which = k >= nq, h = at.slot + (which ? k - nq : k) * at.slots, heads = p.heads[which];
       if (k == 0 || k == nq) {
         if (k > 0) add_dw(0);
-        load_weight<T, VEC>(p.w[which], l * VEC, in_row, w);
+        const int which = k >= nq;
+        coefficients<T, VEC, STAGE>(own, other, cs + (at.on ? at.t : 0) * half, l * VEC, half, d, -1.f, p.scale[which], nullptr);
+        load_weight<T, VEC>(p.w[which], l * VEC, d, w);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) dw[e] = 0.f;
+        for (int e = 0; e < VEC / 2; ++e) dw[e] = 0;
+        dst = static_cast<T*>(p.out[which]) + (at.tok * p.heads[which] + at.slot) * d + l * VEC;
+        dst_step = at.slots * d;
+        h = at.slot;
+        heads = live ? p.heads[which] : 0;
       }
-      fetch(k + D - 1);
+      fetch();
       copy_wait<D - 1>();
-      float x[VEC], g[VEC];
-      widen(ring_all[k % D * 2 * kThreads + threadIdx.x], x);
-      widen(ring_all[(k % D * 2 + 1) * kThreads + threadIdx.x], g);
-      float s = 0.f;
+      const bool on = h < heads;
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      const uint4 xr = on ? ring[k % D * (2 * kThreads)] : zero;
+      const uint4 gr = on ? ring[(k % D * 2 + 1) * kThreads] : zero;
+      uint64_t x[VEC / 2], g[VEC / 2], o[VEC / 2];
+      widen<VEC>(xr, x);
+      widen<VEC>(gr, g);
+      others<VEC, STAGE>(gr, g, o, l, half, stage);
+      const float r = rsqrtf(fmaf(group_sum<G>(sum_products(x, x)), inv_d, eps));
+      const uint64_t rr = f2(r, r);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) s = fmaf(x[e], x[e], s);
-      const float r = rsqrtf(fmaf(group_sum<G>(s), inv_d, p.eps));
-      turn_row<VEC, STAGE>(g, turn, l, p.half, stage);
-      float dot = 0.f;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        g[e] *= p.scale[which];
-        x[e] *= r;
-        dw[e] = fmaf(g[e], x[e], dw[e]);
-        g[e] *= w[e];
-        dot = fmaf(g[e], x[e], dot);
+      for (int e = 0; e < VEC / 2; ++e) {
+        g[e] = fma2(o[e], other[e], mul2(g[e], own[e]));  // turned back and scaled
+        x[e] = mul2(x[e], rr);
+        dw[e] = fma2(g[e], x[e], dw[e]);
+        g[e] = mul2(g[e], w[e]);
       }
-      dot = group_sum<G>(dot) * inv_d;
+      const float dot = -group_sum<G>(sum_products(g, x)) * inv_d;
+      const uint64_t dd = f2(dot, dot);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) g[e] = r * fmaf(-x[e], dot, g[e]);
-      if (live && h < heads) store_vec<T, VEC>(static_cast<T*>(p.out[which]) + (at.tok * heads + h) * d + l * VEC, g);
+      for (int e = 0; e < VEC / 2; ++e) g[e] = mul2(fma2(x[e], dd, g[e]), rr);
+      if (on) *reinterpret_cast<uint4*>(dst) = narrow<VEC>(g);
+      dst += dst_step;
+      h += at.slots;
     }
     if (total > 0) add_dw(total > nq ? 1 : 0);
   }
@@ -590,11 +673,13 @@ static size_t extent(const Args& a, const int64_t* s, int64_t heads, size_t es) 
   return ((size_t)((a.B - 1) * s[0] + (a.N - 1) * s[1] + (heads - 1) * s[2] + a.d)) * es;
 }
 
-// Tokens of a tile, a power of two: at most eight, and fewer where that would leave an
-// SM less than six tiles.
+// Tokens of a tile, a power of two: one for each group of a CTA (its set-up - angles,
+// their coefficients - is then done once a token; B4 N2K with 8 of 16: 1.15 times the
+// time), fewer where that would leave an SM less than three tiles.
 static int tile_of(const Args& a, int sms) {
-  int64_t t = 8;
-  while (t > 1 && a.B * a.N < t * 6 * sms) t /= 2;
+  const int64_t lanes = a.d / (a.dt == LA2_BF16 ? 8 : 4);
+  int64_t t = lanes <= 8 ? 32 : lanes <= 16 ? 16 : 8;
+  while (t > 1 && a.B * a.N < t * 3 * sms) t /= 2;
   return static_cast<int>(t);
 }
 
@@ -756,7 +841,7 @@ size_t la2_qk_norm_rope_backward_workspace_size(int64_t B, int64_t N, int64_t H,
   rope::Args a{};
   a.B = B;
   a.N = N;
-  return (size_t)rope::bwd_grid(a, rope::tile_of(a, sms), sms) * 2 * d * sizeof(float);
+  return (size_t)rope::bwd_grid(a, 1, sms) * 2 * d * sizeof(float);  // (the type and its tile are not known here)
 }
 
 la2_status la2_qk_norm_rope_backward(const void* dq_out, const void* dk_out, const void* q, const void* k,
