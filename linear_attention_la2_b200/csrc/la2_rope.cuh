@@ -19,18 +19,19 @@
 //
 // Bound by HBM: each row is read once and written once (backwards: two reads).
 // A CTA takes a tile of consecutive tokens and their heads. The angles are computed
-// once a token, into shared memory: the turns in fp64 (at position 2^20 an fp32 product
-// is 0.06 rad off), and only their fraction goes on to fp32. A group of lanes, 16 bytes
-// of a row each, keeps one token's cosines and sines in registers and walks the heads;
-// its neighbours hold the next tokens, so that the tile's rows of a head leave as one
-// piece of the output. Rows arrive by asynchronous copies into places of the loading
-// thread's own, kDepth rows ahead: in registers as many would halve the warps.
+// once a token: the turns in fp64 (at position 2^20 an fp32 product is 0.06 rad off),
+// and only their fraction goes on to fp32. A group of lanes, each with two 16-byte
+// pieces of a row that are one another's pairs, keeps one token's cosines and sines in
+// registers and walks the heads; its neighbours hold the next tokens, so that the
+// tile's rows of a head leave as one piece of the output. Rows arrive by
+// asynchronous copies into places of the loading thread's own, several ahead: in
+// registers as many would halve the warps.
 #pragma once
 
 namespace la2 {
 namespace rope {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxD = 256;
 constexpr int kMaxAxes = 4;
@@ -45,7 +46,7 @@ struct Params {
   int64_t sb[2], sn[2], sh[2];  // input strides in elements
   int64_t N, tokens;       // tokens = B * N
   int32_t heads[2];
-  int32_t d, half, tile, splits;
+  int32_t d, half, tile, splits, axes;
   float eps, scale[2];
   double turn[kMaxD / 2];  // base^(-2i/rot) / (2 pi)
   uint8_t axis[kMaxD / 2];
@@ -126,97 +127,153 @@ __device__ __forceinline__ uint4 narrow(const uint64_t (&x)[VEC / 2]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 template <int N>
-__device__ __forceinline__ float sum_products(const uint64_t (&x)[N], const uint64_t (&y)[N]) {
-  uint64_t s = mul2(x[0], y[0]);
+__device__ __forceinline__ float sum_products(const uint64_t (&x)[2][N], const uint64_t (&y)[2][N]) {
+  uint64_t s = mul2(x[0][0], y[0][0]);
 #pragma unroll
-  for (int i = 1; i < N; ++i) s = fma2(x[i], y[i], s);
+  for (int i = 1; i < 2 * N; ++i) s = fma2(x[i / N][i % N], y[i / N][i % N], s);
   float a, b;
   unpack(s, a, b);
   return a + b;
 }
+// A lane's pieces of a weight as stored (loaded ahead), and widened times f (f where
+// there is no weight).
 template <typename T>
-__device__ __forceinline__ float weight_at(const void* w, int i) {
-  return w ? to_f32(static_cast<const T*>(w)[i]) : 1.f;
+__device__ __forceinline__ void fetch_weight(const void* w, const int (&at)[2], uint4 (&raw)[2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    raw[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (w && at[i] >= 0) raw[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(w) + at[i]);
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void widen_weight(const void* w, const uint4 (&raw)[2], float f, uint64_t (&x)[2][VEC / 2]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    widen<VEC>(raw[i], x[i]);
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) x[i][e] = w ? mul2(x[i][e], f2(f, f)) : f2(f, f);
+  }
 }
 
-// The other value of each of a lane's pairs. STAGE false: half is a multiple of VEC, and
-// it sits at the same place half / VEC lanes away. STAGE true: the group's row goes
-// through shared memory (9 words for every 8, so that lanes meet no conflicts).
+// The two pieces (of VEC values) of lane l of a row's group. With half a multiple of VEC
+// (STAGE false) the first half / VEC lanes hold the pairs, and the pieces behind the
+// rotated ones are halved over the lanes after them; otherwise all pieces are halved
+// over the lanes, and the pairs meet in shared memory. A lane may have one or none (-1).
 template <int VEC, bool STAGE>
-__device__ __forceinline__ void others(const uint4& raw, const uint64_t (&x)[VEC / 2], uint64_t (&o)[VEC / 2], int l,
-                                       int half, float* stage) {
-  if constexpr (!STAGE) {
-    const int hl = half / VEC, lane = threadIdx.x & 31;
-    const int src = l < hl ? lane + hl : (l < 2 * hl ? lane - hl : lane);
-    uint4 r;
-    r.x = __shfl_sync(0xffffffffu, raw.x, src);
-    r.y = __shfl_sync(0xffffffffu, raw.y, src);
-    r.z = __shfl_sync(0xffffffffu, raw.z, src);
-    r.w = __shfl_sync(0xffffffffu, raw.w, src);
-    widen<VEC>(r, o);
+__device__ __forceinline__ void pieces_of(int l, int half, int d, int (&at)[2]) {
+  const int n = d / VEC, hl = STAGE ? 0 : half / VEC;
+  if (l < hl) {
+    at[0] = l * VEC;
+    at[1] = (l + hl) * VEC;
   } else {
-    auto at = [](int i) { return i + (i >> 3); };
+    const int rest = n - 2 * hl, k = l - hl, first = (rest + 1) / 2;
+    at[0] = k < first ? (2 * hl + k) * VEC : -1;
+    at[1] = k < first && first + k < rest ? (2 * hl + first + k) * VEC : -1;
+  }
+}
+// Lanes that a row takes.
+template <int VEC>
+__host__ __device__ __forceinline__ int lanes_of(int half, int d) {
+  const int n = d / VEC, hl = half % VEC ? 0 : half / VEC;
+  return hl + (n - 2 * hl + 1) / 2;
+}
+
+// Frequencies and axes of the pairs, out of the parameters (whose bank serves one
+// address at a time) into shared memory. A barrier must follow.
+struct Pairs {
+  double turn[kMaxD / 2];
+  uint8_t axis[kMaxD / 2];
+};
+__device__ __forceinline__ void load_pairs(const Params& p, Pairs& s) {
+  for (int i = threadIdx.x; i < p.half; i += kThreads) {
+    s.turn[i] = p.turn[i];
+    s.axis[i] = p.axis[i];
+  }
+}
+// A token's positions on every axis.
+struct Positions {
+  int32_t at[kMaxAxes];
+};
+__device__ __forceinline__ Positions positions_of(const Params& p, int64_t tok, int64_t n) {
+  Positions x;
+#pragma unroll
+  for (int a = 0; a < kMaxAxes; ++a)
+    x.at[a] = !p.pos ? static_cast<int32_t>(n) : a < p.axes ? p.pos[a * p.tokens + tok] : 0;
+  return x;
+}
+// (cos, sin) of pair j.
+__device__ __forceinline__ float2 angle_of(const Pairs& s, const Positions& at, int j) {
+  const int ax = s.axis[j];
+  const int32_t n = ax == 0 ? at.at[0] : ax == 1 ? at.at[1] : ax == 2 ? at.at[2] : at.at[3];
+  const double a = static_cast<double>(n) * s.turn[j];
+  float2 r;
+  sincospif(2.f * static_cast<float>(a - rint(a)), &r.y, &r.x);
+  return r;
+}
+
+// One token's turn of a lane's two pieces: value <- own value + other (its pair's other
+// value). STAGE false: the pieces are each other's, own = cos and other = -+ sin.
+template <int VEC, bool STAGE>
+struct Turn {
+  uint64_t own[STAGE ? 2 : 1][VEC / 2], other[STAGE ? 2 : 1][VEC / 2];
+};
+// sign -1 turns back.
+template <int VEC, bool STAGE>
+__device__ __forceinline__ void load_turn(Turn<VEC, STAGE>& c, const Pairs& s, const Positions& pos, const int (&at)[2],
+                                          int half, float sign) {
+#pragma unroll
+  for (int i = 0; i < (STAGE ? 2 : 1); ++i)
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) {
+      float o[2], t[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int v = at[i] + 2 * e + u;
+        o[u] = 1.f;
+        t[u] = 0.f;
+        if (at[i] >= 0 && v < 2 * half && (STAGE || v < half)) {
+          const float2 a = angle_of(s, pos, v < half ? v : v - half);
+          o[u] = a.x;
+          t[u] = STAGE && v < half ? -sign * a.y : sign * a.y;
+        }
+      }
+      c.own[i][e] = f2(o[0], o[1]);
+      c.other[i][e] = f2(t[0], t[1]);
+    }
+}
+// The staging row of a group: 9 words for every 8, so that lanes meet few conflicts.
+template <int VEC, bool STAGE>
+__device__ __forceinline__ void turn_row(uint64_t (&x)[2][VEC / 2], const Turn<VEC, STAGE>& c, const int (&at)[2],
+                                         int half, float* stage) {
+  if constexpr (!STAGE) {
+    const uint64_t minus = f2(-1.f, -1.f);
+#pragma unroll
+    for (int e = 0; e < VEC / 2; ++e) {
+      const uint64_t a = fma2(mul2(x[1][e], minus), c.other[0][e], mul2(x[0][e], c.own[0][e]));
+      x[1][e] = fma2(x[0][e], c.other[0][e], mul2(x[1][e], c.own[0][e]));
+      x[0][e] = a;
+    }
+  } else {
+    auto word = [](int i) { return i + (i >> 3); };
     __syncwarp();
 #pragma unroll
-    for (int e = 0; e < VEC / 2; ++e)
-      unpack(x[e], stage[at(VEC * l + 2 * e)], stage[at(VEC * l + 2 * e + 1)]);
-    __syncwarp();
-    auto other = [&](int i) { return stage[at(i < half ? i + half : (i < 2 * half ? i - half : i))]; };
+    for (int i = 0; i < 2; ++i)
+      if (at[i] >= 0)
 #pragma unroll
-    for (int e = 0; e < VEC / 2; ++e) o[e] = f2(other(VEC * l + 2 * e), other(VEC * l + 2 * e + 1));
+        for (int e = 0; e < VEC / 2; ++e)
+          unpack(x[i][e], stage[word(at[i] + 2 * e)], stage[word(at[i] + 2 * e + 1)]);
+    __syncwarp();
+    auto other = [&](int v) { return stage[word(v < half ? v + half : (v < 2 * half ? v - half : v))]; };
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (at[i] >= 0)
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e)
+          x[i][e] = fma2(f2(other(at[i] + 2 * e), other(at[i] + 2 * e + 1)), c.other[i][e], mul2(x[i][e], c.own[i][e]));
   }
 }
 // Floats of a group's staging row.
-__host__ __device__ constexpr int stage_floats(int vec, int g) { return vec * g + vec * g / 8; }
-
-// A lane's piece of a weight (ones without one, or behind the row).
-template <typename T, int VEC>
-__device__ __forceinline__ void load_weight(const void* w, int first, int d, uint64_t (&x)[VEC / 2]) {
-  if (w && first < d)
-    widen<VEC>(*reinterpret_cast<const uint4*>(static_cast<const T*>(w) + first), x);
-  else
-#pragma unroll
-    for (int e = 0; e < VEC / 2; ++e) x[e] = f2(1.f, 1.f);
-}
-
-// Coefficients of a lane's turned values: own[e] times the value plus other[e] times its
-// pair's other one. `turn` is one token's cosines and sines, sign -1 turns back, f scales;
-// with a weight, which comes before the turn, each value's own.
-template <typename T, int VEC, bool STAGE>
-__device__ __forceinline__ void coefficients(uint64_t (&own)[VEC / 2], uint64_t (&other)[VEC / 2], const float2* turn,
-                                             int first, int half, int d, float sign, float f, const void* weight) {
-  if constexpr (!STAGE) {  // pieces lie on one side of half, and so do their pairs' others
-    const bool lo = first < half, on = first < 2 * half;
-    const int j = lo ? first : first - half;
-    const float so = lo ? -sign * f : sign * f;
-    uint64_t w[VEC / 2], wo[VEC / 2];
-    load_weight<T, VEC>(weight, first, d, w);
-    load_weight<T, VEC>(weight, on ? (lo ? first + half : j) : d, d, wo);
-#pragma unroll
-    for (int e = 0; e < VEC / 2; ++e) {
-      const float4 a = on ? *reinterpret_cast<const float4*>(turn + j + 2 * e) : make_float4(1.f, 0.f, 1.f, 0.f);
-      own[e] = mul2(w[e], f2(f * a.x, f * a.z));
-      other[e] = mul2(wo[e], f2(so * a.y, so * a.w));
-    }
-  } else {
-    float c[VEC], s[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int i = first + e;
-      c[e] = s[e] = 0.f;
-      if (i >= d) continue;
-      const int j = i < half ? i + half : i - half;
-      const float2 a = i < 2 * half ? turn[i < half ? i : j] : make_float2(1.f, 0.f);
-      c[e] = f * weight_at<T>(weight, i) * a.x;
-      if (i < 2 * half) s[e] = (i < half ? -sign : sign) * f * weight_at<T>(weight, j) * a.y;
-    }
-#pragma unroll
-    for (int e = 0; e < VEC / 2; ++e) {
-      own[e] = f2(c[2 * e], c[2 * e + 1]);
-      other[e] = f2(s[2 * e], s[2 * e + 1]);
-    }
-  }
-}
+__host__ __device__ constexpr int stage_floats(int vec, int g) { return 2 * vec * g + 2 * vec * g / 8; }
 
 // The token and first head of a thread's group: groups run over the tile's tokens,
 // then over its share of the heads (`slots` heads at a time).
@@ -249,73 +306,94 @@ template <int N>
 __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-constexpr int kDepth = 8;   // 16-byte pieces a thread has in flight (backwards: half as many rows)
+constexpr int kDepth = 4;   // rows a thread has in flight, of two pieces (backwards: 3, of two times two)
+constexpr int kDepthBwd = 3;
 
 template <typename T, int VEC, int G, bool STAGE>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 5)
 rope_fwd_vec_kernel(const __grid_constant__ Params p) {
-  extern __shared__ uint4 ring_all[];  // [kDepth][kThreads]
-  float2* cs = reinterpret_cast<float2*>(ring_all + kDepth * kThreads);
+  extern __shared__ uint4 ring_all[];  // [kDepth][2][kThreads]
+  __shared__ Pairs pairs;
   __shared__ float stage_all[STAGE ? kThreads / G * stage_floats(VEC, G) : 1];
+  load_pairs(p, pairs);
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tile;
-  const Place at = place_of<G>(p, tok0);
-  const int l = threadIdx.x % G, d = p.d, half = p.half;
-  const float inv_d = 1.f / static_cast<float>(d), eps = p.eps;
+  const Place at = place_of<G>(p, static_cast<int64_t>(blockIdx.x) * p.tile);
+  const int half = p.half;
+  int pc[2];
+  pieces_of<VEC, STAGE>(threadIdx.x % G, half, p.d, pc);
+  const float inv_d = 1.f / static_cast<float>(p.d), eps = p.eps;
   float* stage = stage_all + (STAGE ? threadIdx.x / G * stage_floats(VEC, G) : 0);
   // rows k of the thread: its share of the queries' heads, then of the keys'
   const int nq = (p.heads[0] + at.slots - 1) / at.slots, total = nq + (p.heads[1] + at.slots - 1) / at.slots;
-  const bool live = l * VEC < d && at.on;
   uint4* ring = ring_all + threadIdx.x;
   // what is fetched next: the row's place, its head, and the step to the next
   const T* src = nullptr;
   int64_t src_step = 0;
-  int fetch_k = 0, fetch_h = 0, fetch_heads = 0;
+  int fetch_k = 0, fetch_h = 0, fetch_heads = 0, fetch_at = 0;
   auto fetch = [&]() {
     if (fetch_k == 0 || fetch_k == nq) {
       const int which = fetch_k >= nq;
-      src = static_cast<const T*>(p.x[which]) + at.b * p.sb[which] + at.n * p.sn[which] + at.slot * p.sh[which] + l * VEC;
+      src = static_cast<const T*>(p.x[which]) + at.b * p.sb[which] + at.n * p.sn[which] + at.slot * p.sh[which];
       src_step = at.slots * p.sh[which];
       fetch_h = at.slot;
-      fetch_heads = live ? p.heads[which] : 0;
+      fetch_heads = at.on ? p.heads[which] : 0;
     }
-    if (fetch_h < fetch_heads) copy_async16(sm100::smem_u32(ring + fetch_k % kDepth * kThreads), src);
+    if (fetch_h < fetch_heads) {
+      const uint32_t to = sm100::smem_u32(ring + fetch_at * 2 * kThreads);
+      if (pc[0] >= 0) copy_async16(to, src + pc[0]);
+      if (pc[1] >= 0) copy_async16(to + kThreads * 16, src + pc[1]);
+    }
     copy_commit();
     src += src_step;
     fetch_h += at.slots;
     ++fetch_k;
+    fetch_at = fetch_at + 1 == kDepth ? 0 : fetch_at + 1;
   };
 #pragma unroll 1
   for (int k = 0; k < kDepth - 1; ++k) fetch();
-  fill_angles(p, tok0, static_cast<int>(imin64(p.tile, p.tokens - tok0)), cs);
+  const Positions pos = positions_of(p, at.tok, at.n);
+  uint4 w_raw[2][2];
+  fetch_weight<T>(p.w[0], pc, w_raw[0]);
+  fetch_weight<T>(p.w[1], pc, w_raw[1]);
   __syncthreads();
-  uint64_t own[VEC / 2], other[VEC / 2];
+  Turn<VEC, STAGE> c;
+  load_turn<VEC, STAGE>(c, pairs, pos, pc, half, 1.f);
+  uint64_t w[2][VEC / 2];
   T* dst = nullptr;
   int64_t dst_step = 0;
-  int h = 0, heads = 0;
+  int h = 0, heads = 0, from = 0;
 #pragma unroll 1
   for (int k = 0; k < total; ++k) {  // (the same for all lanes of a warp)
     if (k == 0 || k == nq) {
       const int which = k >= nq;
-      coefficients<T, VEC, STAGE>(own, other, cs + (at.on ? at.t : 0) * half, l * VEC, half, d, 1.f, p.scale[which], p.w[which]);
-      dst = static_cast<T*>(p.out[which]) + ((at.b * p.heads[which] + at.slot) * p.N + at.n) * d + l * VEC;
-      dst_step = at.slots * p.N * d;
+      widen_weight<VEC>(p.w[which], which ? w_raw[1] : w_raw[0], p.scale[which], w);
+      dst = static_cast<T*>(p.out[which]) + ((at.b * p.heads[which] + at.slot) * p.N + at.n) * p.d;
+      dst_step = at.slots * p.N * p.d;
       h = at.slot;
-      heads = live ? p.heads[which] : 0;
+      heads = at.on ? p.heads[which] : 0;
     }
     fetch();
     copy_wait<kDepth - 1>();
     const bool on = h < heads;
-    const uint4 raw = on ? ring[k % kDepth * kThreads] : make_uint4(0u, 0u, 0u, 0u);
-    uint64_t x[VEC / 2], o[VEC / 2];
-    widen<VEC>(raw, x);
-    others<VEC, STAGE>(raw, x, o, l, half, stage);
+    uint64_t x[2][VEC / 2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      widen<VEC>(on && pc[i] >= 0 ? ring[(2 * from + i) * kThreads] : make_uint4(0u, 0u, 0u, 0u), x[i]);
+    from = from + 1 == kDepth ? 0 : from + 1;
     const float r = rsqrtf(fmaf(group_sum<G>(sum_products(x, x)), inv_d, eps));
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < VEC / 2; ++e) x[i][e] = mul2(x[i][e], w[i][e]);
+    turn_row<VEC, STAGE>(x, c, pc, half, stage);
     const uint64_t rr = f2(r, r);
 #pragma unroll
-    for (int e = 0; e < VEC / 2; ++e) x[e] = mul2(fma2(o[e], other[e], mul2(x[e], own[e])), rr);
-    if (on) *reinterpret_cast<uint4*>(dst) = narrow<VEC>(x);
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int e = 0; e < VEC / 2; ++e) x[i][e] = mul2(x[i][e], rr);
+      if (on && pc[i] >= 0) *reinterpret_cast<uint4*>(dst + pc[i]) = narrow<VEC>(x[i]);
+    }
     dst += dst_step;
     h += at.slots;
   }
@@ -333,114 +411,134 @@ __device__ __forceinline__ void store_dw(const Params& p, const float* smem_dw) 
 }
 
 template <typename T, int VEC, int G, bool STAGE>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 4)
 rope_bwd_vec_kernel(const __grid_constant__ Params p) {
-  constexpr int D = kDepth / 2;  // rows in flight, two reads each
-  extern __shared__ uint4 ring_all[];  // [D][2][kThreads]
-  float2* cs = reinterpret_cast<float2*>(ring_all + 2 * D * kThreads);
-  float* sdw = reinterpret_cast<float*>(cs + p.tile * p.half);  // [kWarps][2][d]
+  constexpr int D = kDepthBwd;
+  extern __shared__ uint4 ring_all[];  // [D][4][kThreads]: two pieces of x, two of dy
+  float* sdw = reinterpret_cast<float*>(ring_all + 4 * D * kThreads);  // [kWarps][2][d]
+  __shared__ Pairs pairs;
   __shared__ float stage_all[STAGE ? kThreads / G * stage_floats(VEC, G) : 1];
+  load_pairs(p, pairs);
   pdl_launch_dependents();
   pdl_wait();
-  const int l = threadIdx.x % G, d = p.d, half = p.half;
-  const bool in_row = l * VEC < d;
+  const int d = p.d, half = p.half;
+  int pc[2];
+  pieces_of<VEC, STAGE>(threadIdx.x % G, half, d, pc);
   const float inv_d = 1.f / static_cast<float>(d), eps = p.eps;
   float* stage = stage_all + (STAGE ? threadIdx.x / G * stage_floats(VEC, G) : 0);
   float* my_dw = sdw + (threadIdx.x >> 5) * 2 * d;
   uint4* ring = ring_all + threadIdx.x;
   for (int i = threadIdx.x & 31; i < 2 * d; i += 32) my_dw[i] = 0.f;
+  uint4 w_raw[2][2];
+  fetch_weight<T>(p.w[0], pc, w_raw[0]);
+  fetch_weight<T>(p.w[1], pc, w_raw[1]);
+  __syncthreads();
   for (int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tile; tok0 < p.tokens;
        tok0 += static_cast<int64_t>(gridDim.x) * p.tile) {
     const Place at = place_of<G>(p, tok0);
     const int nq = (p.heads[0] + at.slots - 1) / at.slots, total = nq + (p.heads[1] + at.slots - 1) / at.slots;
-    const bool live = in_row && at.on;
     const T *xs = nullptr, *gs = nullptr;  // fetched next
     int64_t x_step = 0, g_step = 0;
-    int fetch_k = 0, fetch_h = 0, fetch_heads = 0;
+    int fetch_k = 0, fetch_h = 0, fetch_heads = 0, fetch_at = 0;
     auto fetch = [&]() {
       if (fetch_k == 0 || fetch_k == nq) {
         const int which = fetch_k >= nq;
-        xs = static_cast<const T*>(p.x[which]) + at.b * p.sb[which] + at.n * p.sn[which] + at.slot * p.sh[which] + l * VEC;
-        gs = static_cast<const T*>(p.dy[which]) + ((at.b * p.heads[which] + at.slot) * p.N + at.n) * d + l * VEC;
+        xs = static_cast<const T*>(p.x[which]) + at.b * p.sb[which] + at.n * p.sn[which] + at.slot * p.sh[which];
+        gs = static_cast<const T*>(p.dy[which]) + ((at.b * p.heads[which] + at.slot) * p.N + at.n) * d;
         x_step = at.slots * p.sh[which];
         g_step = at.slots * p.N * d;
         fetch_h = at.slot;
-        fetch_heads = live ? p.heads[which] : 0;
+        fetch_heads = at.on ? p.heads[which] : 0;
       }
       if (fetch_h < fetch_heads) {
-        const uint32_t to = sm100::smem_u32(ring + fetch_k % D * (2 * kThreads));
-        copy_async16(to, xs);
-        copy_async16(to + kThreads * 16, gs);
+        const uint32_t to = sm100::smem_u32(ring + fetch_at * 4 * kThreads);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (pc[i] >= 0) {
+            copy_async16(to + i * kThreads * 16, xs + pc[i]);
+            copy_async16(to + (2 + i) * kThreads * 16, gs + pc[i]);
+          }
       }
       copy_commit();
       xs += x_step;
       gs += g_step;
       fetch_h += at.slots;
       ++fetch_k;
+      fetch_at = fetch_at + 1 == D ? 0 : fetch_at + 1;
     };
 #pragma unroll 1
     for (int k = 0; k < D - 1; ++k) fetch();
-    __syncthreads();  // the last tile's angles are done with
-    fill_angles(p, tok0, static_cast<int>(imin64(p.tile, p.tokens - tok0)), cs);
-    __syncthreads();
-    uint64_t own[VEC / 2], other[VEC / 2], w[VEC / 2], dw[VEC / 2];
+    Turn<VEC, STAGE> c;
+    load_turn<VEC, STAGE>(c, pairs, positions_of(p, at.tok, at.n), pc, half, -1.f);
+    uint64_t w[2][VEC / 2], dw[2][VEC / 2];
     T* dst = nullptr;
     int64_t dst_step = 0;
-    int h = 0, heads = 0;
+    int h = 0, heads = 0, from = 0;
     auto add_dw = [&](int which) {
 #pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) {
-        float a, b;
-        unpack(dw[e], a, b);
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int m = G; m < 32; m <<= 1) {  // the groups of a warp
-          a += __shfl_xor_sync(0xffffffffu, a, m);
-          b += __shfl_xor_sync(0xffffffffu, b, m);
+        for (int e = 0; e < VEC / 2; ++e) {
+          float a, b;
+          unpack(dw[i][e], a, b);
+#pragma unroll
+          for (int m = G; m < 32; m <<= 1) {  // the groups of a warp
+            a += __shfl_xor_sync(0xffffffffu, a, m);
+            b += __shfl_xor_sync(0xffffffffu, b, m);
+          }
+          if ((threadIdx.x & 31) < G && pc[i] >= 0) {
+            my_dw[which * d + pc[i] + 2 * e] += a;
+            my_dw[which * d + pc[i] + 2 * e + 1] += b;
+          }
         }
-        if ((threadIdx.x & 31) < G && in_row) {
-          my_dw[which * d + l * VEC + 2 * e] += a;
-          my_dw[which * d + l * VEC + 2 * e + 1] += b;
-        }
-      }
     };
 #pragma unroll 1
     for (int k = 0; k < total; ++k) {  // (the same for all lanes of a warp)
       if (k == 0 || k == nq) {
         if (k > 0) add_dw(0);
         const int which = k >= nq;
-        coefficients<T, VEC, STAGE>(own, other, cs + (at.on ? at.t : 0) * half, l * VEC, half, d, -1.f, p.scale[which], nullptr);
-        load_weight<T, VEC>(p.w[which], l * VEC, d, w);
+        widen_weight<VEC>(p.w[which], which ? w_raw[1] : w_raw[0], 1.f, w);
 #pragma unroll
-        for (int e = 0; e < VEC / 2; ++e) dw[e] = 0;
-        dst = static_cast<T*>(p.out[which]) + (at.tok * p.heads[which] + at.slot) * d + l * VEC;
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < VEC / 2; ++e) dw[i][e] = 0;
+        dst = static_cast<T*>(p.out[which]) + (at.tok * p.heads[which] + at.slot) * d;
         dst_step = at.slots * d;
         h = at.slot;
-        heads = live ? p.heads[which] : 0;
+        heads = at.on ? p.heads[which] : 0;
       }
       fetch();
       copy_wait<D - 1>();
       const bool on = h < heads;
-      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-      const uint4 xr = on ? ring[k % D * (2 * kThreads)] : zero;
-      const uint4 gr = on ? ring[(k % D * 2 + 1) * kThreads] : zero;
-      uint64_t x[VEC / 2], g[VEC / 2], o[VEC / 2];
-      widen<VEC>(xr, x);
-      widen<VEC>(gr, g);
-      others<VEC, STAGE>(gr, g, o, l, half, stage);
-      const float r = rsqrtf(fmaf(group_sum<G>(sum_products(x, x)), inv_d, eps));
-      const uint64_t rr = f2(r, r);
+      uint64_t x[2][VEC / 2], g[2][VEC / 2];
 #pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) {
-        g[e] = fma2(o[e], other[e], mul2(g[e], own[e]));  // turned back and scaled
-        x[e] = mul2(x[e], rr);
-        dw[e] = fma2(g[e], x[e], dw[e]);
-        g[e] = mul2(g[e], w[e]);
+      for (int i = 0; i < 2; ++i) {
+        const bool have = on && pc[i] >= 0;
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        widen<VEC>(have ? ring[(4 * from + i) * kThreads] : zero, x[i]);
+        widen<VEC>(have ? ring[(4 * from + 2 + i) * kThreads] : zero, g[i]);
       }
+      from = from + 1 == D ? 0 : from + 1;
+      const float r = rsqrtf(fmaf(group_sum<G>(sum_products(x, x)), inv_d, eps));
+      const uint64_t rr = f2(r, r), ff = f2(k >= nq ? p.scale[1] : p.scale[0], k >= nq ? p.scale[1] : p.scale[0]);
+      turn_row<VEC, STAGE>(g, c, pc, half, stage);  // back
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e) {
+          x[i][e] = mul2(x[i][e], rr);
+          g[i][e] = mul2(g[i][e], ff);
+          dw[i][e] = fma2(g[i][e], x[i][e], dw[i][e]);
+          g[i][e] = mul2(g[i][e], w[i][e]);
+        }
       const float dot = -group_sum<G>(sum_products(g, x)) * inv_d;
       const uint64_t dd = f2(dot, dot);
 #pragma unroll
-      for (int e = 0; e < VEC / 2; ++e) g[e] = mul2(fma2(x[e], dd, g[e]), rr);
-      if (on) *reinterpret_cast<uint4*>(dst) = narrow<VEC>(g);
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int e = 0; e < VEC / 2; ++e) g[i][e] = mul2(fma2(x[i][e], dd, g[i][e]), rr);
+        if (on && pc[i] >= 0) *reinterpret_cast<uint4*>(dst + pc[i]) = narrow<VEC>(g[i]);
+      }
       dst += dst_step;
       h += at.slots;
     }
@@ -673,12 +771,17 @@ static size_t extent(const Args& a, const int64_t* s, int64_t heads, size_t es) 
   return ((size_t)((a.B - 1) * s[0] + (a.N - 1) * s[1] + (heads - 1) * s[2] + a.d)) * es;
 }
 
-// Tokens of a tile, a power of two: one for each group of a CTA (its set-up - angles,
-// their coefficients - is then done once a token; B4 N2K with 8 of 16: 1.15 times the
-// time), fewer where that would leave an SM less than three tiles.
+// Lanes of a row's group, a power of two (the kernels are instantiated for 4 to 32).
+static int group_of(const Args& a) {
+  const int half = (int)a.rot / 2, d = (int)a.d;
+  const int lanes = a.dt == LA2_BF16 ? lanes_of<8>(half, d) : lanes_of<4>(half, d);
+  return lanes <= 4 ? 4 : lanes <= 8 ? 8 : lanes <= 16 ? 16 : 32;
+}
+// Tokens of a tile, a power of two: at most one for each group of a CTA, whose set-up
+// (angles, coefficients) is then done once a token, and at most 16; fewer where that
+// would leave an SM less than three tiles.
 static int tile_of(const Args& a, int sms) {
-  const int64_t lanes = a.d / (a.dt == LA2_BF16 ? 8 : 4);
-  int64_t t = lanes <= 8 ? 32 : lanes <= 16 ? 16 : 8;
+  int64_t t = std::min(8, kThreads / group_of(a));
   while (t > 1 && a.B * a.N < t * 3 * sms) t /= 2;
   return static_cast<int>(t);
 }
@@ -706,6 +809,7 @@ static Params params(const Args& a, int tile) {
   p.half = (int)a.rot / 2;
   p.tile = tile;
   p.splits = 1;
+  p.axes = (int)a.axes;
   p.eps = (float)a.eps;
   p.scale[0] = (float)a.q_scale;
   p.scale[1] = (float)a.k_scale;
@@ -720,7 +824,7 @@ static Params params(const Args& a, int tile) {
 // Whether rows can be taken in 16-byte pieces.
 static bool vec_ok(const Args& a, const void* const* more, int n) {
   const int64_t es = a.dt == LA2_BF16 ? 2 : 4, vec = 16 / es;
-  if (a.d % vec || a.d / vec > 32) return false;
+  if (a.d % vec) return false;
   for (int i = 0; i < 3; ++i)
     if (a.qs[i] % vec || a.ks[i] % vec) return false;
   if (!is_aligned(a.q, 16) || !is_aligned(a.k, 16) || !is_aligned(a.wq, 16) || !is_aligned(a.wk, 16)) return false;
@@ -730,7 +834,6 @@ static bool vec_ok(const Args& a, const void* const* more, int n) {
 }
 
 using Kernel = void (*)(const Params);
-// Lanes a row (8, 16 or 32), and whether pairs are whole 16-byte pieces apart.
 template <typename T, bool BWD, int G, bool STAGE>
 static Kernel vec_kernel() {
   if constexpr (BWD)
@@ -739,20 +842,22 @@ static Kernel vec_kernel() {
     return rope_fwd_vec_kernel<T, 16 / sizeof(T), G, STAGE>;
 }
 template <typename T, bool BWD, bool STAGE>
-static Kernel vec_kernel(int lanes) {
-  return lanes <= 8 ? vec_kernel<T, BWD, 8, STAGE>() : lanes <= 16 ? vec_kernel<T, BWD, 16, STAGE>()
-                                                                   : vec_kernel<T, BWD, 32, STAGE>();
+static Kernel vec_kernel(int g) {
+  return g == 4   ? vec_kernel<T, BWD, 4, STAGE>()
+         : g == 8  ? vec_kernel<T, BWD, 8, STAGE>()
+         : g == 16 ? vec_kernel<T, BWD, 16, STAGE>()
+                   : vec_kernel<T, BWD, 32, STAGE>();
 }
 template <typename T, bool BWD>
 static Kernel vec_kernel(const Args& a) {
-  constexpr int VEC = 16 / sizeof(T);
-  const int lanes = (int)a.d / VEC;
-  return (a.rot / 2) % VEC ? vec_kernel<T, BWD, true>(lanes) : vec_kernel<T, BWD, false>(lanes);
+  // (pairs a whole number of 16-byte pieces apart stay within a lane)
+  return (a.rot / 2) % (16 / (int)sizeof(T)) ? vec_kernel<T, BWD, true>(group_of(a))
+                                             : vec_kernel<T, BWD, false>(group_of(a));
 }
 
 // Dynamic shared memory beyond the default limit (wide rows, with their static part).
 static bool allow_smem(Kernel kern, size_t bytes) {
-  return bytes <= 36 * 1024 ||
+  return bytes <= 32 * 1024 ||
          cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
 }
 
@@ -761,8 +866,8 @@ static la2_status launch_fwd(const Args& a, Params p, bool vec, int sms, cudaStr
   const int64_t tiles = (p.tokens + p.tile - 1) / p.tile;
   // few tokens (a decode batch): their heads over several CTAs
   const int64_t rows = (int64_t)p.tile * (a.H + a.Hkv);
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(2 * sms / tiles, (rows + 15) / 16));
-  const size_t smem = (size_t)p.tile * p.half * sizeof(float2) + (vec ? kDepth * kThreads * 16 : 0);
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(3 * sms / tiles, (rows + 15) / 16));
+  const size_t smem = vec ? (size_t)2 * kDepth * kThreads * 16 : (size_t)p.tile * p.half * sizeof(float2);
   const dim3 grid((unsigned)tiles, (unsigned)p.splits), block(kThreads);
   const Kernel kern = vec ? vec_kernel<T, false>(a) : a.d <= 128 ? rope_fwd_row_kernel<T, 2> : rope_fwd_row_kernel<T, 4>;
   if (!allow_smem(kern, smem)) return LA2_ERR_CUDA;
@@ -774,8 +879,8 @@ static la2_status launch_fwd(const Args& a, Params p, bool vec, int sms, cudaStr
 template <typename T>
 static la2_status launch_bwd(const Args& a, const Params& p, bool vec, int grid, void* dwq, void* dwk,
                              cudaStream_t st) {
-  const size_t smem = (size_t)p.tile * p.half * sizeof(float2) + (size_t)kWarps * 2 * p.d * sizeof(float) +
-                      (vec ? kDepth * kThreads * 16 : 0);
+  const size_t smem = (size_t)kWarps * 2 * p.d * sizeof(float) +
+                      (vec ? (size_t)4 * kDepthBwd * kThreads * 16 : (size_t)p.tile * p.half * sizeof(float2));
   const Kernel kern = vec ? vec_kernel<T, true>(a) : a.d <= 128 ? rope_bwd_row_kernel<T, 2> : rope_bwd_row_kernel<T, 4>;
   if (!allow_smem(kern, smem)) return LA2_ERR_CUDA;
   {
