@@ -162,17 +162,12 @@ struct TcCfg {
   static constexpr int OFF_TAB = OFF_OUT + 2 * kTile;
   static constexpr int OFF_DOT = OFF_TAB + kTabs * kTab * 4;
   static constexpr int OFF_BAR = OFF_DOT + (GRAD ? 2 * 4 * 64 * 4 : 0);
-  static constexpr int NBAR = 4 * KS + 4 + 4 + 2 + 3 + 5 + 3 + kTabs + 1;
+  static constexpr int NBAR = 4 * KS + 3 + 4 + 2 + 3 + 2 + 3 + kTabs + 1;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
-// TMEM columns: the state; its copy (value, and with GRAD remainder); two buffers of S;
-// near; far, two buffers of it where the copy has no remainder.
-constexpr uint32_t kColState = 0, kColS = 128, kColNear = 256, kColCopy = 320;
-template <bool GRAD>
-__device__ __forceinline__ uint32_t col_far(int i) {
-  return GRAD ? 448 : 384 + 64 * (i & 1);
-}
+// TMEM columns: the state, its copy (value, remainder), S, two buffers of far, near
+constexpr uint32_t kColState = 0, kColCopy = 128, kColS = 256, kColFar = 320, kColNear = 448;
 
 // Packed fp32 pairs (two multiply-adds an instruction: the roles share the issue slots).
 __device__ __forceinline__ uint64_t f2(float x, float y) {
@@ -286,11 +281,11 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
   uint64_t* z_empty = z_full + KS;
   uint64_t* s_full = z_empty + KS;
   uint64_t* s_empty = s_full + 2;
-  uint64_t *p_full = s_empty + 2, *p_empty = p_full + 2;
+  uint64_t *p_full = s_empty + 1, *p_empty = p_full + 2;
   uint64_t *y_full = p_empty + 2, *y_empty = y_full + 1;
   uint64_t *copy_full = y_empty + 1, *copy_empty = copy_full + 1, *updated = copy_empty + 1;
-  uint64_t *o_full = updated + 1, *near_empty = o_full + 2, *far_empty = near_empty + 1;
-  uint64_t *staged = far_empty + 2, *tile_free = staged + 1;
+  uint64_t *o_full = updated + 1, *o_empty = o_full + 1;
+  uint64_t *staged = o_empty + 1, *tile_free = staged + 1;
   uint64_t* tab_full = tile_free + 2;
   uint64_t* drain = tab_full + kTabs;
   uint32_t* tmem_base = reinterpret_cast<uint32_t*>(drain + 1);
@@ -309,18 +304,17 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       s::mbar_init(&in_full[i], 1);
       s::mbar_init(&in_empty[i], 1);
       s::mbar_init(&z_full[i], 1);
-      s::mbar_init(&z_empty[i], 2);
+      s::mbar_init(&z_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       s::mbar_init(&s_full[i], 1);
       s::mbar_init(&p_full[i], 128);
       s::mbar_init(&p_empty[i], 1);
       s::mbar_init(&tile_free[i], 1);
-      s::mbar_init(&o_full[i], 2);
-      s::mbar_init(&far_empty[i], 128);
-      s::mbar_init(&s_empty[i], 128);
     }
-    s::mbar_init(near_empty, 128);
+    s::mbar_init(s_empty, 128);
+    s::mbar_init(o_full, 1);
+    s::mbar_init(o_empty, 128);
     s::mbar_init(y_full, 128);
     s::mbar_init(y_empty, 1);
     s::mbar_init(copy_full, 256);
@@ -328,7 +322,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     s::mbar_init(updated, 1);
     s::mbar_init(staged, 128);
     for (int i = 0; i < kTabs; ++i) s::mbar_init(&tab_full[i], 32);
-    s::mbar_init(drain, 2);
+    s::mbar_init(drain, 1);
     *abort_flag = 0;
     s::fence_barrier_init();
   }
@@ -360,17 +354,99 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
   const uint32_t lane_off = static_cast<uint32_t>(32 * w4) << 16;
 
   if (warp == 0) {
-    // ================================================ loads, and the gate tables
-    // A table: the running sums c [64]; the epilogue's factors of far [64]; and for
+    // ================================================================ loads
+    if (lane == 0) {
+      int issued = 0, issued_z = 0;
+      for (int i = 0; i < n; ++i) {
+        const int st = i % KS, row = static_cast<int>(row_of(i)), z = static_cast<int>(bh);
+        uint8_t* dst = smem + st * 3 * kTile;
+        if (!s::wait_bar(&in_empty[st], ((i / KS) & 1) ^ 1, lim, abort_flag, 70)) break;
+        s::mbar_expect_tx(&in_full[st], 2 * kTile);
+        for (int p = 0; p < 2; ++p) s::tma_load_3d(dst + p * 8192, &tm_x, &in_full[st], 64 * p, row, z);
+        for (int p = 0; p < 2; ++p) s::tma_load_3d(dst + kTile + p * 8192, &tm_y, &in_full[st], 64 * p, row, z);
+        ++issued;
+        if (!s::wait_bar(&z_empty[st], ((i / KS) & 1) ^ 1, lim, abort_flag, 87)) break;
+        s::mbar_expect_tx(&z_full[st], kTile);
+        for (int p = 0; p < 2; ++p) s::tma_load_3d(dst + 2 * kTile + p * 8192, &tm_z, &z_full[st], 64 * p, row, z);
+        ++issued_z;
+      }
+      if (issued_z < n) {  // after an abort: let every load this thread issued land before the CTA exits
+        for (int j = max(0, issued - KS); j < issued; ++j) s::drain_wait(&in_full[j % KS], (j / KS) & 1);
+        for (int j = max(0, issued_z - KS); j < issued_z; ++j) s::drain_wait(&z_full[j % KS], (j / KS) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    // ================================================================== MMA
+    constexpr uint32_t ID_S = s::make_idesc(64, 64, false, false);
+    constexpr uint32_t ID_FAR = s::make_idesc(128, 64, false, false);
+    constexpr uint32_t ID_UPD = s::make_idesc(128, 128, true, true);
+    constexpr uint32_t ID_NEAR = s::make_idesc(128, 64, true, false);
+    const uint32_t lead = elect_one();
+    const uint32_t base = s::smem_u32(smem);
+    // Operand descriptors at their first 16 k: X and Y by rows (S, far), Y~ and Z by
+    // columns (update, near) of stage 0; a stage further on is 3 kTile.
+    constexpr uint32_t kStage = 3 * kTile / 16, kY = kTile / 16, kZ = 2 * kTile / 16;
+    const uint64_t row_d = s::make_desc(base, 16, 1024), col_d = s::make_desc(base, 8192, 1024);
+    const uint64_t lo_d = s::make_desc(base + CF::OFF_LO, 8192, 1024), p_d = s::make_desc(base + CF::OFF_P, 16, 1024);
+    auto scores = [&](int i) -> bool {  // S of block i
+      if (!wait(&in_full[i % KS], (i / KS) & 1, 71)) return false;
+      if (!wait(s_empty, (i & 1) ^ 1, 72)) return false;
+      s::tc_fence_after();
+      const uint32_t st = (i % KS) * kStage;
+      mma_run<8>(lead, tmem + kColS, row_d + st, row_d + st + kY, 2, 2, 504, 504, ID_S, 0);
+      commit(lead, &s_full[i & 1]);
+      return true;
+    };
+    bool ok = scores(0);
+    for (int i = 0; i < n && ok; ++i) {
+      const uint32_t st = (i % KS) * kStage;
+      const bool far = i >= first_copy;
+      ok = false;
+      if (i + 1 < n && !scores(i + 1)) break;
+      if (!wait(&z_full[i % KS], (i / KS) & 1, 87)) break;
+      if (far && !wait(copy_full, (i - first_copy) & 1, 74)) break;
+      if (i + 1 < n) {  // the state past the chunk's last block is not needed
+        if (!wait(y_full, i & 1, 75)) break;
+        s::tc_fence_after();
+        mma_run<4>(lead, tmem + kColState, col_d + st + kZ, col_d + st + kY, 128, 128, 0, 0, ID_UPD, far);
+        mma_run<4>(lead, tmem + kColState, col_d + st + kZ, lo_d, 128, 128, 0, 0, ID_UPD, 1);
+        commit(lead, updated);
+        commit(lead, y_empty);
+      }
+      if (far) {  // (its buffer: the epilogue has read block i - 2, see near of i - 1)
+        s::tc_fence_after();
+        if (lead) {
+#pragma unroll
+          for (int k = 0; k < 8 * PARTS; ++k)
+            mma_ts(tmem + kColFar + 64 * (i & 1), tmem + kColCopy + 8 * k,
+                   row_d + st + ((k & 7) >> 2) * 512 + (k & 3) * 2, ID_FAR, k > 0);
+        }
+        __syncwarp();
+        commit(lead, copy_empty);
+      }
+      commit(lead, &in_empty[i % KS]);  // X and Y are done with, Z is not
+      if (!wait(&p_full[i & 1], (i >> 1) & 1, 76)) break;
+      if (!wait(o_empty, (i & 1) ^ 1, 73)) break;  // the epilogue has read near of block i - 1
+      s::tc_fence_after();
+      mma_run<4>(lead, tmem + kColNear, col_d + st + kZ, p_d + (i & 1) * 512, 128, 2, 0, 0, ID_NEAR, 0);
+      commit(lead, o_full);
+      commit(lead, &p_empty[i & 1]);
+      commit(lead, &z_empty[i % KS]);
+      ok = true;
+    }
+    commit(lead, drain);  // every MMA issued must finish before TMEM is released
+    s::drain_wait(drain, 0);
+  } else if (warp == 2) {
+    // =========================================================== gate tables
+    // Per block: the running sums c [64]; the epilogue's factors of far [64]; and for
     // the mask, whose rows and columns meet in 16 x 16 squares, e^(c_E(s) - c_s) [64]
     // with E(s) the last row of s' sixteen, and e^(c_t - c_E) for the first three E
     // [3][64] (read for later t only): off the diagonal e^(c_t - c_s) is one of each,
     // neither above 1 unless gates are. Table i goes into slot i % 8 when block i - KS
-    // has released its Z: everything of it is done but its epilogue, and before its
-    // near was issued the epilogue had read block i - KS - 1 (near_empty), so readers
-    // of block i - 8 are long done.
+    // has released its stage (z_empty): everything of it is done but its epilogue,
+    // and before its near was issued the epilogue had read block i - KS - 1 (o_empty),
+    // so readers of block i - 8 are long done.
     const __nv_bfloat16* g = prm.gate + bh * prm.N;
-    int issued = 0, issued_z = 0;
     for_gates(
         n, lane,
         [&](int i, int r) {
@@ -380,21 +456,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
           return t > 0 || __hisnan(x) ? x : __float2bfloat16(0.f);
         },
         [&](int i, __nv_bfloat16 gx, __nv_bfloat16 gy) {
-          const int st = i % KS, row = static_cast<int>(row_of(i)), z = static_cast<int>(bh);
-          uint8_t* dst = smem + st * 3 * kTile;
-          if (!wait(&in_empty[st], ((i / KS) & 1) ^ 1, 70)) return false;
-          if (lane == 0) {
-            s::mbar_expect_tx(&in_full[st], 2 * kTile);
-            for (int p = 0; p < 2; ++p) s::tma_load_3d(dst + p * 8192, &tm_x, &in_full[st], 64 * p, row, z);
-            for (int p = 0; p < 2; ++p) s::tma_load_3d(dst + kTile + p * 8192, &tm_y, &in_full[st], 64 * p, row, z);
-          }
-          ++issued;
-          if (!wait(&z_empty[st], ((i / KS) & 1) ^ 1, 87)) return false;
-          if (lane == 0) {
-            s::mbar_expect_tx(&z_full[st], kTile);
-            for (int p = 0; p < 2; ++p) s::tma_load_3d(dst + 2 * kTile + p * 8192, &tm_z, &z_full[st], 64 * p, row, z);
-          }
-          ++issued_z;
+          if (i >= KS && !wait(&z_empty[i % KS], (i / KS - 1) & 1, 77)) return false;
           float a, b;
           warp_sums(gate_log2(gx), gate_log2(gy), lane, a, b);
           const float all = __shfl_sync(0xffffffffu, b, 31);
@@ -411,86 +473,6 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
           s::mbar_arrive(&tab_full[i % kTabs]);
           return true;
         });
-    if (issued_z < n && lane == 0) {  // after an abort: let every load issued land before the CTA exits
-      for (int j = max(0, issued - KS); j < issued; ++j) s::drain_wait(&in_full[j % KS], (j / KS) & 1);
-      for (int j = max(0, issued_z - KS); j < issued_z; ++j) s::drain_wait(&z_full[j % KS], (j / KS) & 1);
-    }
-  } else if (warp == 1 || warp == 2) {
-    // ================================================================= MMAs
-    // Warp 1 issues S and near, warp 2 the update and far: each wait and commit costs
-    // an issuing warp about a hundred cycles, and one warp for all of them was as long
-    // as the loop-carried path.
-    const uint32_t lead = elect_one();
-    const uint32_t base = s::smem_u32(smem);
-    // Operand descriptors at their first 16 k: X and Y by rows (S, far), Y~ and Z by
-    // columns (update, near) of stage 0; a stage further on is 3 kTile.
-    constexpr uint32_t kStage = 3 * kTile / 16, kY = kTile / 16, kZ = 2 * kTile / 16;
-    const uint64_t row_d = s::make_desc(base, 16, 1024), col_d = s::make_desc(base, 8192, 1024);
-    if (warp == 1) {
-      constexpr uint32_t ID_S = s::make_idesc(64, 64, false, false);
-      constexpr uint32_t ID_NEAR = s::make_idesc(128, 64, true, false);
-      const uint64_t p_d = s::make_desc(base + CF::OFF_P, 16, 1024);
-      auto scores = [&](int i) -> bool {  // S of block i
-        if (!wait(&in_full[i % KS], (i / KS) & 1, 71)) return false;
-        if (!wait(&s_empty[i & 1], ((i >> 1) & 1) ^ 1, 72)) return false;
-        s::tc_fence_after();
-        const uint32_t st = (i % KS) * kStage;
-        mma_run<8>(lead, tmem + kColS + 64 * (i & 1), row_d + st, row_d + st + kY, 2, 2, 504, 504, ID_S, 0);
-        commit(lead, &s_full[i & 1]);
-        return true;
-      };
-      bool ok = scores(0);
-      for (int i = 0; i < n && ok; ++i) {
-        ok = false;
-        if (i + 1 < n && !scores(i + 1)) break;
-        if (!wait(&z_full[i % KS], (i / KS) & 1, 73)) break;
-        if (!wait(&p_full[i & 1], (i >> 1) & 1, 76)) break;
-        if (!wait(near_empty, (i & 1) ^ 1, 98)) break;  // the epilogue has read near of block i - 1
-        s::tc_fence_after();
-        mma_run<4>(lead, tmem + kColNear, col_d + (i % KS) * kStage + kZ, p_d + (i & 1) * 512, 128, 2, 0, 0, ID_NEAR, 0);
-        commit(lead, &o_full[i & 1]);
-        commit(lead, &p_empty[i & 1]);
-        commit(lead, &z_empty[i % KS]);
-        ok = true;
-      }
-    } else {
-      constexpr uint32_t ID_FAR = s::make_idesc(128, 64, false, false);
-      constexpr uint32_t ID_UPD = s::make_idesc(128, 128, true, true);
-      const uint64_t lo_d = s::make_desc(base + CF::OFF_LO, 8192, 1024);
-      for (int i = 0; i < n; ++i) {
-        const uint32_t st = (i % KS) * kStage;
-        const bool far = i >= first_copy;
-        if (!wait(&in_full[i % KS], (i / KS) & 1, 99)) break;
-        if (!wait(&z_full[i % KS], (i / KS) & 1, 100)) break;
-        if (i + 1 < n && !wait(y_full, i & 1, 75)) break;
-        if (far && !wait(copy_full, (i - first_copy) & 1, 74)) break;
-        s::tc_fence_after();
-        if (i + 1 < n) {  // the state past the chunk's last block is not needed
-          mma_run<4>(lead, tmem + kColState, col_d + st + kZ, col_d + st + kY, 128, 128, 0, 0, ID_UPD, far);
-          mma_run<4>(lead, tmem + kColState, col_d + st + kZ, lo_d, 128, 128, 0, 0, ID_UPD, 1);
-          commit(lead, updated);
-          commit(lead, y_empty);
-        }
-        if (far) {
-          // its buffer: the epilogue has read block i - 2 (GRAD: i - 1)
-          if (!(GRAD ? wait(far_empty, (i & 1) ^ 1, 101) : wait(&far_empty[i & 1], ((i >> 1) & 1) ^ 1, 101))) break;
-          s::tc_fence_after();
-          if (lead) {
-#pragma unroll
-            for (int k = 0; k < 8 * PARTS; ++k)
-              mma_ts(tmem + col_far<GRAD>(i), tmem + kColCopy + 8 * k,
-                     row_d + st + ((k & 7) >> 2) * 512 + (k & 3) * 2, ID_FAR, k > 0);
-          }
-          __syncwarp();
-          commit(lead, copy_empty);
-        }
-        commit(lead, &o_full[i & 1]);
-        commit(lead, &in_empty[i % KS]);
-        commit(lead, &z_empty[i % KS]);
-      }
-    }
-    commit(lead, drain);  // every MMA issued must finish before TMEM is released
-    s::drain_wait(drain, 0);
   } else if (wg == 4) {
     // ===================================================================== Y~
     // Two threads a row: the value over Y once S has read it, the remainder into its
@@ -535,21 +517,11 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       if (!wait(&s_full[i & 1], (i >> 1) & 1, 81)) break;
       s::tc_fence_after();
       if (!wait(&p_empty[i & 1], ((i >> 1) & 1) ^ 1, 82)) break;  // near of block i - 2 has read its P
-      const uint32_t ts = tmem + kColS + 64 * (i & 1) + lane_off;
-      uint32_t next[16];
-      tmem_ld16(ts + 16 * h0, next);
 #pragma unroll 1
       for (int h = h0; h <= h1; ++h) {
         uint32_t v[16], w[8];
+        tmem_ld16(tmem + kColS + 16 * h + lane_off, v);
         s::tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) v[e] = next[e];
-        if (h < h1) {
-          tmem_ld16(ts + 16 * (h + 1), next);
-        } else {
-          s::tc_fence_before();
-          s::mbar_arrive(&s_empty[i & 1]);
-        }
         if (r >= 0) {
           if (h == w4) {
             const float cr = c[r];
@@ -578,6 +550,8 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
           s::st_shared_v4(p_at(i & 1, 2 * h + 1), w[4], w[5], w[6], w[7]);
         }
       }
+      s::tc_fence_before();
+      s::mbar_arrive(s_empty);
       s::fence_proxy_async();
       s::mbar_arrive(&p_full[i & 1]);
     }
@@ -681,7 +655,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       head += 64 + 2 * (lane & 3);
       // the tile: the dots' rows have landed (GRAD), or the store of block i - 2 has read it
       if (!wait(&tile_free[i & 1], ((i >> 1) & 1) ^ (GRAD ? 0 : 1), 89)) break;
-      if (!wait(&o_full[i & 1], (i >> 1) & 1, 86)) break;
+      if (!wait(o_full, i & 1, 86)) break;
       s::tc_fence_after();
       uint64_t dot[8];  // columns 8 g + 2 j, + 1 of this thread, summed over its lanes
 #pragma unroll
@@ -695,7 +669,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         for (int part = 0; part < 4; ++part) {  // 16 rows of the output
           uint32_t near[8], v[8], x[4], pk[4];
           tmem_ld_frag2(tmem + kColNear + 16 * part + t_lane, near);
-          if (far) tmem_ld_frag2(tmem + col_far<GRAD>(i) + 16 * part + t_lane, v);
+          if (far) tmem_ld_frag2(tmem + kColFar + 64 * (i & 1) + 16 * part + t_lane, v);
           if (GRAD) ldmatrix_t4(row0 + part * 2048, x);
           s::tmem_ld_wait();
 #pragma unroll
@@ -716,8 +690,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         }
       }
       s::tc_fence_before();
-      s::mbar_arrive(near_empty);
-      s::mbar_arrive(&far_empty[GRAD ? 0 : i & 1]);
+      s::mbar_arrive(o_empty);
       if (GRAD) {
         // over the eight threads with the same columns: each keeps half at every step
         float d[16];
