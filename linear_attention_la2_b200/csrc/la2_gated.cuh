@@ -43,8 +43,8 @@ static la2_status check(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, 
 // is a running difference of row dots (see la2_gated_simt.cuh). Tensor cores: one CTA
 // an SM, so the count is the one whose waves of CTAs, times blocks a chunk and a fixed
 // cost, are shortest; more than one chunk adds the pass over the chunks' own states.
-static Plan make_plan(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, la2_dtype dt, Need need,
-                      int sms) {
+static Plan make_plan_uncached(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, la2_dtype dt, Need need,
+                               int sms) {
   Plan p;
   const int64_t BH = B * H, T = (N + kRows - 1) / kRows;
   p.tc = dt == LA2_BF16 && d == 128 && dv == 128;
@@ -104,6 +104,33 @@ static Plan make_plan(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, la
   p.off_kdk = at;
   if (need == NEED_BWD) at += round256((size_t)BH * N * sizeof(float));
   p.bytes = at;
+  return p;
+}
+
+// Plans are pure functions of the arguments, the split override and the SM count; a
+// workspace query and its call ask for the same one, so recent plans are kept.
+static Plan make_plan(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, la2_dtype dt, Need need, int sms) {
+  struct Key {
+    int64_t v[9];
+    bool operator==(const Key& o) const { return std::memcmp(v, o.v, sizeof(v)) == 0; }
+  };
+  constexpr int kSlots = 16;
+  static Key keys[kSlots];
+  static Plan plans[kSlots];
+  static int used = 0, next_slot = 0;
+  static std::mutex mu;
+  const Key k{{B, H, N, d, dv, dt, need, sms, g_chunk_len}};
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < used; ++i)
+      if (keys[i] == k) return plans[i];
+  }
+  const Plan p = make_plan_uncached(B, H, N, d, dv, dt, need, sms);
+  std::lock_guard<std::mutex> lock(mu);
+  keys[next_slot] = k;
+  plans[next_slot] = p;
+  next_slot = (next_slot + 1) % kSlots;
+  used = used < kSlots ? used + 1 : kSlots;
   return p;
 }
 
