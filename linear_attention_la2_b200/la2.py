@@ -532,6 +532,9 @@ def backward_sp(q, k, v, do, prefix_states=None, suffix_states=None, block: int 
 
 
 # ---------------------------------------------------------------- gated form
+#
+# The calls below are short next to their Python: pointers go to ctypes as plain
+# integers, and each tensor is checked in one place.
 
 
 def _sized(n) -> int:
@@ -544,21 +547,54 @@ def workspace_bytes_gated(B, H, N, d, dv, dtype_code, is_backward) -> int:
     return _sized(la2_workspace_size_gated(B, H, N, d, dv, dtype_code, int(is_backward)))
 
 
+def _dense(t, shape, dtype, device):
+    """Refuses a tensor that is not a contiguous CUDA one of this shape, type and device."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_cuda or not t.is_contiguous():
+        raise La2Error(LA2_ERR_INVALID_ARG)
+
+
+def _dense_ref(t, dims):
+    """The same for a call's first tensor: its shape, type, type code and device."""
+    if t.dim() != dims or not t.is_cuda or not t.is_contiguous():
+        raise La2Error(LA2_ERR_INVALID_ARG)
+    return t.shape, t.dtype, _dtype_code(t), t.device
+
+
 _HERE = contextlib.nullcontext()
 
 
-def _call_on(ref, stream):
-    """Context of one call: ref's device and the call's stream are current, so what
-    is allocated inside belongs to the stream that the kernels run on."""
+def _call_on(device, stream):
+    """Context of one call: its device and stream are current, so what is allocated
+    inside belongs to the stream that the kernels run on."""
     import torch
 
     if stream is not None:
-        if stream.device != ref.device:
+        if stream.device != device:
             raise La2Error(LA2_ERR_INVALID_ARG)
         return torch.cuda.stream(stream)
-    if ref.device.index == torch.cuda.current_device():
+    if device.index == torch.cuda.current_device():
         return _HERE
-    return torch.cuda.device(ref.device)
+    return torch.cuda.device(device)
+
+
+def _raw_stream(device, stream):
+    import torch
+
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _scratch(need, given, device):
+    """(tensor, pointer, bytes) of a call's workspace: the caller's, or one allocated on
+    the current stream (kept by the caller of this until the launch is made)."""
+    import torch
+
+    if given is None:
+        if need == 0:
+            return None, 0, 0
+        given = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _check_workspace(given, need, device)
+    return given, given.data_ptr(), given.numel()
 
 
 def forward_gated(q, k, v, gate, out=None, workspace=None, stream=None):
@@ -567,25 +603,21 @@ def forward_gated(q, k, v, gate, out=None, workspace=None, stream=None):
     the state); returns O."""
     import torch
 
-    _check_inputs(q, k, v, gate)
-    if q.dim() != 4 or v.dim() != 4:
-        raise La2Error(LA2_ERR_INVALID_ARG)
-    B, H, N, d = q.shape
+    shape, dtype, dt, device = _dense_ref(q, 4)
+    B, H, N, d = shape
     dv = v.shape[-1]
-    dt = _dtype_code(q)
-    _check_like(q, q.shape, q.dtype, k)
-    _check_like(q, (B, H, N, dv), q.dtype, v)
-    _check_like(q, (B, H, N), q.dtype, gate)
-    with _call_on(q, stream):
+    vshape = (B, H, N, dv)
+    _dense(k, shape, dtype, device)
+    _dense(v, vshape, dtype, device)
+    _dense(gate, shape[:3], dtype, device)
+    with _call_on(device, stream):
         if out is None:
-            out = torch.empty((B, H, N, dv), dtype=q.dtype, device=q.device)
-        _check_inputs(out)
-        _check_like(q, (B, H, N, dv), q.dtype, out)
-        need = workspace_bytes_gated(B, H, N, d, dv, dt, False)
-        ws = workspace if workspace is not None else _workspace(need, q.device, None)
-        _check_workspace(ws, need, q.device)
-        _raise(la2_forward_gated(_ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(out), B, H, N, d, dv, dt,
-                                 _ptr(ws), ws.numel() if ws is not None else 0, _stream_handle(stream)))
+            out = torch.empty(vshape, dtype=dtype, device=device)
+        else:
+            _dense(out, vshape, dtype, device)
+        ws, wp, wn = _scratch(workspace_bytes_gated(B, H, N, d, dv, dt, False), workspace, device)
+        _raise(la2_forward_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(), out.data_ptr(), B, H,
+                                 N, d, dv, dt, wp, wn, _raw_stream(device, stream)))
     return out
 
 
@@ -594,40 +626,50 @@ def backward_gated(q, k, v, gate, do, outs=None, workspace=None, stream=None):
     gradient by the log gates."""
     import torch
 
-    _check_inputs(q, k, v, gate, do)
-    if q.dim() != 4 or v.dim() != 4:
-        raise La2Error(LA2_ERR_INVALID_ARG)
-    B, H, N, d = q.shape
+    shape, dtype, dt, device = _dense_ref(q, 4)
+    B, H, N, d = shape
     dv = v.shape[-1]
-    dt = _dtype_code(q)
-    _check_like(q, q.shape, q.dtype, k)
-    _check_like(q, (B, H, N, dv), q.dtype, v, do)
-    _check_like(q, (B, H, N), q.dtype, gate)
-    with _call_on(q, stream):
+    vshape, gshape = (B, H, N, dv), shape[:3]
+    _dense(k, shape, dtype, device)
+    _dense(v, vshape, dtype, device)
+    _dense(do, vshape, dtype, device)
+    _dense(gate, gshape, dtype, device)
+    with _call_on(device, stream):
         if outs is None:
-            outs = tuple(torch.empty_like(t) for t in (q, k, v, gate))
+            outs = tuple(torch.empty(x, dtype=dtype, device=device) for x in (shape, shape, vshape, gshape))
         dq, dk, dvv, dgate = outs
-        _check_inputs(dq, dk, dvv, dgate)
-        _check_like(q, q.shape, q.dtype, dq, dk)
-        _check_like(q, (B, H, N, dv), q.dtype, dvv)
-        _check_like(q, (B, H, N), q.dtype, dgate)
-        need = workspace_bytes_gated(B, H, N, d, dv, dt, True)
-        ws = workspace if workspace is not None else _workspace(need, q.device, None)
-        _check_workspace(ws, need, q.device)
-        _raise(la2_backward_gated(_ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(do), _ptr(dq), _ptr(dk),
-                                  _ptr(dvv), _ptr(dgate), B, H, N, d, dv, dt, _ptr(ws),
-                                  ws.numel() if ws is not None else 0, _stream_handle(stream)))
+        _dense(dq, shape, dtype, device)
+        _dense(dk, shape, dtype, device)
+        _dense(dvv, vshape, dtype, device)
+        _dense(dgate, gshape, dtype, device)
+        ws, wp, wn = _scratch(workspace_bytes_gated(B, H, N, d, dv, dt, True), workspace, device)
+        _raise(la2_backward_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(), do.data_ptr(),
+                                  dq.data_ptr(), dk.data_ptr(), dvv.data_ptr(), dgate.data_ptr(), B, H, N, d, dv,
+                                  dt, wp, wn, _raw_stream(device, stream)))
     return dq, dk, dvv, dgate
 
 
-def _index_list(ref, t, n=None):
-    """A contiguous int32 index list on ref's device (length ``n`` if given)."""
+def _index_list(t, n, device):
+    """Pointer of a contiguous int32 CUDA index list of n entries."""
     import torch
 
-    _check_inputs(t)
-    if t.dim() != 1 or t.dtype != torch.int32 or t.device != ref.device or (n is not None and t.numel() != n):
+    _dense(t, (n,), torch.int32, device)
+    return t.data_ptr()
+
+
+def _pool(state, tail, B, slots, device):
+    """(slot count, pointer of the slot list) of a pool [S,H,d,dv] that B rows work on."""
+    import torch
+
+    if state.dim() != 4 or state.shape[1:] != tail:
         raise La2Error(LA2_ERR_INVALID_ARG)
-    return t
+    S = state.shape[0]
+    _dense(state, state.shape, torch.float32, device)
+    if slots is not None:
+        return S, _index_list(slots, B, device)
+    if S != B:
+        raise La2Error(LA2_ERR_INVALID_ARG)
+    return S, 0
 
 
 def kv_state_gated(k, v, gate, state=None, slots=None, workspace=None, stream=None):
@@ -637,42 +679,22 @@ def kv_state_gated(k, v, gate, state=None, slots=None, workspace=None, stream=No
     slot b. Returns the state."""
     import torch
 
-    _check_inputs(k, v, gate)
-    if k.dim() != 4 or v.dim() != 4:
-        raise La2Error(LA2_ERR_INVALID_ARG)
-    B, H, N, d = k.shape
+    shape, dtype, dt, device = _dense_ref(k, 4)
+    B, H, N, d = shape
     dv = v.shape[-1]
-    dt = _dtype_code(k)
-    _check_like(k, (B, H, N, dv), k.dtype, v)
-    _check_like(k, (B, H, N), k.dtype, gate)
+    _dense(v, (B, H, N, dv), dtype, device)
+    _dense(gate, shape[:3], dtype, device)
     if state is None and slots is not None:
         raise La2Error(LA2_ERR_INVALID_ARG)
-    with _call_on(k, stream):
+    with _call_on(device, stream):
         if state is None:
-            state = torch.zeros((B, H, d, dv), dtype=torch.float32, device=k.device)
-        S = _pool_slots(k, state, (H, d, dv), B, slots)
+            state = torch.zeros((B, H, d, dv), dtype=torch.float32, device=device)
+        S, sp = _pool(state, (H, d, dv), B, slots, device)
         need = _sized(la2_kv_state_gated_workspace_size(B, H, N, d, dv, dt))
-        ws = workspace if workspace is not None else _workspace(need, k.device, None)
-        _check_workspace(ws, need, k.device)
-        _raise(la2_kv_state_gated(_ptr(k), _ptr(v), _ptr(gate), _ptr(state), _ptr(slots), S, B, H, N, d, dv,
-                                  dt, _ptr(ws), ws.numel() if ws is not None else 0,
-                                  _stream_handle(stream)))
+        ws, wp, wn = _scratch(need, workspace, device)
+        _raise(la2_kv_state_gated(k.data_ptr(), v.data_ptr(), gate.data_ptr(), state.data_ptr(), sp, S, B, H, N,
+                                  d, dv, dt, wp, wn, _raw_stream(device, stream)))
     return state
-
-
-def _pool_slots(ref, state, tail, B, slots):
-    """Slot count of a pool [S,H,d,dv] that B batch rows work on."""
-    import torch
-
-    _check_inputs(state)
-    if state.dim() != 4 or tuple(state.shape[1:]) != tuple(tail) or state.dtype != torch.float32 \
-            or state.device != ref.device:
-        raise La2Error(LA2_ERR_INVALID_ARG)
-    if slots is not None:
-        _index_list(ref, slots, B)
-    elif state.shape[0] != B:
-        raise La2Error(LA2_ERR_INVALID_ARG)
-    return state.shape[0]
 
 
 def decode_step_gated(q, k, v, gate, state, slots=None, out=None, stream=None):
@@ -683,43 +705,45 @@ def decode_step_gated(q, k, v, gate, state, slots=None, out=None, stream=None):
     ``out`` is omitted)."""
     import torch
 
-    _check_inputs(q, k, v, gate)
-    if q.dim() != 3 or v.dim() != 3:
-        raise La2Error(LA2_ERR_INVALID_ARG)
-    B, H, d = q.shape
+    shape, dtype, dt, device = _dense_ref(q, 3)
+    B, H, d = shape
     dv = v.shape[-1]
-    dt = _dtype_code(q)
-    _check_like(q, q.shape, q.dtype, k)
-    _check_like(q, (B, H, dv), q.dtype, v)
-    _check_like(q, (B, H), q.dtype, gate)
-    S = _pool_slots(q, state, (H, d, dv), B, slots)
-    with _call_on(q, stream):
+    _dense(k, shape, dtype, device)
+    _dense(v, (B, H, dv), dtype, device)
+    _dense(gate, (B, H), dtype, device)
+    S, sp = _pool(state, (H, d, dv), B, slots, device)
+    with _call_on(device, stream):
         if out is None:
             make = torch.empty if slots is None else torch.zeros
-            out = make((B, H, dv), dtype=q.dtype, device=q.device)
-        _check_inputs(out)
-        _check_like(q, (B, H, dv), q.dtype, out)
-        _raise(la2_decode_step_gated(_ptr(q), _ptr(k), _ptr(v), _ptr(gate), _ptr(out), _ptr(state),
-                                     _ptr(slots), S, B, H, d, dv, dt, _stream_handle(stream)))
+            out = make((B, H, dv), dtype=dtype, device=device)
+        else:
+            _dense(out, (B, H, dv), dtype, device)
+        _raise(la2_decode_step_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(), out.data_ptr(),
+                                     state.data_ptr(), sp, S, B, H, d, dv, dt, _raw_stream(device, stream)))
     return out
 
 
 # --------------------------------------------------------------- state slots
 
 
+def _whole_pool(state):
+    import torch
+
+    if state.dim() != 4 or not state.is_cuda:
+        raise La2Error(LA2_ERR_INVALID_ARG)
+    _dense(state, state.shape, torch.float32, state.device)
+    return state.device
+
+
 def state_copy(state, src, dst, stream=None):
     """Slot dst[i] of the pool ``state`` [S,H,d,dv] float32 <- slot src[i], or zeros
     where src[i] is -1; dst[i] = -1 does nothing (int32 CUDA lists). Returns the pool."""
-    import torch
-
-    _check_inputs(state)
-    if state.dim() != 4 or state.dtype != torch.float32:
-        raise La2Error(LA2_ERR_INVALID_ARG)
-    n = _index_list(state, src).numel()
-    _index_list(state, dst, n)
+    device = _whole_pool(state)
+    n = src.numel()
+    sp, dp = _index_list(src, n, device), _index_list(dst, n, device)
     S, H, d, dv = state.shape
-    with _call_on(state, stream):
-        _raise(la2_state_copy(_ptr(state), _ptr(src), _ptr(dst), n, S, H, d, dv, _stream_handle(stream)))
+    with _call_on(device, stream):
+        _raise(la2_state_copy(state.data_ptr(), sp, dp, n, S, H, d, dv, _raw_stream(device, stream)))
     return state
 
 
@@ -729,57 +753,54 @@ def state_compact(state, live, moved=None, stream=None):
     (int32 [S], -1: was not live)."""
     import torch
 
-    _check_inputs(state)
-    if state.dim() != 4 or state.dtype != torch.float32:
-        raise La2Error(LA2_ERR_INVALID_ARG)
+    device = _whole_pool(state)
     S, H, d, dv = state.shape
-    _index_list(state, live, S)
-    with _call_on(state, stream):
+    lp = _index_list(live, S, device)
+    with _call_on(device, stream):
         if moved is None:
             moved = torch.empty_like(live)
-        _index_list(state, moved, S)
-        _raise(la2_state_compact(_ptr(state), _ptr(live), _ptr(moved), S, H, d, dv, _stream_handle(stream)))
+        mp = _index_list(moved, S, device)
+        _raise(la2_state_compact(state.data_ptr(), lp, mp, S, H, d, dv, _raw_stream(device, stream)))
     return moved
 
 
 # ------------------------------------------- queries and keys: norm, rotation
 
-
-def _strided(x):
-    """(data pointer, element strides of batch, token, head) of a [B,N,heads,d]
-    CUDA tensor with a dense last dimension."""
-    if not x.is_cuda or x.dim() != 4 or (x.shape[-1] > 1 and x.stride(-1) != 1):
-        raise La2Error(LA2_ERR_INVALID_ARG)
-    return _ptr(x), (_i64 * 3)(*x.stride()[:3])
+_i64x3 = _i64 * 3
 
 
 def _rope_args(q, k, wq, wk, positions, rot, sections):
+    """Shapes and pointers of a call; q and k may have any strides but a dense last
+    dimension."""
     import torch
 
-    qp, qs = _strided(q)
-    kp, ks = _strided(k)
+    if q.dim() != 4 or k.dim() != 4 or not q.is_cuda:
+        raise La2Error(LA2_ERR_INVALID_ARG)
+    dt, dtype, device = _dtype_code(q), q.dtype, q.device
     B, N, H, d = q.shape
     Hkv = k.shape[2]
-    _check_like(q, (B, N, Hkv, d), q.dtype, k)
-    dt = _dtype_code(q)
+    qs, ks = q.stride(), k.stride()
+    if k.shape != (B, N, Hkv, d) or k.dtype is not dtype or k.device != device or (d > 1 and (qs[3] != 1 or ks[3] != 1)):
+        raise La2Error(LA2_ERR_INVALID_ARG)
     for w in (wq, wk):
         if w is not None:
-            _check_inputs(w)
-            _check_like(q, (d,), q.dtype, w)
-    rot = d if rot is None else int(rot)
-    axes = 1
+            _dense(w, (d,), dtype, device)
+    axes, pp = 1, 0
     if positions is not None:
-        _check_inputs(positions)
-        axes = positions.shape[0] if positions.dim() == 3 else 1
-        if positions.dtype != torch.int32 or positions.device != q.device \
-                or tuple(positions.shape[-2:]) != (B, N) or positions.dim() not in (2, 3):
-            raise La2Error(LA2_ERR_INVALID_ARG)
+        if positions.dim() == 3:
+            axes = positions.shape[0]
+        _dense(positions, (axes, B, N) if positions.dim() == 3 else (B, N), torch.int32, device)
+        pp = positions.data_ptr()
     elif sections is not None:
         axes = len(sections)
-    if sections is not None and len(sections) != axes:
-        raise La2Error(LA2_ERR_INVALID_ARG)
-    sec = None if sections is None else (_i64 * axes)(*[int(x) for x in sections])
-    return qp, kp, qs, ks, B, N, H, Hkv, d, rot, axes, sec, dt
+    sec = None
+    if sections is not None:
+        if len(sections) != axes:
+            raise La2Error(LA2_ERR_INVALID_ARG)
+        sec = (_i64 * axes)(*sections)
+    return (q.data_ptr(), k.data_ptr(), _i64x3(qs[0], qs[1], qs[2]), _i64x3(ks[0], ks[1], ks[2]),
+            wq.data_ptr() if wq is not None else 0, wk.data_ptr() if wk is not None else 0, pp, B, N, H, Hkv, d,
+            d if rot is None else rot, axes, sec, dt, dtype, device)
 
 
 def qk_norm_rope(q, k, wq=None, wk=None, positions=None, base: float = 10000.0, rot=None, sections=None,
@@ -792,18 +813,18 @@ def qk_norm_rope(q, k, wq=None, wk=None, positions=None, base: float = 10000.0, 
     all). Returns (q_out, k_out)."""
     import torch
 
-    qp, kp, qs, ks, B, N, H, Hkv, d, rot, axes, sec, dt = _rope_args(q, k, wq, wk, positions, rot, sections)
-    with _call_on(q, stream):
+    (qp, kp, qs, ks, wqp, wkp, pp, B, N, H, Hkv, d, rot, axes, sec, dt, dtype,
+     device) = _rope_args(q, k, wq, wk, positions, rot, sections)
+    with _call_on(device, stream):
         if outs is None:
-            outs = (torch.empty((B, H, N, d), dtype=q.dtype, device=q.device),
-                    torch.empty((B, Hkv, N, d), dtype=q.dtype, device=q.device))
-        qo, ko = outs
-        _check_inputs(qo, ko)
-        _check_like(q, (B, H, N, d), q.dtype, qo)
-        _check_like(q, (B, Hkv, N, d), q.dtype, ko)
-        _raise(la2_qk_norm_rope(qp, kp, qs, ks, _ptr(wq), _ptr(wk), _ptr(positions), _ptr(qo), _ptr(ko), B, N,
-                                H, Hkv, d, rot, axes, sec, base, eps, q_scale, k_scale, dt,
-                                _stream_handle(stream)))
+            qo = torch.empty((B, H, N, d), dtype=dtype, device=device)
+            ko = torch.empty((B, Hkv, N, d), dtype=dtype, device=device)
+        else:
+            qo, ko = outs
+            _dense(qo, (B, H, N, d), dtype, device)
+            _dense(ko, (B, Hkv, N, d), dtype, device)
+        _raise(la2_qk_norm_rope(qp, kp, qs, ks, wqp, wkp, pp, qo.data_ptr(), ko.data_ptr(), B, N, H, Hkv, d, rot,
+                                axes, sec, base, eps, q_scale, k_scale, dt, _raw_stream(device, stream)))
     return qo, ko
 
 
@@ -815,25 +836,28 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, wq=None, wk=None, positions=None
     None where the weight is)."""
     import torch
 
-    qp, kp, qs, ks, B, N, H, Hkv, d, rot, axes, sec, dt = _rope_args(q, k, wq, wk, positions, rot, sections)
-    _check_inputs(dq_out, dk_out)
-    _check_like(q, (B, H, N, d), q.dtype, dq_out)
-    _check_like(q, (B, Hkv, N, d), q.dtype, dk_out)
-    with _call_on(q, stream):
+    (qp, kp, qs, ks, wqp, wkp, pp, B, N, H, Hkv, d, rot, axes, sec, dt, dtype,
+     device) = _rope_args(q, k, wq, wk, positions, rot, sections)
+    _dense(dq_out, (B, H, N, d), dtype, device)
+    _dense(dk_out, (B, Hkv, N, d), dtype, device)
+    with _call_on(device, stream):
         if outs is None:
-            outs = (torch.empty((B, N, H, d), dtype=q.dtype, device=q.device),
-                    torch.empty((B, N, Hkv, d), dtype=q.dtype, device=q.device),
-                    None if wq is None else torch.empty_like(wq), None if wk is None else torch.empty_like(wk))
-        dq, dk, dwq, dwk = outs
-        _check_inputs(dq, dk, *(w for w in (dwq, dwk) if w is not None))
-        _check_like(q, (B, N, H, d), q.dtype, dq)
-        _check_like(q, (B, N, Hkv, d), q.dtype, dk)
-        _check_like(q, (d,), q.dtype, *(w for w in (dwq, dwk) if w is not None))
+            dq = torch.empty((B, N, H, d), dtype=dtype, device=device)
+            dk = torch.empty((B, N, Hkv, d), dtype=dtype, device=device)
+            dwq = None if wq is None else torch.empty_like(wq)
+            dwk = None if wk is None else torch.empty_like(wk)
+        else:
+            dq, dk, dwq, dwk = outs
+            _dense(dq, (B, N, H, d), dtype, device)
+            _dense(dk, (B, N, Hkv, d), dtype, device)
+            for w in (dwq, dwk):
+                if w is not None:
+                    _dense(w, (d,), dtype, device)
         need = _sized(la2_qk_norm_rope_backward_workspace_size(B, N, H, Hkv, d))
-        ws = workspace if workspace is not None else _workspace(need, q.device, None)
-        _check_workspace(ws, need, q.device)
-        _raise(la2_qk_norm_rope_backward(_ptr(dq_out), _ptr(dk_out), qp, kp, qs, ks, _ptr(wq), _ptr(wk),
-                                         _ptr(positions), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk), B, N, H,
-                                         Hkv, d, rot, axes, sec, base, eps, q_scale, k_scale, dt, _ptr(ws),
-                                         ws.numel() if ws is not None else 0, _stream_handle(stream)))
+        ws, wp, wn = _scratch(need, workspace, device)
+        _raise(la2_qk_norm_rope_backward(dq_out.data_ptr(), dk_out.data_ptr(), qp, kp, qs, ks, wqp, wkp, pp,
+                                         dq.data_ptr(), dk.data_ptr(), dwq.data_ptr() if dwq is not None else 0,
+                                         dwk.data_ptr() if dwk is not None else 0, B, N, H, Hkv, d, rot, axes,
+                                         sec, base, eps, q_scale, k_scale, dt, wp, wn,
+                                         _raw_stream(device, stream)))
     return dq, dk, dwq, dwk
