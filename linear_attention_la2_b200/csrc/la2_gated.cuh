@@ -9,6 +9,7 @@ namespace gated {
 struct Plan {
   int64_t L = 0, C = 1;
   bool tc = false;
+  int nel = 0;  // floats of a chunk's state in the workspace
   // Tensor cores: the pieces whose own states are computed (Ls rows, K a sequence,
   // `per` a chunk); per = 0 (and K = C): a scan turns them into the chunks' states.
   int64_t Ls = 0, K = 1, per = 0;
@@ -32,7 +33,7 @@ static la2_status check(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, 
   if (dt == LA2_BF16 && ((d != 64 && d != 128) || (dv != 64 && dv != 128))) return LA2_ERR_UNSUPPORTED;
   if (N > 0x7fffffff - kRows) return LA2_ERR_UNSUPPORTED;  // rows are TMA coordinates
   // one CTA a (sequence, chunk of at least a block), 256 elements of a state a CTA
-  const double nb = std::ceil(double(d) * double(dv) / kThreads);
+  const double nel = dt == LA2_BF16 ? 128.0 * 128.0 : double(d) * double(dv), nb = std::ceil(nel / kThreads);
   if (double(B) * double(H) * std::max(std::ceil(double(N) / kRows), nb) > 2147483647.0)
     return LA2_ERR_UNSUPPORTED;
   return LA2_OK;
@@ -47,7 +48,8 @@ static Plan make_plan_uncached(int64_t B, int64_t H, int64_t N, int64_t d, int64
                                int sms) {
   Plan p;
   const int64_t BH = B * H, T = (N + kRows - 1) / kRows;
-  p.tc = dt == LA2_BF16 && d == 128 && dv == 128;
+  p.tc = dt == LA2_BF16;
+  p.nel = p.tc ? 128 * 128 : static_cast<int>(d * dv);
   int64_t per = 1;
   if (g_chunk_len > 0) {
     p.L = (g_chunk_len + kRows - 1) / kRows * kRows;
@@ -91,7 +93,7 @@ static Plan make_plan_uncached(int64_t B, int64_t H, int64_t N, int64_t d, int64
     p.per = p.K <= kSumPieces ? p.L / p.Ls : 0;
   }
   const bool states = p.C > 1 || need == NEED_STATE;
-  const size_t one = states ? round256((size_t)BH * p.K * d * dv * sizeof(float)) : 0;
+  const size_t one = states ? round256((size_t)BH * p.K * p.nel * sizeof(float)) : 0;
   size_t at = one;
   p.off_suffix = at;
   if (need == NEED_BWD) at += one;
@@ -139,19 +141,19 @@ static bool raise_smem(Kernel kern, size_t bytes) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
 }
 
-template <typename T, bool SUFFIX>
+template <bool SUFFIX>
 static la2_status chunk_states(const void* a, const void* b, const void* gate, float* out, double* tot,
                                int64_t BH, const Shape& sh, cudaStream_t st) {
   const size_t smem = smem_bytes(sh.d, sh.dv, 1, 1, 0);
-  if (!raise_smem(chunk_state_kernel<T, SUFFIX>, smem)) return LA2_ERR_CUDA;
+  if (!raise_smem(chunk_state_kernel<SUFFIX>, smem)) return LA2_ERR_CUDA;
   LaunchTimer t(K_GATED_STATE, st);
-  chunk_state_kernel<T, SUFFIX><<<(unsigned)(BH * sh.C), kThreads, smem, st>>>(
-      static_cast<const T*>(a), static_cast<const T*>(b), static_cast<const T*>(gate), out, tot, sh);
+  chunk_state_kernel<SUFFIX><<<(unsigned)(BH * sh.C), kThreads, smem, st>>>(
+      static_cast<const float*>(a), static_cast<const float*>(b), static_cast<const float*>(gate), out, tot, sh);
   return launch_status();
 }
 
-static la2_status scan(float* s, const double* tot, int64_t BH, const Shape& sh, int mode, cudaStream_t st) {
-  const int nel = sh.d * sh.dv, nb = (nel + kThreads - 1) / kThreads;
+static la2_status scan(float* s, const double* tot, int64_t BH, const Shape& sh, int nel, int mode, cudaStream_t st) {
+  const int nb = (nel + kThreads - 1) / kThreads;
   LaunchTimer t(K_GATED_SCAN, st);
   if (launch_pdl(scan_kernel, dim3((unsigned)(BH * nb)), dim3(kThreads), 0, st, s, tot, sh.C, nel, mode) !=
       cudaSuccess)
@@ -159,22 +161,21 @@ static la2_status scan(float* s, const double* tot, int64_t BH, const Shape& sh,
   return launch_status();
 }
 
-template <typename T>
 static la2_status forward(const void* q, const void* k, const void* v, const void* gate, void* o, char* ws,
                           const Plan& p, int64_t BH, const Shape& sh, cudaStream_t st) {
   float* states = p.C > 1 ? reinterpret_cast<float*>(ws) : nullptr;
   la2_status s = LA2_OK;
   if (states) {
     double* tot = reinterpret_cast<double*>(ws + p.off_tot);
-    if ((s = chunk_states<T, false>(k, v, gate, states, tot, BH, sh, st)) != LA2_OK) return s;
-    if ((s = scan(states, tot, BH, sh, 0, st)) != LA2_OK) return s;
+    if ((s = chunk_states<false>(k, v, gate, states, tot, BH, sh, st)) != LA2_OK) return s;
+    if ((s = scan(states, tot, BH, sh, p.nel, 0, st)) != LA2_OK) return s;
   }
   const size_t smem = smem_bytes(sh.d, sh.dv, 2, 1, 1);
-  if (!raise_smem(fwd_kernel<T>, smem)) return LA2_ERR_CUDA;
+  if (!raise_smem(fwd_kernel, smem)) return LA2_ERR_CUDA;
   LaunchTimer t(K_GATED_FWD, st);
-  fwd_kernel<T><<<(unsigned)(BH * sh.C), kThreads, smem, st>>>(
-      static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
-      static_cast<const T*>(gate), static_cast<T*>(o), states, sh);
+  fwd_kernel<<<(unsigned)(BH * sh.C), kThreads, smem, st>>>(
+      static_cast<const float*>(q), static_cast<const float*>(k), static_cast<const float*>(v),
+      static_cast<const float*>(gate), static_cast<float*>(o), states, sh);
   return launch_status();
 }
 
@@ -197,15 +198,15 @@ static la2_status states_tc(const void* y, const void* z, const void* gate, floa
   p.spin_limit = spin_limit();
   {
     LaunchTimer t(K_GATED_STATE, st);
-    const cudaError_t e = kind == FOR_DK_DV ? launch_state_sm100<true, false>(y, z, p, BH, st)
-                          : kind == FOR_O   ? launch_state_sm100<false, true>(y, z, p, BH, st)
-                                            : launch_state_sm100<false, false>(y, z, p, BH, st);
+    const cudaError_t e = kind == FOR_DK_DV ? launch_state_sm100<true, false>(y, z, sh.d, sh.dv, p, BH, st)
+                          : kind == FOR_O   ? launch_state_sm100<false, true>(y, z, sh.d, sh.dv, p, BH, st)
+                                            : launch_state_sm100<false, false>(y, z, sh.d, sh.dv, p, BH, st);
     if (e != cudaSuccess) return LA2_ERR_CUDA;
   }
   la2_status s = launch_status();
   if (s != LA2_OK || kind == FOR_POOL || pl.per > 0) return s;
-  s = scan(out, tot, BH, sh, kind == FOR_DK_DV ? 1 : 0, st);
-  return s != LA2_OK || !out_t ? s : scan(out_t, tot, BH, sh, 1, st);
+  s = scan(out, tot, BH, sh, pl.nel, kind == FOR_DK_DV ? 1 : 0, st);
+  return s != LA2_OK || !out_t ? s : scan(out_t, tot, BH, sh, pl.nel, 1, st);
 }
 
 static TcParams tc_params(const void* gate, const float* init, const double* tot, const Shape& sh, const Plan& pl) {
@@ -231,7 +232,7 @@ static la2_status forward_tc(const void* q, const void* k, const void* v, const 
     if (s != LA2_OK) return s;
   }
   LaunchTimer t(K_GATED_FWD, st);
-  if (launch_sm100<false, false>(q, k, v, o, nullptr, tc_params(gate, states, tot, sh, p), BH, st) != cudaSuccess)
+  if (launch_sm100<false, false>(q, k, v, o, nullptr, sh.d, sh.dv, tc_params(gate, states, tot, sh, p), BH, st) != cudaSuccess)
     return LA2_ERR_CUDA;
   return launch_status();
 }
@@ -259,15 +260,15 @@ static la2_status backward_tc(const void* q, const void* k, const void* v, const
     TcParams t = tc_params(gate, prefix, tot, sh, p);
     t.dots = qdq;
     LaunchTimer lt(K_GATED_DQ, st);
-    if (launch_sm100<false, true>(dout, v, k, dq, q, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
+    if (launch_sm100<false, true>(dout, v, k, dq, q, sh.dv, sh.d, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
   }
   {
     TcParams t = tc_params(gate, suffix_t, tot, sh, p);
     LaunchTimer lt(K_GATED_DKDV, st);
-    if (launch_sm100<true, false>(k, q, dout, dvv, nullptr, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
+    if (launch_sm100<true, false>(k, q, dout, dvv, nullptr, sh.d, sh.dv, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
     t.init = suffix;
     t.dots = kdk;
-    if (launch_sm100<true, true>(v, dout, q, dk, k, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
+    if (launch_sm100<true, true>(v, dout, q, dk, k, sh.dv, sh.d, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
   }
   if ((s = launch_status()) != LA2_OK) return s;
   return gate_grad<__nv_bfloat16>(gate, qdq, kdk, prefix, suffix, tot, dgate, BH, sh, p, st);
@@ -280,12 +281,11 @@ static la2_status gate_grad(const void* gate, const float* qdq, const float* kdk
   LaunchTimer t(K_GATED_GATE, st);
   if (launch_pdl(gate_grad_kernel<T>, dim3((unsigned)(BH * sh.C)), dim3(kGradThreads), 0, st,
                  static_cast<const T*>(gate), qdq, kdk, prefix, suffix, tot, static_cast<T*>(dgate), sh.N,
-                 sh.L, sh.C, sh.d * sh.dv, p.K, p.per) != cudaSuccess)
+                 sh.L, sh.C, p.nel, p.K, p.per) != cudaSuccess)
     return LA2_ERR_CUDA;
   return launch_status();
 }
 
-template <typename T>
 static la2_status backward(const void* q, const void* k, const void* v, const void* gate, const void* dout,
                            void* dq, void* dk, void* dvv, void* dgate, char* ws, const Plan& p, int64_t BH,
                            const Shape& sh, cudaStream_t st) {
@@ -296,30 +296,30 @@ static la2_status backward(const void* q, const void* k, const void* v, const vo
   double* tot = reinterpret_cast<double*>(ws + p.off_tot);
   la2_status s = LA2_OK;
   if (prefix) {
-    if ((s = chunk_states<T, false>(k, v, gate, prefix, tot, BH, sh, st)) != LA2_OK) return s;
-    if ((s = scan(prefix, tot, BH, sh, 0, st)) != LA2_OK) return s;
-    if ((s = chunk_states<T, true>(q, dout, gate, suffix, tot, BH, sh, st)) != LA2_OK) return s;
-    if ((s = scan(suffix, tot, BH, sh, 1, st)) != LA2_OK) return s;
+    if ((s = chunk_states<false>(k, v, gate, prefix, tot, BH, sh, st)) != LA2_OK) return s;
+    if ((s = scan(prefix, tot, BH, sh, p.nel, 0, st)) != LA2_OK) return s;
+    if ((s = chunk_states<true>(q, dout, gate, suffix, tot, BH, sh, st)) != LA2_OK) return s;
+    if ((s = scan(suffix, tot, BH, sh, p.nel, 1, st)) != LA2_OK) return s;
   }
-  const T *tq = static_cast<const T*>(q), *tk = static_cast<const T*>(k), *tv = static_cast<const T*>(v),
-          *tg = static_cast<const T*>(gate), *td = static_cast<const T*>(dout);
+  const float *tq = static_cast<const float*>(q), *tk = static_cast<const float*>(k), *tv = static_cast<const float*>(v),
+          *tg = static_cast<const float*>(gate), *td = static_cast<const float*>(dout);
   const unsigned grid = (unsigned)(BH * sh.C);
   {
     const size_t smem = smem_bytes(sh.d, sh.dv, 1, 2, 1);
-    if (!raise_smem(bwd_dq_kernel<T>, smem)) return LA2_ERR_CUDA;
+    if (!raise_smem(bwd_dq_kernel, smem)) return LA2_ERR_CUDA;
     LaunchTimer t(K_GATED_DQ, st);
-    bwd_dq_kernel<T><<<grid, kThreads, smem, st>>>(tq, tk, tv, tg, td, static_cast<T*>(dq), qdq, prefix, sh);
+    bwd_dq_kernel<<<grid, kThreads, smem, st>>>(tq, tk, tv, tg, td, static_cast<float*>(dq), qdq, prefix, sh);
   }
   if ((s = launch_status()) != LA2_OK) return s;
   {
     const size_t smem = smem_bytes(sh.d, sh.dv, 2, 2, 1);
-    if (!raise_smem(bwd_dkdv_kernel<T>, smem)) return LA2_ERR_CUDA;
+    if (!raise_smem(bwd_dkdv_kernel, smem)) return LA2_ERR_CUDA;
     LaunchTimer t(K_GATED_DKDV, st);
-    bwd_dkdv_kernel<T><<<grid, kThreads, smem, st>>>(tq, tk, tv, tg, td, static_cast<T*>(dk),
-                                                     static_cast<T*>(dvv), kdk, suffix, sh);
+    bwd_dkdv_kernel<<<grid, kThreads, smem, st>>>(tq, tk, tv, tg, td, static_cast<float*>(dk),
+                                                     static_cast<float*>(dvv), kdk, suffix, sh);
   }
   if ((s = launch_status()) != LA2_OK) return s;
-  return gate_grad<T>(gate, qdq, kdk, prefix, suffix, tot, dgate, BH, sh, p, st);
+  return gate_grad<float>(gate, qdq, kdk, prefix, suffix, tot, dgate, BH, sh, p, st);
 }
 
 // Pointers of a call: every one non-null and aligned, no output over an input,
@@ -389,8 +389,7 @@ la2_status la2_forward_gated(const void* q, const void* k, const void* v, const 
   const gated::Shape sh{N, p.L, p.C, (int)d, (int)dv};
   char* ws = static_cast<char*>(workspace);
   if (p.tc) return gated::forward_tc(q, k, v, gate, o, ws, p, B * H, sh, st);
-  return dt == LA2_BF16 ? gated::forward<__nv_bfloat16>(q, k, v, gate, o, ws, p, B * H, sh, st)
-                        : gated::forward<float>(q, k, v, gate, o, ws, p, B * H, sh, st);
+  return gated::forward(q, k, v, gate, o, ws, p, B * H, sh, st);
 }
 
 la2_status la2_backward_gated(const void* q, const void* k, const void* v, const void* gate,
@@ -414,9 +413,7 @@ la2_status la2_backward_gated(const void* q, const void* k, const void* v, const
   const gated::Shape sh{N, p.L, p.C, (int)d, (int)dv};
   char* ws = static_cast<char*>(workspace);
   if (p.tc) return gated::backward_tc(q, k, v, gate, dout, dq, dk, dvv, dgate, ws, p, B * H, sh, st);
-  return dt == LA2_BF16
-             ? gated::backward<__nv_bfloat16>(q, k, v, gate, dout, dq, dk, dvv, dgate, ws, p, B * H, sh, st)
-             : gated::backward<float>(q, k, v, gate, dout, dq, dk, dvv, dgate, ws, p, B * H, sh, st);
+  return gated::backward(q, k, v, gate, dout, dq, dk, dvv, dgate, ws, p, B * H, sh, st);
 }
 
 size_t la2_kv_state_gated_workspace_size(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, la2_dtype dt) {
@@ -451,14 +448,13 @@ la2_status la2_kv_state_gated(const void* k, const void* v, const void* gate, fl
   if (p.tc)
     s = gated::states_tc(k, v, gate, chunks, nullptr, tot, B * H, sh, p, gated::FOR_POOL, st);
   else
-    s = dt == LA2_BF16 ? gated::chunk_states<__nv_bfloat16, false>(k, v, gate, chunks, tot, B * H, sh, st)
-                       : gated::chunk_states<float, false>(k, v, gate, chunks, tot, B * H, sh, st);
+    s = gated::chunk_states<false>(k, v, gate, chunks, tot, B * H, sh, st);
   if (s != LA2_OK) return s;
   const int64_t nb = (d * dv + gated::kThreads - 1) / gated::kThreads;
   LaunchTimer t(K_GATED_POOL, st);
   if (launch_pdl(gated::pool_update_kernel, dim3((unsigned)(B * H * nb)), dim3(gated::kThreads), 0, st,
                  static_cast<const float*>(chunks), static_cast<const double*>(tot), state, slots, n_slots,
-                 p.C, (int)H, (int)d, (int)dv, p.tc ? 1 : 0) != cudaSuccess)
+                 p.C, (int)H, (int)d, (int)dv, p.nel, p.tc ? 128 : 0) != cudaSuccess)
     return LA2_ERR_CUDA;
   return launch_status();
 }

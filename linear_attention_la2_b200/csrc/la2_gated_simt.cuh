@@ -124,12 +124,11 @@ struct One1 { __device__ float operator()(int) const { return 1.f; } };
 struct NoRow { __device__ void operator()(int, float, int) const {} };
 
 // Rows [0, rows) of a [*, w] tensor into an fp32 tile of stride odd(w); the rest zero.
-template <typename T>
-__device__ __forceinline__ void load_rows(float* dst, const T* __restrict__ src, int rows, int w) {
+__device__ __forceinline__ void load_rows(float* dst, const float* __restrict__ src, int rows, int w) {
   const int ld = odd(w);
   for (int i = threadIdx.x; i < kRows * w; i += kThreads) {
     const int r = i / w, c = i - r * w;
-    dst[r * ld + c] = r < rows ? to_f32(src[i]) : 0.f;
+    dst[r * ld + c] = r < rows ? src[i] : 0.f;
   }
 }
 
@@ -137,14 +136,13 @@ __device__ __forceinline__ void load_rows(float* dst, const T* __restrict__ src,
 // and the weights e^(c_t) and e^(c_R - c_t). `start`: the block opens its sequence,
 // where nothing comes before the first token for its gate to pass on (0, unless NaN).
 // Ends with a barrier.
-template <typename T>
-__device__ __forceinline__ void gate_tables(const T* __restrict__ gate, int rows, bool start, double* c,
+__device__ __forceinline__ void gate_tables(const float* __restrict__ gate, int rows, bool start, double* c,
                                             float* head, float* tail) {
   if (threadIdx.x < 32) {
     const int i = 2 * threadIdx.x;
-    double x = i < rows ? gate_log(to_f32(gate[i])) : 0.0;
+    double x = i < rows ? gate_log(gate[i]) : 0.0;
     if (start && i == 0 && x == x) x = 0.0;
-    const double y = i + 1 < rows ? gate_log(to_f32(gate[i + 1])) : 0.0;
+    const double y = i + 1 < rows ? gate_log(gate[i + 1]) : 0.0;
     double s = x + y;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -204,9 +202,9 @@ __host__ __device__ __forceinline__ size_t smem_bytes(int d, int dv, int a, int 
 // Own state of every chunk: SUFFIX false, sum_s e^(rest of the chunk's gates) a_s^T b_s
 // (the state after the chunk); SUFFIX true, sum_t e^(the chunk's gates up to t)
 // a_t^T b_t (decayed back to the row before the chunk). tot: the chunk's sum of gates.
-template <typename T, bool SUFFIX>
+template <bool SUFFIX>
 __global__ void __launch_bounds__(kThreads)
-chunk_state_kernel(const T* __restrict__ a, const T* __restrict__ b, const T* __restrict__ gate,
+chunk_state_kernel(const float* __restrict__ a, const float* __restrict__ b, const float* __restrict__ gate,
                    float* __restrict__ out, double* __restrict__ tot, const Shape sh) {
   extern __shared__ double smem_d[];
   double* c = smem_d;
@@ -237,10 +235,9 @@ chunk_state_kernel(const T* __restrict__ a, const T* __restrict__ b, const T* __
   if (threadIdx.x == 0) tot[blockIdx.x] = sum;
 }
 
-template <typename T>
 __global__ void __launch_bounds__(kThreads)
-fwd_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
-           const T* __restrict__ gate, T* __restrict__ o, const float* __restrict__ states, const Shape sh) {
+fwd_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
+           const float* __restrict__ gate, float* __restrict__ o, const float* __restrict__ states, const Shape sh) {
   extern __shared__ double smem_d[];
   const int d = sh.d, dv = sh.dv, ld = odd(d), lv = odd(dv), ls = odd(kRows);
   double* c = smem_d;
@@ -270,13 +267,13 @@ fwd_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict
         },
         NoRow{});
     __syncthreads();
-    T* ob = o + row * dv;
+    float* ob = o + row * dv;
     tile_product(
         rows, dv, d, [&](int r, int x) { return Qs[r * ld + x]; }, [&](int x, int e) { return S[x * lv + e]; },
         [&](int r) { return head[r]; }, rows, [&](int r, int j) { return P[r * ls + j]; },
         [&](int j, int e) { return Vs[j * lv + e]; },
         [&](int t, int e, float x) {
-          ob[t * dv + e] = from_f32<T>(x);
+          ob[t * dv + e] = x;
           return 0.f;
         },
         NoRow{});
@@ -286,10 +283,9 @@ fwd_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict
 }
 
 // dQ_t = sum_{j<=t} e^(c_t - c_j) (dO_t . v_j) k_j + e^(c_t) dO_t KV^T, and q_t . dq_t.
-template <typename T>
 __global__ void __launch_bounds__(kThreads)
-bwd_dq_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
-              const T* __restrict__ gate, const T* __restrict__ dout, T* __restrict__ dq,
+bwd_dq_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
+              const float* __restrict__ gate, const float* __restrict__ dout, float* __restrict__ dq,
               float* __restrict__ qdq, const float* __restrict__ states, const Shape sh) {
   extern __shared__ double smem_d[];
   const int d = sh.d, dv = sh.dv, ld = odd(d), lv = odd(dv), ls = odd(kRows);
@@ -321,15 +317,15 @@ bwd_dq_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restr
         },
         NoRow{});
     __syncthreads();
-    const T* qb = q + row * d;
-    T* ob = dq + row * d;
+    const float* qb = q + row * d;
+    float* ob = dq + row * d;
     tile_product(
         rows, d, dv, [&](int r, int e) { return Gs[r * lv + e]; }, [&](int e, int x) { return S[x * lv + e]; },
         [&](int r) { return head[r]; }, rows, [&](int r, int j) { return A[r * ls + j]; },
         [&](int j, int x) { return Ks[j * ld + x]; },
         [&](int t, int x, float y) {
-          ob[t * d + x] = from_f32<T>(y);
-          return to_f32(qb[t * d + x]) * y;
+          ob[t * d + x] = y;
+          return qb[t * d + x] * y;
         },
         [&](int r, float dot, int tc) {
           dot = half_warp_sum(dot);
@@ -342,11 +338,10 @@ bwd_dq_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restr
 }
 
 // dK, dV and k_j . dk_j, blocks of a chunk last to first.
-template <typename T>
 __global__ void __launch_bounds__(kThreads)
-bwd_dkdv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
-                const T* __restrict__ gate, const T* __restrict__ dout, T* __restrict__ dk,
-                T* __restrict__ dvv, float* __restrict__ kdk, const float* __restrict__ states,
+bwd_dkdv_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
+                const float* __restrict__ gate, const float* __restrict__ dout, float* __restrict__ dk,
+                float* __restrict__ dvv, float* __restrict__ kdk, const float* __restrict__ states,
                 const Shape sh) {
   extern __shared__ double smem_d[];
   const int d = sh.d, dv = sh.dv, ld = odd(d), lv = odd(dv), ls = odd(kRows);
@@ -383,13 +378,13 @@ bwd_dkdv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __res
         },
         NoRow{});
     __syncthreads();
-    T* vb = dvv + row * dv;
+    float* vb = dvv + row * dv;
     tile_product(
         rows, dv, d, [&](int j, int x) { return Ks[j * ld + x]; }, [&](int x, int e) { return U[x * lv + e]; },
         [&](int j) { return tail[j]; }, rows, [&](int j, int t) { return P[t * ls + j]; },
         [&](int t, int e) { return Gs[t * lv + e]; },
         [&](int j, int e, float y) {
-          vb[j * dv + e] = from_f32<T>(y);
+          vb[j * dv + e] = y;
           return 0.f;
         },
         NoRow{});
@@ -403,13 +398,13 @@ bwd_dkdv_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __res
         },
         NoRow{});
     __syncthreads();
-    T* kb = dk + row * d;
+    float* kb = dk + row * d;
     tile_product(
         rows, d, dv, [&](int j, int e) { return Vs[j * lv + e]; }, [&](int e, int x) { return U[x * lv + e]; },
         [&](int j) { return tail[j]; }, rows, [&](int j, int t) { return P[t * ls + j]; },
         [&](int t, int x) { return Qs[t * ld + x]; },
         [&](int j, int x, float y) {
-          kb[j * d + x] = from_f32<T>(y);
+          kb[j * d + x] = y;
           return Ks[j * ld + x] * y;
         },
         [&](int j, float dot, int tc) {
@@ -475,12 +470,12 @@ __device__ __forceinline__ int64_t checked_slot(const int32_t* __restrict__ slot
 }
 
 // pool[slot of b][h] <- e^(all gates) pool[slot][h] + the chunks' states decayed to
-// the last token, added in chunk order. chunk_major: the tensor-core layout of the
-// chunk states (float4 j of row r at j*d + r). Grid: ceil(d*dv / 256) blocks a sequence.
+// the last token, added in chunk order. A chunk's state is `nel_c` floats; ld > 0: in
+// the tensor cores' layout of ld rows (float4 j of row r at j*ld + r). Grid: ceil(d*dv / 256) blocks a sequence.
 __global__ void __launch_bounds__(kThreads)
 pool_update_kernel(const float* __restrict__ chunks, const double* __restrict__ tot, float* __restrict__ pool,
                    const int32_t* __restrict__ slots, int64_t n_slots, int64_t C, int H, int d, int dv,
-                   int chunk_major) {
+                   int nel_c, int ld) {
   pdl_launch_dependents();
   pdl_wait();
   const int nel = d * dv, nb = (nel + kThreads - 1) / kThreads;
@@ -489,11 +484,11 @@ pool_update_kernel(const float* __restrict__ chunks, const double* __restrict__ 
   const int e = static_cast<int>(blockIdx.x % nb) * kThreads + threadIdx.x;
   if (slot < 0 || e >= nel) return;
   const int r = e / dv, c = e % dv;
-  const float* p = chunks + bh * C * nel + (chunk_major ? ((c >> 2) * d + r) * 4 + (c & 3) : e);
+  const float* p = chunks + bh * C * nel_c + (ld ? ((c >> 2) * ld + r) * 4 + (c & 3) : e);
   float* out = pool + (slot * H + (bh - b * H)) * nel + e;
   float run = *out;
   for (int64_t ch = 0; ch < C; ++ch)
-    run = fmaf(expf(static_cast<float>(tot[bh * C + ch])), run, p[ch * nel]);
+    run = fmaf(expf(static_cast<float>(tot[bh * C + ch])), run, p[ch * nel_c]);
   *out = run;
 }
 

@@ -1,4 +1,4 @@
-// Tensor-core kernels of the gated recurrence (bf16, d = dv = 128, sm_100a); the
+// Tensor-core kernels of the gated recurrence (bf16, d and dv 64 or 128, sm_100a); the
 // formulas are at the top of la2_gated_simt.cuh. The PTX wrappers, operand
 // descriptors, bounded waits and TMEM layouts are those of la2_sm100.cuh.
 //
@@ -44,6 +44,11 @@
 // products, the same weights), so the near parts agree; for the far parts the state's
 // copy is kept as value and remainder too (2^-17 instead of 2^-9). The dots' rows are
 // loaded into the output's staging tile, read there and overwritten by the output.
+//
+// Widths of 64 run as 128: the tensor maps end at the tensor's width, so that the tiles'
+// second 64 columns arrive as zeros and are not stored, and the chunk states' other rows
+// and columns are zeros. The blocks' time is that of 128, a third of the CUDA cores' at
+// 64 (B4 H4 N2K: forward 97 -> 31 us, gradients 245 -> 105 us).
 //
 // The roles' inner loops stay rolled: five roles share each scheduler, and unrolled
 // over a block their instructions came from beyond its instruction cache.
@@ -150,6 +155,7 @@ struct TcParams {
   // behind it), each decayed over those between. per = 0: init holds one state a
   // chunk, scanned already.
   int32_t K, per;
+  int32_t halves;  // 64-column halves of an output row
 };
 
 template <bool GRAD>
@@ -732,7 +738,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       if (!wait(staged, i & 1, 91)) break;
       if (lane == 0) {
         // A chunk ends on a block boundary or at N, where the tensor map clips.
-        for (int p = 0; p < 2; ++p)
+        for (int p = 0; p < prm.halves; ++p)
           s::tma_store_3d(&tm_o, smem + CF::OFF_OUT + (i & 1) * kTile + p * 8192, 64 * p,
                           static_cast<int>(row_of(i)), static_cast<int>(bh));
         s::bulk_commit_group();
@@ -972,22 +978,25 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
 // -------------------------------------------------------------------- launches
 
 template <bool SUFFIX, bool ROWS_Z>
-inline cudaError_t launch_state_sm100(const void* y, const void* z, const TcStateParams& p, int64_t BH, cudaStream_t st) {
+inline cudaError_t launch_state_sm100(const void* y, const void* z, int wy, int wz, const TcStateParams& p, int64_t BH,
+                                      cudaStream_t st) {
   CUtensorMap ty, tz;
-  if (!make_tmap_3d(&ty, y, BH, p.N, 128, 64) || !make_tmap_3d(&tz, z, BH, p.N, 128, 64)) return cudaErrorInvalidValue;
+  if (!make_tmap_3d(&ty, y, BH, p.N, wy, 64) || !make_tmap_3d(&tz, z, BH, p.N, wz, 64)) return cudaErrorInvalidValue;
   auto kern = gated_state_sm100_kernel<SUFFIX, ROWS_Z>;
   static bool done[128];
   if (!smem_attribute_set(kern, StateCfg::SMEM, done)) return cudaErrorInvalidValue;
   return launch_pdl(kern, dim3((unsigned)(BH * p.count)), dim3(384), StateCfg::SMEM, st, ty, tz, p);
 }
 
+// Widths: x and y wx; z, the output and the dots' rows wz.
 template <bool BACK, bool GRAD>
 inline cudaError_t launch_sm100(const void* x, const void* y, const void* z, void* o, const void* dot_rows,
-                                const TcParams& p, int64_t BH, cudaStream_t st) {
+                                int wx, int wz, TcParams p, int64_t BH, cudaStream_t st) {
+  p.halves = wz / 64;
   CUtensorMap tx, ty, tz, to, td;
-  if (!make_tmap_3d(&tx, x, BH, p.N, 128, 64) || !make_tmap_3d(&ty, y, BH, p.N, 128, 64) ||
-      !make_tmap_3d(&tz, z, BH, p.N, 128, 64) || !make_tmap_3d(&to, o, BH, p.N, 128, 64) ||
-      !make_tmap_3d(&td, GRAD ? dot_rows : x, BH, p.N, 128, 64))
+  if (!make_tmap_3d(&tx, x, BH, p.N, wx, 64) || !make_tmap_3d(&ty, y, BH, p.N, wx, 64) ||
+      !make_tmap_3d(&tz, z, BH, p.N, wz, 64) || !make_tmap_3d(&to, o, BH, p.N, wz, 64) ||
+      !make_tmap_3d(&td, GRAD ? dot_rows : z, BH, p.N, wz, 64))
     return cudaErrorInvalidValue;
   auto kern = gated_sm100_kernel<BACK, GRAD>;
   static bool done[128];
