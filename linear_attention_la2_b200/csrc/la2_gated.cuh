@@ -39,11 +39,10 @@ static la2_status check(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, 
   return LA2_OK;
 }
 
-// Chunks of a sequence run in parallel. CUDA cores: about two CTAs an SM, at least
-// two blocks each; in the backward at most 512 rows, over which the gates' gradient
-// is a running difference of row dots (see la2_gated_simt.cuh). Tensor cores: one CTA
-// an SM, so the count is the one whose waves of CTAs, times blocks a chunk and a fixed
-// cost, are shortest; more than one chunk adds the pass over the chunks' own states.
+// Chunks of a sequence run in parallel: the count is the one whose waves of CTAs, times
+// blocks a chunk and a fixed cost, are shortest; more than one chunk adds the pass over
+// the chunks' own states. CUDA cores: in the backward at most 512 rows a chunk, over
+// which the gates' gradient is a running difference of row dots (see la2_gated_simt.cuh).
 static Plan make_plan_uncached(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, la2_dtype dt, Need need,
                                int sms) {
   Plan p;
@@ -79,16 +78,34 @@ static Plan make_plan_uncached(int64_t B, int64_t H, int64_t N, int64_t d, int64
     p.Ls = (T + best_c * per - 1) / (best_c * per) * kRows;
     p.L = p.Ls * per;
   } else {
-    const int64_t want = (2 * (int64_t)std::max(sms, 1) + BH - 1) / BH;
-    const int64_t C = std::min<int64_t>(want, std::max<int64_t>(1, T / 2));
-    p.L = (T + C - 1) / C * kRows;
+    // in blocks of the main pass (both gradients count as two of its CTAs): its waves,
+    // a block of the state pass, and the launches that more than one chunk adds
+    const double block = need == NEED_BWD ? 0.25 : 0.4;
+    const size_t smem = need == NEED_BWD   ? smem_bytes((int)d, (int)dv, 2, 2, 1)
+                        : need == NEED_FWD ? smem_bytes((int)d, (int)dv, 2, 1, 1)
+                                           : smem_bytes((int)d, (int)dv, 1, 1, 0);
+    const int64_t slots = std::max(sms, 1) * (smem <= 113 * 1024 ? 2 : 1), ctas = need == NEED_BWD ? 2 : 1;
+    auto waves = [&](int64_t units) { return static_cast<double>((units + slots - 1) / slots); };
+    double best = -1.0;
+    for (int64_t c = 1; c <= T && (c == 1 || BH * (c - 1) < 4 * slots); ++c) {
+      const int64_t rows = (T + c - 1) / c;
+      double cost = need == NEED_STATE ? 0.0 : waves(ctas * BH * c) * (static_cast<double>(rows) + 0.3);
+      if (need == NEED_STATE || c > 1) cost += waves(ctas * BH * c) * (block * static_cast<double>(rows) + 0.3);
+      if (c > kSumPieces) cost += 0.4;
+      if (best < 0.0 || cost < best) {
+        best = cost;
+        p.L = rows * kRows;
+      }
+    }
     if (need == NEED_BWD) p.L = std::min<int64_t>(p.L, 512);
   }
   p.L = std::max<int64_t>(p.L, kRows);
   p.C = std::max<int64_t>(1, (N + p.L - 1) / p.L);
   p.K = p.C;
   if (p.tc && p.Ls == 0) p.Ls = p.L;
-  if (p.tc && need != NEED_STATE) {
+  if (!p.tc) {
+    p.per = p.C <= kSumPieces ? 1 : 0;
+  } else if (need != NEED_STATE) {
     p.K = std::max<int64_t>(1, (N + p.Ls - 1) / p.Ls);
     p.per = p.K <= kSumPieces ? p.L / p.Ls : 0;
   }
@@ -141,22 +158,37 @@ static bool raise_smem(Kernel kern, size_t bytes) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
 }
 
-template <bool SUFFIX>
-static la2_status chunk_states(const void* a, const void* b, const void* gate, float* out, double* tot,
-                               int64_t BH, const Shape& sh, cudaStream_t st) {
+// CUDA cores: the chunks' own states of (a0, b0) as prefixes and, with out1, of
+// (a1, b1) as suffixes; `all`: every chunk's.
+static la2_status chunk_states(const void* a0, const void* b0, const void* a1, const void* b1, const void* gate,
+                               float* out0, float* out1, double* tot, bool all, int64_t BH, const Shape& sh,
+                               cudaStream_t st) {
   const size_t smem = smem_bytes(sh.d, sh.dv, 1, 1, 0);
-  if (!raise_smem(chunk_state_kernel<SUFFIX>, smem)) return LA2_ERR_CUDA;
+  if (!raise_smem(chunk_state_kernel, smem)) return LA2_ERR_CUDA;
+  StateArgs p{};
+  p.a[0] = static_cast<const float*>(a0);
+  p.b[0] = static_cast<const float*>(b0);
+  p.a[1] = static_cast<const float*>(a1);
+  p.b[1] = static_cast<const float*>(b1);
+  p.gate = static_cast<const float*>(gate);
+  p.out[0] = out0;
+  p.out[1] = out1;
+  p.tot = tot;
+  p.all = all;
   LaunchTimer t(K_GATED_STATE, st);
-  chunk_state_kernel<SUFFIX><<<(unsigned)(BH * sh.C), kThreads, smem, st>>>(
-      static_cast<const float*>(a), static_cast<const float*>(b), static_cast<const float*>(gate), out, tot, sh);
+  if (launch_pdl(chunk_state_kernel, dim3((unsigned)(BH * sh.C), out1 ? 2 : 1), dim3(kThreads), smem, st, p, sh) !=
+      cudaSuccess)
+    return LA2_ERR_CUDA;
   return launch_status();
 }
 
-static la2_status scan(float* s, const double* tot, int64_t BH, const Shape& sh, int nel, int mode, cudaStream_t st) {
+// Scans s0 in mode0 and, where given, s1 in mode 1 (see scan_kernel).
+static la2_status scan(float* s0, float* s1, const double* tot, int64_t BH, const Shape& sh, int nel, int mode0,
+                       cudaStream_t st) {
   const int nb = (nel + kThreads - 1) / kThreads;
   LaunchTimer t(K_GATED_SCAN, st);
-  if (launch_pdl(scan_kernel, dim3((unsigned)(BH * nb)), dim3(kThreads), 0, st, s, tot, sh.C, nel, mode) !=
-      cudaSuccess)
+  if (launch_pdl(scan_kernel, dim3((unsigned)(BH * nb), s1 ? 2 : 1), dim3(kThreads), 0, st, s0, s1, tot, sh.C, nel,
+                 mode0) != cudaSuccess)
     return LA2_ERR_CUDA;
   return launch_status();
 }
@@ -164,18 +196,21 @@ static la2_status scan(float* s, const double* tot, int64_t BH, const Shape& sh,
 static la2_status forward(const void* q, const void* k, const void* v, const void* gate, void* o, char* ws,
                           const Plan& p, int64_t BH, const Shape& sh, cudaStream_t st) {
   float* states = p.C > 1 ? reinterpret_cast<float*>(ws) : nullptr;
+  double* tot = reinterpret_cast<double*>(ws + p.off_tot);
   la2_status s = LA2_OK;
   if (states) {
-    double* tot = reinterpret_cast<double*>(ws + p.off_tot);
-    if ((s = chunk_states<false>(k, v, gate, states, tot, BH, sh, st)) != LA2_OK) return s;
-    if ((s = scan(states, tot, BH, sh, p.nel, 0, st)) != LA2_OK) return s;
+    // (all: the scan reads every chunk's)
+    if ((s = chunk_states(k, v, nullptr, nullptr, gate, states, nullptr, tot, !p.per, BH, sh, st)) != LA2_OK) return s;
+    if (!p.per && (s = scan(states, nullptr, tot, BH, sh, p.nel, 0, st)) != LA2_OK) return s;
   }
   const size_t smem = smem_bytes(sh.d, sh.dv, 2, 1, 1);
   if (!raise_smem(fwd_kernel, smem)) return LA2_ERR_CUDA;
   LaunchTimer t(K_GATED_FWD, st);
-  fwd_kernel<<<(unsigned)(BH * sh.C), kThreads, smem, st>>>(
-      static_cast<const float*>(q), static_cast<const float*>(k), static_cast<const float*>(v),
-      static_cast<const float*>(gate), static_cast<float*>(o), states, sh);
+  if (launch_pdl(fwd_kernel, dim3((unsigned)(BH * sh.C)), dim3(kThreads), smem, st, static_cast<const float*>(q),
+                 static_cast<const float*>(k), static_cast<const float*>(v), static_cast<const float*>(gate),
+                 static_cast<float*>(o), static_cast<const float*>(states), static_cast<const double*>(tot),
+                 sh) != cudaSuccess)
+    return LA2_ERR_CUDA;
   return launch_status();
 }
 
@@ -205,8 +240,7 @@ static la2_status states_tc(const void* y, const void* z, const void* gate, floa
   }
   la2_status s = launch_status();
   if (s != LA2_OK || kind == FOR_POOL || pl.per > 0) return s;
-  s = scan(out, tot, BH, sh, pl.nel, kind == FOR_DK_DV ? 1 : 0, st);
-  return s != LA2_OK || !out_t ? s : scan(out_t, tot, BH, sh, pl.nel, 1, st);
+  return scan(out, out_t, tot, BH, sh, pl.nel, kind == FOR_DK_DV ? 1 : 0, st);  // (out_t: suffixes only)
 }
 
 static TcParams tc_params(const void* gate, const float* init, const double* tot, const Shape& sh, const Plan& pl) {
@@ -291,35 +325,35 @@ static la2_status backward(const void* q, const void* k, const void* v, const vo
                            const Shape& sh, cudaStream_t st) {
   float* prefix = p.C > 1 ? reinterpret_cast<float*>(ws) : nullptr;
   float* suffix = p.C > 1 ? reinterpret_cast<float*>(ws + p.off_suffix) : nullptr;
-  float* qdq = reinterpret_cast<float*>(ws + p.off_qdq);
-  float* kdk = reinterpret_cast<float*>(ws + p.off_kdk);
   double* tot = reinterpret_cast<double*>(ws + p.off_tot);
   la2_status s = LA2_OK;
   if (prefix) {
-    if ((s = chunk_states<false>(k, v, gate, prefix, tot, BH, sh, st)) != LA2_OK) return s;
-    if ((s = scan(prefix, tot, BH, sh, p.nel, 0, st)) != LA2_OK) return s;
-    if ((s = chunk_states<true>(q, dout, gate, suffix, tot, BH, sh, st)) != LA2_OK) return s;
-    if ((s = scan(suffix, tot, BH, sh, p.nel, 1, st)) != LA2_OK) return s;
+    if ((s = chunk_states(k, v, q, dout, gate, prefix, suffix, tot, !p.per, BH, sh, st)) != LA2_OK) return s;
+    if (!p.per && (s = scan(prefix, suffix, tot, BH, sh, p.nel, 0, st)) != LA2_OK) return s;
   }
-  const float *tq = static_cast<const float*>(q), *tk = static_cast<const float*>(k), *tv = static_cast<const float*>(v),
-          *tg = static_cast<const float*>(gate), *td = static_cast<const float*>(dout);
-  const unsigned grid = (unsigned)(BH * sh.C);
-  {
-    const size_t smem = smem_bytes(sh.d, sh.dv, 1, 2, 1);
-    if (!raise_smem(bwd_dq_kernel, smem)) return LA2_ERR_CUDA;
-    LaunchTimer t(K_GATED_DQ, st);
-    bwd_dq_kernel<<<grid, kThreads, smem, st>>>(tq, tk, tv, tg, td, static_cast<float*>(dq), qdq, prefix, sh);
-  }
-  if ((s = launch_status()) != LA2_OK) return s;
+  BwdArgs a{};
+  a.q = static_cast<const float*>(q);
+  a.k = static_cast<const float*>(k);
+  a.v = static_cast<const float*>(v);
+  a.gate = static_cast<const float*>(gate);
+  a.dout = static_cast<const float*>(dout);
+  a.dq = static_cast<float*>(dq);
+  a.dk = static_cast<float*>(dk);
+  a.dv = static_cast<float*>(dvv);
+  a.qdq = reinterpret_cast<float*>(ws + p.off_qdq);
+  a.kdk = reinterpret_cast<float*>(ws + p.off_kdk);
+  a.prefix = prefix;
+  a.suffix = suffix;
+  a.tot = tot;
   {
     const size_t smem = smem_bytes(sh.d, sh.dv, 2, 2, 1);
-    if (!raise_smem(bwd_dkdv_kernel, smem)) return LA2_ERR_CUDA;
-    LaunchTimer t(K_GATED_DKDV, st);
-    bwd_dkdv_kernel<<<grid, kThreads, smem, st>>>(tq, tk, tv, tg, td, static_cast<float*>(dk),
-                                                     static_cast<float*>(dvv), kdk, suffix, sh);
+    if (!raise_smem(bwd_kernel, smem)) return LA2_ERR_CUDA;
+    LaunchTimer t(K_GATED_DKDV, st);  // (dQ too)
+    if (launch_pdl(bwd_kernel, dim3((unsigned)(BH * sh.C), 2), dim3(kThreads), smem, st, a, sh) != cudaSuccess)
+      return LA2_ERR_CUDA;
   }
   if ((s = launch_status()) != LA2_OK) return s;
-  return gate_grad<float>(gate, qdq, kdk, prefix, suffix, tot, dgate, BH, sh, p, st);
+  return gate_grad<float>(gate, a.qdq, a.kdk, prefix, suffix, tot, dgate, BH, sh, p, st);
 }
 
 // Pointers of a call: every one non-null and aligned, no output over an input,
@@ -386,7 +420,7 @@ la2_status la2_forward_gated(const void* q, const void* k, const void* v, const 
   s = gated::workspace_ok(workspace, workspace_bytes, p.bytes, in, 4, out, 1);
   if (s != LA2_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const gated::Shape sh{N, p.L, p.C, (int)d, (int)dv};
+  const gated::Shape sh{N, p.L, p.C, (int)d, (int)dv, p.per > 0};
   char* ws = static_cast<char*>(workspace);
   if (p.tc) return gated::forward_tc(q, k, v, gate, o, ws, p, B * H, sh, st);
   return gated::forward(q, k, v, gate, o, ws, p, B * H, sh, st);
@@ -410,7 +444,7 @@ la2_status la2_backward_gated(const void* q, const void* k, const void* v, const
   s = gated::workspace_ok(workspace, workspace_bytes, p.bytes, in, 5, out, 4);
   if (s != LA2_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const gated::Shape sh{N, p.L, p.C, (int)d, (int)dv};
+  const gated::Shape sh{N, p.L, p.C, (int)d, (int)dv, p.per > 0};
   char* ws = static_cast<char*>(workspace);
   if (p.tc) return gated::backward_tc(q, k, v, gate, dout, dq, dk, dvv, dgate, ws, p, B * H, sh, st);
   return gated::backward(q, k, v, gate, dout, dq, dk, dvv, dgate, ws, p, B * H, sh, st);
@@ -442,13 +476,13 @@ la2_status la2_kv_state_gated(const void* k, const void* v, const void* gate, fl
   s = gated::workspace_ok(workspace, workspace_bytes, p.bytes, in, n_in, out, 1);
   if (s != LA2_OK) return s;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const gated::Shape sh{N, p.L, p.C, (int)d, (int)dv};
+  const gated::Shape sh{N, p.L, p.C, (int)d, (int)dv, p.per > 0};
   float* chunks = static_cast<float*>(workspace);
   double* tot = reinterpret_cast<double*>(static_cast<char*>(workspace) + p.off_tot);
   if (p.tc)
     s = gated::states_tc(k, v, gate, chunks, nullptr, tot, B * H, sh, p, gated::FOR_POOL, st);
   else
-    s = gated::chunk_states<false>(k, v, gate, chunks, tot, B * H, sh, st);
+    s = gated::chunk_states(k, v, nullptr, nullptr, gate, chunks, nullptr, tot, true, B * H, sh, st);
   if (s != LA2_OK) return s;
   const int64_t nb = (d * dv + gated::kThreads - 1) / gated::kThreads;
   LaunchTimer t(K_GATED_POOL, st);

@@ -1,5 +1,5 @@
-// CUDA-core kernels of the gated recurrence (every shape and type that the
-// tensor-core kernels of la2_gated_sm100.cuh do not take), and the small fp32
+// CUDA-core kernels of the gated recurrence in fp32 (bf16 is on the tensor cores, see
+// la2_gated_sm100.cuh), and the small fp32
 // kernels both paths share: the scan of chunk states, the pool update after a
 // prefill, and the gradient of the gates.
 //
@@ -30,8 +30,9 @@
 // dQ and dK passes in fp32; the flow at a chunk's end is <KV, U> of the two chunk
 // states there, so the running difference only spans one chunk.
 //
-// What bounds it: shared-memory reads (8 words for 16 multiply-adds per thread),
-// about half of the fp32 rate; the workload is short sequences in fp32.
+// The workload is short sequences in fp32: what counts is how many blocks run at once
+// and how long one takes. A chunk may be a single block; a call's independent parts
+// (both states, both gradients) share a launch.
 #pragma once
 
 #include <algorithm>
@@ -49,67 +50,92 @@ constexpr double kLogZero = -1.0e4;
 __device__ __forceinline__ double gate_log(float x) {
   return x < static_cast<float>(kLogZero) ? kLogZero : static_cast<double>(x);
 }
-__host__ __device__ __forceinline__ int odd(int w) { return w | 1; }  // row stride of a tile in smem
+__host__ __device__ __forceinline__ int round4(int w) { return (w + 3) & ~3; }
+// Row stride of a tile of w columns: whole float4s, an odd number of them, so that a
+// float4 of eight neighbouring rows comes from eight different groups of banks.
+__host__ __device__ __forceinline__ int stride_of(int w) { return ((w + 3) / 4 | 1) * 4; }
 
-// out(r, c) = sum_k a(r, k) b(k, c), optionally scaled per row and continued with
-// a second sum: r < R, c < Cn. Threads are 16 x 16; a thread owns rows tr + 16 i
-// and columns tc + 16 j, so neighbouring lanes read neighbouring (or odd-strided)
-// words. ep(r, c, value) returns what the row's dot adds; rowend(r, dot) is called
-// by one lane a row, always the same one, after each tile of 64 columns.
-template <class A1, class B1, class SC, class A2, class B2, class EP, class RE>
-__device__ __forceinline__ void tile_product(int R, int Cn, int K1, A1 a1, B1 b1, SC scale, int K2, A2 a2,
-                                             B2 b2, EP ep, RE rowend) {
-  const int tc = threadIdx.x & 15, tr = threadIdx.x >> 4;
-  for (int c0 = 0; c0 < Cn; c0 += 64) {
-    for (int r0 = 0; r0 < R; r0 += 64) {
-      float acc[4][4];
-      int rr[4], cc[4];
+// Products of 64 x 64 outputs: threads are 16 x 16 and own rows 4 tr + i and columns
+// 4 tc + j (WIDE) or tc + 16 j. An operand's values lie along k within a row of its
+// tile (AK, BK: read as float4 of four k) or across rows (read as float4 of four
+// rows, columns; of columns tc + 16 j one by one). Four steps of k take 8 (or 20)
+// reads for 64 multiply-adds a thread; with one word a read (8 for 16) the forward
+// kernel took 222 us instead of 130 (B2 H8 N2K, 128 wide).
+__device__ __forceinline__ int tile_col() { return threadIdx.x & 15; }
+__device__ __forceinline__ int tile_row() { return 4 * (threadIdx.x >> 4); }
+
+// acc += sum over k < K (a multiple of 4) of [w_k] a(r0 + i, k) b(k, cc[j]) (WIDE: cc[0] + j)
+template <bool AK, bool BK, bool WIDE, bool WEIGHT>
+__device__ __forceinline__ void accumulate(float (&acc)[4][4], const float* a, int la, int r0, const float* b, int lb,
+                                           const int (&cc)[4], int K, const float* w) {
+#pragma unroll 2
+  for (int k = 0; k < K; k += 4) {
+    float x[4][4], y[4][4];  // [k][row], [k][column]
+    if constexpr (AK) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        rr[i] = min(r0 + tr + 16 * i, R - 1);
-        cc[i] = min(c0 + tc + 16 * i, Cn - 1);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+        const float4 v = *reinterpret_cast<const float4*>(a + (r0 + i) * la + k);
+        x[0][i] = v.x; x[1][i] = v.y; x[2][i] = v.z; x[3][i] = v.w;
       }
-#pragma unroll 4
-      for (int k = 0; k < K1; ++k) {
-        float x[4], y[4];
+    } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) { x[i] = a1(rr[i], k); y[i] = b1(k, cc[i]); }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float f = scale(rr[i]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] *= f;
-      }
-#pragma unroll 4
-      for (int k = 0; k < K2; ++k) {
-        float x[4], y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) { x[i] = a2(rr[i], k); y[i] = b2(k, cc[i]); }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = r0 + tr + 16 * i;
-        float dot = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c = c0 + tc + 16 * j;
-          if (r < R && c < Cn) dot += ep(r, c, acc[i][j]);
-        }
-        rowend(r, dot, tc);
+      for (int e = 0; e < 4; ++e) {
+        const float4 v = *reinterpret_cast<const float4*>(a + (k + e) * la + r0);
+        x[e][0] = v.x; x[e][1] = v.y; x[e][2] = v.z; x[e][3] = v.w;
       }
     }
+    if constexpr (BK) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 v = *reinterpret_cast<const float4*>(b + cc[j] * lb + k);
+        y[0][j] = v.x; y[1][j] = v.y; y[2][j] = v.z; y[3][j] = v.w;
+      }
+    } else if constexpr (WIDE) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 v = *reinterpret_cast<const float4*>(b + (k + e) * lb + cc[0]);
+        y[e][0] = v.x; y[e][1] = v.y; y[e][2] = v.z; y[e][3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[e][j] = b[(k + e) * lb + cc[j]];
+    }
+    if constexpr (WEIGHT) {
+      const float4 v = *reinterpret_cast<const float4*>(w + k);
+      const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[e][i] *= f[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[e][i], y[e][j], acc[i][j]);
   }
+}
+__device__ __forceinline__ void clear(float (&acc)[4][4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+}
+__device__ __forceinline__ void scale_rows(float (&acc)[4][4], const float* f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float x = f[tile_row() + i];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] *= x;
+  }
+}
+// Columns c0 + tc + 16 j, the last one standing in for those behind it.
+__device__ __forceinline__ void spread_columns(int (&cc)[4], int c0, int n) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) cc[j] = min(c0 + tile_col() + 16 * j, n - 1);
 }
 
 // Sum of `x` over the 16 lanes of a half warp.
@@ -119,23 +145,42 @@ __device__ __forceinline__ float half_warp_sum(float x) {
   return x;
 }
 
-struct Zero2 { __device__ float operator()(int, int) const { return 0.f; } };
-struct One1 { __device__ float operator()(int) const { return 1.f; } };
-struct NoRow { __device__ void operator()(int, float, int) const {} };
-
-// Rows [0, rows) of a [*, w] tensor into an fp32 tile of stride odd(w); the rest zero.
+// Starts the copies of rows [0, rows) of a [*, w] tensor into a tile; the rest of its
+// 64 rows and round4(w) columns become zeros. copies_done() and a barrier end them.
+template <int BYTES>
+__device__ __forceinline__ void copy_or_zero(float* dst, const float* src, bool on) {
+  const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(on ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
 __device__ __forceinline__ void load_rows(float* dst, const float* __restrict__ src, int rows, int w) {
-  const int ld = odd(w);
-  for (int i = threadIdx.x; i < kRows * w; i += kThreads) {
-    const int r = i / w, c = i - r * w;
-    dst[r * ld + c] = r < rows ? src[i] : 0.f;
+  const int ld = stride_of(w);
+  if (w % 4 == 0) {
+#pragma unroll
+    for (int u = 0; u < kRows / 16; ++u) {
+      const int r = (threadIdx.x >> 4) + 16 * u;
+      for (int c = 4 * (threadIdx.x & 15); c < w; c += 64)
+        copy_or_zero<16>(dst + r * ld + c, r < rows ? src + r * w + c : src, r < rows);
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < kRows / 16; ++u) {
+      const int r = (threadIdx.x >> 4) + 16 * u;
+      for (int c = threadIdx.x & 15; c < round4(w); c += 16) {
+        const bool on = r < rows && c < w;
+        copy_or_zero<4>(dst + r * ld + c, on ? src + r * w + c : src, on);
+      }
+    }
   }
 }
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // The block's gate sums: c[t] for t < kRows (rows behind the last one repeat it)
 // and the weights e^(c_t) and e^(c_R - c_t). `start`: the block opens its sequence,
 // where nothing comes before the first token for its gate to pass on (0, unless NaN).
-// Ends with a barrier.
+// Waits for the thread's copies; ends with a barrier.
 __device__ __forceinline__ void gate_tables(const float* __restrict__ gate, int rows, bool start, double* c,
                                             float* head, float* tail) {
   if (threadIdx.x < 32) {
@@ -157,99 +202,176 @@ __device__ __forceinline__ void gate_tables(const float* __restrict__ gate, int 
     head[threadIdx.x] = expf(static_cast<float>(c[threadIdx.x]));
     tail[threadIdx.x] = expf(static_cast<float>(c[kRows - 1] - c[threadIdx.x]));
   }
+  copies_done();
   __syncthreads();
 }
 
-__device__ __forceinline__ float pair_weight(const double* c, int t, int s) {
-  return s <= t ? expf(static_cast<float>(c[t] - c[s])) : 0.f;
-}
-
-// state (d x dv, stride odd(dv)) <- e^(c_R) state + sum_t w_t a_t^T b_t
-template <class W>
-__device__ __forceinline__ void update_state(float* S, const float* a, const float* b, W w, int d, int dv,
-                                             int rows, float whole) {
-  const int la = odd(d), lb = odd(dv);
-  tile_product(
-      d, dv, rows, [&](int r, int k) { return w(k) * a[k * la + r]; },
-      [&](int k, int c) { return b[k * lb + c]; }, One1{}, 0, Zero2{}, Zero2{},
-      [&](int r, int c, float x) {
-        S[r * lb + c] = fmaf(whole, S[r * lb + c], x);
-        return 0.f;
-      },
-      NoRow{});
-}
-
-__device__ __forceinline__ void load_state_tile(float* S, const float* __restrict__ src, int d, int dv) {
-  const int ld = odd(dv);
-  for (int i = threadIdx.x; i < d * dv; i += kThreads) {
-    const int r = i / dv, c = i - r * dv;
-    S[r * ld + c] = src ? src[i] : 0.f;
+// P[t][j] = e^(c_t - c_j) (a_t . b_j) for j <= t, else 0, over all 64 rows.
+__device__ __forceinline__ void scores(float* P, const float* a, const float* b, int ld, int K, const double* c) {
+  float acc[4][4];
+  int cc[4];
+  clear(acc);
+  spread_columns(cc, 0, kRows);
+  accumulate<true, true, false, false>(acc, a, ld, tile_row(), b, ld, cc, K, nullptr);
+  const int lp = stride_of(kRows);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = tile_row() + i;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      P[t * lp + cc[j]] = cc[j] <= t ? acc[i][j] * expf(static_cast<float>(c[t] - c[cc[j]])) : 0.f;
   }
+}
+
+// Four values of a row from column c on, w columns wide.
+__device__ __forceinline__ void store4(float* row, int c, int w, const float (&x)[4]) {
+  if (w % 4 == 0) {
+    *reinterpret_cast<float4*>(row + c) = make_float4(x[0], x[1], x[2], x[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c + j < w) row[c + j] = x[j];
+  }
+}
+
+// S (d rows) <- e^(c_R) S + sum over K rows of w_t a_t^T b_t (`fresh`: S was 0), into
+// S or, as dense rows of dv, into `out`.
+__device__ __forceinline__ void update_state(float* S, const float* a, const float* b, const float* w, int d, int dv,
+                                             int K, float whole, bool fresh, float* out) {
+  const int la = stride_of(d), lb = stride_of(dv);
+  for (int c0 = 0; c0 < dv; c0 += 64)
+    for (int r0 = 0; r0 < d; r0 += 64) {
+      const int c = c0 + 4 * tile_col(), r = r0 + tile_row();
+      const int cc[4] = {min(c, round4(dv) - 4), 0, 0, 0};
+      float acc[4][4];
+      clear(acc);
+      accumulate<false, false, true, true>(acc, a, la, min(r, round4(d) - 4), b, lb, cc, K, w);
+      if (c < dv)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (r + i >= d) break;
+          float4* s = reinterpret_cast<float4*>(S + (r + i) * lb + c);
+          if (!fresh) {
+            const float4 x = *s;
+            acc[i][0] = fmaf(whole, x.x, acc[i][0]);
+            acc[i][1] = fmaf(whole, x.y, acc[i][1]);
+            acc[i][2] = fmaf(whole, x.z, acc[i][2]);
+            acc[i][3] = fmaf(whole, x.w, acc[i][3]);
+          }
+          if (out)
+            store4(out + (r + i) * dv, c, dv, acc[i]);
+          else
+            *s = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        }
+    }
 }
 
 struct Shape {
   int64_t N, L, C;
   int d, dv;
+  int pieces;  // 1: the chunks add up the others' own states; 0: a scan has done it
 };
 
-// Floats of shared memory: a state, `a` tiles of d and `b` of dv columns, `s` score tiles, the tables.
-__host__ __device__ __forceinline__ size_t smem_bytes(int d, int dv, int a, int b, int s) {
-  return kRows * sizeof(double) +
-         sizeof(float) * ((size_t)d * odd(dv) + (size_t)kRows * (a * odd(d) + b * odd(dv)) +
-                          (size_t)s * kRows * odd(kRows) + 3 * kRows);
+// The state that chunk ch of a sequence starts from, in rows of stride_of(dv), zeros
+// around it: the scanned one, or the own states of the chunks before it (BACK: behind
+// it), nearest first, each decayed over the nearer ones.
+template <bool BACK>
+__device__ __forceinline__ void load_state(float* S, const float* __restrict__ states, const double* __restrict__ tot,
+                                           int64_t bh, int64_t ch, const Shape& sh) {
+  const int ld = stride_of(sh.dv), w = ld / 4, nel = sh.d * sh.dv;
+  const int n = !states ? 0 : sh.pieces ? static_cast<int>(BACK ? sh.C - 1 - ch : ch) : 1;
+  const int64_t first = bh * sh.C + (sh.pieces ? (BACK ? ch + 1 : ch - 1) : ch);
+  const int step = BACK ? 1 : -1;
+  for (int i = threadIdx.x; i < round4(sh.d) * w; i += kThreads) {
+    const int r = i / w, c = 4 * (i - r * w);
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (r < sh.d && c < sh.dv) {
+      float f = 1.f;
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const float* src = states + (first + j * step) * nel + r * sh.dv + c;
+        if (sh.dv % 4 == 0) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          x[0] = fmaf(f, v.x, x[0]); x[1] = fmaf(f, v.y, x[1]); x[2] = fmaf(f, v.z, x[2]); x[3] = fmaf(f, v.w, x[3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + e < sh.dv) x[e] = fmaf(f, src[e], x[e]);
+        }
+        if (j + 1 < n) f *= expf(static_cast<float>(tot[first + j * step]));
+      }
+    }
+    *reinterpret_cast<float4*>(S + r * ld + c) = make_float4(x[0], x[1], x[2], x[3]);
+  }
 }
 
-// Own state of every chunk: SUFFIX false, sum_s e^(rest of the chunk's gates) a_s^T b_s
-// (the state after the chunk); SUFFIX true, sum_t e^(the chunk's gates up to t)
-// a_t^T b_t (decayed back to the row before the chunk). tot: the chunk's sum of gates.
-template <bool SUFFIX>
-__global__ void __launch_bounds__(kThreads)
-chunk_state_kernel(const float* __restrict__ a, const float* __restrict__ b, const float* __restrict__ gate,
-                   float* __restrict__ out, double* __restrict__ tot, const Shape sh) {
+// Bytes of shared memory: a state, `a` tiles of d and `b` of dv columns, `s` score tiles, the tables.
+__host__ __device__ __forceinline__ size_t smem_bytes(int d, int dv, int a, int b, int s) {
+  return kRows * sizeof(double) +
+         sizeof(float) * ((size_t)round4(d) * stride_of(dv) + (size_t)kRows * (a * stride_of(d) + b * stride_of(dv)) +
+                          (size_t)s * kRows * stride_of(kRows) + 2 * kRows);
+}
+
+// Own state of every chunk: prefix (blockIdx.y 0, of k and v), sum_s e^(rest of the
+// chunk's gates) a_s^T b_s, the state after the chunk; suffix (blockIdx.y 1, of q and
+// dO), sum_t e^(the chunk's gates up to t) a_t^T b_t, decayed back to the row before
+// the chunk. tot: the chunk's sum of gates. `all` false: not the last chunk's prefix
+// nor the first one's suffix, which nothing starts from.
+struct StateArgs {
+  const float *a[2], *b[2], *gate;
+  float* out[2];
+  double* tot;
+  int all;
+};
+__global__ void __launch_bounds__(kThreads, 2)
+chunk_state_kernel(const StateArgs p, const Shape sh) {
+  pdl_launch_dependents();
+  pdl_wait();
   extern __shared__ double smem_d[];
+  const int d = sh.d, dv = sh.dv;
   double* c = smem_d;
-  float* S = reinterpret_cast<float*>(c + kRows);
-  float* As = S + sh.d * odd(sh.dv);
-  float* Bs = As + kRows * odd(sh.d);
-  float *head = Bs + kRows * odd(sh.dv), *tail = head + kRows;
+  float *head = reinterpret_cast<float*>(c + kRows), *tail = head + kRows;
+  float* S = tail + kRows;
+  float* As = S + round4(d) * stride_of(dv);
+  float* Bs = As + kRows * stride_of(d);
+  const bool suffix = blockIdx.y;
   const int64_t bh = blockIdx.x / sh.C, ch = blockIdx.x % sh.C;
   const int64_t t0 = ch * sh.L, t1 = imin64(sh.N, t0 + sh.L);
   const int nblk = static_cast<int>((t1 - t0 + kRows - 1) / kRows);
-  load_state_tile(S, nullptr, sh.d, sh.dv);
+  if (!p.all && (suffix ? ch == 0 : ch + 1 == sh.C)) return;
   double sum = 0.0;
   for (int n = 0; n < nblk; ++n) {
-    const int64_t i0 = t0 + static_cast<int64_t>(SUFFIX ? nblk - 1 - n : n) * kRows;
+    const int64_t i0 = t0 + static_cast<int64_t>(suffix ? nblk - 1 - n : n) * kRows;
     const int rows = static_cast<int>(imin64(kRows, t1 - i0));
     __syncthreads();
-    load_rows(As, a + (bh * sh.N + i0) * sh.d, rows, sh.d);
-    load_rows(Bs, b + (bh * sh.N + i0) * sh.dv, rows, sh.dv);
-    gate_tables(gate + bh * sh.N + i0, rows, false, c, head, tail);
+    load_rows(As, p.a[suffix] + (bh * sh.N + i0) * d, rows, d);
+    load_rows(Bs, p.b[suffix] + (bh * sh.N + i0) * dv, rows, dv);
+    gate_tables(p.gate + bh * sh.N + i0, rows, false, c, head, tail);
     sum += c[kRows - 1];
-    const float whole = head[kRows - 1];
-    const float* w = SUFFIX ? head : tail;
-    update_state(S, As, Bs, [&](int k) { return w[k]; }, sh.d, sh.dv, rows, whole);
+    update_state(S, As, Bs, suffix ? head : tail, d, dv, round4(rows), head[kRows - 1], n == 0,
+                 n + 1 < nblk ? nullptr : p.out[suffix] + static_cast<int64_t>(blockIdx.x) * d * dv);
   }
-  __syncthreads();
-  float* o = out + static_cast<int64_t>(blockIdx.x) * sh.d * sh.dv;
-  for (int i = threadIdx.x; i < sh.d * sh.dv; i += kThreads) o[i] = S[(i / sh.dv) * odd(sh.dv) + i % sh.dv];
-  if (threadIdx.x == 0) tot[blockIdx.x] = sum;
+  // (of both launches' chunks each sum is written once: its blocks add up in another order)
+  if (threadIdx.x == 0 && (!suffix || ch + 1 == sh.C)) p.tot[blockIdx.x] = sum;
 }
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 fwd_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
-           const float* __restrict__ gate, float* __restrict__ o, const float* __restrict__ states, const Shape sh) {
+           const float* __restrict__ gate, float* __restrict__ o, const float* __restrict__ states,
+           const double* __restrict__ tot, const Shape sh) {
+  pdl_launch_dependents();
+  pdl_wait();
   extern __shared__ double smem_d[];
-  const int d = sh.d, dv = sh.dv, ld = odd(d), lv = odd(dv), ls = odd(kRows);
+  const int d = sh.d, dv = sh.dv, ld = stride_of(d), lv = stride_of(dv), lp = stride_of(kRows);
   double* c = smem_d;
-  float* S = reinterpret_cast<float*>(c + kRows);
-  float* Qs = S + d * lv;
+  float *head = reinterpret_cast<float*>(c + kRows), *tail = head + kRows;
+  float* S = tail + kRows;
+  float* Qs = S + round4(d) * lv;
   float* Ks = Qs + kRows * ld;
   float* Vs = Ks + kRows * ld;
   float* P = Vs + kRows * lv;
-  float *head = P + kRows * ls, *tail = head + kRows;
   const int64_t bh = blockIdx.x / sh.C, ch = blockIdx.x % sh.C;
   const int64_t t0 = ch * sh.L, t1 = imin64(sh.N, t0 + sh.L);
-  load_state_tile(S, states ? states + static_cast<int64_t>(blockIdx.x) * d * dv : nullptr, d, dv);
   for (int64_t i0 = t0; i0 < t1; i0 += kRows) {
     const int rows = static_cast<int>(imin64(kRows, t1 - i0));
     const int64_t row = bh * sh.N + i0;
@@ -257,173 +379,189 @@ fwd_kernel(const float* __restrict__ q, const float* __restrict__ k, const float
     load_rows(Qs, q + row * d, rows, d);
     load_rows(Ks, k + row * d, rows, d);
     load_rows(Vs, v + row * dv, rows, dv);
+    if (i0 == t0) load_state<false>(S, states, tot, bh, ch, sh);
     gate_tables(gate + row, rows, i0 == 0, c, head, tail);
-    tile_product(
-        rows, rows, d, [&](int r, int x) { return Qs[r * ld + x]; }, [&](int x, int j) { return Ks[j * ld + x]; },
-        One1{}, 0, Zero2{}, Zero2{},
-        [&](int t, int j, float x) {
-          P[t * ls + j] = j <= t ? x * pair_weight(c, t, j) : 0.f;
-          return 0.f;
-        },
-        NoRow{});
+    scores(P, Qs, Ks, ld, round4(d), c);
     __syncthreads();
-    float* ob = o + row * dv;
-    tile_product(
-        rows, dv, d, [&](int r, int x) { return Qs[r * ld + x]; }, [&](int x, int e) { return S[x * lv + e]; },
-        [&](int r) { return head[r]; }, rows, [&](int r, int j) { return P[r * ls + j]; },
-        [&](int j, int e) { return Vs[j * lv + e]; },
-        [&](int t, int e, float x) {
-          ob[t * dv + e] = x;
-          return 0.f;
-        },
-        NoRow{});
-    __syncthreads();
-    update_state(S, Ks, Vs, [&](int j) { return tail[j]; }, d, dv, rows, head[kRows - 1]);
+    for (int c0 = 0; c0 < dv; c0 += 64) {
+      const int col = c0 + 4 * tile_col(), cc[4] = {min(col, round4(dv) - 4), 0, 0, 0};
+      float acc[4][4];
+      clear(acc);
+      accumulate<true, false, true, false>(acc, Qs, ld, tile_row(), S, lv, cc, round4(d), nullptr);
+      scale_rows(acc, head);
+      accumulate<true, false, true, false>(acc, P, lp, tile_row(), Vs, lv, cc, round4(rows), nullptr);
+      if (col < dv)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (tile_row() + i < rows) store4(o + (row + tile_row() + i) * dv, col, dv, acc[i]);
+    }
+    if (i0 + kRows < t1) {  // (the state past the chunk's last block is not needed)
+      __syncthreads();
+      update_state(S, Ks, Vs, tail, d, dv, round4(rows), head[kRows - 1], false, nullptr);
+    }
+  }
+}
+
+struct BwdArgs {
+  const float *q, *k, *v, *gate, *dout;
+  float *dq, *dk, *dv;
+  float *qdq, *kdk;                // the rows' dots
+  const float *prefix, *suffix;    // chunk states, or null
+  const double* tot;
+};
+// Rows' values 4 tr + i of columns cc[j] out, and their dots with `x` (row stride lx)
+// added to dot.
+__device__ __forceinline__ void store_spread(float* out, int w, const float* x, int lx, const float (&acc)[4][4], int c0,
+                                             int rows, float (&dot)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = tile_row() + i;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = c0 + tile_col() + 16 * j;
+      if (t < rows && c < w) {
+        out[t * w + c] = acc[i][j];
+        dot[i] = fmaf(x[t * lx + c], acc[i][j], dot[i]);
+      }
+    }
+  }
+}
+__device__ __forceinline__ void store_dots(float* out, float (&dot)[4], int rows) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float x = half_warp_sum(dot[i]);
+    if (tile_col() == 0 && tile_row() + i < rows) out[tile_row() + i] = x;
   }
 }
 
 // dQ_t = sum_{j<=t} e^(c_t - c_j) (dO_t . v_j) k_j + e^(c_t) dO_t KV^T, and q_t . dq_t.
-__global__ void __launch_bounds__(kThreads)
-bwd_dq_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
-              const float* __restrict__ gate, const float* __restrict__ dout, float* __restrict__ dq,
-              float* __restrict__ qdq, const float* __restrict__ states, const Shape sh) {
-  extern __shared__ double smem_d[];
-  const int d = sh.d, dv = sh.dv, ld = odd(d), lv = odd(dv), ls = odd(kRows);
+__device__ __forceinline__ void bwd_dq(const BwdArgs& p, const Shape& sh, double* smem_d) {
+  const int d = sh.d, dv = sh.dv, ld = stride_of(d), lv = stride_of(dv), lp = stride_of(kRows);
   double* c = smem_d;
-  float* S = reinterpret_cast<float*>(c + kRows);
-  float* Ks = S + d * lv;
+  float *head = reinterpret_cast<float*>(c + kRows), *tail = head + kRows;
+  float* S = tail + kRows;
+  float* Ks = S + round4(d) * lv;
   float* Vs = Ks + kRows * ld;
   float* Gs = Vs + kRows * lv;
-  float* A = Gs + kRows * lv;
-  float *head = A + kRows * ls, *tail = head + kRows, *dots = tail + kRows;
+  float* Qs = Gs + kRows * lv;
+  float* A = Qs + kRows * ld;
   const int64_t bh = blockIdx.x / sh.C, ch = blockIdx.x % sh.C;
   const int64_t t0 = ch * sh.L, t1 = imin64(sh.N, t0 + sh.L);
-  load_state_tile(S, states ? states + static_cast<int64_t>(blockIdx.x) * d * dv : nullptr, d, dv);
   for (int64_t i0 = t0; i0 < t1; i0 += kRows) {
     const int rows = static_cast<int>(imin64(kRows, t1 - i0));
     const int64_t row = bh * sh.N + i0;
     __syncthreads();
-    load_rows(Ks, k + row * d, rows, d);
-    load_rows(Vs, v + row * dv, rows, dv);
-    load_rows(Gs, dout + row * dv, rows, dv);
-    if (threadIdx.x < kRows) dots[threadIdx.x] = 0.f;
-    gate_tables(gate + row, rows, i0 == 0, c, head, tail);
-    tile_product(
-        rows, rows, dv, [&](int r, int x) { return Gs[r * lv + x]; }, [&](int x, int j) { return Vs[j * lv + x]; },
-        One1{}, 0, Zero2{}, Zero2{},
-        [&](int t, int j, float x) {
-          A[t * ls + j] = j <= t ? x * pair_weight(c, t, j) : 0.f;
-          return 0.f;
-        },
-        NoRow{});
+    load_rows(Gs, p.dout + row * dv, rows, dv);
+    load_rows(Vs, p.v + row * dv, rows, dv);
+    load_rows(Ks, p.k + row * d, rows, d);
+    load_rows(Qs, p.q + row * d, rows, d);
+    if (i0 == t0) load_state<false>(S, p.prefix, p.tot, bh, ch, sh);
+    gate_tables(p.gate + row, rows, i0 == 0, c, head, tail);
+    scores(A, Gs, Vs, lv, round4(dv), c);
     __syncthreads();
-    const float* qb = q + row * d;
-    float* ob = dq + row * d;
-    tile_product(
-        rows, d, dv, [&](int r, int e) { return Gs[r * lv + e]; }, [&](int e, int x) { return S[x * lv + e]; },
-        [&](int r) { return head[r]; }, rows, [&](int r, int j) { return A[r * ls + j]; },
-        [&](int j, int x) { return Ks[j * ld + x]; },
-        [&](int t, int x, float y) {
-          ob[t * d + x] = y;
-          return qb[t * d + x] * y;
-        },
-        [&](int r, float dot, int tc) {
-          dot = half_warp_sum(dot);
-          if (tc == 0 && r < rows) dots[r] += dot;
-        });
-    __syncthreads();
-    if (threadIdx.x < rows) qdq[row + threadIdx.x] = dots[threadIdx.x];
-    update_state(S, Ks, Vs, [&](int j) { return tail[j]; }, d, dv, rows, head[kRows - 1]);
+    float dot[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int c0 = 0; c0 < d; c0 += 64) {
+      float acc[4][4];
+      int cc[4];
+      clear(acc);
+      spread_columns(cc, c0, d);
+      accumulate<true, true, false, false>(acc, Gs, lv, tile_row(), S, lv, cc, round4(dv), nullptr);
+      scale_rows(acc, head);
+      accumulate<true, false, false, false>(acc, A, lp, tile_row(), Ks, ld, cc, round4(rows), nullptr);
+      store_spread(p.dq + row * d, d, Qs, ld, acc, c0, rows, dot);
+    }
+    store_dots(p.qdq + row, dot, rows);
+    if (i0 + kRows < t1) {
+      __syncthreads();
+      update_state(S, Ks, Vs, tail, d, dv, round4(rows), head[kRows - 1], false, nullptr);
+    }
   }
 }
 
 // dK, dV and k_j . dk_j, blocks of a chunk last to first.
-__global__ void __launch_bounds__(kThreads)
-bwd_dkdv_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
-                const float* __restrict__ gate, const float* __restrict__ dout, float* __restrict__ dk,
-                float* __restrict__ dvv, float* __restrict__ kdk, const float* __restrict__ states,
-                const Shape sh) {
-  extern __shared__ double smem_d[];
-  const int d = sh.d, dv = sh.dv, ld = odd(d), lv = odd(dv), ls = odd(kRows);
+__device__ __forceinline__ void bwd_dkdv(const BwdArgs& p, const Shape& sh, double* smem_d) {
+  const int d = sh.d, dv = sh.dv, ld = stride_of(d), lv = stride_of(dv), lp = stride_of(kRows);
   double* c = smem_d;
-  float* U = reinterpret_cast<float*>(c + kRows);
-  float* Qs = U + d * lv;
+  float *head = reinterpret_cast<float*>(c + kRows), *tail = head + kRows;
+  float* U = tail + kRows;
+  float* Qs = U + round4(d) * lv;
   float* Ks = Qs + kRows * ld;
   float* Vs = Ks + kRows * ld;
   float* Gs = Vs + kRows * lv;
   float* P = Gs + kRows * lv;
-  float *head = P + kRows * ls, *tail = head + kRows, *dots = tail + kRows;
   const int64_t bh = blockIdx.x / sh.C, ch = blockIdx.x % sh.C;
   const int64_t t0 = ch * sh.L, t1 = imin64(sh.N, t0 + sh.L);
   const int nblk = static_cast<int>((t1 - t0 + kRows - 1) / kRows);
-  load_state_tile(U, states ? states + static_cast<int64_t>(blockIdx.x) * d * dv : nullptr, d, dv);
   for (int n = nblk - 1; n >= 0; --n) {
     const int64_t i0 = t0 + static_cast<int64_t>(n) * kRows;
     const int rows = static_cast<int>(imin64(kRows, t1 - i0));
     const int64_t row = bh * sh.N + i0;
     __syncthreads();
-    load_rows(Qs, q + row * d, rows, d);
-    load_rows(Ks, k + row * d, rows, d);
-    load_rows(Vs, v + row * dv, rows, dv);
-    load_rows(Gs, dout + row * dv, rows, dv);
-    if (threadIdx.x < kRows) dots[threadIdx.x] = 0.f;
-    gate_tables(gate + row, rows, i0 == 0, c, head, tail);
+    load_rows(Qs, p.q + row * d, rows, d);
+    load_rows(Ks, p.k + row * d, rows, d);
+    load_rows(Gs, p.dout + row * dv, rows, dv);
+    load_rows(Vs, p.v + row * dv, rows, dv);
+    if (n == nblk - 1) load_state<true>(U, p.suffix, p.tot, bh, ch, sh);
+    gate_tables(p.gate + row, rows, i0 == 0, c, head, tail);
     // P[t][j] = D (q_t . k_j), then dV; the same tile then holds D (dO_t . v_j) for dK
-    tile_product(
-        rows, rows, d, [&](int r, int x) { return Qs[r * ld + x]; }, [&](int x, int j) { return Ks[j * ld + x]; },
-        One1{}, 0, Zero2{}, Zero2{},
-        [&](int t, int j, float x) {
-          P[t * ls + j] = j <= t ? x * pair_weight(c, t, j) : 0.f;
-          return 0.f;
-        },
-        NoRow{});
+    scores(P, Qs, Ks, ld, round4(d), c);
     __syncthreads();
-    float* vb = dvv + row * dv;
-    tile_product(
-        rows, dv, d, [&](int j, int x) { return Ks[j * ld + x]; }, [&](int x, int e) { return U[x * lv + e]; },
-        [&](int j) { return tail[j]; }, rows, [&](int j, int t) { return P[t * ls + j]; },
-        [&](int t, int e) { return Gs[t * lv + e]; },
-        [&](int j, int e, float y) {
-          vb[j * dv + e] = y;
-          return 0.f;
-        },
-        NoRow{});
+    for (int c0 = 0; c0 < dv; c0 += 64) {
+      const int col = c0 + 4 * tile_col(), cc[4] = {min(col, round4(dv) - 4), 0, 0, 0};
+      float acc[4][4];
+      clear(acc);
+      accumulate<true, false, true, false>(acc, Ks, ld, tile_row(), U, lv, cc, round4(d), nullptr);
+      scale_rows(acc, tail);
+      accumulate<false, false, true, false>(acc, P, lp, tile_row(), Gs, lv, cc, round4(rows), nullptr);
+      if (col < dv)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (tile_row() + i < rows) store4(p.dv + (row + tile_row() + i) * dv, col, dv, acc[i]);
+    }
     __syncthreads();
-    tile_product(
-        rows, rows, dv, [&](int r, int x) { return Gs[r * lv + x]; }, [&](int x, int j) { return Vs[j * lv + x]; },
-        One1{}, 0, Zero2{}, Zero2{},
-        [&](int t, int j, float x) {
-          P[t * ls + j] = j <= t ? x * pair_weight(c, t, j) : 0.f;
-          return 0.f;
-        },
-        NoRow{});
+    scores(P, Gs, Vs, lv, round4(dv), c);
     __syncthreads();
-    float* kb = dk + row * d;
-    tile_product(
-        rows, d, dv, [&](int j, int e) { return Vs[j * lv + e]; }, [&](int e, int x) { return U[x * lv + e]; },
-        [&](int j) { return tail[j]; }, rows, [&](int j, int t) { return P[t * ls + j]; },
-        [&](int t, int x) { return Qs[t * ld + x]; },
-        [&](int j, int x, float y) {
-          kb[j * d + x] = y;
-          return Ks[j * ld + x] * y;
-        },
-        [&](int j, float dot, int tc) {
-          dot = half_warp_sum(dot);
-          if (tc == 0 && j < rows) dots[j] += dot;
-        });
-    __syncthreads();
-    if (threadIdx.x < rows) kdk[row + threadIdx.x] = dots[threadIdx.x];
-    update_state(U, Qs, Gs, [&](int t) { return head[t]; }, d, dv, rows, head[kRows - 1]);
+    float dot[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int c0 = 0; c0 < d; c0 += 64) {
+      float acc[4][4];
+      int cc[4];
+      clear(acc);
+      spread_columns(cc, c0, d);
+      accumulate<true, true, false, false>(acc, Vs, lv, tile_row(), U, lv, cc, round4(dv), nullptr);
+      scale_rows(acc, tail);
+      accumulate<false, false, false, false>(acc, P, lp, tile_row(), Qs, ld, cc, round4(rows), nullptr);
+      store_spread(p.dk + row * d, d, Ks, ld, acc, c0, rows, dot);
+    }
+    store_dots(p.kdk + row, dot, rows);
+    if (n > 0) {
+      __syncthreads();
+      update_state(U, Qs, Gs, head, d, dv, round4(rows), head[kRows - 1], false, nullptr);
+    }
   }
+}
+
+// Both gradients in one launch, the longer one's CTAs first: neither reads the other's.
+__global__ void __launch_bounds__(kThreads, 2)
+bwd_kernel(const BwdArgs p, const Shape sh) {
+  pdl_launch_dependents();
+  pdl_wait();
+  extern __shared__ double smem_d[];
+  if (blockIdx.y == 0)
+    bwd_dkdv(p, sh, smem_d);
+  else
+    bwd_dq(p, sh, smem_d);
 }
 
 // ------------------------------------------------ shared with the tensor cores
 
 // In place, per (sequence, element): the chunks' own states become the state
 // before each chunk (mode 0) or the decayed sum of the later chunks (mode 1).
-// Grid: ceil(nel / 256) blocks a sequence.
+// Grid: ceil(nel / 256) blocks a sequence; blockIdx.y 1 scans s1 in mode 1.
 __global__ void __launch_bounds__(kThreads)
-scan_kernel(float* __restrict__ s, const double* __restrict__ tot, int64_t C, int nel, int mode) {
+scan_kernel(float* __restrict__ s0, float* __restrict__ s1, const double* __restrict__ tot, int64_t C, int nel,
+            int mode0) {
+  float* s = blockIdx.y ? s1 : s0;
+  const int mode = blockIdx.y ? 1 : mode0;
   pdl_launch_dependents();
   pdl_wait();
   const int nb = (nel + kThreads - 1) / kThreads;
@@ -487,8 +625,11 @@ pool_update_kernel(const float* __restrict__ chunks, const double* __restrict__ 
   const float* p = chunks + bh * C * nel_c + (ld ? ((c >> 2) * ld + r) * 4 + (c & 3) : e);
   float* out = pool + (slot * H + (bh - b * H)) * nel + e;
   float run = *out;
-  for (int64_t ch = 0; ch < C; ++ch)
-    run = fmaf(expf(static_cast<float>(tot[bh * C + ch])), run, p[ch * nel_c]);
+  for (int64_t ch = 0; ch < C; ++ch) {
+    const float f = expf(static_cast<float>(tot[bh * C + ch]));
+    // (a restart drops what was there, be it no number)
+    run = f == 0.f ? p[ch * nel_c] : fmaf(f, run, p[ch * nel_c]);
+  }
   *out = run;
 }
 
