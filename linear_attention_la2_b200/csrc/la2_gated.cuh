@@ -230,6 +230,7 @@ static la2_status states_tc(const void* y, const void* z, const void* gate, floa
   p.K = pl.K;
   p.first = kind == FOR_DK_DV ? per : 0;
   p.count = kind == FOR_POOL ? pl.K : kind == FOR_DK_DV ? pl.K - per : (pl.C - 1) * per;
+  p.beside = kind == FOR_DK_DV && pl.per > 0;  // (the prefixes' pass came before, without a scan)
   p.spin_limit = spin_limit();
   {
     LaunchTimer t(K_GATED_STATE, st);
@@ -298,6 +299,7 @@ static la2_status backward_tc(const void* q, const void* k, const void* v, const
   }
   {
     TcParams t = tc_params(gate, suffix_t, tot, sh, p);
+    t.beside = 1;
     LaunchTimer lt(K_GATED_DKDV, st);
     if (launch_sm100<true, false>(k, q, dout, dvv, nullptr, sh.d, sh.dv, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
     t.init = suffix;

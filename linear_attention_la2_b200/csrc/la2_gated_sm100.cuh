@@ -145,6 +145,20 @@ __device__ __forceinline__ void for_gates(int n, int lane, G get, F f) {
   }
 }
 
+// Launches of one call that do not read one another's results (the two state passes;
+// dQ, dV and dK) run side by side: all but the first are `beside` the one before. Such a
+// grid does not wait for it at its start: that one let this grid start only once all
+// its CTAs had passed their own wait (or were beside theirs), so everything older is
+// complete. It waits at its end instead, so that whoever waits for it finds the whole
+// group done. (B2 H32 N8K gradients: the tails of three launches overlap.)
+__device__ __forceinline__ void begin_grid(int beside) {
+  if (!beside) pdl_wait();
+  pdl_launch_dependents();
+}
+__device__ __forceinline__ void end_grid(int beside) {
+  if (beside) pdl_wait();
+}
+
 struct TcParams {
   const __nv_bfloat16* gate;   // [BH][N]
   const float* init;           // [BH][K][128*128] (state_f4): states of the sequence's pieces, or null
@@ -156,6 +170,7 @@ struct TcParams {
   // chunk, scanned already.
   int32_t K, per;
   int32_t halves;  // 64-column halves of an output row
+  int32_t beside;  // the launch before is independent: see begin_grid
 };
 
 template <bool GRAD>
@@ -348,8 +363,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
   s::tc_fence_after();
   const uint32_t tmem = *tmem_base;
   const int64_t lim = prm.spin_limit;
-  pdl_launch_dependents();  // global memory is touched only after this point
-  pdl_wait();
+  begin_grid(prm.beside);  // global memory is touched only after this point
 
   auto wait = [&](uint64_t* bar, uint32_t parity, int where) -> bool {
     return __all_sync(0xffffffffu, s::wait_bar(bar, parity, lim, abort_flag, where));
@@ -770,6 +784,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     }
   }
 
+  end_grid(prm.beside);
   s::tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -805,6 +820,7 @@ struct TcStateParams {
   float* out_t;    // its transpose, or null
   double* tot;     // [BH][K]
   int64_t N, L, K, first, count, spin_limit;  // pieces [first, first + count) of the K of every sequence
+  int32_t beside;  // the launch before is independent: see begin_grid
 };
 
 // ROWS_Z: the state's rows are z's columns (what O and dV start from), else y's.
@@ -857,8 +873,7 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
   s::tc_fence_after();
   const uint32_t tmem = *tmem_base;
   const int64_t lim = prm.spin_limit;
-  pdl_launch_dependents();
-  pdl_wait();
+  begin_grid(prm.beside);
   auto wait = [&](uint64_t* bar, uint32_t parity, int where) -> bool {
     return __all_sync(0xffffffffu, s::wait_bar(bar, parity, lim, abort_flag, where));
   };
@@ -967,6 +982,7 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
     }
   }
 
+  end_grid(prm.beside);
   s::tc_fence_before();
   __syncthreads();
   if (warp == 1) {
