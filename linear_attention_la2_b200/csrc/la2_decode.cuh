@@ -138,8 +138,8 @@ decode_step_v4_kernel(const T* __restrict__ q, const T* __restrict__ k, const T*
 
 // The gated step on a pool of slots: S <- e^gate S + k^T v, o = q S, with the
 // state of batch row b in pool slot slots[b] (b itself without `slots`). Rows that
-// checked_slot refuses leave their output and the pool as they were. The same two
-// layouts as the step above.
+// checked_slot refuses leave their output and the pool as they were. A restart (e^gate
+// = 0) drops what the slot held, be it no number. The same two layouts as the step above.
 template <typename T>
 __global__ void __launch_bounds__(32 * kDecodeWarps)
 decode_gated_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
@@ -162,7 +162,8 @@ decode_gated_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* _
     float* col = pool + (slot * H + (bh - b * H)) * static_cast<int64_t>(d) * dv + j;
 #pragma unroll 8
     for (int i = w; i < d; i += kDecodeWarps) {
-      const float s = fmaf(g, col[static_cast<int64_t>(i) * dv], to_f32(kb[i]) * vj);
+      const float kv = to_f32(kb[i]) * vj;
+      const float s = g == 0.f ? kv : fmaf(g, col[static_cast<int64_t>(i) * dv], kv);
       col[static_cast<int64_t>(i) * dv] = s;
       acc += to_f32(qb[i]) * s;
     }
@@ -210,6 +211,7 @@ decode_gated_v4_kernel(const T* __restrict__ q, const T* __restrict__ k, const T
         const int i = w + (h * kRows / 2 + t) * kDecodeWarps;
         if (i < d) {
           const float ki = to_f32(kb[i]), qi = to_f32(qb[i]);
+          if (g == 0.f) x[t] = make_float4(0.f, 0.f, 0.f, 0.f);
           x[t].x = fmaf(g, x[t].x, ki * vj.x);
           x[t].y = fmaf(g, x[t].y, ki * vj.y);
           x[t].z = fmaf(g, x[t].z, ki * vj.z);

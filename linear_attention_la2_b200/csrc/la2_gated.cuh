@@ -217,7 +217,7 @@ static la2_status forward(const void* q, const void* k, const void* v, const voi
 // Tensor cores: states of the pieces that a chunk starts from, and their scan where
 // the chunks do not add them up themselves. kind: what they are for.
 enum States { FOR_O, FOR_DQ, FOR_DK_DV, FOR_POOL };
-static la2_status states_tc(const void* y, const void* z, const void* gate, float* out, float* out_t, double* tot,
+static la2_status states_tc(const Tile& y, const Tile& z, const void* gate, float* out, float* out_t, double* tot,
                             int64_t BH, const Shape& sh, const Plan& pl, States kind, cudaStream_t st) {
   const int64_t per = std::max<int64_t>(1, pl.per);
   TcStateParams p{};
@@ -234,9 +234,9 @@ static la2_status states_tc(const void* y, const void* z, const void* gate, floa
   p.spin_limit = spin_limit();
   {
     LaunchTimer t(K_GATED_STATE, st);
-    const cudaError_t e = kind == FOR_DK_DV ? launch_state_sm100<true, false>(y, z, sh.d, sh.dv, p, BH, st)
-                          : kind == FOR_O   ? launch_state_sm100<false, true>(y, z, sh.d, sh.dv, p, BH, st)
-                                            : launch_state_sm100<false, false>(y, z, sh.d, sh.dv, p, BH, st);
+    const cudaError_t e = kind == FOR_DK_DV ? launch_state_sm100<true, false>(y, z, p, BH, st)
+                          : kind == FOR_O   ? launch_state_sm100<false, true>(y, z, p, BH, st)
+                                            : launch_state_sm100<false, false>(y, z, p, BH, st);
     if (e != cudaSuccess) return LA2_ERR_CUDA;
   }
   la2_status s = launch_status();
@@ -262,12 +262,13 @@ static la2_status forward_tc(const void* q, const void* k, const void* v, const 
                              const Plan& p, int64_t BH, const Shape& sh, cudaStream_t st) {
   float* states = p.C > 1 ? reinterpret_cast<float*>(ws) : nullptr;
   double* tot = reinterpret_cast<double*>(ws + p.off_tot);
+  const Tile tq(q, BH, sh.N, sh.d), tk(k, BH, sh.N, sh.d), tv(v, BH, sh.N, sh.dv), to(o, BH, sh.N, sh.dv);
   if (states) {
-    const la2_status s = states_tc(k, v, gate, states, nullptr, tot, BH, sh, p, FOR_O, st);
+    const la2_status s = states_tc(tk, tv, gate, states, nullptr, tot, BH, sh, p, FOR_O, st);
     if (s != LA2_OK) return s;
   }
   LaunchTimer t(K_GATED_FWD, st);
-  if (launch_sm100<false, false>(q, k, v, o, nullptr, sh.d, sh.dv, tc_params(gate, states, tot, sh, p), BH, st) != cudaSuccess)
+  if (launch_sm100<false, false>(tq, tk, tv, to, to, tc_params(gate, states, tot, sh, p), BH, st) != cudaSuccess)
     return LA2_ERR_CUDA;
   return launch_status();
 }
@@ -286,25 +287,27 @@ static la2_status backward_tc(const void* q, const void* k, const void* v, const
   float* qdq = reinterpret_cast<float*>(ws + p.off_qdq);
   float* kdk = reinterpret_cast<float*>(ws + p.off_kdk);
   double* tot = reinterpret_cast<double*>(ws + p.off_tot);
+  const Tile tq(q, BH, sh.N, sh.d), tk(k, BH, sh.N, sh.d), tv(v, BH, sh.N, sh.dv), tdo(dout, BH, sh.N, sh.dv);
+  const Tile tdq(dq, BH, sh.N, sh.d), tdk(dk, BH, sh.N, sh.d), tdv(dvv, BH, sh.N, sh.dv);
   la2_status s = LA2_OK;
   if (prefix) {
-    if ((s = states_tc(k, v, gate, prefix, nullptr, tot, BH, sh, p, FOR_DQ, st)) != LA2_OK) return s;
-    if ((s = states_tc(q, dout, gate, suffix, suffix_t, tot, BH, sh, p, FOR_DK_DV, st)) != LA2_OK) return s;
+    if ((s = states_tc(tk, tv, gate, prefix, nullptr, tot, BH, sh, p, FOR_DQ, st)) != LA2_OK) return s;
+    if ((s = states_tc(tq, tdo, gate, suffix, suffix_t, tot, BH, sh, p, FOR_DK_DV, st)) != LA2_OK) return s;
   }
   {
     TcParams t = tc_params(gate, prefix, tot, sh, p);
     t.dots = qdq;
     LaunchTimer lt(K_GATED_DQ, st);
-    if (launch_sm100<false, true>(dout, v, k, dq, q, sh.dv, sh.d, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
+    if (launch_sm100<false, true>(tdo, tv, tk, tdq, tq, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
   }
   {
     TcParams t = tc_params(gate, suffix_t, tot, sh, p);
     t.beside = 1;
     LaunchTimer lt(K_GATED_DKDV, st);
-    if (launch_sm100<true, false>(k, q, dout, dvv, nullptr, sh.d, sh.dv, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
+    if (launch_sm100<true, false>(tk, tq, tdo, tdv, tdv, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
     t.init = suffix;
     t.dots = kdk;
-    if (launch_sm100<true, true>(v, dout, q, dk, k, sh.dv, sh.d, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
+    if (launch_sm100<true, true>(tv, tdo, tq, tdk, tk, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
   }
   if ((s = launch_status()) != LA2_OK) return s;
   return gate_grad<__nv_bfloat16>(gate, qdq, kdk, prefix, suffix, tot, dgate, BH, sh, p, st);
@@ -482,13 +485,16 @@ la2_status la2_kv_state_gated(const void* k, const void* v, const void* gate, fl
   float* chunks = static_cast<float*>(workspace);
   double* tot = reinterpret_cast<double*>(static_cast<char*>(workspace) + p.off_tot);
   if (p.tc)
-    s = gated::states_tc(k, v, gate, chunks, nullptr, tot, B * H, sh, p, gated::FOR_POOL, st);
+    s = gated::states_tc(gated::Tile(k, B * H, N, (int)d), gated::Tile(v, B * H, N, (int)dv), gate, chunks, nullptr, tot,
+                         B * H, sh, p, gated::FOR_POOL, st);
   else
     s = gated::chunk_states(k, v, nullptr, nullptr, gate, chunks, nullptr, tot, true, B * H, sh, st);
   if (s != LA2_OK) return s;
-  const int64_t nb = (d * dv + gated::kThreads - 1) / gated::kThreads;
+  const int V = dv % 4 == 0 ? 4 : 1;  // (state: 16-byte aligned, see spans_ok)
+  const int64_t nb = (d * dv + gated::kThreads * V - 1) / (gated::kThreads * V);
   LaunchTimer t(K_GATED_POOL, st);
-  if (launch_pdl(gated::pool_update_kernel, dim3((unsigned)(B * H * nb)), dim3(gated::kThreads), 0, st,
+  if (launch_pdl(V == 4 ? gated::pool_update_kernel<4> : gated::pool_update_kernel<1>, dim3((unsigned)(B * H * nb)),
+                 dim3(gated::kThreads), 0, st,
                  static_cast<const float*>(chunks), static_cast<const double*>(tot), state, slots, n_slots,
                  p.C, (int)H, (int)d, (int)dv, p.nel, p.tc ? 128 : 0) != cudaSuccess)
     return LA2_ERR_CUDA;

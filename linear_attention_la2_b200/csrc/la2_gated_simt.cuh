@@ -609,28 +609,52 @@ __device__ __forceinline__ int64_t checked_slot(const int32_t* __restrict__ slot
 
 // pool[slot of b][h] <- e^(all gates) pool[slot][h] + the chunks' states decayed to
 // the last token, added in chunk order. A chunk's state is `nel_c` floats; ld > 0: in
-// the tensor cores' layout of ld rows (float4 j of row r at j*ld + r). Grid: ceil(d*dv / 256) blocks a sequence.
+// the tensor cores' layout of ld rows (float4 j of row r at j*ld + r). V values a
+// thread, dv a multiple of V; in that layout a warp takes 4 rows x 8 float4s, so that
+// both sides move in whole sectors. Grid: ceil(d*dv / (256 V)) blocks a sequence.
+template <int V>
 __global__ void __launch_bounds__(kThreads)
 pool_update_kernel(const float* __restrict__ chunks, const double* __restrict__ tot, float* __restrict__ pool,
                    const int32_t* __restrict__ slots, int64_t n_slots, int64_t C, int H, int d, int dv,
                    int nel_c, int ld) {
   pdl_launch_dependents();
   pdl_wait();
-  const int nel = d * dv, nb = (nel + kThreads - 1) / kThreads;
+  const int nel = d * dv, nb = (nel + kThreads * V - 1) / (kThreads * V);
   const int64_t bh = blockIdx.x / nb, b = bh / H;
   const int64_t slot = checked_slot(slots, b, n_slots);
-  const int e = static_cast<int>(blockIdx.x % nb) * kThreads + threadIdx.x;
-  if (slot < 0 || e >= nel) return;
-  const int r = e / dv, c = e % dv;
-  const float* p = chunks + bh * C * nel_c + (ld ? ((c >> 2) * ld + r) * 4 + (c & 3) : e);
-  float* out = pool + (slot * H + (bh - b * H)) * nel + e;
-  float run = *out;
-  for (int64_t ch = 0; ch < C; ++ch) {
-    const float f = expf(static_cast<float>(tot[bh * C + ch]));
-    // (a restart drops what was there, be it no number)
-    run = f == 0.f ? p[ch * nel_c] : fmaf(f, run, p[ch * nel_c]);
+  const int i = static_cast<int>(blockIdx.x % nb) * kThreads + threadIdx.x;
+  if (slot < 0 || i * V >= nel) return;
+  int to = i * V, from = to;
+  if (V == 4 && ld) {
+    const int tiles = dv / 32, t = i >> 5, r = t / tiles * 4 + (i & 3), j = t % tiles * 8 + ((i & 31) >> 2);
+    to = r * dv + 4 * j;
+    from = (j * ld + r) * 4;
   }
-  *out = run;
+  const float* p = chunks + bh * C * nel_c + from;
+  float* out = pool + (slot * H + (bh - b * H)) * nel + to;
+  float run[V];
+  auto get = [](const float* src, float (&x)[V]) {
+    if constexpr (V == 4) {
+      const float4 y = *reinterpret_cast<const float4*>(src);
+      x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+    } else {
+      x[0] = *src;
+    }
+  };
+  get(out, run);
+#pragma unroll 4
+  for (int64_t ch = 0; ch < C; ++ch) {
+    float x[V];
+    get(p + ch * nel_c, x);
+    const float f = expf(static_cast<float>(tot[bh * C + ch]));
+#pragma unroll
+    for (int e = 0; e < V; ++e)  // (a restart drops what was there, be it no number)
+      run[e] = f == 0.f ? x[e] : fmaf(f, run[e], x[e]);
+  }
+  if constexpr (V == 4)
+    *reinterpret_cast<float4*>(out) = make_float4(run[0], run[1], run[2], run[3]);
+  else
+    *out = run[0];
 }
 
 // dl_t = flow at the chunk's end + sum over the chunk's rows from t on of

@@ -993,31 +993,34 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
 
 // -------------------------------------------------------------------- launches
 
+// A [BH, N, w] tensor and its map (64 rows x 64 columns a copy), made once a call.
+struct Tile {
+  CUtensorMap map;
+  int w;
+  bool ok;
+  Tile(const void* base, int64_t BH, int64_t N, int w_) : w(w_), ok(make_tmap_3d(&map, base, BH, N, w_, 64)) {}
+};
+
 template <bool SUFFIX, bool ROWS_Z>
-inline cudaError_t launch_state_sm100(const void* y, const void* z, int wy, int wz, const TcStateParams& p, int64_t BH,
-                                      cudaStream_t st) {
-  CUtensorMap ty, tz;
-  if (!make_tmap_3d(&ty, y, BH, p.N, wy, 64) || !make_tmap_3d(&tz, z, BH, p.N, wz, 64)) return cudaErrorInvalidValue;
+inline cudaError_t launch_state_sm100(const Tile& y, const Tile& z, const TcStateParams& p, int64_t BH, cudaStream_t st) {
+  if (!y.ok || !z.ok) return cudaErrorInvalidValue;
   auto kern = gated_state_sm100_kernel<SUFFIX, ROWS_Z>;
   static bool done[128];
   if (!smem_attribute_set(kern, StateCfg::SMEM, done)) return cudaErrorInvalidValue;
-  return launch_pdl(kern, dim3((unsigned)(BH * p.count)), dim3(384), StateCfg::SMEM, st, ty, tz, p);
+  return launch_pdl(kern, dim3((unsigned)(BH * p.count)), dim3(384), StateCfg::SMEM, st, y.map, z.map, p);
 }
 
-// Widths: x and y wx; z, the output and the dots' rows wz.
+// dot_rows: GRAD (else any).
 template <bool BACK, bool GRAD>
-inline cudaError_t launch_sm100(const void* x, const void* y, const void* z, void* o, const void* dot_rows,
-                                int wx, int wz, TcParams p, int64_t BH, cudaStream_t st) {
-  p.halves = wz / 64;
-  CUtensorMap tx, ty, tz, to, td;
-  if (!make_tmap_3d(&tx, x, BH, p.N, wx, 64) || !make_tmap_3d(&ty, y, BH, p.N, wx, 64) ||
-      !make_tmap_3d(&tz, z, BH, p.N, wz, 64) || !make_tmap_3d(&to, o, BH, p.N, wz, 64) ||
-      !make_tmap_3d(&td, GRAD ? dot_rows : z, BH, p.N, wz, 64))
-    return cudaErrorInvalidValue;
+inline cudaError_t launch_sm100(const Tile& x, const Tile& y, const Tile& z, const Tile& o, const Tile& dot_rows,
+                                TcParams p, int64_t BH, cudaStream_t st) {
+  if (!x.ok || !y.ok || !z.ok || !o.ok || !dot_rows.ok) return cudaErrorInvalidValue;
+  p.halves = o.w / 64;
   auto kern = gated_sm100_kernel<BACK, GRAD>;
   static bool done[128];
   if (!smem_attribute_set(kern, TcCfg<GRAD>::SMEM, done)) return cudaErrorInvalidValue;
-  return launch_pdl(kern, dim3((unsigned)(BH * p.C)), dim3(kMainThreads), TcCfg<GRAD>::SMEM, st, tx, ty, tz, to, td, p);
+  return launch_pdl(kern, dim3((unsigned)(BH * p.C)), dim3(kMainThreads), TcCfg<GRAD>::SMEM, st, x.map, y.map, z.map,
+                    o.map, dot_rows.map, p);
 }
 
 }  // namespace gated
