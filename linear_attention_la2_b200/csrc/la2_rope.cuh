@@ -35,6 +35,7 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxD = 256;
 constexpr int kMaxAxes = 4;
+constexpr int kRowTile = 4;
 
 struct Params {
   const void* x[2];        // queries, keys (backward: the forward's inputs)
@@ -604,6 +605,17 @@ struct WarpRow {
   __device__ __forceinline__ float at(int s) const { return s < M ? a[s] : (s < 2 * M ? b[s - M] : c[s - 2 * M]); }
 };
 
+// Both weights' values of a lane (ones where there is no weight).
+template <typename T, int M>
+__device__ __forceinline__ void load_weights(const Params& p, WarpRow<T, M> (&w)[2], int lane) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (p.w[i])
+      w[i].load(static_cast<const T*>(p.w[i]), lane, p.half, p.d);
+    else
+      w[i].each([](float& v, int) { v = 1.f; });
+}
+
 template <typename T, int M>
 __global__ void __launch_bounds__(kThreads)
 rope_fwd_row_kernel(const __grid_constant__ Params p) {
@@ -616,6 +628,8 @@ rope_fwd_row_kernel(const __grid_constant__ Params p) {
   const float inv_d = 1.f / static_cast<float>(d);
   const int rows = ntok * (p.heads[0] + p.heads[1]);
   fill_angles(p, tok0, ntok, cs);
+  WarpRow<T, M> w[2];
+  load_weights(p, w, lane);
   __syncthreads();
   const int step = kWarps * p.splits;
   for (int r0 = (threadIdx.x >> 5) + kWarps * blockIdx.y; r0 < rows; r0 += 2 * step) {
@@ -635,11 +649,7 @@ rope_fwd_row_kernel(const __grid_constant__ Params p) {
       s = group_sum<32>(s);
       const float r = rsqrtf(fmaf(s, inv_d, p.eps));
       x[u].each([&](float& v, int) { v *= r; });
-      if (p.w[which]) {
-        WarpRow<T, M> w;
-        w.load(static_cast<const T*>(p.w[which]), lane, half, d);
-        x[u].each([&](float& v, int i) { v *= w.at(i); });
-      }
+      x[u].each([&](float& v, int i) { v *= which ? w[1].at(i) : w[0].at(i); });
       x[u].turn(cs + row[u].t * half, lane, half, 1.f);
       const float f = p.scale[which];
       x[u].each([&](float& v, int) { v *= f; });
@@ -660,6 +670,8 @@ rope_bwd_row_kernel(const __grid_constant__ Params p) {
   float dw[2][4 * M];
 #pragma unroll
   for (int i = 0; i < 4 * M; ++i) dw[0][i] = dw[1][i] = 0.f;
+  WarpRow<T, M> w[2];
+  load_weights(p, w, lane);
   for (int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tile; tok0 < p.tokens;
        tok0 += static_cast<int64_t>(gridDim.x) * p.tile) {
     const int ntok = static_cast<int>(imin64(p.tile, p.tokens - tok0));
@@ -683,11 +695,7 @@ rope_bwd_row_kernel(const __grid_constant__ Params p) {
         v *= f;
         if (row.which) dw[1][i] += v * x.at(i); else dw[0][i] += v * x.at(i);
       });
-      if (p.w[row.which]) {
-        WarpRow<T, M> w;
-        w.load(static_cast<const T*>(p.w[row.which]), lane, half, d);
-        g.each([&](float& v, int i) { v *= w.at(i); });
-      }
+      g.each([&](float& v, int i) { v *= row.which ? w[1].at(i) : w[0].at(i); });
       float dot = 0.f;
       g.each([&](float& v, int i) { dot = fmaf(v, x.at(i), dot); });
       dot = group_sum<32>(dot) * inv_d;
@@ -780,9 +788,10 @@ static int group_of(const Args& a) {
 // Tokens of a tile, a power of two: one for each group of a CTA, whose set-up (angles,
 // coefficients) is then done once a token and whose rows of a head leave as one piece
 // (B4 N2K, 32 heads of 128, bf16: 16 tokens 27.9 and 43.3 us forward and back, 8 tokens
-// 31.1 and 48.1); fewer where that would leave an SM less than three tiles.
-static int tile_of(const Args& a, int sms) {
-  int64_t t = kThreads / group_of(a);
+// 31.1 and 48.1); fewer where that would leave an SM less than three tiles. A warp a row
+// hides its loads behind other warps: few tokens, many CTAs.
+static int tile_of(const Args& a, bool vec, int sms) {
+  int64_t t = vec ? kThreads / group_of(a) : kRowTile;
   while (t > 1 && a.B * a.N < t * 3 * sms) t /= 2;
   return static_cast<int>(t);
 }
@@ -933,11 +942,11 @@ la2_status la2_qk_norm_rope(const void* q, const void* k, const int64_t* q_strid
   if (nq && nk && overlaps(q_out, nq, k_out, nk)) return LA2_ERR_INVALID_ARG;
   const int sms = device_sm_count();
   if (sms <= 0) return LA2_ERR_CUDA;
-  rope::Params p = rope::params(a, rope::tile_of(a, sms));
-  p.out[0] = q_out;
-  p.out[1] = k_out;
   const void* outs[2] = {q_out, k_out};
   const bool vec = rope::vec_ok(a, outs, 2);
+  rope::Params p = rope::params(a, rope::tile_of(a, vec, sms));
+  p.out[0] = q_out;
+  p.out[1] = k_out;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return dt == LA2_BF16 ? rope::launch_fwd<__nv_bfloat16>(a, p, vec, sms, st)
                         : rope::launch_fwd<float>(a, p, vec, sms, st);
@@ -984,7 +993,9 @@ la2_status la2_qk_norm_rope_backward(const void* dq_out, const void* dk_out, con
   if ((H > 0 && (!q || !dq || !dq_out)) || (Hkv > 0 && (!k || !dk || !dk_out))) return LA2_ERR_INVALID_ARG;
   const int sms = device_sm_count();
   if (sms <= 0) return LA2_ERR_CUDA;
-  const int tile = rope::tile_of(a, sms), grid = rope::bwd_grid(a, tile, sms);
+  const void* more[4] = {dq, dk, dq_out, dk_out};
+  const bool vec = rope::vec_ok(a, more, 4);
+  const int tile = rope::tile_of(a, vec, sms), grid = rope::bwd_grid(a, tile, sms);
   const size_t need = (size_t)grid * 2 * d * sizeof(float);
   if (!workspace || workspace_bytes < need) return LA2_ERR_WORKSPACE;
   if (!is_aligned(workspace, 256)) return LA2_ERR_INVALID_ARG;
@@ -1007,8 +1018,6 @@ la2_status la2_qk_norm_rope_backward(const void* dq_out, const void* dk_out, con
   p.dy[0] = dq_out;
   p.dy[1] = dk_out;
   p.dw_part = static_cast<float*>(workspace);
-  const void* more[4] = {dq, dk, dq_out, dk_out};
-  const bool vec = rope::vec_ok(a, more, 4);
   return dt == LA2_BF16 ? rope::launch_bwd<__nv_bfloat16>(a, p, vec, grid, dwq, dwk, st)
                         : rope::launch_bwd<float>(a, p, vec, grid, dwq, dwk, st);
 }
