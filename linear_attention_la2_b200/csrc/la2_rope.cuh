@@ -35,7 +35,7 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxD = 256;
 constexpr int kMaxAxes = 4;
-constexpr int kRowTile = 4;
+constexpr int kRowTile = kWarps;  // tokens of a CTA, a warp a row
 
 struct Params {
   const void* x[2];        // queries, keys (backward: the forward's inputs)
@@ -52,42 +52,6 @@ struct Params {
   double turn[kMaxD / 2];  // base^(-2i/rot) / (2 pi)
   uint8_t axis[kMaxD / 2];
 };
-
-// cos and sin of every angle of the tile's tokens.
-__device__ __forceinline__ void fill_angles(const Params& p, int64_t tok0, int ntok, float2* cs) {
-  for (int i = threadIdx.x; i < ntok * p.half; i += kThreads) {
-    const int t = i / p.half, j = i - t * p.half;
-    const int64_t tok = tok0 + t;
-    const int64_t at = p.pos ? p.pos[p.axis[j] * p.tokens + tok]
-                             : static_cast<uint32_t>(tok) % static_cast<uint32_t>(p.N);
-    const double a = static_cast<double>(at) * p.turn[j];
-    float s, c;
-    sincospif(2.f * static_cast<float>(a - rint(a)), &s, &c);
-    cs[i] = make_float2(c, s);
-  }
-}
-
-struct Row {
-  int which;               // 0 query, 1 key
-  int64_t in, out;         // element offsets (out: [B,H,N,d]); flat: [B,N,H,d]
-  int64_t flat;
-  int t;                   // token within the tile
-};
-// Row r of the tile (the kernels of a warp a row): heads outermost, so that
-// neighbouring rows are neighbouring tokens of one head.
-__device__ __forceinline__ Row row_of(const Params& p, int64_t tok0, int ntok, int r) {
-  Row x;
-  int h = r / ntok;
-  x.t = r - h * ntok;
-  x.which = h >= p.heads[0];
-  if (x.which) h -= p.heads[0];
-  const int64_t tok = tok0 + x.t;  // below 2^31
-  const int64_t b = static_cast<uint32_t>(tok) / static_cast<uint32_t>(p.N), n = tok - b * p.N;
-  x.in = b * p.sb[x.which] + n * p.sn[x.which] + h * p.sh[x.which];
-  x.out = ((b * p.heads[x.which] + h) * p.N + n) * p.d;
-  x.flat = (tok * p.heads[x.which] + h) * p.d;
-  return x;
-}
 
 template <int G>
 __device__ __forceinline__ float group_sum(float x) {
@@ -548,21 +512,25 @@ rope_bwd_vec_kernel(const __grid_constant__ Params p) {
   store_dw(p, sdw);
 }
 
-// A warp a row. Value slots of a lane: M pairs (a, b), then 2M single values.
-template <typename T, int M>
+// A warp a row. Value slots of a lane: M pairs (a, b), then (REST: rot < d) 2M single
+// values. A warp keeps one token: its angles and both weights stay in the lanes'
+// registers while it walks the heads (with rows found one by one, and the slots behind
+// the rotated values always there, 88 and 147 us at B4 N2K, 32 heads of 90).
+template <typename T, int M, bool REST>
 struct WarpRow {
-  float a[M], b[M], c[2 * M];
+  static constexpr int R = REST ? 2 * M : 0, SLOTS = 2 * M + R;
+  float x[SLOTS];  // a, b, rest
   __device__ __forceinline__ void load(const T* p, int lane, int half, int d) {
 #pragma unroll
     for (int m = 0; m < M; ++m) {
       const int j = lane + 32 * m;
-      a[m] = j < half ? to_f32(p[j]) : 0.f;
-      b[m] = j < half ? to_f32(p[half + j]) : 0.f;
+      x[m] = j < half ? to_f32(p[j]) : 0.f;
+      x[M + m] = j < half ? to_f32(p[half + j]) : 0.f;
     }
 #pragma unroll
-    for (int m = 0; m < 2 * M; ++m) {
+    for (int m = 0; m < R; ++m) {
       const int j = 2 * half + lane + 32 * m;
-      c[m] = j < d ? to_f32(p[j]) : 0.f;
+      x[2 * M + m] = j < d ? to_f32(p[j]) : 0.f;
     }
   }
   __device__ __forceinline__ void store(T* p, int lane, int half, int d) const {
@@ -570,146 +538,159 @@ struct WarpRow {
     for (int m = 0; m < M; ++m) {
       const int j = lane + 32 * m;
       if (j < half) {
-        p[j] = from_f32<T>(a[m]);
-        p[half + j] = from_f32<T>(b[m]);
+        p[j] = from_f32<T>(x[m]);
+        p[half + j] = from_f32<T>(x[M + m]);
       }
     }
 #pragma unroll
-    for (int m = 0; m < 2 * M; ++m) {
+    for (int m = 0; m < R; ++m) {
       const int j = 2 * half + lane + 32 * m;
-      if (j < d) p[j] = from_f32<T>(c[m]);
+      if (j < d) p[j] = from_f32<T>(x[2 * M + m]);
     }
   }
-  __device__ __forceinline__ void turn(const float2* cs, int lane, int half, float sign) {
+  __device__ __forceinline__ void turn(const float2 (&cs)[M], float sign) {
 #pragma unroll
     for (int m = 0; m < M; ++m) {
-      const int j = lane + 32 * m;
-      if (j < half) {
-        const float2 t = cs[j];
-        const float x = a[m], y = b[m];
-        a[m] = fmaf(x, t.x, -sign * t.y * y);
-        b[m] = fmaf(y, t.x, sign * t.y * x);
-      }
+      const float u = x[m], v = x[M + m], sn = sign * cs[m].y;
+      x[m] = fmaf(u, cs[m].x, -sn * v);
+      x[M + m] = fmaf(v, cs[m].x, sn * u);
     }
   }
-  template <class F>
-  __device__ __forceinline__ void each(F f) {  // f(slot)
-#pragma unroll
-    for (int m = 0; m < M; ++m) {
-      f(a[m], m);
-      f(b[m], M + m);
-    }
-#pragma unroll
-    for (int m = 0; m < 2 * M; ++m) f(c[m], 2 * M + m);
-  }
-  __device__ __forceinline__ float at(int s) const { return s < M ? a[s] : (s < 2 * M ? b[s - M] : c[s - 2 * M]); }
 };
-
-// Both weights' values of a lane (ones where there is no weight).
-template <typename T, int M>
-__device__ __forceinline__ void load_weights(const Params& p, WarpRow<T, M> (&w)[2], int lane) {
+// Both weights' values of a lane, times f (f where there is no weight).
+template <typename T, int M, bool REST>
+__device__ __forceinline__ void load_weights(const Params& p, WarpRow<T, M, REST> (&w)[2], int lane, float f0, float f1) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (p.w[i])
-      w[i].load(static_cast<const T*>(p.w[i]), lane, p.half, p.d);
-    else
-      w[i].each([](float& v, int) { v = 1.f; });
+  for (int i = 0; i < 2; ++i) {
+    if (p.w[i]) w[i].load(static_cast<const T*>(p.w[i]), lane, p.half, p.d);
+#pragma unroll
+    for (int e = 0; e < w[i].SLOTS; ++e) w[i].x[e] = (p.w[i] ? w[i].x[e] : 1.f) * (i ? f1 : f0);
+  }
+}
+// cos and sin of a lane's pairs.
+template <int M>
+__device__ __forceinline__ void load_angles(const Params& p, const Place& at, int lane, float2 (&cs)[M]) {
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    const int j = lane + 32 * m;
+    cs[m] = make_float2(1.f, 0.f);
+    if (j < p.half) {
+      const int64_t n = p.pos ? p.pos[p.axis[j] * p.tokens + at.tok] : at.n;
+      const double a = static_cast<double>(n) * p.turn[j];
+      sincospif(2.f * static_cast<float>(a - rint(a)), &cs[m].y, &cs[m].x);
+    }
+  }
 }
 
-template <typename T, int M>
+template <typename T, int M, bool REST>
 __global__ void __launch_bounds__(kThreads)
 rope_fwd_row_kernel(const __grid_constant__ Params p) {
-  extern __shared__ float2 cs[];
+  using Row = WarpRow<T, M, REST>;
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tile;
-  const int ntok = static_cast<int>(imin64(p.tile, p.tokens - tok0));
   const int lane = threadIdx.x & 31, d = p.d, half = p.half;
   const float inv_d = 1.f / static_cast<float>(d);
-  const int rows = ntok * (p.heads[0] + p.heads[1]);
-  fill_angles(p, tok0, ntok, cs);
-  WarpRow<T, M> w[2];
-  load_weights(p, w, lane);
-  __syncthreads();
-  const int step = kWarps * p.splits;
-  for (int r0 = (threadIdx.x >> 5) + kWarps * blockIdx.y; r0 < rows; r0 += 2 * step) {
-    WarpRow<T, M> x[2];
-    Row row[2];
+  const Place at = place_of<32>(p, static_cast<int64_t>(blockIdx.x) * p.tile);
+  if (!at.on) return;
+  float2 cs[M];
+  load_angles(p, at, lane, cs);
+  Row w[2];
+  load_weights(p, w, lane, p.scale[0], p.scale[1]);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      row[u] = row_of(p, tok0, ntok, min(r0 + u * step, rows - 1));
-      x[u].load(static_cast<const T*>(p.x[row[u].which]) + row[u].in, lane, half, d);
-    }
+  for (int which = 0; which < 2; ++which) {
+    const T* src = static_cast<const T*>(p.x[which]) + at.b * p.sb[which] + at.n * p.sn[which] + at.slot * p.sh[which];
+    T* dst = static_cast<T*>(p.out[which]) + ((at.b * p.heads[which] + at.slot) * p.N + at.n) * d;
+    const int64_t src_step = at.slots * p.sh[which], dst_step = at.slots * p.N * d;
+#pragma unroll 1
+    for (int h = at.slot; h < p.heads[which]; h += 2 * at.slots) {
+      const bool two = h + at.slots < p.heads[which];
+      Row x[2];
+      x[0].load(src, lane, half, d);
+      x[1].load(two ? src + src_step : src, lane, half, d);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if (r0 + u * step >= rows) break;
-      const int which = row[u].which;
-      float s = 0.f;
-      x[u].each([&](float& v, int) { s = fmaf(v, v, s); });
-      s = group_sum<32>(s);
-      const float r = rsqrtf(fmaf(s, inv_d, p.eps));
-      x[u].each([&](float& v, int) { v *= r; });
-      x[u].each([&](float& v, int i) { v *= which ? w[1].at(i) : w[0].at(i); });
-      x[u].turn(cs + row[u].t * half, lane, half, 1.f);
-      const float f = p.scale[which];
-      x[u].each([&](float& v, int) { v *= f; });
-      x[u].store(static_cast<T*>(p.out[which]) + row[u].out, lane, half, d);
+      for (int u = 0; u < 2; ++u) {
+        if (u && !two) break;
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < Row::SLOTS; ++e) s = fmaf(x[u].x[e], x[u].x[e], s);
+        const float r = rsqrtf(fmaf(group_sum<32>(s), inv_d, p.eps));
+#pragma unroll
+        for (int e = 0; e < Row::SLOTS; ++e) x[u].x[e] *= r * w[which].x[e];
+        x[u].turn(cs, 1.f);
+        x[u].store(dst + u * dst_step, lane, half, d);
+      }
+      src += 2 * src_step;
+      dst += 2 * dst_step;
     }
   }
 }
 
-template <typename T, int M>
+template <typename T, int M, bool REST>
 __global__ void __launch_bounds__(kThreads)
 rope_bwd_row_kernel(const __grid_constant__ Params p) {
-  extern __shared__ float2 cs[];
-  float* sdw = reinterpret_cast<float*>(cs + p.tile * p.half);  // [kWarps][2][d]
+  using Row = WarpRow<T, M, REST>;
+  extern __shared__ float row_dw[];  // [kWarps][2][d]
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, d = p.d, half = p.half;
   const float inv_d = 1.f / static_cast<float>(d);
-  float dw[2][4 * M];
+  Row w[2];
+  load_weights(p, w, lane, 1.f, 1.f);
+  WarpRow<float, M, REST> dw[2];
 #pragma unroll
-  for (int i = 0; i < 4 * M; ++i) dw[0][i] = dw[1][i] = 0.f;
-  WarpRow<T, M> w[2];
-  load_weights(p, w, lane);
+  for (int e = 0; e < Row::SLOTS; ++e) dw[0].x[e] = dw[1].x[e] = 0.f;
   for (int64_t tok0 = static_cast<int64_t>(blockIdx.x) * p.tile; tok0 < p.tokens;
        tok0 += static_cast<int64_t>(gridDim.x) * p.tile) {
-    const int ntok = static_cast<int>(imin64(p.tile, p.tokens - tok0));
-    const int rows = ntok * (p.heads[0] + p.heads[1]);
-    __syncthreads();
-    fill_angles(p, tok0, ntok, cs);
-    __syncthreads();
-    for (int r0 = threadIdx.x >> 5; r0 < rows; r0 += kWarps) {
-      const Row row = row_of(p, tok0, ntok, r0);
-      WarpRow<T, M> x, g;
-      x.load(static_cast<const T*>(p.x[row.which]) + row.in, lane, half, d);
-      g.load(static_cast<const T*>(p.dy[row.which]) + row.out, lane, half, d);
-      float s = 0.f;
-      x.each([&](float& v, int) { s = fmaf(v, v, s); });
-      s = group_sum<32>(s);
-      const float r = rsqrtf(fmaf(s, inv_d, p.eps));
-      x.each([&](float& v, int) { v *= r; });
-      g.turn(cs + row.t * half, lane, half, -1.f);
-      const float f = p.scale[row.which];
-      g.each([&](float& v, int i) {
-        v *= f;
-        if (row.which) dw[1][i] += v * x.at(i); else dw[0][i] += v * x.at(i);
-      });
-      g.each([&](float& v, int i) { v *= row.which ? w[1].at(i) : w[0].at(i); });
-      float dot = 0.f;
-      g.each([&](float& v, int i) { dot = fmaf(v, x.at(i), dot); });
-      dot = group_sum<32>(dot) * inv_d;
-      g.each([&](float& v, int i) { v = r * fmaf(-x.at(i), dot, v); });
-      g.store(static_cast<T*>(p.out[row.which]) + row.flat, lane, half, d);
+    const Place at = place_of<32>(p, tok0);
+    if (!at.on) continue;
+    float2 cs[M];
+    load_angles(p, at, lane, cs);
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const T* xs = static_cast<const T*>(p.x[which]) + at.b * p.sb[which] + at.n * p.sn[which] + at.slot * p.sh[which];
+      const T* gs = static_cast<const T*>(p.dy[which]) + ((at.b * p.heads[which] + at.slot) * p.N + at.n) * d;
+      T* dst = static_cast<T*>(p.out[which]) + (at.tok * p.heads[which] + at.slot) * d;
+      const int64_t x_step = at.slots * p.sh[which], g_step = at.slots * p.N * d, dst_step = at.slots * d;
+#pragma unroll 1
+      for (int h = at.slot; h < p.heads[which]; h += 2 * at.slots) {
+        const bool two = h + at.slots < p.heads[which];
+        Row x[2], g[2];
+        x[0].load(xs, lane, half, d);
+        g[0].load(gs, lane, half, d);
+        x[1].load(two ? xs + x_step : xs, lane, half, d);
+        g[1].load(two ? gs + g_step : gs, lane, half, d);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (u && !two) break;
+          float s = 0.f;
+#pragma unroll
+          for (int e = 0; e < Row::SLOTS; ++e) s = fmaf(x[u].x[e], x[u].x[e], s);
+          const float r = rsqrtf(fmaf(group_sum<32>(s), inv_d, p.eps));
+          g[u].turn(cs, -1.f);
+          float dot = 0.f;
+#pragma unroll
+          for (int e = 0; e < Row::SLOTS; ++e) {
+            x[u].x[e] *= r;
+            g[u].x[e] *= p.scale[which];
+            dw[which].x[e] = fmaf(g[u].x[e], x[u].x[e], dw[which].x[e]);
+            g[u].x[e] *= w[which].x[e];
+            dot = fmaf(g[u].x[e], x[u].x[e], dot);
+          }
+          dot = group_sum<32>(dot) * inv_d;
+#pragma unroll
+          for (int e = 0; e < Row::SLOTS; ++e) g[u].x[e] = r * fmaf(-x[u].x[e], dot, g[u].x[e]);
+          g[u].store(dst + u * dst_step, lane, half, d);
+        }
+        xs += 2 * x_step;
+        gs += 2 * g_step;
+        dst += 2 * dst_step;
+      }
     }
   }
-  WarpRow<float, M> o;
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    o.each([&](float& v, int i) { v = dw[which][i]; });
-    o.store(sdw + ((threadIdx.x >> 5) * 2 + which) * d, lane, half, d);
-  }
-  store_dw(p, sdw);
+  for (int which = 0; which < 2; ++which)
+    dw[which].store(row_dw + ((threadIdx.x >> 5) * 2 + which) * d, lane, half, d);
+  store_dw(p, row_dw);
 }
 
 // dw of the queries' and keys' weights from the CTAs' sums, in fp64 and a fixed order.
@@ -870,6 +851,20 @@ static Kernel vec_kernel(const Args& a) {
                                              : vec_kernel<T, BWD, false>(group_of(a));
 }
 
+template <typename T, bool BWD, int M>
+static Kernel row_kernel_of(bool rest) {
+  if constexpr (BWD)
+    return rest ? rope_bwd_row_kernel<T, M, true> : rope_bwd_row_kernel<T, M, false>;
+  else
+    return rest ? rope_fwd_row_kernel<T, M, true> : rope_fwd_row_kernel<T, M, false>;
+}
+template <typename T, bool BWD>
+static Kernel row_kernel(const Args& a) {
+  const bool rest = a.rot < a.d;
+  return a.d <= 64 ? row_kernel_of<T, BWD, 1>(rest) : a.d <= 128 ? row_kernel_of<T, BWD, 2>(rest)
+                                                                : row_kernel_of<T, BWD, 4>(rest);
+}
+
 // Dynamic shared memory beyond the default limit (wide rows, with their static part).
 static bool allow_smem(Kernel kern, size_t bytes) {
   return bytes <= 32 * 1024 ||
@@ -882,9 +877,9 @@ static la2_status launch_fwd(const Args& a, Params p, bool vec, int sms, cudaStr
   // few tokens (a decode batch): their heads over several CTAs
   const int64_t rows = (int64_t)p.tile * (a.H + a.Hkv);
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(3 * sms / tiles, (rows + 15) / 16));
-  const size_t smem = vec ? (size_t)2 * kDepth * kThreads * 16 : (size_t)p.tile * p.half * sizeof(float2);
+  const size_t smem = vec ? (size_t)2 * kDepth * kThreads * 16 : 0;
   const dim3 grid((unsigned)tiles, (unsigned)p.splits), block(kThreads);
-  const Kernel kern = vec ? vec_kernel<T, false>(a) : a.d <= 128 ? rope_fwd_row_kernel<T, 2> : rope_fwd_row_kernel<T, 4>;
+  const Kernel kern = vec ? vec_kernel<T, false>(a) : row_kernel<T, false>(a);
   if (!allow_smem(kern, smem)) return LA2_ERR_CUDA;
   LaunchTimer t(K_QK_ROPE, st);
   if (launch_pdl(kern, grid, block, smem, st, p) != cudaSuccess) return LA2_ERR_CUDA;
@@ -895,8 +890,8 @@ template <typename T>
 static la2_status launch_bwd(const Args& a, const Params& p, bool vec, int grid, void* dwq, void* dwk,
                              cudaStream_t st) {
   const size_t smem = (size_t)kWarps * 2 * p.d * sizeof(float) +
-                      (vec ? (size_t)4 * kDepthBwd * kThreads * 16 : (size_t)p.tile * p.half * sizeof(float2));
-  const Kernel kern = vec ? vec_kernel<T, true>(a) : a.d <= 128 ? rope_bwd_row_kernel<T, 2> : rope_bwd_row_kernel<T, 4>;
+                      (vec ? (size_t)4 * kDepthBwd * kThreads * 16 : 0);
+  const Kernel kern = vec ? vec_kernel<T, true>(a) : row_kernel<T, true>(a);
   if (!allow_smem(kern, smem)) return LA2_ERR_CUDA;
   {
     LaunchTimer t(K_QK_ROPE_BWD, st);
