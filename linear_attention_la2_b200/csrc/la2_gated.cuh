@@ -153,9 +153,11 @@ static Plan make_plan(int64_t B, int64_t H, int64_t N, int64_t d, int64_t dv, la
   return p;
 }
 
-template <typename Kernel>
-static bool raise_smem(Kernel kern, size_t bytes) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+// Lets a CUDA-core kernel take what a CTA may have (once a device).
+template <auto KERNEL>
+static bool raise_smem() {
+  static bool done[128];
+  return smem_attribute_set(KERNEL, 227 * 1024, done);
 }
 
 // CUDA cores: the chunks' own states of (a0, b0) as prefixes and, with out1, of
@@ -164,7 +166,7 @@ static la2_status chunk_states(const void* a0, const void* b0, const void* a1, c
                                float* out0, float* out1, double* tot, bool all, int64_t BH, const Shape& sh,
                                cudaStream_t st) {
   const size_t smem = smem_bytes(sh.d, sh.dv, 1, 1, 0);
-  if (!raise_smem(chunk_state_kernel, smem)) return LA2_ERR_CUDA;
+  if (!raise_smem<chunk_state_kernel>()) return LA2_ERR_CUDA;
   StateArgs p{};
   p.a[0] = static_cast<const float*>(a0);
   p.b[0] = static_cast<const float*>(b0);
@@ -204,7 +206,7 @@ static la2_status forward(const void* q, const void* k, const void* v, const voi
     if (!p.per && (s = scan(states, nullptr, tot, BH, sh, p.nel, 0, st)) != LA2_OK) return s;
   }
   const size_t smem = smem_bytes(sh.d, sh.dv, 2, 1, 1);
-  if (!raise_smem(fwd_kernel, smem)) return LA2_ERR_CUDA;
+  if (!raise_smem<fwd_kernel>()) return LA2_ERR_CUDA;
   LaunchTimer t(K_GATED_FWD, st);
   if (launch_pdl(fwd_kernel, dim3((unsigned)(BH * sh.C)), dim3(kThreads), smem, st, static_cast<const float*>(q),
                  static_cast<const float*>(k), static_cast<const float*>(v), static_cast<const float*>(gate),
@@ -352,7 +354,7 @@ static la2_status backward(const void* q, const void* k, const void* v, const vo
   a.tot = tot;
   {
     const size_t smem = smem_bytes(sh.d, sh.dv, 2, 2, 1);
-    if (!raise_smem(bwd_kernel, smem)) return LA2_ERR_CUDA;
+    if (!raise_smem<bwd_kernel>()) return LA2_ERR_CUDA;
     LaunchTimer t(K_GATED_DKDV, st);  // (dQ too)
     if (launch_pdl(bwd_kernel, dim3((unsigned)(BH * sh.C), 2), dim3(kThreads), smem, st, a, sh) != cudaSuccess)
       return LA2_ERR_CUDA;

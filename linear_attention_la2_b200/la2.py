@@ -583,17 +583,17 @@ def _raw_stream(device, stream):
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _scratch(need, given, device):
+def _scratch(need, given, ref):
     """(tensor, pointer, bytes) of a call's workspace: the caller's, or one allocated on
-    the current stream (kept by the caller of this until the launch is made)."""
+    ref's device and the current stream (kept by the caller of this until the launch is made)."""
     import torch
 
     if given is None:
         if need == 0:
             return None, 0, 0
-        given = torch.empty(need, dtype=torch.uint8, device=device)
+        given = ref.new_empty(need, dtype=torch.uint8)
     else:
-        _check_workspace(given, need, device)
+        _check_workspace(given, need, ref.device)
     return given, given.data_ptr(), given.numel()
 
 
@@ -612,10 +612,10 @@ def forward_gated(q, k, v, gate, out=None, workspace=None, stream=None):
     _dense(gate, shape[:3], dtype, device)
     with _call_on(device, stream):
         if out is None:
-            out = torch.empty(vshape, dtype=dtype, device=device)
+            out = torch.empty_like(v)
         else:
             _dense(out, vshape, dtype, device)
-        ws, wp, wn = _scratch(workspace_bytes_gated(B, H, N, d, dv, dt, False), workspace, device)
+        ws, wp, wn = _scratch(workspace_bytes_gated(B, H, N, d, dv, dt, False), workspace, q)
         _raise(la2_forward_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(), out.data_ptr(), B, H,
                                  N, d, dv, dt, wp, wn, _raw_stream(device, stream)))
     return out
@@ -636,13 +636,13 @@ def backward_gated(q, k, v, gate, do, outs=None, workspace=None, stream=None):
     _dense(gate, gshape, dtype, device)
     with _call_on(device, stream):
         if outs is None:
-            outs = tuple(torch.empty(x, dtype=dtype, device=device) for x in (shape, shape, vshape, gshape))
+            outs = tuple(map(torch.empty_like, (q, k, v, gate)))
         dq, dk, dvv, dgate = outs
         _dense(dq, shape, dtype, device)
         _dense(dk, shape, dtype, device)
         _dense(dvv, vshape, dtype, device)
         _dense(dgate, gshape, dtype, device)
-        ws, wp, wn = _scratch(workspace_bytes_gated(B, H, N, d, dv, dt, True), workspace, device)
+        ws, wp, wn = _scratch(workspace_bytes_gated(B, H, N, d, dv, dt, True), workspace, q)
         _raise(la2_backward_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(), do.data_ptr(),
                                   dq.data_ptr(), dk.data_ptr(), dvv.data_ptr(), dgate.data_ptr(), B, H, N, d, dv,
                                   dt, wp, wn, _raw_stream(device, stream)))
@@ -691,7 +691,7 @@ def kv_state_gated(k, v, gate, state=None, slots=None, workspace=None, stream=No
             state = torch.zeros((B, H, d, dv), dtype=torch.float32, device=device)
         S, sp = _pool(state, (H, d, dv), B, slots, device)
         need = _sized(la2_kv_state_gated_workspace_size(B, H, N, d, dv, dt))
-        ws, wp, wn = _scratch(need, workspace, device)
+        ws, wp, wn = _scratch(need, workspace, k)
         _raise(la2_kv_state_gated(k.data_ptr(), v.data_ptr(), gate.data_ptr(), state.data_ptr(), sp, S, B, H, N,
                                   d, dv, dt, wp, wn, _raw_stream(device, stream)))
     return state
@@ -714,8 +714,7 @@ def decode_step_gated(q, k, v, gate, state, slots=None, out=None, stream=None):
     S, sp = _pool(state, (H, d, dv), B, slots, device)
     with _call_on(device, stream):
         if out is None:
-            make = torch.empty if slots is None else torch.zeros
-            out = make((B, H, dv), dtype=dtype, device=device)
+            out = torch.empty_like(v) if slots is None else torch.zeros_like(v)
         else:
             _dense(out, (B, H, dv), dtype, device)
         _raise(la2_decode_step_gated(q.data_ptr(), k.data_ptr(), v.data_ptr(), gate.data_ptr(), out.data_ptr(),
@@ -817,8 +816,7 @@ def qk_norm_rope(q, k, wq=None, wk=None, positions=None, base: float = 10000.0, 
      device) = _rope_args(q, k, wq, wk, positions, rot, sections)
     with _call_on(device, stream):
         if outs is None:
-            qo = torch.empty((B, H, N, d), dtype=dtype, device=device)
-            ko = torch.empty((B, Hkv, N, d), dtype=dtype, device=device)
+            qo, ko = q.new_empty((B, H, N, d)), k.new_empty((B, Hkv, N, d))
         else:
             qo, ko = outs
             _dense(qo, (B, H, N, d), dtype, device)
@@ -842,8 +840,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, wq=None, wk=None, positions=None
     _dense(dk_out, (B, Hkv, N, d), dtype, device)
     with _call_on(device, stream):
         if outs is None:
-            dq = torch.empty((B, N, H, d), dtype=dtype, device=device)
-            dk = torch.empty((B, N, Hkv, d), dtype=dtype, device=device)
+            dq, dk = q.new_empty(q.shape), k.new_empty(k.shape)
             dwq = None if wq is None else torch.empty_like(wq)
             dwk = None if wk is None else torch.empty_like(wk)
         else:
@@ -854,7 +851,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, wq=None, wk=None, positions=None
                 if w is not None:
                     _dense(w, (d,), dtype, device)
         need = _sized(la2_qk_norm_rope_backward_workspace_size(B, N, H, Hkv, d))
-        ws, wp, wn = _scratch(need, workspace, device)
+        ws, wp, wn = _scratch(need, workspace, q)
         _raise(la2_qk_norm_rope_backward(dq_out.data_ptr(), dk_out.data_ptr(), qp, kp, qs, ks, wqp, wkp, pp,
                                          dq.data_ptr(), dk.data_ptr(), dwq.data_ptr() if dwq is not None else 0,
                                          dwk.data_ptr() if dwk is not None else 0, B, N, H, Hkv, d, rot, axes,
