@@ -13,13 +13,11 @@ struct Plan {
   // Tensor cores: the pieces whose own states are computed (Ls rows, K a sequence,
   // `per` a chunk); per = 0 (and K = C): a scan turns them into the chunks' states.
   int64_t Ls = 0, K = 1, per = 0;
-  size_t off_suffix = 0, off_suffix_t = 0, off_tot = 0, off_qdq = 0, off_kdk = 0;  // prefix states at 0
+  size_t off_suffix = 0, off_suffix_t = 0, off_sum = 0, off_tot = 0, off_qdq = 0, off_kdk = 0;  // prefix states at 0
   size_t bytes = 0;
 };
 
 constexpr int64_t kSumPieces = 12;  // pieces a chunk adds up itself; more are scanned
-
-static_assert(kSumPieces <= kMaxPieces, "the gates' gradient sums as many");
 
 enum Need { NEED_FWD, NEED_BWD, NEED_STATE };
 
@@ -116,6 +114,9 @@ static Plan make_plan_uncached(int64_t B, int64_t H, int64_t N, int64_t d, int64
   if (need == NEED_BWD) at += one;
   p.off_suffix_t = at;  // tensor cores: the suffix states transposed, for dV
   if (need == NEED_BWD && p.tc) at += one;
+  // the starts of the dQ and then of the dK pass's chunks, where the chunks add them up
+  p.off_sum = at;
+  if (need == NEED_BWD && states && p.per > 0) at += 2 * round256((size_t)BH * p.C * p.nel * sizeof(float));
   p.off_tot = at;
   if (states) at += round256((size_t)BH * p.K * sizeof(double));
   p.off_qdq = at;
@@ -275,10 +276,25 @@ static la2_status forward_tc(const void* q, const void* k, const void* v, const 
   return launch_status();
 }
 
+// The gates' gradient, from the chunks' starts: the sums left by the gradient passes,
+// or the scanned states.
 template <typename T>
 static la2_status gate_grad(const void* gate, const float* qdq, const float* kdk, const float* prefix,
-                            const float* suffix, const double* tot, void* dgate, int64_t BH, const Shape& sh,
-                            const Plan& p, cudaStream_t st);
+                            const float* suffix, void* dgate, int64_t BH, const Shape& sh, const Plan& p,
+                            cudaStream_t st) {
+  LaunchTimer t(K_GATED_GATE, st);
+  if (launch_pdl(gate_grad_kernel<T>, dim3((unsigned)(BH * sh.C)), dim3(kGradThreads), 0, st,
+                 static_cast<const T*>(gate), qdq, kdk, prefix, suffix, static_cast<T*>(dgate), sh.N, sh.L, sh.C,
+                 p.nel) != cudaSuccess)
+    return LA2_ERR_CUDA;
+  return launch_status();
+}
+
+// Where the dQ (0) and dK (1) passes leave the chunks' starts, or null: no chunks, or scanned.
+static float* start_sums(char* ws, const Plan& p, int64_t BH, int which) {
+  if (p.C == 1 || p.per == 0) return nullptr;
+  return reinterpret_cast<float*>(ws + p.off_sum + which * round256((size_t)BH * p.C * p.nel * sizeof(float)));
+}
 
 static la2_status backward_tc(const void* q, const void* k, const void* v, const void* gate, const void* dout,
                               void* dq, void* dk, void* dvv, void* dgate, char* ws, const Plan& p, int64_t BH,
@@ -288,6 +304,7 @@ static la2_status backward_tc(const void* q, const void* k, const void* v, const
   float* suffix_t = p.C > 1 ? reinterpret_cast<float*>(ws + p.off_suffix_t) : nullptr;
   float* qdq = reinterpret_cast<float*>(ws + p.off_qdq);
   float* kdk = reinterpret_cast<float*>(ws + p.off_kdk);
+  float *prefix_sum = start_sums(ws, p, BH, 0), *suffix_sum = start_sums(ws, p, BH, 1);
   double* tot = reinterpret_cast<double*>(ws + p.off_tot);
   const Tile tq(q, BH, sh.N, sh.d), tk(k, BH, sh.N, sh.d), tv(v, BH, sh.N, sh.dv), tdo(dout, BH, sh.N, sh.dv);
   const Tile tdq(dq, BH, sh.N, sh.d), tdk(dk, BH, sh.N, sh.d), tdv(dvv, BH, sh.N, sh.dv);
@@ -299,6 +316,7 @@ static la2_status backward_tc(const void* q, const void* k, const void* v, const
   {
     TcParams t = tc_params(gate, prefix, tot, sh, p);
     t.dots = qdq;
+    t.sum = prefix_sum;
     LaunchTimer lt(K_GATED_DQ, st);
     if (launch_sm100<false, true>(tdo, tv, tk, tdq, tq, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
   }
@@ -309,22 +327,12 @@ static la2_status backward_tc(const void* q, const void* k, const void* v, const
     if (launch_sm100<true, false>(tk, tq, tdo, tdv, tdv, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
     t.init = suffix;
     t.dots = kdk;
+    t.sum = suffix_sum;
     if (launch_sm100<true, true>(tv, tdo, tq, tdk, tk, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
   }
   if ((s = launch_status()) != LA2_OK) return s;
-  return gate_grad<__nv_bfloat16>(gate, qdq, kdk, prefix, suffix, tot, dgate, BH, sh, p, st);
-}
-
-template <typename T>
-static la2_status gate_grad(const void* gate, const float* qdq, const float* kdk, const float* prefix,
-                            const float* suffix, const double* tot, void* dgate, int64_t BH, const Shape& sh,
-                            const Plan& p, cudaStream_t st) {
-  LaunchTimer t(K_GATED_GATE, st);
-  if (launch_pdl(gate_grad_kernel<T>, dim3((unsigned)(BH * sh.C)), dim3(kGradThreads), 0, st,
-                 static_cast<const T*>(gate), qdq, kdk, prefix, suffix, tot, static_cast<T*>(dgate), sh.N,
-                 sh.L, sh.C, p.nel, p.K, p.per) != cudaSuccess)
-    return LA2_ERR_CUDA;
-  return launch_status();
+  return gate_grad<__nv_bfloat16>(gate, qdq, kdk, prefix_sum ? prefix_sum : prefix, suffix_sum ? suffix_sum : suffix,
+                                  dgate, BH, sh, p, st);
 }
 
 static la2_status backward(const void* q, const void* k, const void* v, const void* gate, const void* dout,
@@ -351,6 +359,8 @@ static la2_status backward(const void* q, const void* k, const void* v, const vo
   a.kdk = reinterpret_cast<float*>(ws + p.off_kdk);
   a.prefix = prefix;
   a.suffix = suffix;
+  a.prefix_sum = start_sums(ws, p, BH, 0);
+  a.suffix_sum = start_sums(ws, p, BH, 1);
   a.tot = tot;
   {
     const size_t smem = smem_bytes(sh.d, sh.dv, 2, 2, 1);
@@ -360,7 +370,8 @@ static la2_status backward(const void* q, const void* k, const void* v, const vo
       return LA2_ERR_CUDA;
   }
   if ((s = launch_status()) != LA2_OK) return s;
-  return gate_grad<float>(gate, a.qdq, a.kdk, prefix, suffix, tot, dgate, BH, sh, p, st);
+  return gate_grad<float>(gate, a.qdq, a.kdk, a.prefix_sum ? a.prefix_sum : prefix,
+                          a.suffix_sum ? a.suffix_sum : suffix, dgate, BH, sh, p, st);
 }
 
 // Pointers of a call: every one non-null and aligned, no output over an input,

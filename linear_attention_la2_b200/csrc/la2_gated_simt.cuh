@@ -274,10 +274,11 @@ struct Shape {
 
 // The state that chunk ch of a sequence starts from, in rows of stride_of(dv), zeros
 // around it: the scanned one, or the own states of the chunks before it (BACK: behind
-// it), nearest first, each decayed over the nearer ones.
+// it), nearest first, each decayed over the nearer ones. With `sum`, it also goes there
+// ([BH][C][d*dv], for the gates' gradient).
 template <bool BACK>
 __device__ __forceinline__ void load_state(float* S, const float* __restrict__ states, const double* __restrict__ tot,
-                                           int64_t bh, int64_t ch, const Shape& sh) {
+                                           int64_t bh, int64_t ch, const Shape& sh, float* sum) {
   const int ld = stride_of(sh.dv), w = ld / 4, nel = sh.d * sh.dv;
   const int n = !states ? 0 : sh.pieces ? static_cast<int>(BACK ? sh.C - 1 - ch : ch) : 1;
   const int64_t first = bh * sh.C + (sh.pieces ? (BACK ? ch + 1 : ch - 1) : ch);
@@ -301,6 +302,7 @@ __device__ __forceinline__ void load_state(float* S, const float* __restrict__ s
         if (j + 1 < n) f *= expf(static_cast<float>(tot[first + j * step]));
       }
     }
+    if (sum && r < sh.d && c < sh.dv) store4(sum + (bh * sh.C + ch) * nel + r * sh.dv, c, sh.dv, x);
     *reinterpret_cast<float4*>(S + r * ld + c) = make_float4(x[0], x[1], x[2], x[3]);
   }
 }
@@ -379,7 +381,7 @@ fwd_kernel(const float* __restrict__ q, const float* __restrict__ k, const float
     load_rows(Qs, q + row * d, rows, d);
     load_rows(Ks, k + row * d, rows, d);
     load_rows(Vs, v + row * dv, rows, dv);
-    if (i0 == t0) load_state<false>(S, states, tot, bh, ch, sh);
+    if (i0 == t0) load_state<false>(S, states, tot, bh, ch, sh, nullptr);
     gate_tables(gate + row, rows, i0 == 0, c, head, tail);
     scores(P, Qs, Ks, ld, round4(d), c);
     __syncthreads();
@@ -407,6 +409,7 @@ struct BwdArgs {
   float *dq, *dk, *dv;
   float *qdq, *kdk;                // the rows' dots
   const float *prefix, *suffix;    // chunk states, or null
+  float *prefix_sum, *suffix_sum;  // where the chunks' starts go, or null
   const double* tot;
 };
 // Rows' values 4 tr + i of columns cc[j] out, and their dots with `x` (row stride lx)
@@ -455,7 +458,7 @@ __device__ __forceinline__ void bwd_dq(const BwdArgs& p, const Shape& sh, double
     load_rows(Vs, p.v + row * dv, rows, dv);
     load_rows(Ks, p.k + row * d, rows, d);
     load_rows(Qs, p.q + row * d, rows, d);
-    if (i0 == t0) load_state<false>(S, p.prefix, p.tot, bh, ch, sh);
+    if (i0 == t0) load_state<false>(S, p.prefix, p.tot, bh, ch, sh, p.prefix_sum);
     gate_tables(p.gate + row, rows, i0 == 0, c, head, tail);
     scores(A, Gs, Vs, lv, round4(dv), c);
     __syncthreads();
@@ -501,7 +504,7 @@ __device__ __forceinline__ void bwd_dkdv(const BwdArgs& p, const Shape& sh, doub
     load_rows(Ks, p.k + row * d, rows, d);
     load_rows(Gs, p.dout + row * dv, rows, dv);
     load_rows(Vs, p.v + row * dv, rows, dv);
-    if (n == nblk - 1) load_state<true>(U, p.suffix, p.tot, bh, ch, sh);
+    if (n == nblk - 1) load_state<true>(U, p.suffix, p.tot, bh, ch, sh, p.suffix_sum);
     gate_tables(p.gate + row, rows, i0 == 0, c, head, tail);
     // P[t][j] = D (q_t . k_j), then dV; the same tile then holds D (dO_t . v_j) for dK
     scores(P, Qs, Ks, ld, round4(d), c);
@@ -659,69 +662,38 @@ pool_update_kernel(const float* __restrict__ chunks, const double* __restrict__ 
 
 // dl_t = flow at the chunk's end + sum over the chunk's rows from t on of
 // (q . dq - k . dk). The flow at the end of chunk c is <state before chunk c + 1, U
-// behind chunk c> (0 for the last chunk); elements in any common order. One CTA a
-// (sequence, chunk). `per` = 0: prefix and suffix hold those states, scanned;
-// otherwise they hold K pieces' own states, `per` a chunk, and are summed here,
-// nearest first, each decayed over the nearer ones (at most kMaxPieces).
+// behind chunk c> (0 for the last chunk): the starts of the dQ and dK passes' chunks,
+// which those passes (or a scan) left there; elements in any common order. One CTA a
+// (sequence, chunk). (Adding those states up from the chunks' pieces here, up to 12 of
+// 64 KB a CTA, took 31 us at B2 H32 N8K.)
 constexpr int kGradThreads = 1024;
-constexpr int kMaxPieces = 16;
 template <typename T>
 __global__ void __launch_bounds__(kGradThreads)
 gate_grad_kernel(const T* __restrict__ gate, const float* __restrict__ qdq, const float* __restrict__ kdk,
-                 const float* __restrict__ prefix, const float* __restrict__ suffix,
-                 const double* __restrict__ tot, T* __restrict__ dgate, int64_t N, int64_t L, int64_t C, int nel,
-                 int64_t K, int64_t per) {
+                 const float* __restrict__ prefix, const float* __restrict__ suffix, T* __restrict__ dgate, int64_t N,
+                 int64_t L, int64_t C, int nel) {
   pdl_launch_dependents();
   pdl_wait();
   constexpr int kWarps = kGradThreads / 32;
   __shared__ double part[kWarps];
-  __shared__ float weight[2][kMaxPieces];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t bh = blockIdx.x / C, ch = blockIdx.x % C;
   const int64_t t0 = ch * L, t1 = imin64(N, t0 + L);
   double carry = 0.0;
   if (ch + 1 < C) {
-    const int64_t edge = (ch + 1) * per;  // first piece behind the chunk
-    const int n_pre = per ? static_cast<int>(edge) : 1, n_suf = per ? static_cast<int>(K - edge) : 1;
-    const float* a = prefix + (bh * K + (per ? edge - 1 : ch + 1)) * nel;
-    const float* b = suffix + (bh * K + (per ? edge : ch)) * nel;
-    if (threadIdx.x < 2) {
-      float f = 1.f;
-      const int n = threadIdx.x ? n_suf : n_pre;
-      for (int j = 0; j < n; ++j) {
-        weight[threadIdx.x][j] = f;
-        if (j + 1 < n) f *= expf(static_cast<float>(tot[bh * K + (threadIdx.x ? edge + j : edge - 1 - j)]));
-      }
-    }
-    __syncthreads();
+    const float* a = prefix + (bh * C + ch + 1) * nel;
+    const float* b = suffix + (bh * C + ch) * nel;
     double x = 0.0;
-    auto term = [&](int i) {
-      float u = 0.f, v = 0.f;
-      for (int j = 0; j < n_pre; ++j) u = fmaf(weight[0][j], a[i - static_cast<int64_t>(j) * nel], u);
-      for (int j = 0; j < n_suf; ++j) v = fmaf(weight[1][j], b[i + static_cast<int64_t>(j) * nel], v);
-      x += static_cast<double>(u) * v;
-    };
-    auto term4 = [&](int i) {
-      float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+    if (nel % 4 == 0) {
 #pragma unroll 4
-      for (int j = 0; j < n_pre; ++j) {
-        const float4 y = *reinterpret_cast<const float4*>(a + i - static_cast<int64_t>(j) * nel);
-        const float f = weight[0][j];
-        u = make_float4(fmaf(f, y.x, u.x), fmaf(f, y.y, u.y), fmaf(f, y.z, u.z), fmaf(f, y.w, u.w));
+      for (int i = 4 * threadIdx.x; i < nel; i += 4 * kGradThreads) {
+        const float4 u = *reinterpret_cast<const float4*>(a + i), v = *reinterpret_cast<const float4*>(b + i);
+        x += (static_cast<double>(u.x) * v.x + static_cast<double>(u.y) * v.y) +
+             (static_cast<double>(u.z) * v.z + static_cast<double>(u.w) * v.w);
       }
-#pragma unroll 4
-      for (int j = 0; j < n_suf; ++j) {
-        const float4 y = *reinterpret_cast<const float4*>(b + i + static_cast<int64_t>(j) * nel);
-        const float f = weight[1][j];
-        v = make_float4(fmaf(f, y.x, v.x), fmaf(f, y.y, v.y), fmaf(f, y.z, v.z), fmaf(f, y.w, v.w));
-      }
-      x += (static_cast<double>(u.x) * v.x + static_cast<double>(u.y) * v.y) +
-           (static_cast<double>(u.z) * v.z + static_cast<double>(u.w) * v.w);
-    };
-    if (nel % 4 == 0)
-      for (int i = 4 * threadIdx.x; i < nel; i += 4 * kGradThreads) term4(i);
-    else
-      for (int i = threadIdx.x; i < nel; i += kGradThreads) term(i);
+    } else {
+      for (int i = threadIdx.x; i < nel; i += kGradThreads) x += static_cast<double>(a[i]) * b[i];
+    }
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
     if (lane == 0) part[w] = x;

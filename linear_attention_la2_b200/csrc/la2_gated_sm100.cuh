@@ -164,6 +164,7 @@ struct TcParams {
   const float* init;           // [BH][K][128*128] (state_f4): states of the sequence's pieces, or null
   const double* tot;           // [BH][K]: sums of their gates
   float* dots;                 // GRAD: [BH][N]
+  float* sum;                  // GRAD, per > 0: [BH][C][128*128], where each chunk leaves the state it starts from
   int64_t N, L, C, spin_limit;
   // Pieces: `per` a chunk; a chunk starts from all pieces before it (walking back:
   // behind it), each decayed over those between. per = 0: init holds one state a
@@ -634,6 +635,13 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
               x[4 * q + 3] = fmaf(f, y.w, x[4 * q + 3]);
             }
             if (j + 1 < pieces) f *= expf(static_cast<float>(prm.tot[at]));
+          }
+          if (GRAD && prm.sum) {
+            float4* dst = reinterpret_cast<float4*>(prm.sum + (bh * prm.C + ch) * 128 * 128);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              dst[s::state_f4<128>(r, col0 / 4 + h * 4 + q)] =
+                  make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(x[e]);
