@@ -367,7 +367,7 @@ LA2_API la2_status la2_decode_step(const void *q, const void *k, const void *v, 
  * la2_kv_state_gated: the state a prefill leaves,
  *   S <- exp(gate_0 + ... + gate_{N-1}) S + sum_t exp(gate_{t+1} + ... + gate_{N-1}) k_t^T v_t,
  * so a later call continues an earlier one, and a zeroed slot (or a first gate of
- * -infinity) starts afresh. k, v, gate as for la2_forward_gated; state 16-byte
+ * -infinity, whatever the slot held) starts afresh. k, v, gate as for la2_forward_gated; state 16-byte
  * aligned; summation order fixed. Workspace: la2_kv_state_gated_workspace_size.
  *
  * la2_decode_step_gated: one new token per row, S <- exp(gate) S + k^T v, o = q S.

@@ -808,7 +808,8 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 // start), so the accumulator is never decayed: the blocks are walked from that edge,
 // and the sum of the gates walked so far goes into the scale of the rows. Y~ is value
 // and remainder, so the fp32 state is good to 2^-17: it is what the caller's pool
-// receives after a prefill. Bound by HBM: K and V are read once. Warps: 0 loads,
+// receives after a prefill (B3 H16 N3001: 4.5e-6 off; with a second remainder 2.1e-6,
+// the tensor core's own sums, for 33 us instead of 28.6). Bound by HBM: K and V are read once. Warps: 0 loads,
 // 1 MMA, 2 the rows' factors, 4-11 scale rows (four threads a row), 4-7 write the
 // state out. Two CTAs an SM: one's scaling (about 1000 cycles a block) runs beside the
 // other's waits, loads and MMAs; one CTA with twice the buffers was 1.4 times slower.

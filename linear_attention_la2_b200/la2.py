@@ -560,6 +560,12 @@ def _dense_ref(t, dims):
     return t.shape, t.dtype, _dtype_code(t), t.device
 
 
+def _width(t):
+    if t.dim() == 0:
+        raise La2Error(LA2_ERR_INVALID_ARG)
+    return t.shape[-1]
+
+
 _HERE = contextlib.nullcontext()
 
 
@@ -605,7 +611,7 @@ def forward_gated(q, k, v, gate, out=None, workspace=None, stream=None):
 
     shape, dtype, dt, device = _dense_ref(q, 4)
     B, H, N, d = shape
-    dv = v.shape[-1]
+    dv = _width(v)
     vshape = (B, H, N, dv)
     _dense(k, shape, dtype, device)
     _dense(v, vshape, dtype, device)
@@ -628,7 +634,7 @@ def backward_gated(q, k, v, gate, do, outs=None, workspace=None, stream=None):
 
     shape, dtype, dt, device = _dense_ref(q, 4)
     B, H, N, d = shape
-    dv = v.shape[-1]
+    dv = _width(v)
     vshape, gshape = (B, H, N, dv), shape[:3]
     _dense(k, shape, dtype, device)
     _dense(v, vshape, dtype, device)
@@ -681,7 +687,7 @@ def kv_state_gated(k, v, gate, state=None, slots=None, workspace=None, stream=No
 
     shape, dtype, dt, device = _dense_ref(k, 4)
     B, H, N, d = shape
-    dv = v.shape[-1]
+    dv = _width(v)
     _dense(v, (B, H, N, dv), dtype, device)
     _dense(gate, shape[:3], dtype, device)
     if state is None and slots is not None:
@@ -707,7 +713,7 @@ def decode_step_gated(q, k, v, gate, state, slots=None, out=None, stream=None):
 
     shape, dtype, dt, device = _dense_ref(q, 3)
     B, H, d = shape
-    dv = v.shape[-1]
+    dv = _width(v)
     _dense(k, shape, dtype, device)
     _dense(v, (B, H, dv), dtype, device)
     _dense(gate, (B, H), dtype, device)
