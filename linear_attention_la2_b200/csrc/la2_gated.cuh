@@ -52,8 +52,12 @@ static Plan make_plan_uncached(int64_t B, int64_t H, int64_t N, int64_t d, int64
     p.L = (g_chunk_len + kRows - 1) / kRows * kRows;
   } else if (p.tc) {
     // in blocks of the main pass: what a launch of it and of the state pass costs
-    // beside its blocks, a block of the state pass (two CTAs an SM), and the scan
-    constexpr double kFixed = 5.0, kStateFixed = 5.0, kStateBlock = 0.7, kScan = 5.0;
+    // beside its blocks, a block of the state pass (two CTAs an SM), a piece's state that
+    // a chunk adds up, and the scan. (Gradients in 2 chunks a sequence of 1, 2, 3, 4, 5, 6
+    // pieces: B2 H32 N8K 561, 506, 483, 473, 507, 521 us, where a pass of 4 is the last
+    // that fits in one wave; B4 H16 N2K 173, 164, 177, 173, -, 200 us.)
+    constexpr double kFixed = 5.0, kStateFixed = 5.0, kStateBlock = 0.7, kPiece = 1.0, kScan = 5.0;
+    const double passes = need == NEED_BWD ? 2 : 1, launches = need == NEED_BWD ? 3 : 1;  // state, main
     const int64_t G = std::max(sms, 1), most = std::max<int64_t>(1, T / 2);
     auto waves = [](int64_t units, int64_t slots) { return static_cast<double>((units + slots - 1) / slots); };
     auto blocks = [&](int64_t parts) { return static_cast<double>((T + parts - 1) / parts); };
@@ -62,10 +66,12 @@ static Plan make_plan_uncached(int64_t B, int64_t H, int64_t N, int64_t d, int64
     for (int64_t c = 1; c <= most && (c == 1 || BH * (c - 1) < 8 * G); ++c) {
       const int64_t mmax = need == NEED_STATE || c == 1 ? 1 : std::max<int64_t>(1, std::min(kSumPieces, T) / c);
       for (int64_t m = 1; m <= mmax; ++m) {
-        double cost = need == NEED_STATE ? 0.0 : waves(BH * c, G) * (blocks(c * m) * m + kFixed);
+        double cost = need == NEED_STATE ? 0.0 : launches * waves(BH * c, G) * (blocks(c * m) * m + kFixed);
         if (need == NEED_STATE || c > 1)
-          cost += waves(BH * (need == NEED_STATE ? c : (c - 1) * m), 2 * G) * (blocks(c * m) * kStateBlock + kStateFixed);
-        if (need != NEED_STATE && c > kSumPieces) cost += kScan;
+          cost += passes * waves(BH * (need == NEED_STATE ? c : (c - 1) * m), 2 * G) *
+                  (blocks(c * m) * kStateBlock + kStateFixed);
+        if (need != NEED_STATE)
+          cost += c > kSumPieces ? passes * kScan : launches * kPiece * static_cast<double>((c - 1) * m);
         if (best < 0.0 || cost < best) {
           best = cost;
           best_c = c;
