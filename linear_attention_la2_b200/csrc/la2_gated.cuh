@@ -53,10 +53,10 @@ static Plan make_plan_uncached(int64_t B, int64_t H, int64_t N, int64_t d, int64
   } else if (p.tc) {
     // in blocks of the main pass: what a launch of it and of the state pass costs
     // beside its blocks, a block of the state pass (two CTAs an SM), a piece's state that
-    // a chunk adds up, and the scan. (Gradients in 2 chunks a sequence of 1, 2, 3, 4, 5, 6
+    // a chunk adds up, and the scan, for itself and for a state. (Gradients in 2 chunks a sequence of 1, 2, 3, 4, 5, 6
     // pieces: B2 H32 N8K 561, 506, 483, 473, 507, 521 us, where a pass of 4 is the last
     // that fits in one wave; B4 H16 N2K 173, 164, 177, 173, -, 200 us.)
-    constexpr double kFixed = 5.0, kStateFixed = 5.0, kStateBlock = 0.7, kPiece = 1.0, kScan = 5.0;
+    constexpr double kFixed = 6.0, kStateFixed = 5.0, kStateBlock = 0.7, kPiece = 1.0, kScan = 4.0, kScanState = 0.0125;
     const double passes = need == NEED_BWD ? 2 : 1, launches = need == NEED_BWD ? 3 : 1;  // state, main
     const int64_t G = std::max(sms, 1), most = std::max<int64_t>(1, T / 2);
     auto waves = [](int64_t units, int64_t slots) { return static_cast<double>((units + slots - 1) / slots); };
@@ -71,7 +71,8 @@ static Plan make_plan_uncached(int64_t B, int64_t H, int64_t N, int64_t d, int64
           cost += passes * waves(BH * (need == NEED_STATE ? c : (c - 1) * m), 2 * G) *
                   (blocks(c * m) * kStateBlock + kStateFixed);
         if (need != NEED_STATE)
-          cost += c > kSumPieces ? passes * kScan : launches * kPiece * static_cast<double>((c - 1) * m);
+          cost += c > kSumPieces ? passes * (kScan + kScanState * static_cast<double>(BH * c))
+                                 : launches * kPiece * static_cast<double>((c - 1) * m);
         if (best < 0.0 || cost < best) {
           best = cost;
           best_c = c;
