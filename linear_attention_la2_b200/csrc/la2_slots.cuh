@@ -105,6 +105,67 @@ compact_plan_kernel(const int32_t* __restrict__ live, int32_t* __restrict__ move
   }
 }
 
+// Up to kSmall slots: plan and moves in one launch. CTA (k, part) finds the k-th live
+// slot from n_live on and the k-th hole below it (there are at most n / 2) and moves its
+// piece; k = 0, part 0 also writes `moved` of the slots that stay or are dead. Every CTA
+// reads all flags, four a thread (48 slots of 2 MB, 32 live: 10.2 us, with a launch for
+// the plan 14.2).
+constexpr int kSmall = 4 * kThreads;
+template <typename V>
+__global__ void __launch_bounds__(kThreads)
+compact_small_kernel(V* __restrict__ pool, const int32_t* __restrict__ live, int32_t* __restrict__ moved, int n,
+                     int64_t slot, int64_t parts) {
+  __shared__ int sums[kThreads / 32], from_to[2];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t k = blockIdx.x / parts, part = blockIdx.x % parts;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  bool on[4];
+  int count = 0;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int i = 4 * threadIdx.x + u;
+    on[u] = i < n && live[i] != 0;
+    count += on[u];
+  }
+  count = __reduce_add_sync(0xffffffffu, count);
+  if (lane == 0) sums[w] = count;
+  if (threadIdx.x < 2) from_to[threadIdx.x] = -1;
+  __syncthreads();
+  int n_live = 0;
+#pragma unroll
+  for (int x = 0; x < kThreads / 32; ++x) n_live += sums[x];
+  __syncthreads();
+  // running counts of the slots to move (low half) and of the holes (high half)
+  auto mark = [&](int u) {
+    const int i = 4 * threadIdx.x + u;
+    return i >= n ? 0 : i < n_live ? (on[u] ? 0 : 1 << 16) : (on[u] ? 1 : 0);
+  };
+  const int own = mark(0) + mark(1) + mark(2) + mark(3);
+  int run = own;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, run, m);
+    if (lane >= m) run += up;
+  }
+  if (lane == 31) sums[w] = run;
+  __syncthreads();
+  run -= own;
+  for (int x = 0; x < w; ++x) run += sums[x];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int i = 4 * threadIdx.x + u, x = mark(u);
+    if (x & 0xffff && (run & 0xffff) == k) from_to[0] = i;
+    if (x >> 16 && run >> 16 == k) from_to[1] = i;
+    if (blockIdx.x == 0 && i < n && !(x & 0xffff)) moved[i] = on[u] ? i : -1;
+    run += x;
+  }
+  __syncthreads();
+  if (from_to[0] < 0) return;  // as many holes as slots to move
+  if (part == 0 && threadIdx.x == 0) moved[from_to[0]] = from_to[1];
+  move_piece(pool + from_to[1] * slot, pool + from_to[0] * slot, false, part, slot);
+}
+
 // Slot i to moved[i]. Sources lie at or behind n_live, destinations below it.
 template <typename V>
 __global__ void __launch_bounds__(kThreads)
@@ -169,6 +230,16 @@ la2_status la2_state_compact(float* state, const int32_t* live, int32_t* moved, 
   const int64_t elems = vec ? slot / 4 : slot, parts = (elems + slots::kPiece - 1) / slots::kPiece;
   if (double(n_slots) * double(parts) > 2147483647.0) return LA2_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (n_slots <= slots::kSmall) {
+    const dim3 grid((unsigned)(std::max<int64_t>(1, n_slots / 2) * parts)), block(slots::kThreads);
+    LaunchTimer t(K_STATE_COMPACT, st);
+    const cudaError_t e =
+        vec ? launch_pdl(slots::compact_small_kernel<float4>, grid, block, 0, st, reinterpret_cast<float4*>(state),
+                         live, moved, (int)n_slots, elems, parts)
+            : launch_pdl(slots::compact_small_kernel<float>, grid, block, 0, st, state, live, moved, (int)n_slots,
+                         elems, parts);
+    return e == cudaSuccess ? launch_status() : LA2_ERR_CUDA;
+  }
   const size_t smem = ni;
   static bool attr_done[128];
   if (smem > 48 * 1024 &&

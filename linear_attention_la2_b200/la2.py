@@ -548,8 +548,8 @@ def workspace_bytes_gated(B, H, N, d, dv, dtype_code, is_backward) -> int:
 
 
 def _dense(t, shape, dtype, device):
-    """Refuses a tensor that is not a contiguous CUDA one of this shape, type and device."""
-    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_cuda or not t.is_contiguous():
+    """Refuses a tensor that is not a contiguous one of this shape, type and (CUDA) device."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise La2Error(LA2_ERR_INVALID_ARG)
 
 
@@ -578,7 +578,7 @@ def _call_on(device, stream):
         if stream.device != device:
             raise La2Error(LA2_ERR_INVALID_ARG)
         return torch.cuda.stream(stream)
-    if device.index == torch.cuda.current_device():
+    if device.index == torch._C._cuda_getDevice():  # (initialised: there are tensors on it)
         return _HERE
     return torch.cuda.device(device)
 

@@ -100,3 +100,17 @@ def test_replayed_from_a_graph_with_other_lists(la2):
     la2.check()
     want, m = oracle.state_compact(oracle.state_copy(ref, [4, -1], [2, 3]), [0, 1, 0, 1, 1])
     assert np.array_equal(pool.cpu().numpy(), want) and moved.cpu().tolist() == m.tolist()
+
+
+@pytest.mark.parametrize("S", [2, 3, 31, 1023, 1024, 1025])
+@pytest.mark.parametrize("front", [True, False])
+def test_compact_around_one_launch(la2, S, front):
+    """Pools up to and beyond those that are compacted by one launch: the dead slots all
+    in front (every live one moves that can), or spread."""
+    _, pool = pool_of(S, 1, 4, 5)
+    live = np.arange(S) >= (S + 1) // 2 if front else np.random.default_rng(S).random(S) < 0.6
+    live = live.astype(np.int32)
+    want, moved = oracle.state_compact(pool.cpu().numpy(), live)
+    got = la2.state_compact(pool, ints(live.tolist()))
+    la2.check()
+    assert got.cpu().tolist() == moved.tolist() and np.array_equal(pool.cpu().numpy(), want)
