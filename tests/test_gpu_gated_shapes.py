@@ -99,3 +99,23 @@ def test_calls_in_a_row_share_a_workspace(la2, dt, d):  # noqa: F811
         for x, y in zip(alone, got):
             assert all(torch.equal(u, w) for u, w in zip(x, y))
     la2.check()
+
+
+@pytest.mark.parametrize("dt,d", [("bf16", 128), ("f32", 64)])
+def test_two_streams_at_once(la2, dt, d):  # noqa: F811
+    """Calls on two streams, each with what it allocates there, give what they give alone."""
+    sets = [{n: t.cuda() for n, t in make(dt, 1, 8, 2000, d, d, 20 + s, "restarts").items()} for s in range(2)]
+    args = [[s[n] for n in ("q", "k", "v", "gate")] for s in sets]
+    alone = [(la2.forward_gated(*a),) + la2.backward_gated(*a, s["do"]) for a, s in zip(args, sets)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(8):
+        for i, st in enumerate(streams):
+            got[i].append((la2.forward_gated(*args[i], stream=st),)
+                          + la2.backward_gated(*args[i], sets[i]["do"], stream=st))
+    torch.cuda.synchronize()
+    la2.check()
+    for want, many in zip(alone, got):
+        for one in many:
+            assert all(torch.equal(x, y) for x, y in zip(want, one))
