@@ -484,7 +484,8 @@ rope_bwd_vec_kernel(const __grid_constant__ Params p) {
         widen<VEC>(have ? ring[(4 * from + 2 + i) * kThreads] : zero, g[i]);
       }
       from = from + 1 == D ? 0 : from + 1;
-      const float r = rsqrtf(fmaf(group_sum<G>(sum_products(x, x)), inv_d, eps));
+      // (a group without a row adds zeros to dw: with eps = 0 the root would make them NaN)
+      const float square = fmaf(group_sum<G>(sum_products(x, x)), inv_d, eps), r = on ? rsqrtf(square) : 0.f;
       const uint64_t rr = f2(r, r), ff = f2(k >= nq ? p.scale[1] : p.scale[0], k >= nq ? p.scale[1] : p.scale[0]);
       turn_row<VEC, STAGE>(g, c, pc, half, stage);  // back
 #pragma unroll
