@@ -661,7 +661,8 @@ pool_update_kernel(const float* __restrict__ chunks, const double* __restrict__ 
 }
 
 // dl_t = flow at the chunk's end + sum over the chunk's rows from t on of
-// (q . dq - k . dk). The flow at the end of chunk c is <state before chunk c + 1, U
+// (q . dq - k . dk), and 0 at a restart, from which the sum starts anew. The flow at
+// the end of chunk c is <state before chunk c + 1, U
 // behind chunk c> (0 for the last chunk): the starts of the dQ and dK passes' chunks,
 // which those passes (or a scan) left there; elements in any common order. One CTA a
 // (sequence, chunk). (Adding those states up from the chunks' pieces here, up to 12 of
@@ -676,6 +677,8 @@ gate_grad_kernel(const T* __restrict__ gate, const float* __restrict__ qdq, cons
   pdl_wait();
   constexpr int kWarps = kGradThreads / 32;
   __shared__ double part[kWarps];
+  __shared__ int part_cut[kWarps];
+  static_assert(kWarps == 32, "a flag a lane");
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t bh = blockIdx.x / C, ch = blockIdx.x % C;
   const int64_t t0 = ch * L, t1 = imin64(N, t0 + L);
@@ -701,29 +704,36 @@ gate_grad_kernel(const T* __restrict__ gate, const float* __restrict__ qdq, cons
     for (int i = 0; i < kWarps; ++i) carry += part[i];
     __syncthreads();
   }
-  // rows of the chunk from its last; thread x holds row hi - x
+  // rows of the chunk from its last; thread x holds row hi - x. A gate of 0 passes
+  // nothing on and its own factor is 0: what has been summed behind it ends there, so
+  // the sums of one document do not reach the gates of another. There is nothing
+  // before the first token for its gate to pass on.
   for (int64_t hi = t1 - 1; hi >= t0; hi -= kGradThreads) {
     const int64_t t = hi - threadIdx.x, at = bh * N + t;
-    double x = t >= t0 ? static_cast<double>(qdq[at]) - static_cast<double>(kdk[at]) : 0.0;
+    bool cut = t >= t0 && (t == 0 || to_f32(gate[at]) < static_cast<float>(kLogZero));
+    double x = t >= t0 && !cut ? static_cast<double>(qdq[at]) - static_cast<double>(kdk[at]) : 0.0;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
       const double up = __shfl_up_sync(0xffffffffu, x, m);
-      if (lane >= m) x += up;
+      const bool up_cut = __shfl_up_sync(0xffffffffu, cut, m);
+      if (lane >= m && !cut) {
+        x += up;
+        cut = up_cut;
+      }
     }
-    if (lane == 31) part[w] = x;
+    if (lane == 31) {
+      part[w] = x;
+      part_cut[w] = cut;
+    }
     __syncthreads();
+    const unsigned cuts = __ballot_sync(0xffffffffu, part_cut[lane]);
     double before = carry;
     for (int i = 0; i < kWarps; ++i) {
-      if (i < w) before += part[i];
-      carry += part[i];
+      const double sum = (cuts >> i & 1 ? 0.0 : carry) + part[i];
+      if (i < w) before = sum;
+      carry = sum;
     }
-    if (t >= t0) {
-      const float l = to_f32(gate[at]);
-      // a gate of 0 passes nothing on, and its own factor is 0; there is nothing
-      // before the first token for its gate to pass on
-      const bool none = t == 0 || l < static_cast<float>(kLogZero);
-      dgate[at] = from_f32<T>(none ? 0.f : static_cast<float>(before + x));
-    }
+    if (t >= t0) dgate[at] = from_f32<T>(static_cast<float>(cut ? x : before + x));
     __syncthreads();
   }
 }

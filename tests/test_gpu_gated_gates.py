@@ -1,0 +1,117 @@
+"""The gated form where its gates are extreme: heads that forget within a few tokens, long
+chunks, many restarts in a block, restarts with growing gates behind them. The reference
+is the recurrence in float64 on the GPU, 64 tokens at a time, with restarts as cuts
+rather than as large numbers, and with the gates' gradient summed over pairs.
+"""
+
+import pytest
+import torch
+
+import oracle
+from test_gpu_gated import DT, chunk, la2, make  # noqa: F401 (la2, chunk: fixtures)
+
+pytestmark = pytest.mark.gpu
+
+R = 64
+
+
+def blocks(x):
+    """[B,H,N,...] -> float64 [T,B,H,64,...], zeros behind the last token."""
+    B, H, N = x.shape[:3]
+    T = (N + R - 1) // R
+    y = torch.zeros(B, H, T * R, *x.shape[3:], dtype=torch.float64, device=x.device)
+    y[:, :, :N] = x
+    return y.view(B, H, T, R, *x.shape[3:]).movedim(2, 0)
+
+
+def whole(parts, N):
+    x = torch.stack(parts).movedim(0, 2)
+    return x.flatten(2, 3)[:, :, :N]
+
+
+class Weights:
+    """Decays inside a block: pairs, from the state before it, to its end, over all of it."""
+
+    def __init__(self, gate):
+        cut = gate == -torch.inf
+        c = gate.masked_fill(cut, 0.0).cumsum(-1)
+        part = cut.long().cumsum(-1)
+        t = torch.arange(R, device=gate.device)
+        same = (part[..., :, None] == part[..., None, :]) & (t[:, None] >= t)
+        self.pair = torch.where(same, c[..., :, None] - c[..., None, :], -torch.inf).exp()
+        self.head = torch.where(part == 0, c, -torch.inf).exp()
+        self.tail = self.pair[..., -1, :]
+        self.all = self.head[..., -1]
+
+
+def reference(q, k, v, gate, do, state=None):
+    """(o, dq, dk, dv, dgate, state behind the last token) in float64."""
+    N = q.shape[2]
+    q, k, v, gate, do = (blocks(x) for x in (q, k, v, gate, do))
+    w = [Weights(g) for g in gate]
+    T = len(w)
+    S = torch.zeros(*q.shape[1:3], q.shape[-1], v.shape[-1], dtype=torch.float64, device=q.device)
+    if state is not None:
+        S = S + state
+    before, o, dq, dk, dv, dg = [], [], [], [], [], []
+    for t in range(T):
+        before.append(S)
+        P = (q[t] @ k[t].mT) * w[t].pair
+        o.append(P @ v[t] + w[t].head[..., None] * (q[t] @ S))
+        S = w[t].all[..., None, None] * S + (k[t] * w[t].tail[..., None]).mT @ v[t]
+    U = torch.zeros_like(S)
+    upper = torch.ones(R, R, device=q.device, dtype=torch.bool).tril(-1)
+    for t in reversed(range(T)):
+        A, P = (do[t] @ v[t].mT) * w[t].pair, (q[t] @ k[t].mT) * w[t].pair
+        q_far = w[t].head[..., None] * (do[t] @ before[t].mT)
+        k_far = w[t].tail[..., None] * (v[t] @ U.mT)
+        dq.append(A @ k[t] + q_far)
+        dk.append(A.mT @ q[t] + k_far)
+        dv.append(P.mT @ do[t] + w[t].tail[..., None] * (k[t] @ U))
+        pairs = A * (q[t] @ k[t].mT)
+        inside = (pairs.flip(-2).cumsum(-2).flip(-2) * upper).sum(-1)  # i >= t > j of the block
+        a, b = (q[t] * q_far).sum(-1), (k[t] * k_far).sum(-1)
+        across = w[t].all * (before[t] * U).sum((-1, -2))
+        dg.append(inside + a.flip(-1).cumsum(-1).flip(-1) + (b.cumsum(-1) - b) + across[..., None])
+        U = w[t].all[..., None, None] * U + (q[t] * w[t].head[..., None]).mT @ do[t]
+    back = [whole(x[::-1], N) for x in (dq, dk, dv, dg)]
+    back[3][:, :, 0] = 0.0  # nothing comes before the first token
+    return whole(o, N), *back, S
+
+
+def by_head(x, ref):
+    """Largest relative Frobenius error of a head."""
+    x, ref = x.double().movedim(1, 0).flatten(1), ref.movedim(1, 0).flatten(1)
+    return float(((x - ref).norm(dim=1) / ref.norm(dim=1)).max())
+
+
+def test_reference():
+    """The float64 reference against the oracle, token by token (no kernel runs)."""
+    ins = make("f32", 1, 2, 150, 6, 5, 1, "restarts")
+    args = [ins[n].double() for n in ("q", "k", "v")]
+    gate, do = ins["gate"].double(), ins["do"].double()
+    got = reference(*args, gate, do)
+    n = [t.numpy() for t in args]
+    want = (oracle.forward_gated(*n, gate.numpy()), *oracle.backward_gated(*n, do.numpy(), gate.numpy()))
+    for x, y in zip(got, want):
+        assert oracle.relative_frobenius(x.numpy(), y) <= 1e-12
+
+
+@pytest.mark.parametrize("dt,d", [("f32", 64), ("bf16", 128), ("bf16", 64)])
+def test_gate_gradient_does_not_cross_a_restart(la2, chunk, dt, d):  # noqa: F811
+    """The last document's gradients, of any size, leave those of the gates before it bit
+    for bit; two tokens before a restart the gradient is that of one pair."""
+    N = 400
+    ins = {n: t.cuda() for n, t in make(dt, 1, 2, N, d, d, 5).items()}
+    ins["gate"][..., 200] = -torch.inf
+    chunk(512)
+    a = la2.backward_gated(*(ins[n] for n in ("q", "k", "v", "gate", "do")))[3]
+    big = ins["do"].clone()
+    big[:, :, 200:] *= 2.0 ** 20
+    b = la2.backward_gated(*(ins[n] for n in ("q", "k", "v", "gate")), big)[3]
+    la2.check()
+    assert torch.equal(a[..., :201], b[..., :201])
+    assert not torch.equal(a[..., 201:], b[..., 201:])
+    want = reference(*(ins[n] for n in ("q", "k", "v", "gate", "do")))[4]
+    few = slice(190, 200)
+    assert by_head(a[..., few], want[..., few]) <= (1e-5 if dt == "f32" else 1e-2)
