@@ -87,10 +87,34 @@ __device__ __forceinline__ void warp_sums(float x, float y, int lane, float& a, 
     if (lane >= m) t += up;
   }
   b = t;
-  a = t - y;
-  // (a from b would be NaN - NaN or lose y's digits next to a restart)
+  // (a as t - y would be NaN - NaN or lose y's digits next to a restart)
   const float before = __shfl_up_sync(0xffffffffu, t, 1);
   a = (lane ? before : 0.f) + x;
+}
+
+// Sums of the gates behind each row instead, of all 64 in `all`.
+__device__ __forceinline__ void warp_sums_behind(float x, float y, int lane, float& a, float& b, float& all) {
+  float t = x + y;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const float down = __shfl_down_sync(0xffffffffu, t, m);
+    if (lane + m < 32) t += down;
+  }
+  all = __shfl_sync(0xffffffffu, t, 0);
+  const float next = __shfl_down_sync(0xffffffffu, t, 1);
+  b = lane < 31 ? next : 0.f;
+  a = y + b;
+}
+__device__ __forceinline__ bool is_restart(__nv_bfloat16 x) { return to_f32(x) * kLog2e < kLog2Zero; }
+// Restarts of a block as ballots of its even and odd rows: whether one lies at or before
+// row 2 lane + odd, or behind it.
+__device__ __forceinline__ bool restart_upto(uint32_t even, uint32_t odd_rows, int lane, int odd) {
+  const uint32_t to = 0xffffffffu >> (31 - lane);
+  return (even & to) | (odd_rows & (odd ? to : to >> 1));
+}
+__device__ __forceinline__ bool restart_behind(uint32_t even, uint32_t odd_rows, int lane, int odd) {
+  const uint32_t from = 0xffffffffu << lane;
+  return (even & (from << 1)) | (odd_rows & (odd ? from << 1 : from));
 }
 
 // One lane of the warp, the same for every MMA and commit of the issuing loop.
@@ -925,9 +949,13 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
     commit(lead, drain);
     s::drain_wait(drain, 0);
   } else if (warp == 2) {
-    // the rows' factors, a block's when block i - KS has released its stage
+    // the rows' factors, a block's when block i - KS has released its stage. Each is the
+    // exponential of a sum over the gates between the row and the piece's edge alone
+    // (walking from the end: those behind the row), so no large sums are subtracted, and 0 beyond
+    // a restart: as a large negative gate in those sums it would cost them their digits.
     const __nv_bfloat16* g = prm.gate + bh * prm.N;
-    double run = 0.0;  // sum of the gates of the blocks walked
+    double run = 0.0;   // sum of the gates of the blocks walked
+    bool dead = false;  // a restart among them: nothing further reaches the edge
     for_gates(
         n, lane,
         [&](int i, int r) {
@@ -936,17 +964,34 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
         },
         [&](int i, __nv_bfloat16 gx, __nv_bfloat16 gy) {
           if (i >= KS && !wait(&in_empty[i % KS], (i / KS - 1) & 1, 96)) return false;
-          float a, b;
-          warp_sums(gate_log2(gx), gate_log2(gy), lane, a, b);
-          const float all = __shfl_sync(0xffffffffu, b, 31);
+          const bool cx = is_restart(gx), cy = is_restart(gy);
+          const uint32_t ex = __ballot_sync(0xffffffffu, cx), ey = __ballot_sync(0xffffffffu, cy);
+          const float x = cx ? 0.f : to_f32(gx) * kLog2e, y = cy ? 0.f : to_f32(gy) * kLog2e;
+          float a, b, all;
+          bool za, zb;
+          if constexpr (SUFFIX) {
+            warp_sums(x, y, lane, a, b);
+            all = __shfl_sync(0xffffffffu, b, 31);
+            za = restart_upto(ex, ey, lane, 0);
+            zb = restart_upto(ex, ey, lane, 1);
+          } else {
+            warp_sums_behind(x, y, lane, a, b, all);
+            // (NaN among the gates reaches every row, as it does in the sum of all)
+            a += 0.f * all;
+            b += 0.f * all;
+            za = restart_behind(ex, ey, lane, 0);
+            zb = restart_behind(ex, ey, lane, 1);
+          }
           reinterpret_cast<float2*>(tab + (i % kTabs) * 64)[lane] =
-              make_float2(ex2(static_cast<float>(run + static_cast<double>(SUFFIX ? a : all - a))),
-                          ex2(static_cast<float>(run + static_cast<double>(SUFFIX ? b : all - b))));
+              make_float2(dead || za ? 0.f : ex2(static_cast<float>(run + static_cast<double>(a))),
+                          dead || zb ? 0.f : ex2(static_cast<float>(run + static_cast<double>(b))));
           run += static_cast<double>(all);
+          dead |= (ex | ey) != 0;
           s::mbar_arrive(&tab_full[i % kTabs]);
           return true;
         });
-    if (lane == 0) prm.tot[bh * prm.K + ch] = run * 0.693147180559945309417;  // natural log
+    // (natural log; -infinity: its exponential is 0 whatever gates above 0 the piece has)
+    if (lane == 0) prm.tot[bh * prm.K + ch] = dead ? -INFINITY : run * 0.693147180559945309417;
   } else if (warp >= 4) {
     const int r = (warp - 4) * 8 + (lane >> 2), ch0 = (lane & 3) * 4;
     bool ok = true;

@@ -115,3 +115,44 @@ def test_gate_gradient_does_not_cross_a_restart(la2, chunk, dt, d):  # noqa: F81
     want = reference(*(ins[n] for n in ("q", "k", "v", "gate", "do")))[4]
     few = slice(190, 200)
     assert by_head(a[..., few], want[..., few]) <= (1e-5 if dt == "f32" else 1e-2)
+
+
+# --------------------------------------------------------------------- restarts in a block
+
+
+@pytest.mark.parametrize("rate", [0.05, 0.3])
+@pytest.mark.parametrize("dt,d,length", [("bf16", 128, 64), ("bf16", 128, 256), ("bf16", 64, 0), ("f32", 48, 64)])
+def test_state_behind_restarts(la2, chunk, dt, d, length, rate):  # noqa: F811
+    """Restarts among the first 40 rows of every block leave the states of what comes
+    behind them as exact as those of a block without: 1e-5, the bound of all states."""
+    B, H, N = 2, 3, 512
+    ins = make(dt, B, H, N, d, d, 8, "weak")
+    g = torch.Generator().manual_seed(1)
+    cut = (torch.rand(B, H, N, generator=g) < rate) & (torch.arange(N) % 64 < 40)
+    ins["gate"] = ins["gate"].masked_fill(cut, -torch.inf)
+    dev = [ins[n].cuda() for n in ("q", "k", "v", "gate", "do")]
+    chunk(length)
+    pool = torch.randn(B, H, d, d, generator=g).cuda()
+    want = reference(*dev, state=pool)[5]
+    la2.kv_state_gated(*dev[1:4], pool)
+    la2.check()
+    assert by_head(pool, want) <= 1e-5
+
+
+@pytest.mark.parametrize("dt,d,length", [("bf16", 128, 0), ("bf16", 64, 64), ("bf16", 128, 128), ("f32", 40, 0),
+                                         ("f32", 33, 64)])
+@pytest.mark.parametrize("at,n,up", [(0, 70, 0.25), (3, 30, 0.5), (70, 200, 0.5)])
+def test_restart_with_growing_gates_drops_what_a_slot_held(la2, chunk, dt, d, length, at, n, up):  # noqa: F811
+    """Gates above 0 behind a restart do not bring back what a slot held, be it no number."""
+    ins = {x: t.cuda() for x, t in make(dt, 2, 2, n, d, d, d).items()}
+    ins["gate"] = torch.full_like(ins["gate"], up)
+    ins["gate"][:, :, :at] = -0.5
+    ins["gate"][:, :, at] = -torch.inf
+    chunk(length)
+    worst = torch.full((2, 2, d, d), float("nan"), device="cuda")
+    worst[1] = float("inf")
+    zero = torch.zeros_like(worst)
+    la2.kv_state_gated(ins["k"], ins["v"], ins["gate"], worst)
+    la2.kv_state_gated(ins["k"], ins["v"], ins["gate"], zero)
+    la2.check()
+    assert torch.equal(worst, zero) and bool(torch.isfinite(zero).all())
