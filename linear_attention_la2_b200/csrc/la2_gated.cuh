@@ -240,6 +240,7 @@ static la2_status states_tc(const Tile& y, const Tile& z, const void* gate, floa
   p.K = pl.K;
   p.first = kind == FOR_DK_DV ? per : 0;
   p.count = kind == FOR_POOL ? pl.K : kind == FOR_DK_DV ? pl.K - per : (pl.C - 1) * per;
+  p.tot_from = kind == FOR_DK_DV ? (pl.C - 1) * per : 0;  // (the others are the prefixes' pass')
   p.beside = kind == FOR_DK_DV && pl.per > 0;  // (the prefixes' pass came before, without a scan)
   p.spin_limit = spin_limit();
   {

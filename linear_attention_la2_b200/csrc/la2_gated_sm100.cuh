@@ -854,6 +854,9 @@ struct TcStateParams {
   float* out_t;    // its transpose, or null
   double* tot;     // [BH][K]
   int64_t N, L, K, first, count, spin_limit;  // pieces [first, first + count) of the K of every sequence
+  // First piece whose sum this launch writes: the prefixes' and the suffixes' passes walk a
+  // piece in opposite orders, which may end on other bits, and run side by side.
+  int64_t tot_from;
   int32_t beside;  // the launch before is independent: see begin_grid
 };
 
@@ -991,7 +994,7 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
           return true;
         });
     // (natural log; -infinity: its exponential is 0 whatever gates above 0 the piece has)
-    if (lane == 0) prm.tot[bh * prm.K + ch] = dead ? -INFINITY : run * 0.693147180559945309417;
+    if (lane == 0 && ch >= prm.tot_from) prm.tot[bh * prm.K + ch] = dead ? -INFINITY : run * 0.693147180559945309417;
   } else if (warp >= 4) {
     const int r = (warp - 4) * 8 + (lane >> 2), ch0 = (lane & 3) * 4;
     bool ok = true;

@@ -156,3 +156,16 @@ def test_restart_with_growing_gates_drops_what_a_slot_held(la2, chunk, dt, d, le
     la2.kv_state_gated(ins["k"], ins["v"], ins["gate"], zero)
     la2.check()
     assert torch.equal(worst, zero) and bool(torch.isfinite(zero).all())
+
+
+def test_gradients_hold_the_same_bits_on_every_call(la2):  # noqa: F811
+    """Pieces of many lengths, chunks that add them up (both state passes run side by
+    side) and scanned ones, gates of very different sizes."""
+    for B, H, N in ((1, 8, 9000), (2, 16, 2048), (1, 1, 5000)):
+        ins = {n: t.cuda() for n, t in make("bf16", B, H, N, 128, 128, 2, "strong").items()}
+        ins["gate"][..., ::7] *= 2.0 ** -20
+        args = [ins[n] for n in ("q", "k", "v", "gate", "do")]
+        first = la2.backward_gated(*args)
+        for _ in range(10):
+            assert all(torch.equal(x, y) for x, y in zip(first, la2.backward_gated(*args)))
+    la2.check()
