@@ -34,9 +34,8 @@
 // against 2850 cycles that a block's share of HBM takes at 148 SMs; the state's copy
 // as an operand in shared memory took 500 (GRAD 1000) more.
 //
-// Gate sums: c in base 2, fp32, at most 64 terms; a log gate under kLog2Zero (in
-// base 2) counts as that, its exponential is 0, so a restart cuts exactly and costs
-// the differences of later sums at most 2^-17 * (number of restarts in the block).
+// Gate sums: c in base 2, fp32, at most 64 terms; a restart (a log gate under kLog2Zero,
+// in base 2) counts as 0 there and cuts the weights made of them.
 //
 // GRAD (dQ, dK) also returns the rows' dots q . dq and k . dk (fp32, from the
 // unrounded rows) for the gates' gradient, a running difference of them: their
@@ -66,17 +65,12 @@ constexpr int kTile = 64 * 128 * 2;       // one 64 x 128 bf16 tile
 constexpr int kMainThreads = 768;
 constexpr float kLog2Zero = -160.f;
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr int kTabs = 8, kTab = 384;      // gate tables in flight, their floats (see the table warp)
+constexpr int kTabs = 8, kTab = 452;      // gate tables in flight, their floats (see the table warp)
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-// A log gate in base 2. A comparison, not fmaxf: NaN stays NaN.
-__device__ __forceinline__ float gate_log2(__nv_bfloat16 x) {
-  const float y = to_f32(x) * kLog2e;
-  return y < kLog2Zero ? kLog2Zero : y;
 }
 // Running sums of 64 gates over a warp: lane l gets those of rows 2l and 2l + 1.
 __device__ __forceinline__ void warp_sums(float x, float y, int lane, float& a, float& b) {
@@ -105,6 +99,7 @@ __device__ __forceinline__ void warp_sums_behind(float x, float y, int lane, flo
   b = lane < 31 ? next : 0.f;
   a = y + b;
 }
+// (NaN is none.)
 __device__ __forceinline__ bool is_restart(__nv_bfloat16 x) { return to_f32(x) * kLog2e < kLog2Zero; }
 // Restarts of a block as ballots of its even and odd rows: whether one lies at or before
 // row 2 lane + odd, or behind it.
@@ -115,6 +110,24 @@ __device__ __forceinline__ bool restart_upto(uint32_t even, uint32_t odd_rows, i
 __device__ __forceinline__ bool restart_behind(uint32_t even, uint32_t odd_rows, int lane, int odd) {
   const uint32_t from = 0xffffffffu << lane;
   return (even & (from << 1)) | (odd_rows & (odd ? from << 1 : from));
+}
+// Bits 0..7 to the even places.
+__device__ __forceinline__ uint32_t spread_bits(uint32_t x) {
+  x = (x | x << 4) & 0x0f0fu;
+  x = (x | x << 2) & 0x3333u;
+  return (x | x << 1) & 0x5555u;
+}
+// The columns that are kept of row l of a square on the diagonal, as bits: those up to l
+// from the last restart at or before it on (BACK: those from l to the restart behind it).
+template <bool BACK>
+__device__ __forceinline__ uint32_t kept_bits(uint32_t restarts, int l) {
+  const uint32_t upto = (2u << l) - 1;
+  if (BACK) {
+    const uint32_t behind = restarts & ~upto;
+    return ((behind & -behind) - 1) & 0xffffu & ~(upto >> 1);
+  }
+  const uint32_t before = restarts & upto;
+  return before ? upto & ~((1u << (31 - __clz(before))) - 1) : upto;
 }
 
 // One lane of the warp, the same for every MMA and commit of the issuing loop.
@@ -484,11 +497,14 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     s::drain_wait(drain, 0);
   } else if (warp == 2) {
     // =========================================================== gate tables
-    // Per block: the running sums c [64]; the epilogue's factors of far [64]; and for
+    // Per block: the running sums c [64]; the epilogue's factors of far [64]; for
     // the mask, whose rows and columns meet in 16 x 16 squares, e^(c_E(s) - c_s) [64]
     // with E(s) the last row of s' sixteen, and e^(c_t - c_E) for the first three E
     // [3][64] (read for later t only): off the diagonal e^(c_t - c_s) is one of each,
-    // neither above 1 unless gates are. Table i goes into slot i % 8 when block i - KS
+    // neither above 1 unless gates are; the factors of Y~ [64]; and the restarts of each
+    // sixteen as bits [4]. Restarts count as 0 in the sums, which keep their digits, and
+    // cut the factors: one that spans a restart is 0, however the gates behind it
+    // grow; squares on the diagonal go by the bits. Table i goes into slot i % 8 when block i - KS
     // has released its stage (z_empty): everything of it is done but its epilogue,
     // and before its near was issued the epilogue had read block i - KS - 1 (o_empty),
     // so readers of block i - 8 are long done.
@@ -503,19 +519,34 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         },
         [&](int i, __nv_bfloat16 gx, __nv_bfloat16 gy) {
           if (i >= KS && !wait(&z_empty[i % KS], (i / KS - 1) & 1, 77)) return false;
+          const bool cx = is_restart(gx), cy = is_restart(gy);
+          const uint32_t ex = __ballot_sync(0xffffffffu, cx), ey = __ballot_sync(0xffffffffu, cy);
           float a, b;
-          warp_sums(gate_log2(gx), gate_log2(gy), lane, a, b);
+          warp_sums(cx ? 0.f : to_f32(gx) * kLog2e, cy ? 0.f : to_f32(gy) * kLog2e, lane, a, b);
           const float all = __shfl_sync(0xffffffffu, b, 31);
           const float end = __shfl_sync(0xffffffffu, b, lane | 7);
-          float2* t = reinterpret_cast<float2*>(tab + (i % kTabs) * kTab);
+          const float2 head = make_float2(restart_upto(ex, ey, lane, 0) ? 0.f : ex2(a),
+                                          restart_upto(ex, ey, lane, 1) ? 0.f : ex2(b));
+          const float2 tail = make_float2(restart_behind(ex, ey, lane, 0) ? 0.f : ex2(all - a),
+                                          restart_behind(ex, ey, lane, 1) ? 0.f : ex2(all - b));
+          const uint32_t own = 0xffu << (lane & 24);  // the row's sixteen
+          float* slot = tab + (i % kTabs) * kTab;
+          float2* t = reinterpret_cast<float2*>(slot);
           t[lane] = make_float2(a, b);
-          t[32 + lane] = BACK ? make_float2(ex2(all - a), ex2(all - b)) : make_float2(ex2(a), ex2(b));
-          t[64 + lane] = make_float2(ex2(end - a), ex2(end - b));
+          t[32 + lane] = BACK ? tail : head;
+          t[64 + lane] = make_float2(restart_behind(ex & own, ey & own, lane, 0) ? 0.f : ex2(end - a),
+                                     restart_behind(ex & own, ey & own, lane, 1) ? 0.f : ex2(end - b));
 #pragma unroll
           for (int h = 0; h < 3; ++h) {
             const float e = __shfl_sync(0xffffffffu, b, 8 * h + 7);
-            t[96 + 32 * h + lane] = make_float2(ex2(a - e), ex2(b - e));
+            const uint32_t later = 0xffffff00u << (8 * h);
+            t[96 + 32 * h + lane] = make_float2(restart_upto(ex & later, ey & later, lane, 0) ? 0.f : ex2(a - e),
+                                                restart_upto(ex & later, ey & later, lane, 1) ? 0.f : ex2(b - e));
           }
+          t[192 + lane] = BACK ? head : tail;
+          if (lane < 4)
+            reinterpret_cast<uint32_t*>(slot)[448 + lane] =
+                spread_bits(ex >> (8 * lane) & 0xffu) | spread_bits(ey >> (8 * lane) & 0xffu) << 1;
           s::mbar_arrive(&tab_full[i % kTabs]);
           return true;
         });
@@ -528,7 +559,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     for (int i = 0; i + 1 < n; ++i) {
       const float* c = tab_of(i, 78);
       if (!c) break;
-      const Factor f = factor(ex2(BACK ? c[r] : c[63] - c[r]));
+      const Factor f = factor(c[384 + r]);
       if (!wait(&s_full[i & 1], (i >> 1) & 1, 79)) break;
       if (!wait(y_empty, (i & 1) ^ 1, 90)) break;
       const uint32_t ya = s::smem_u32(smem + (i % KS) * 3 * kTile + kTile) + half * 8192 + r * 128;
@@ -571,13 +602,14 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         if (r >= 0) {
           if (h == w4) {
             const float cr = c[r];
+            const uint32_t kept = kept_bits<BACK>(reinterpret_cast<const uint32_t*>(c)[448 + w4], lane);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const int col = 16 * h + 2 * e;
               const float2 cc = *reinterpret_cast<const float2*>(c + col);
               const float wa = ex2(BACK ? cc.x - cr : cr - cc.x), wb = ex2(BACK ? cc.y - cr : cr - cc.y);
-              const float a = (BACK ? col >= r : col <= r) ? __uint_as_float(v[2 * e]) * wa : 0.f;
-              const float b = (BACK ? col + 1 >= r : col + 1 <= r) ? __uint_as_float(v[2 * e + 1]) * wb : 0.f;
+              const float a = kept & (1u << (2 * e)) ? __uint_as_float(v[2 * e]) * wa : 0.f;
+              const float b = kept & (2u << (2 * e)) ? __uint_as_float(v[2 * e + 1]) * wb : 0.f;
               w[e] = s::pack_bf16x2(a, b);
             }
           } else {
@@ -639,7 +671,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         // the pieces between this chunk and the sequence's start (walking back: its
         // end), nearest first, each decayed over the nearer ones
         const int pieces = prm.per == 0 ? 1 : static_cast<int>(BACK ? prm.K - (ch + 1) * prm.per : ch * prm.per);
-        const float whole = ex2(c[63]);
+        const float whole = c[BACK ? 447 : 127];  // e^(c_R)
 #pragma unroll 1
         for (int h = 0; h < 4; ++h) {
           float x[16];
@@ -678,7 +710,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     for (int i = 1; i < n && ok; ++i) {
       const float* c = tab_of(i, 83);
       if (!c) break;
-      const float whole = ex2(c[63]);
+      const float whole = c[BACK ? 447 : 127];
       if (!wait(updated, (i - 1) & 1, 84)) break;
       // far of the block before has read the copy
       if (i > first_copy && !wait(copy_empty, (i - 1 - first_copy) & 1, 88)) break;

@@ -158,6 +158,30 @@ def test_restart_with_growing_gates_drops_what_a_slot_held(la2, chunk, dt, d, le
     assert torch.equal(worst, zero) and bool(torch.isfinite(zero).all())
 
 
+@pytest.mark.parametrize("dt,d,length", [("bf16", 128, 0), ("bf16", 128, 64), ("bf16", 64, 128), ("f32", 32, 0)])
+@pytest.mark.parametrize("at", [10, 63, 130])
+def test_restart_with_growing_gates_hides_what_was_before(la2, chunk, dt, d, length, at):  # noqa: F811
+    """Values before a restart, of any finite size, leave all outputs and gradients behind
+    it bit for bit, however small those are and whatever the gates behind it."""
+    N = 200
+    ins = {n: t.cuda() for n, t in make(dt, 1, 2, N, d, d, 9).items()}
+    ins["gate"] = torch.full_like(ins["gate"], -0.5)
+    ins["gate"][..., at] = -torch.inf
+    ins["gate"][..., at + 1:at + 60] = 1.0
+    chunk(length)
+    ins["k"][:, :, at:] *= 2.0 ** -60
+    far = {n: ins[n].clone() for n in ("k", "v")}
+    far["k"][:, :, :at] *= 2.0 ** 50
+    far["v"][:, :, :at] *= 2.0 ** 50
+    q, gate, do = ins["q"], ins["gate"], ins["do"]
+    a = (la2.forward_gated(q, ins["k"], ins["v"], gate), *la2.backward_gated(q, ins["k"], ins["v"], gate, do))
+    b = (la2.forward_gated(q, far["k"], far["v"], gate), *la2.backward_gated(q, far["k"], far["v"], gate, do))
+    la2.check()
+    for x, y, name in zip(a, b, ("o", "dq", "dk", "dv", "dgate")):
+        assert torch.equal(x[:, :, at:], y[:, :, at:]), name
+    assert bool(torch.isfinite(a[0].float()).all())
+
+
 def test_gradients_hold_the_same_bits_on_every_call(la2):  # noqa: F811
     """Pieces of many lengths, chunks that add them up (both state passes run side by
     side) and scanned ones, gates of very different sizes."""
