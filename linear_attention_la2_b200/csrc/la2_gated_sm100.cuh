@@ -222,7 +222,7 @@ struct TcCfg {
   static constexpr int OFF_TAB = OFF_OUT + 2 * kTile;
   static constexpr int OFF_DOT = OFF_TAB + kTabs * kTab * 4;
   static constexpr int OFF_BAR = OFF_DOT + (GRAD ? 2 * 4 * 64 * 4 : 0);
-  static constexpr int NBAR = 4 * KS + 3 + 4 + 2 + 3 + 2 + 3 + kTabs + 1;
+  static constexpr int NBAR = 4 * KS + 3 + 4 + 2 + 3 + 2 + 4 + kTabs + 1;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
@@ -345,7 +345,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
   uint64_t *y_full = p_empty + 2, *y_empty = y_full + 1;
   uint64_t *copy_full = y_empty + 1, *copy_empty = copy_full + 1, *updated = copy_empty + 1;
   uint64_t *o_full = updated + 1, *o_empty = o_full + 1;
-  uint64_t *staged = o_empty + 1, *tile_free = staged + 1;
+  uint64_t *staged = o_empty + 1, *tile_free = staged + 2;
   uint64_t* tab_full = tile_free + 2;
   uint64_t* drain = tab_full + kTabs;
   uint32_t* tmem_base = reinterpret_cast<uint32_t*>(drain + 1);
@@ -371,6 +371,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       s::mbar_init(&p_full[i], 128);
       s::mbar_init(&p_empty[i], 1);
       s::mbar_init(&tile_free[i], 1);
+      s::mbar_init(&staged[i], 128);
     }
     s::mbar_init(s_empty, 128);
     s::mbar_init(o_full, 1);
@@ -380,7 +381,6 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     s::mbar_init(copy_full, 256);
     s::mbar_init(copy_empty, 1);
     s::mbar_init(updated, 1);
-    s::mbar_init(staged, 128);
     for (int i = 0; i < kTabs; ++i) s::mbar_init(&tab_full[i], 32);
     s::mbar_init(drain, 1);
     *abort_flag = 0;
@@ -795,12 +795,14 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         *reinterpret_cast<float2*>(dotbuf + (i & 1) * 256 + w4 * 64 + 8 * g + 2 * (lane & 3)) = make_float2(d[0], d[1]);
       }
       s::fence_proxy_async();
-      s::mbar_arrive(staged);
+      s::mbar_arrive(&staged[i & 1]);
     }
   } else if (warp == 3) {
     // ==================================== stores, and the rows of the dots (GRAD)
     // A staging tile: [dots' rows loaded ->] output written (staged) -> store has
-    // read it -> free (tile_free: then, or when the dots' rows two blocks on have landed). The
+    // read it -> free (tile_free: then, or when the dots' rows two blocks on have landed). Each
+    // tile has its own staged: with one for both, a pair of blocks that are staged before
+    // this warp comes back to wait would look like none. The
     // dots of a block meet here, before its tile and their buffer are free again.
     const float* dotbuf = reinterpret_cast<const float*>(smem + CF::OFF_DOT);
     auto load_dot_rows = [&](int i) {
@@ -814,7 +816,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       for (; issued < min(n, 2); ++issued)
         if (lane == 0) load_dot_rows(issued);
     for (int i = 0; i < n; ++i) {
-      if (!wait(staged, i & 1, 91)) break;
+      if (!wait(&staged[i & 1], (i >> 1) & 1, 91)) break;
       if (lane == 0) {
         // A chunk ends on a block boundary or at N, where the tensor map clips.
         for (int p = 0; p < prm.halves; ++p)

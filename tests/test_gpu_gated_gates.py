@@ -193,3 +193,21 @@ def test_gradients_hold_the_same_bits_on_every_call(la2):  # noqa: F811
         for _ in range(10):
             assert all(torch.equal(x, y) for x, y in zip(first, la2.backward_gated(*args)))
     la2.check()
+
+
+def test_two_streams_many_times(la2):  # noqa: F811
+    """Calls on two streams share the memory system and the instruction caches, so that a
+    CTA's roles meet at other times than alone: no wait runs out, and the bits stay."""
+    sets = [{n: t.cuda() for n, t in make("bf16", 1, 8, 2000, 128, 128, 30 + s, "restarts").items()} for s in range(2)]
+    args = [[s[n] for n in ("q", "k", "v", "gate")] for s in sets]
+    alone = [(la2.forward_gated(*a),) + la2.backward_gated(*a, s["do"]) for a, s in zip(args, sets)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(200):
+        got = [[(la2.forward_gated(*a, stream=st),) + la2.backward_gated(*a, s["do"], stream=st) for _ in range(3)]
+               for a, s, st in zip(args, sets, streams)]
+        torch.cuda.synchronize()
+        la2.check()
+        for want, many in zip(alone, got):
+            for one in many:
+                assert all(torch.equal(x, y) for x, y in zip(want, one))
