@@ -429,10 +429,10 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         for (int p = 0; p < 2; ++p) s::tma_load_3d(dst + 2 * kTile + p * 8192, &tm_z, &z_full[st], 64 * p, row, z);
         ++issued_z;
       }
-      if (issued_z < n) {  // after an abort: let every load this thread issued land before the CTA exits
-        for (int j = max(0, issued - KS); j < issued; ++j) s::drain_wait(&in_full[j % KS], (j / KS) & 1);
-        for (int j = max(0, issued_z - KS); j < issued_z; ++j) s::drain_wait(&z_full[j % KS], (j / KS) & 1);
-      }
+      // Every load lands before the CTA exits, also where another role has given up and
+      // nobody else waits for the last ones.
+      for (int j = max(0, issued - KS); j < issued; ++j) s::drain_wait(&in_full[j % KS], (j / KS) & 1);
+      for (int j = max(0, issued_z - KS); j < issued_z; ++j) s::drain_wait(&z_full[j % KS], (j / KS) & 1);
     }
   } else if (warp == 1) {
     // ================================================================== MMA
@@ -952,10 +952,9 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
   if (warp == 0) {
     if (lane == 0) {
       int issued = 0;
-      bool ok = true;
       for (int i = 0; i < n; ++i) {
         const int st = i % KS;
-        if (!s::wait_bar(&in_empty[st], ((i / KS) & 1) ^ 1, lim, abort_flag, 90)) { ok = false; break; }
+        if (!s::wait_bar(&in_empty[st], ((i / KS) & 1) ^ 1, lim, abort_flag, 90)) break;
         const int row = static_cast<int>(row_of(i)), z = static_cast<int>(bh);
         uint8_t* dst = smem + st * 2 * kTile;
         s::mbar_expect_tx(&in_full[st], 2 * kTile);
@@ -963,8 +962,8 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
         for (int p = 0; p < 2; ++p) s::tma_load_3d(dst + kTile + p * 8192, &tm_z, &in_full[st], 64 * p, row, z);
         ++issued;
       }
-      if (!ok)
-        for (int j = max(0, issued - KS); j < issued; ++j) s::drain_wait(&in_full[j % KS], (j / KS) & 1);
+      // (every load lands before the CTA exits, whoever has given up)
+      for (int j = max(0, issued - KS); j < issued; ++j) s::drain_wait(&in_full[j % KS], (j / KS) & 1);
     }
   } else if (warp == 1) {
     constexpr uint32_t ID_UPD = s::make_idesc(128, 128, true, true);
