@@ -618,13 +618,11 @@ la2_fwd_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
           ++issued_q;
         }
       }
-      if (!ok) {
-        // Let every load this thread issued land before the CTA exits.
-        for (int j = max(0, issued_kv - CF::KS); j < issued_kv; ++j)
-          drain_wait(&b.kv_full[j % CF::KS], (j / CF::KS) & 1);
-        for (int j = max(0, issued_q - CF::QS); j < issued_q; ++j)
-          drain_wait(&b.q_full[j % CF::QS], (j / CF::QS) & 1);
-      }
+      // Let every load this thread issued land before the CTA exits, whichever role gave up.
+      for (int j = max(0, issued_kv - CF::KS); j < issued_kv; ++j)
+        drain_wait(&b.kv_full[j % CF::KS], (j / CF::KS) & 1);
+      for (int j = max(0, issued_q - CF::QS); j < issued_q; ++j)
+        drain_wait(&b.q_full[j % CF::QS], (j / CF::QS) & 1);
     }
   } else if (warp == kWarpMma) {
     // ================================================================ MMA

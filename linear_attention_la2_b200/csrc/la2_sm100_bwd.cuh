@@ -236,8 +236,8 @@ la2_bwd_dkdv_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
         }
         ++issued;
       }
-      if (!ok)
-        for (int j = max(0, issued - CF::NS); j < issued; ++j) drain_wait(&st_full[j % CF::NS], (j / CF::NS) & 1);
+      // (every load lands before the CTA exits, whichever role gave up)
+      for (int j = max(0, issued - CF::NS); j < issued; ++j) drain_wait(&st_full[j % CF::NS], (j / CF::NS) & 1);
     }
   } else if (warp == kWarpMma) {
     // The whole warp runs the issue loop; one elected lane issues each

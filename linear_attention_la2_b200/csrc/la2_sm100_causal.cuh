@@ -538,12 +538,11 @@ la2_causal_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
           ++m;
         }
       }
-      if (!ok) {
-        for (int j = max(0, issued_kv - CF::KS); j < issued_kv; ++j)
-          drain_wait(&kv_full[j % CF::KS], (j / CF::KS) & 1);
-        for (int j = max(0, issued_q - CF::QS); j < issued_q; ++j)
-          drain_wait(&q_full[j % CF::QS], (j / CF::QS) & 1);
-      }
+      // (every load lands before the CTA exits, whichever role gave up)
+      for (int j = max(0, issued_kv - CF::KS); j < issued_kv; ++j)
+        drain_wait(&kv_full[j % CF::KS], (j / CF::KS) & 1);
+      for (int j = max(0, issued_q - CF::QS); j < issued_q; ++j)
+        drain_wait(&q_full[j % CF::QS], (j / CF::QS) & 1);
     }
   } else if (warp == kWarpMma) {
     // ================================================================ MMA
