@@ -660,10 +660,23 @@ pool_update_kernel(const float* __restrict__ chunks, const double* __restrict__ 
     *out = run[0];
 }
 
+// Sum of x over the lanes up to this one, from the last that is cut on; cut: whether one is.
+__device__ __forceinline__ void sum_up_to_cut(double& x, bool& cut, int lane) {
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const double up = __shfl_up_sync(0xffffffffu, x, m);
+    const bool up_cut = __shfl_up_sync(0xffffffffu, cut, m);
+    if (lane >= m && !cut) {
+      x += up;
+      cut = up_cut;
+    }
+  }
+}
+
 // dl_t = flow at the chunk's end + sum over the chunk's rows from t on of
 // (q . dq - k . dk), and 0 at a restart, from which the sum starts anew. The flow at
-// the end of chunk c is <state before chunk c + 1, U
-// behind chunk c> (0 for the last chunk): the starts of the dQ and dK passes' chunks,
+// the end of chunk c is <state before chunk c + 1, U behind chunk c> (0 for the last
+// chunk): the starts of the dQ and dK passes' chunks,
 // which those passes (or a scan) left there; elements in any common order. One CTA a
 // (sequence, chunk). (Adding those states up from the chunks' pieces here, up to 12 of
 // 64 KB a CTA, took 31 us at B2 H32 N8K.)
@@ -712,27 +725,18 @@ gate_grad_kernel(const T* __restrict__ gate, const float* __restrict__ qdq, cons
     const int64_t t = hi - threadIdx.x, at = bh * N + t;
     bool cut = t >= t0 && (t == 0 || to_f32(gate[at]) < static_cast<float>(kLogZero));
     double x = t >= t0 && !cut ? static_cast<double>(qdq[at]) - static_cast<double>(kdk[at]) : 0.0;
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-      const double up = __shfl_up_sync(0xffffffffu, x, m);
-      const bool up_cut = __shfl_up_sync(0xffffffffu, cut, m);
-      if (lane >= m && !cut) {
-        x += up;
-        cut = up_cut;
-      }
-    }
+    sum_up_to_cut(x, cut, lane);
     if (lane == 31) {
       part[w] = x;
       part_cut[w] = cut;
     }
     __syncthreads();
-    const unsigned cuts = __ballot_sync(0xffffffffu, part_cut[lane]);
-    double before = carry;
-    for (int i = 0; i < kWarps; ++i) {
-      const double sum = (cuts >> i & 1 ? 0.0 : carry) + part[i];
-      if (i < w) before = sum;
-      carry = sum;
-    }
+    double sum = part[lane];  // (every warp sums the warps' own up)
+    bool any = part_cut[lane];
+    sum_up_to_cut(sum, any, lane);
+    if (!any) sum += carry;
+    const double before = w ? __shfl_sync(0xffffffffu, sum, w - 1) : carry;
+    carry = __shfl_sync(0xffffffffu, sum, 31);
     if (t >= t0) dgate[at] = from_f32<T>(static_cast<float>(cut ? x : before + x));
     __syncthreads();
   }
