@@ -22,7 +22,7 @@
 // No exponent is ever positive unless a gate is: nothing is divided by a decay.
 // The sums c are fp64 here (their differences are what is exponentiated; in fp32
 // a sum of 64 gates of -1 would leave the weights 4e-6 off, a fifth of what an
-// fp32 result may be); a gate of -inf counts as kLogZero, whose exponential is 0.
+// fp32 result may be); a restart counts as kLogZero, whose exponential is 0.
 //
 // The gate's gradient is the flow of pairs across its token,
 //   dl_t = sum_{i >= t > j} D[i][j] (q_i . k_j)(dO_i . v_j),
@@ -44,11 +44,14 @@ namespace gated {
 
 constexpr int kThreads = 256;
 constexpr int kRows = 64;
+// A log gate below this is 0 (a restart), as its exponential in fp32 is. In the fp64 sums
+// such a gate counts as kLogZero, which no gates above 0 outweigh in fp32 ones.
+constexpr float kRestart = -104.f;
 constexpr double kLogZero = -1.0e4;
 
 // A log gate as the sums take it. A comparison, not fmax: NaN stays NaN.
 __device__ __forceinline__ double gate_log(float x) {
-  return x < static_cast<float>(kLogZero) ? kLogZero : static_cast<double>(x);
+  return x < kRestart ? kLogZero : static_cast<double>(x);
 }
 __host__ __device__ __forceinline__ int round4(int w) { return (w + 3) & ~3; }
 // Row stride of a tile of w columns: whole float4s, an odd number of them, so that a
@@ -723,7 +726,7 @@ gate_grad_kernel(const T* __restrict__ gate, const float* __restrict__ qdq, cons
   // before the first token for its gate to pass on.
   for (int64_t hi = t1 - 1; hi >= t0; hi -= kGradThreads) {
     const int64_t t = hi - threadIdx.x, at = bh * N + t;
-    bool cut = t >= t0 && (t == 0 || to_f32(gate[at]) < static_cast<float>(kLogZero));
+    bool cut = t >= t0 && (t == 0 || to_f32(gate[at]) < kRestart);
     double x = t >= t0 && !cut ? static_cast<double>(qdq[at]) - static_cast<double>(kdk[at]) : 0.0;
     sum_up_to_cut(x, cut, lane);
     if (lane == 31) {

@@ -34,8 +34,8 @@
 // against 2850 cycles that a block's share of HBM takes at 148 SMs; the state's copy
 // as an operand in shared memory took 500 (GRAD 1000) more.
 //
-// Gate sums: c in base 2, fp32, at most 64 terms; a restart (a log gate under kLog2Zero,
-// in base 2) counts as 0 there and cuts the weights made of them.
+// Gate sums: c in base 2, fp32, at most 64 terms; a restart counts as 0 there and cuts the
+// weights made of them.
 //
 // GRAD (dQ, dK) also returns the rows' dots q . dq and k . dk (fp32, from the
 // unrounded rows) for the gates' gradient, a running difference of them: their
@@ -63,7 +63,6 @@ namespace s = sm100;
 
 constexpr int kTile = 64 * 128 * 2;       // one 64 x 128 bf16 tile
 constexpr int kMainThreads = 768;
-constexpr float kLog2Zero = -160.f;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kTabs = 8, kTab = 452;      // gate tables in flight, their floats (see the table warp)
 
@@ -100,7 +99,7 @@ __device__ __forceinline__ void warp_sums_behind(float x, float y, int lane, flo
   a = y + b;
 }
 // (NaN is none.)
-__device__ __forceinline__ bool is_restart(__nv_bfloat16 x) { return to_f32(x) * kLog2e < kLog2Zero; }
+__device__ __forceinline__ bool is_restart(__nv_bfloat16 x) { return to_f32(x) < kRestart; }
 // Restarts of a block as ballots of its even and odd rows: whether one lies at or before
 // row 2 lane + odd, or behind it.
 __device__ __forceinline__ bool restart_upto(uint32_t even, uint32_t odd_rows, int lane, int odd) {

@@ -182,6 +182,29 @@ def test_restart_with_growing_gates_hides_what_was_before(la2, chunk, dt, d, len
     assert bool(torch.isfinite(a[0].float()).all())
 
 
+@pytest.mark.parametrize("low", [-105.0, -150.0, -9000.0])
+@pytest.mark.parametrize("dt,d", [("bf16", 128), ("f32", 32)])
+def test_gates_that_are_zero_in_fp32_are_restarts(la2, dt, d, low):  # noqa: F811
+    """A gate below -104 is one of -infinity in every call, growing gates behind it or not:
+    large values before it and small ones behind would show the difference."""
+    N = 150
+    ins = {n: t.cuda() for n, t in make(dt, 1, 2, N, d, d, 4).items()}
+    ins["gate"][..., 21:60] = 2.0
+    ins["k"][:, :, 20:] *= 2.0 ** -20
+    got = []
+    for x in (low, -torch.inf):
+        gate = ins["gate"].clone()
+        gate[..., 20] = x
+        args = (ins["q"], ins["k"], ins["v"], gate)
+        pool = torch.full((1, 2, d, d), 1e38, device="cuda")
+        la2.kv_state_gated(*args[1:], pool)
+        one = [t[:, :, 20].contiguous() for t in args]
+        step = la2.decode_step_gated(*one, pool)
+        got.append((la2.forward_gated(*args), *la2.backward_gated(*args, ins["do"]), pool, step))
+    la2.check()
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+
+
 def test_gradients_hold_the_same_bits_on_every_call(la2):  # noqa: F811
     """Pieces of many lengths, chunks that add them up (both state passes run side by
     side) and scanned ones, gates of very different sizes."""
