@@ -287,13 +287,14 @@ static la2_status forward_tc(const void* q, const void* k, const void* v, const 
 // The gates' gradient, from the chunks' starts: the sums left by the gradient passes,
 // or the scanned states.
 template <typename T>
-static la2_status gate_grad(const void* gate, const float* qdq, const float* kdk, const float* prefix,
-                            const float* suffix, void* dgate, int64_t BH, const Shape& sh, const Plan& p,
-                            cudaStream_t st) {
+static la2_status gate_grad(const void* q, const void* k, const void* v, const void* gate, const void* dout,
+                            const float* qdq, const float* kdk, const float* prefix, const float* suffix, void* dgate,
+                            int64_t BH, const Shape& sh, const Plan& p, cudaStream_t st) {
   LaunchTimer t(K_GATED_GATE, st);
   if (launch_pdl(gate_grad_kernel<T>, dim3((unsigned)(BH * sh.C)), dim3(kGradThreads), 0, st,
                  static_cast<const T*>(gate), qdq, kdk, prefix, suffix, static_cast<T*>(dgate), sh.N, sh.L, sh.C,
-                 p.nel) != cudaSuccess)
+                 p.nel, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
+                 static_cast<const T*>(dout), sh.d, sh.dv) != cudaSuccess)
     return LA2_ERR_CUDA;
   return launch_status();
 }
@@ -339,8 +340,8 @@ static la2_status backward_tc(const void* q, const void* k, const void* v, const
     if (launch_sm100<true, true>(tv, tdo, tq, tdk, tk, t, BH, st) != cudaSuccess) return LA2_ERR_CUDA;
   }
   if ((s = launch_status()) != LA2_OK) return s;
-  return gate_grad<__nv_bfloat16>(gate, qdq, kdk, prefix_sum ? prefix_sum : prefix, suffix_sum ? suffix_sum : suffix,
-                                  dgate, BH, sh, p, st);
+  return gate_grad<__nv_bfloat16>(q, k, v, gate, dout, qdq, kdk, prefix_sum ? prefix_sum : prefix,
+                                  suffix_sum ? suffix_sum : suffix, dgate, BH, sh, p, st);
 }
 
 static la2_status backward(const void* q, const void* k, const void* v, const void* gate, const void* dout,
@@ -378,7 +379,7 @@ static la2_status backward(const void* q, const void* k, const void* v, const vo
       return LA2_ERR_CUDA;
   }
   if ((s = launch_status()) != LA2_OK) return s;
-  return gate_grad<float>(gate, a.qdq, a.kdk, a.prefix_sum ? a.prefix_sum : prefix,
+  return gate_grad<float>(q, k, v, gate, dout, a.qdq, a.kdk, a.prefix_sum ? a.prefix_sum : prefix,
                           a.suffix_sum ? a.suffix_sum : suffix, dgate, BH, sh, p, st);
 }
 

@@ -28,7 +28,12 @@
 //   dl_t = sum_{i >= t > j} D[i][j] (q_i . k_j)(dO_i . v_j),
 // and satisfies dl_t = dl_(t+1) + q_t . dq_t - k_t . dk_t. The row dots leave the
 // dQ and dK passes in fp32; the flow at a chunk's end is <KV, U> of the two chunk
-// states there, so the running difference only spans one chunk.
+// states there, so the running difference only spans one chunk. The pairs i = j are in
+// both dots and cancel; of a head that forgets within a token the dots hold little else,
+// and what is left would be their rounding (12 % of dl at log gates of -12 over 500
+// rows). These kernels leave the pairs i = j out of both dots; the tensor cores' do not, and
+// where all gates around a token are that low its few pairs are summed instead
+// (see gate_grad_kernel).
 //
 // The workload is short sequences in fp32: what counts is how many blocks run at once
 // and how long one takes. A chunk may be a single block; a call's independent parts
@@ -209,8 +214,10 @@ __device__ __forceinline__ void gate_tables(const float* __restrict__ gate, int 
   __syncthreads();
 }
 
-// P[t][j] = e^(c_t - c_j) (a_t . b_j) for j <= t, else 0, over all 64 rows.
-__device__ __forceinline__ void scores(float* P, const float* a, const float* b, int ld, int K, const double* c) {
+// P[t][j] = e^(c_t - c_j) (a_t . b_j) for j <= t, else 0, over all 64 rows. With `diag`
+// the products a_t . b_t go there and P has zeros in their place.
+__device__ __forceinline__ void scores(float* P, const float* a, const float* b, int ld, int K, const double* c,
+                                       float* diag) {
   float acc[4][4];
   int cc[4];
   clear(acc);
@@ -221,8 +228,11 @@ __device__ __forceinline__ void scores(float* P, const float* a, const float* b,
   for (int i = 0; i < 4; ++i) {
     const int t = tile_row() + i;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      P[t * lp + cc[j]] = cc[j] <= t ? acc[i][j] * expf(static_cast<float>(c[t] - c[cc[j]])) : 0.f;
+    for (int j = 0; j < 4; ++j) {
+      const bool own = diag && cc[j] == t;
+      P[t * lp + cc[j]] = cc[j] <= t && !own ? acc[i][j] * expf(static_cast<float>(c[t] - c[cc[j]])) : 0.f;
+      if (own) diag[t] = acc[i][j];
+    }
   }
 }
 
@@ -310,11 +320,12 @@ __device__ __forceinline__ void load_state(float* S, const float* __restrict__ s
   }
 }
 
-// Bytes of shared memory: a state, `a` tiles of d and `b` of dv columns, `s` score tiles, the tables.
+// Bytes of shared memory: a state, `a` tiles of d and `b` of dv columns, `s` score tiles with
+// their diagonals, the tables.
 __host__ __device__ __forceinline__ size_t smem_bytes(int d, int dv, int a, int b, int s) {
   return kRows * sizeof(double) +
          sizeof(float) * ((size_t)round4(d) * stride_of(dv) + (size_t)kRows * (a * stride_of(d) + b * stride_of(dv)) +
-                          (size_t)s * kRows * stride_of(kRows) + 2 * kRows);
+                          (size_t)s * kRows * (stride_of(kRows) + 1) + 2 * kRows);
 }
 
 // Own state of every chunk: prefix (blockIdx.y 0, of k and v), sum_s e^(rest of the
@@ -386,7 +397,7 @@ fwd_kernel(const float* __restrict__ q, const float* __restrict__ k, const float
     load_rows(Vs, v + row * dv, rows, dv);
     if (i0 == t0) load_state<false>(S, states, tot, bh, ch, sh, nullptr);
     gate_tables(gate + row, rows, i0 == 0, c, head, tail);
-    scores(P, Qs, Ks, ld, round4(d), c);
+    scores(P, Qs, Ks, ld, round4(d), c, nullptr);
     __syncthreads();
     for (int c0 = 0; c0 < dv; c0 += 64) {
       const int col = c0 + 4 * tile_col(), cc[4] = {min(col, round4(dv) - 4), 0, 0, 0};
@@ -416,9 +427,11 @@ struct BwdArgs {
   const double* tot;
 };
 // Rows' values 4 tr + i of columns cc[j] out, and their dots with `x` (row stride lx)
-// added to dot.
+// added to dot. The pairs of a token with itself, diag_t z_t, are in the values and not
+// in the dots: they cancel between the two passes, and beside the pairs that a head
+// which forgets within a token keeps, their rounding would be all that was left.
 __device__ __forceinline__ void store_spread(float* out, int w, const float* x, int lx, const float (&acc)[4][4], int c0,
-                                             int rows, float (&dot)[4]) {
+                                             int rows, const float* diag, const float* z, float (&dot)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int t = tile_row() + i;
@@ -426,7 +439,7 @@ __device__ __forceinline__ void store_spread(float* out, int w, const float* x, 
     for (int j = 0; j < 4; ++j) {
       const int c = c0 + tile_col() + 16 * j;
       if (t < rows && c < w) {
-        out[t * w + c] = acc[i][j];
+        out[t * w + c] = fmaf(diag[t], z[t * lx + c], acc[i][j]);
         dot[i] = fmaf(x[t * lx + c], acc[i][j], dot[i]);
       }
     }
@@ -440,7 +453,7 @@ __device__ __forceinline__ void store_dots(float* out, float (&dot)[4], int rows
   }
 }
 
-// dQ_t = sum_{j<=t} e^(c_t - c_j) (dO_t . v_j) k_j + e^(c_t) dO_t KV^T, and q_t . dq_t.
+// dQ_t = sum_{j<=t} e^(c_t - c_j) (dO_t . v_j) k_j + e^(c_t) dO_t KV^T, and q_t . dq_t of j < t.
 __device__ __forceinline__ void bwd_dq(const BwdArgs& p, const Shape& sh, double* smem_d) {
   const int d = sh.d, dv = sh.dv, ld = stride_of(d), lv = stride_of(dv), lp = stride_of(kRows);
   double* c = smem_d;
@@ -451,6 +464,7 @@ __device__ __forceinline__ void bwd_dq(const BwdArgs& p, const Shape& sh, double
   float* Gs = Vs + kRows * lv;
   float* Qs = Gs + kRows * lv;
   float* A = Qs + kRows * ld;
+  float* diag = A + kRows * lp;
   const int64_t bh = blockIdx.x / sh.C, ch = blockIdx.x % sh.C;
   const int64_t t0 = ch * sh.L, t1 = imin64(sh.N, t0 + sh.L);
   for (int64_t i0 = t0; i0 < t1; i0 += kRows) {
@@ -463,7 +477,7 @@ __device__ __forceinline__ void bwd_dq(const BwdArgs& p, const Shape& sh, double
     load_rows(Qs, p.q + row * d, rows, d);
     if (i0 == t0) load_state<false>(S, p.prefix, p.tot, bh, ch, sh, p.prefix_sum);
     gate_tables(p.gate + row, rows, i0 == 0, c, head, tail);
-    scores(A, Gs, Vs, lv, round4(dv), c);
+    scores(A, Gs, Vs, lv, round4(dv), c, diag);
     __syncthreads();
     float dot[4] = {0.f, 0.f, 0.f, 0.f};
     for (int c0 = 0; c0 < d; c0 += 64) {
@@ -474,7 +488,7 @@ __device__ __forceinline__ void bwd_dq(const BwdArgs& p, const Shape& sh, double
       accumulate<true, true, false, false>(acc, Gs, lv, tile_row(), S, lv, cc, round4(dv), nullptr);
       scale_rows(acc, head);
       accumulate<true, false, false, false>(acc, A, lp, tile_row(), Ks, ld, cc, round4(rows), nullptr);
-      store_spread(p.dq + row * d, d, Qs, ld, acc, c0, rows, dot);
+      store_spread(p.dq + row * d, d, Qs, ld, acc, c0, rows, diag, Ks, dot);
     }
     store_dots(p.qdq + row, dot, rows);
     if (i0 + kRows < t1) {
@@ -484,7 +498,7 @@ __device__ __forceinline__ void bwd_dq(const BwdArgs& p, const Shape& sh, double
   }
 }
 
-// dK, dV and k_j . dk_j, blocks of a chunk last to first.
+// dK, dV and k_j . dk_j of t > j, blocks of a chunk last to first.
 __device__ __forceinline__ void bwd_dkdv(const BwdArgs& p, const Shape& sh, double* smem_d) {
   const int d = sh.d, dv = sh.dv, ld = stride_of(d), lv = stride_of(dv), lp = stride_of(kRows);
   double* c = smem_d;
@@ -495,6 +509,7 @@ __device__ __forceinline__ void bwd_dkdv(const BwdArgs& p, const Shape& sh, doub
   float* Vs = Ks + kRows * ld;
   float* Gs = Vs + kRows * lv;
   float* P = Gs + kRows * lv;
+  float* diag = P + kRows * lp;
   const int64_t bh = blockIdx.x / sh.C, ch = blockIdx.x % sh.C;
   const int64_t t0 = ch * sh.L, t1 = imin64(sh.N, t0 + sh.L);
   const int nblk = static_cast<int>((t1 - t0 + kRows - 1) / kRows);
@@ -510,7 +525,7 @@ __device__ __forceinline__ void bwd_dkdv(const BwdArgs& p, const Shape& sh, doub
     if (n == nblk - 1) load_state<true>(U, p.suffix, p.tot, bh, ch, sh, p.suffix_sum);
     gate_tables(p.gate + row, rows, i0 == 0, c, head, tail);
     // P[t][j] = D (q_t . k_j), then dV; the same tile then holds D (dO_t . v_j) for dK
-    scores(P, Qs, Ks, ld, round4(d), c);
+    scores(P, Qs, Ks, ld, round4(d), c, nullptr);
     __syncthreads();
     for (int c0 = 0; c0 < dv; c0 += 64) {
       const int col = c0 + 4 * tile_col(), cc[4] = {min(col, round4(dv) - 4), 0, 0, 0};
@@ -525,7 +540,7 @@ __device__ __forceinline__ void bwd_dkdv(const BwdArgs& p, const Shape& sh, doub
           if (tile_row() + i < rows) store4(p.dv + (row + tile_row() + i) * dv, col, dv, acc[i]);
     }
     __syncthreads();
-    scores(P, Gs, Vs, lv, round4(dv), c);
+    scores(P, Gs, Vs, lv, round4(dv), c, diag);
     __syncthreads();
     float dot[4] = {0.f, 0.f, 0.f, 0.f};
     for (int c0 = 0; c0 < d; c0 += 64) {
@@ -536,7 +551,7 @@ __device__ __forceinline__ void bwd_dkdv(const BwdArgs& p, const Shape& sh, doub
       accumulate<true, true, false, false>(acc, Vs, lv, tile_row(), U, lv, cc, round4(dv), nullptr);
       scale_rows(acc, tail);
       accumulate<false, false, false, false>(acc, P, lp, tile_row(), Qs, ld, cc, round4(rows), nullptr);
-      store_spread(p.dk + row * d, d, Ks, ld, acc, c0, rows, dot);
+      store_spread(p.dk + row * d, d, Ks, ld, acc, c0, rows, diag, Qs, dot);
     }
     store_dots(p.kdk + row, dot, rows);
     if (n > 0) {
@@ -676,6 +691,64 @@ __device__ __forceinline__ void sum_up_to_cut(double& x, bool& cut, int lane) {
   }
 }
 
+// Where the gates of a bf16 sequence are below this for kNear - 1 tokens on both sides of a
+// token, the gate's gradient is summed over pairs at most kNear tokens apart: the
+// others are e^-32 of its factor. Above it the running difference loses less
+// than e^4 2^-24 of the pairs a row.
+constexpr float kForgets = -4.f;
+constexpr int kNear = 8;
+
+// dl_t of the lanes that want it, lane l the row top - l of its sequence: the sum over
+// i >= t > j, i - j <= kNear of e^(l_(j+1) + ... + l_i) (q_i . k_j)(dO_i . v_j). Row by row i:
+// four lanes a distance i - j take the two dots, and each lane picks the distances
+// that reach across its t. Out of line: rarely run, and it would cost the scan registers.
+__device__ __noinline__ float sum_near_pairs(const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
+                                             const __nv_bfloat16* dout, const __nv_bfloat16* gate, int64_t N, int d,
+                                             int dv, int64_t top, unsigned wanted, int lane) {
+  const int64_t t = top - lane, last = imin64(N - 1, top - (__ffs(wanted) - 1) + kNear - 1);
+  const int apart = lane / 4 + 1, part = lane % 4;
+  auto dot = [&](const __nv_bfloat16* a, const __nv_bfloat16* b, int w) {  // this lane's quarter
+    float x = 0.f;
+    for (int c = 8 * part; c < w; c += 32) {
+      const uint4 ua = *reinterpret_cast<const uint4*>(a + c), ub = *reinterpret_cast<const uint4*>(b + c);
+      const uint32_t wa[4] = {ua.x, ua.y, ua.z, ua.w}, wb[4] = {ub.x, ub.y, ub.z, ub.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x = fmaf(__uint_as_float(wa[e] << 16), __uint_as_float(wb[e] << 16), x);
+        x = fmaf(__uint_as_float(wa[e] & 0xffff0000u), __uint_as_float(wb[e] & 0xffff0000u), x);
+      }
+    }
+    return x;
+  };
+  float sum = 0.f;
+#pragma unroll 1
+  for (int64_t i = top - (31 - __clz(wanted)); i <= last; ++i) {
+    const int64_t j = i - apart;
+    float qk = 0.f, ov = 0.f, l = 0.f;
+    if (j >= 0) {
+      qk = dot(q + i * d, k + j * d, d);
+      ov = dot(dout + i * dv, v + j * dv, dv);
+      for (int u = part; u < apart; u += 4) l += to_f32(gate[i - u]);
+    }
+#pragma unroll
+    for (int m = 1; m < 4; m <<= 1) {
+      qk += __shfl_xor_sync(0xffffffffu, qk, m);
+      ov += __shfl_xor_sync(0xffffffffu, ov, m);
+      l += __shfl_xor_sync(0xffffffffu, l, m);
+    }
+    float pair = j >= 0 ? qk * ov * expf(l) : 0.f;  // then summed with those further apart
+#pragma unroll
+    for (int m = 4; m < 32; m <<= 1) {
+      const float down = __shfl_down_sync(0xffffffffu, pair, m);
+      if (lane + m < 32) pair += down;
+    }
+    const int64_t behind = i - t;
+    const float x = __shfl_sync(0xffffffffu, pair, 4 * static_cast<int>(behind & (kNear - 1)));
+    if (behind >= 0 && behind < kNear) sum += x;
+  }
+  return sum;
+}
+
 // dl_t = flow at the chunk's end + sum over the chunk's rows from t on of
 // (q . dq - k . dk), and 0 at a restart, from which the sum starts anew. The flow at
 // the end of chunk c is <state before chunk c + 1, U behind chunk c> (0 for the last
@@ -688,7 +761,8 @@ template <typename T>
 __global__ void __launch_bounds__(kGradThreads)
 gate_grad_kernel(const T* __restrict__ gate, const float* __restrict__ qdq, const float* __restrict__ kdk,
                  const float* __restrict__ prefix, const float* __restrict__ suffix, T* __restrict__ dgate, int64_t N,
-                 int64_t L, int64_t C, int nel) {
+                 int64_t L, int64_t C, int nel, const T* __restrict__ q, const T* __restrict__ k,
+                 const T* __restrict__ v, const T* __restrict__ dout, int d, int dv) {
   pdl_launch_dependents();
   pdl_wait();
   constexpr int kWarps = kGradThreads / 32;
@@ -726,8 +800,20 @@ gate_grad_kernel(const T* __restrict__ gate, const float* __restrict__ qdq, cons
   // before the first token for its gate to pass on.
   for (int64_t hi = t1 - 1; hi >= t0; hi -= kGradThreads) {
     const int64_t t = hi - threadIdx.x, at = bh * N + t;
-    bool cut = t >= t0 && (t == 0 || to_f32(gate[at]) < kRestart);
+    const float l = t >= t0 ? to_f32(gate[at]) : 0.f;
+    bool cut = t >= t0 && (t == 0 || l < kRestart);
     double x = t >= t0 && !cut ? static_cast<double>(qdq[at]) - static_cast<double>(kdk[at]) : 0.0;
+    float near = 0.f;
+    bool forgets = false;
+    if constexpr (sizeof(T) == 2) {
+      forgets = l < kForgets && !cut;
+      for (int u = 1; u < kNear && forgets; ++u)  // (the first token's gate decides nothing)
+        forgets = (t - u < 1 || to_f32(gate[at - u]) < kForgets) && (t + u >= N || to_f32(gate[at + u]) < kForgets);
+      const unsigned wanted = __ballot_sync(0xffffffffu, forgets);
+      if (wanted)
+        near = sum_near_pairs(q + bh * N * d, k + bh * N * d, v + bh * N * dv, dout + bh * N * dv, gate + bh * N, N, d,
+                              dv, t + lane, wanted, lane);
+    }
     sum_up_to_cut(x, cut, lane);
     if (lane == 31) {
       part[w] = x;
@@ -740,7 +826,7 @@ gate_grad_kernel(const T* __restrict__ gate, const float* __restrict__ qdq, cons
     if (!any) sum += carry;
     const double before = w ? __shfl_sync(0xffffffffu, sum, w - 1) : carry;
     carry = __shfl_sync(0xffffffffu, sum, 31);
-    if (t >= t0) dgate[at] = from_f32<T>(static_cast<float>(cut ? x : before + x));
+    if (t >= t0) dgate[at] = from_f32<T>(forgets ? near : static_cast<float>(cut ? x : before + x));
     __syncthreads();
   }
 }

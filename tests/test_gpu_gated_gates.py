@@ -97,6 +97,50 @@ def test_reference():
         assert oracle.relative_frobenius(x.numpy(), y) <= 1e-12
 
 
+# ------------------------------------------------- the gradient of the gates, head by head
+#
+# fp32: a row's dot of q and dq is off by a few 2^-24 of the pairs behind it, and a gate's
+# gradient adds up to 512 such rows (a chunk), at random signs: 512^0.5 * 2 * 4 * 2^-24
+# = 1.1e-5 of the pairs across it, which is what the gradient of a head that forgets at
+# once consists of; 5e-5 is allowed. bf16: a score is rounded alike in both passes (2^-9
+# of each pair), the output once (2^-9), states to 2^-17 a row, which over 8192 rows adds
+# 8192^0.5 * 2^-17 = 7e-4: 1e-2, the bound of the other gradients.
+GATE_TOL = {"f32": 5e-5, "bf16": 1e-2}
+
+FORGETTING = [
+    # dtype, N, d, dv, chunk length, restarts
+    ("f32", 500, 64, 64, 512, False),
+    ("f32", 777, 48, 80, 0, False),
+    ("f32", 300, 128, 128, 512, True),
+    ("bf16", 500, 128, 128, 512, False),
+    ("bf16", 8192, 128, 128, 8192, False),
+    ("bf16", 8192, 128, 128, 8192, True),
+    ("bf16", 6001, 64, 64, 4096, True),
+    ("bf16", 3000, 64, 128, 0, False),
+    ("bf16", 2500, 128, 64, 128, True),  # more chunks than add their states up: scanned
+]
+
+
+@pytest.mark.parametrize("case", FORGETTING, ids=lambda c: "-".join(map(str, c)))
+def test_gate_gradient_of_each_head(la2, chunk, case):  # noqa: F811
+    dt, N, d, dv, length, restarts = case
+    g = torch.Generator().manual_seed(N + d)
+    level = torch.tensor([-0.001, -0.05, -1.0, -4.0, -8.0, -10.0, -12.0, -20.0])
+    H = len(level)
+    q, k, v, do = (torch.randn(1, H, N, w, generator=g) / w ** 0.5 for w in (d, d, dv, dv))
+    gate = level[:, None] * (0.9 + 0.2 * torch.rand(1, H, N, generator=g))
+    if restarts:
+        gate = gate.masked_fill(torch.rand(1, 1, N, generator=g) < 0.02, -torch.inf)
+    ins = [x.to(DT[dt]).cuda() for x in (q, k, v, gate, do)]
+    chunk(length)
+    got = la2.backward_gated(*ins)
+    la2.check()
+    want = reference(*ins)[1:5]
+    for x, y, name in zip(got, want, ("dq", "dk", "dv", "dgate")):
+        assert by_head(x, y) <= (GATE_TOL[dt] if name == "dgate" else 1e-5 if dt == "f32" else 1e-2), name
+    assert not got[3][ins[3] == -torch.inf].any()
+
+
 @pytest.mark.parametrize("dt,d", [("f32", 64), ("bf16", 128), ("bf16", 64)])
 def test_gate_gradient_does_not_cross_a_restart(la2, chunk, dt, d):  # noqa: F811
     """The last document's gradients, of any size, leave those of the gates before it bit
@@ -115,6 +159,22 @@ def test_gate_gradient_does_not_cross_a_restart(la2, chunk, dt, d):  # noqa: F81
     want = reference(*(ins[n] for n in ("q", "k", "v", "gate", "do")))[4]
     few = slice(190, 200)
     assert by_head(a[..., few], want[..., few]) <= (1e-5 if dt == "f32" else 1e-2)
+
+
+@pytest.mark.parametrize("dt,d,N", [("bf16", 128, 65536)])
+def test_one_chunk_of_many_rows(la2, chunk, dt, d, N):  # noqa: F811
+    """A sequence that one CTA walks from end to end: 65536^0.5 * 2^-17 = 2e-3 beside the
+    roundings above."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    level = torch.tensor([-0.0005, -0.02, -1.0, -6.0], device="cuda")
+    q, k, v, do = (torch.randn(1, 4, N, d, generator=g, device="cuda") / d ** 0.5 for _ in range(4))
+    gate = level[:, None] * (0.5 + torch.rand(1, 4, N, generator=g, device="cuda"))
+    ins = [x.to(DT[dt]) for x in (q, k, v, gate, do)]
+    chunk(N)
+    got = la2.backward_gated(*ins)
+    la2.check()
+    for x, y in zip(got, reference(*ins)[1:5]):
+        assert by_head(x, y) <= 1e-2
 
 
 # --------------------------------------------------------------------- restarts in a block
