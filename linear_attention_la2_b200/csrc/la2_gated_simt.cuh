@@ -32,8 +32,8 @@
 // both dots and cancel; of a head that forgets within a token the dots hold little else,
 // and what is left would be their rounding (12 % of dl at log gates of -12 over 500
 // rows). These kernels leave the pairs i = j out of both dots; the tensor cores' do not, and
-// where all gates around a token are that low its few pairs are summed instead
-// (see gate_grad_kernel).
+// where all gates around a token are that low its few pairs are summed instead (see
+// sum_near_pairs).
 //
 // The workload is short sequences in fp32: what counts is how many blocks run at once
 // and how long one takes. A chunk may be a single block; a call's independent parts
@@ -691,60 +691,111 @@ __device__ __forceinline__ void sum_up_to_cut(double& x, bool& cut, int lane) {
   }
 }
 
-// Where the gates of a bf16 sequence are below this for kNear - 1 tokens on both sides of a
+// Where the gates of a bf16 sequence are below this for kNear tokens on both sides of a
 // token, the gate's gradient is summed over pairs at most kNear tokens apart: the
-// others are e^-32 of its factor. Above it the running difference loses less
-// than e^4 2^-24 of the pairs a row.
-constexpr float kForgets = -4.f;
-constexpr int kNear = 8;
+// others carry e^-20 of its factor. Above it the running difference loses less
+// than e^5 2^-24 = 9e-6 of the pairs a row, at random signs.
+constexpr float kForgets = -5.f;
+constexpr int kNear = 4;
 
 // dl_t of the lanes that want it, lane l the row top - l of its sequence: the sum over
-// i >= t > j, i - j <= kNear of e^(l_(j+1) + ... + l_i) (q_i . k_j)(dO_i . v_j). Row by row i:
-// four lanes a distance i - j take the two dots, and each lane picks the distances
-// that reach across its t. Out of line: rarely run, and it would cost the scan registers.
+// i >= t > j, i - j <= kNear of e^(l_(j+1) + ... + l_i) (q_i . k_j)(dO_i . v_j). A warp walks
+// the rows i with the last kNear rows of k and v in registers, each lane two or four
+// columns; the eight dots of a row meet in nine shuffles, and each lane takes the
+// distances that reach across its t. With d and dv from 64 to 128 in steps of 64. Out
+// of line: it is rarely run and would cost the scan registers. (Gradients of B2 H32 N8K:
+// 490 us with no such token, 759 us with all gates at -8; with the rows read anew for every
+// distance 1163 us.)
+struct NearRow {
+  uint32_t x[2];  // columns 2 lane, + 1 and 64 + 2 lane, + 1
+  __device__ __forceinline__ void load(const __nv_bfloat16* base, int64_t row, int w, int lane) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(base + row * w) + lane;
+    x[0] = row >= 0 ? p[0] : 0u;
+    x[1] = row >= 0 && w == 128 ? p[32] : 0u;
+  }
+  __device__ __forceinline__ float dot(const NearRow& o) const {
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      s = fmaf(__uint_as_float(x[e] << 16), __uint_as_float(o.x[e] << 16), s);
+      s = fmaf(__uint_as_float(x[e] & 0xffff0000u), __uint_as_float(o.x[e] & 0xffff0000u), s);
+    }
+    return s;
+  }
+};
 __device__ __noinline__ float sum_near_pairs(const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
                                              const __nv_bfloat16* dout, const __nv_bfloat16* gate, int64_t N, int d,
                                              int dv, int64_t top, unsigned wanted, int lane) {
-  const int64_t t = top - lane, last = imin64(N - 1, top - (__ffs(wanted) - 1) + kNear - 1);
-  const int apart = lane / 4 + 1, part = lane % 4;
-  auto dot = [&](const __nv_bfloat16* a, const __nv_bfloat16* b, int w) {  // this lane's quarter
-    float x = 0.f;
-    for (int c = 8 * part; c < w; c += 32) {
-      const uint4 ua = *reinterpret_cast<const uint4*>(a + c), ub = *reinterpret_cast<const uint4*>(b + c);
-      const uint32_t wa[4] = {ua.x, ua.y, ua.z, ua.w}, wb[4] = {ub.x, ub.y, ub.z, ub.w};
+  const int64_t t = top - lane, first = top - (31 - __clz(wanted));
+  const int64_t last = imin64(N - 1, top - (__ffs(wanted) - 1) + kNear - 1);
+  const int apart = (lane >> 2 & 3) + 1;  // the distance whose pair this lane ends up with
+  NearRow kr[kNear], vr[kNear];           // rows i - 1, i - 2, ...
+  float gr[kNear];                        // gates i, i - 1, ...
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x = fmaf(__uint_as_float(wa[e] << 16), __uint_as_float(wb[e] << 16), x);
-        x = fmaf(__uint_as_float(wa[e] & 0xffff0000u), __uint_as_float(wb[e] & 0xffff0000u), x);
+  for (int a = 0; a < kNear; ++a) {
+    kr[a].load(k, first - 1 - a, d, lane);
+    vr[a].load(v, first - 1 - a, dv, lane);
+    gr[a] = first - 1 - a >= 0 ? to_f32(gate[first - 1 - a]) : 0.f;  // (gate i is put in front)
+  }
+  float sum = 0.f;
+  q += first * d;
+  k += first * d;
+  v += first * dv;
+  dout += first * dv;
+  NearRow qi, oi, ki, vi;
+  float gi;
+  auto fetch = [&](int64_t i) {
+    qi.load(q, 0, d, lane);
+    oi.load(dout, 0, dv, lane);
+    ki.load(k, 0, d, lane);
+    vi.load(v, 0, dv, lane);
+    gi = to_f32(gate[i]);
+    q += d;
+    k += d;
+    v += dv;
+    dout += dv;
+  };
+  fetch(first);
+#pragma unroll 4
+  for (int64_t i = first; i <= last; ++i) {
+    float s[8];
+#pragma unroll
+    for (int a = 0; a < kNear; ++a) {
+      s[a] = qi.dot(kr[a]);
+      s[4 + a] = oi.dot(vr[a]);
+    }
+#pragma unroll
+    for (int a = kNear - 1; a > 0; --a) {
+      kr[a] = kr[a - 1];
+      vr[a] = vr[a - 1];
+      gr[a] = gr[a - 1];
+    }
+    kr[0] = ki;
+    vr[0] = vi;
+    gr[0] = gi;
+    if (i < last) fetch(i + 1);
+#pragma unroll
+    for (int step = 0; step < 3; ++step) {  // each lane keeps half: lanes from 16 on the dots of dO and v
+      const int keep = 4 >> step, bit = 16 >> step;
+      const bool up = lane & bit;
+#pragma unroll
+      for (int e = 0; e < keep; ++e) {
+        const float mine = up ? s[e + keep] : s[e], other = up ? s[e] : s[e + keep];
+        s[e] = mine + __shfl_xor_sync(0xffffffffu, other, bit);
       }
     }
-    return x;
-  };
-  float sum = 0.f;
-#pragma unroll 1
-  for (int64_t i = top - (31 - __clz(wanted)); i <= last; ++i) {
-    const int64_t j = i - apart;
-    float qk = 0.f, ov = 0.f, l = 0.f;
-    if (j >= 0) {
-      qk = dot(q + i * d, k + j * d, d);
-      ov = dot(dout + i * dv, v + j * dv, dv);
-      for (int u = part; u < apart; u += 4) l += to_f32(gate[i - u]);
-    }
-#pragma unroll
-    for (int m = 1; m < 4; m <<= 1) {
-      qk += __shfl_xor_sync(0xffffffffu, qk, m);
-      ov += __shfl_xor_sync(0xffffffffu, ov, m);
-      l += __shfl_xor_sync(0xffffffffu, l, m);
-    }
-    float pair = j >= 0 ? qk * ov * expf(l) : 0.f;  // then summed with those further apart
-#pragma unroll
-    for (int m = 4; m < 32; m <<= 1) {
-      const float down = __shfl_down_sync(0xffffffffu, pair, m);
-      if (lane + m < 32) pair += down;
-    }
+    float x = s[0];
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    x *= __shfl_xor_sync(0xffffffffu, x, 16);
+    const float l = gr[0] + (apart > 1 ? gr[1] : 0.f) + (apart > 2 ? gr[2] : 0.f) + (apart > 3 ? gr[3] : 0.f);
+    x = i >= apart ? x * expf(l) : 0.f;
     const int64_t behind = i - t;
-    const float x = __shfl_sync(0xffffffffu, pair, 4 * static_cast<int>(behind & (kNear - 1)));
-    if (behind >= 0 && behind < kNear) sum += x;
+#pragma unroll
+    for (int a = 0; a < kNear; ++a) {
+      const float pair = __shfl_sync(0xffffffffu, x, 4 * a);
+      if (behind >= 0 && behind <= a) sum += pair;
+    }
   }
   return sum;
 }
@@ -807,7 +858,7 @@ gate_grad_kernel(const T* __restrict__ gate, const float* __restrict__ qdq, cons
     bool forgets = false;
     if constexpr (sizeof(T) == 2) {
       forgets = l < kForgets && !cut;
-      for (int u = 1; u < kNear && forgets; ++u)  // (the first token's gate decides nothing)
+      for (int u = 1; u <= kNear && forgets; ++u)  // (the first token's gate decides nothing)
         forgets = (t - u < 1 || to_f32(gate[at - u]) < kForgets) && (t + u >= N || to_f32(gate[at + u]) < kForgets);
       const unsigned wanted = __ballot_sync(0xffffffffu, forgets);
       if (wanted)
