@@ -245,9 +245,10 @@ static la2_status states_tc(const Tile& y, const Tile& z, const void* gate, floa
   p.spin_limit = spin_limit();
   {
     LaunchTimer t(K_GATED_STATE, st);
-    const cudaError_t e = kind == FOR_DK_DV ? launch_state_sm100<true, false>(y, z, p, BH, st)
-                          : kind == FOR_O   ? launch_state_sm100<false, true>(y, z, p, BH, st)
-                                            : launch_state_sm100<false, false>(y, z, p, BH, st);
+    const cudaError_t e = kind == FOR_DK_DV ? launch_state_sm100<true, false, false>(y, z, p, BH, st)
+                          : kind == FOR_O   ? launch_state_sm100<false, true, false>(y, z, p, BH, st)
+                          : kind == FOR_DQ  ? launch_state_sm100<false, false, false>(y, z, p, BH, st)
+                                            : launch_state_sm100<false, false, true>(y, z, p, BH, st);
     if (e != cudaSuccess) return LA2_ERR_CUDA;
   }
   la2_status s = launch_status();

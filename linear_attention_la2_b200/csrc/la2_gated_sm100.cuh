@@ -879,15 +879,19 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 // from (q, dO): sum of w_t y_t^T z_t with the weight taken to the piece's end (its
 // start), so the accumulator is never decayed: the blocks are walked from that edge,
 // and the sum of the gates walked so far goes into the scale of the rows. Y~ is value
-// and remainder, so the fp32 state is good to 2^-17: it is what the caller's pool
-// receives after a prefill (B3 H16 N3001: 4.5e-6 off; with a second remainder 2.1e-6,
-// the tensor core's own sums, for 33 us instead of 28.6). Bound by HBM: K and V are read once. Warps: 0 loads,
+// and remainder: a state that only starts chunks is good to 2^-17, well under the
+// rounding of the outputs made from it. FULL: a state that the caller receives in fp32 (a
+// pool's, after a prefill). Its Y~ is fp32's 24 bits as three bf16 values, the first over Y,
+// and the other two have a sum of their own, so that the first's loses no digits to as
+// many small addends again (B3 H16 N3001: 7e-7 off, as la2_kv_state's exact products are, in 33 us;
+// with value and remainder 4.5e-6 in 28.5 us). Bound by HBM, where K and V are read once, and, FULL,
+// by shared memory (192 KB a block: 1500 cycles against 1350 of HBM). Warps: 0 loads,
 // 1 MMA, 2 the rows' factors, 4-11 scale rows (four threads a row), 4-7 write the
 // state out. Two CTAs an SM: one's scaling (about 1000 cycles a block) runs beside the
 // other's waits, loads and MMAs; one CTA with twice the buffers was 1.4 times slower.
 struct StateCfg {
   static constexpr int KS = 2;
-  static constexpr int OFF_Y2 = KS * 2 * kTile;            // value and remainder
+  static constexpr int OFF_Y2 = KS * 2 * kTile;            // value and remainder (FULL: two remainders)
   static constexpr int OFF_TAB = OFF_Y2 + 2 * kTile;       // rows' factors, kTabs blocks of 64
   static constexpr int OFF_BAR = OFF_TAB + kTabs * 64 * 4;
   static constexpr int NBAR = 2 * KS + 2 + 2 + kTabs;
@@ -907,13 +911,23 @@ struct TcStateParams {
   int32_t beside;  // the launch before is independent: see begin_grid
 };
 
+// x as three bf16 values.
+__device__ __forceinline__ void split3(float x, float y, uint32_t& a, uint32_t& b, uint32_t& c) {
+  a = s::pack_bf16x2(x, y);
+  x -= __uint_as_float(a << 16);
+  y -= __uint_as_float(a & 0xffff0000u);
+  b = s::pack_bf16x2(x, y);
+  c = s::pack_bf16x2(x - __uint_as_float(b << 16), y - __uint_as_float(b & 0xffff0000u));
+}
+
 // ROWS_Z: the state's rows are z's columns (what O and dV start from), else y's.
-template <bool SUFFIX, bool ROWS_Z>
+template <bool SUFFIX, bool ROWS_Z, bool FULL>
 __global__ void __launch_bounds__(384, 2)
 gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_z,
                          const TcStateParams prm) {
   using CF = StateCfg;
   constexpr int KS = CF::KS;
+  constexpr uint32_t kCols = FULL ? 256 : 128;  // (two CTAs an SM share 512)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -949,7 +963,7 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
     s::tma_prefetch(&tm_z);
   }
   if (warp == 1) {
-    s::tmem_alloc(tmem_base, 128);
+    s::tmem_alloc(tmem_base, kCols);
     s::tmem_relinquish();
   }
   s::tc_fence_before();
@@ -987,10 +1001,16 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
       ok = wait(&in_full[i % KS], (i / KS) & 1, 91) && wait(y2_full, i & 1, 92);
       if (!ok) break;
       s::tc_fence_after();
-      const uint64_t y2 = in_d + CF::OFF_Y2 / 16, z = in_d + ((i % KS) * 2 * kTile + kTile) / 16;
+      const uint64_t y2 = in_d + CF::OFF_Y2 / 16, y = in_d + (i % KS) * 2 * kTile / 16, z = y + kTile / 16;
       const uint64_t lo = y2 + kTile / 16;
-      mma_run<4>(lead, tmem, ROWS_Z ? z : y2, ROWS_Z ? y2 : z, 128, 128, 0, 0, ID_UPD, i > 0);
-      mma_run<4>(lead, tmem, ROWS_Z ? z : lo, ROWS_Z ? lo : z, 128, 128, 0, 0, ID_UPD, 1);
+      if constexpr (FULL) {
+        mma_run<4>(lead, tmem, y, z, 128, 128, 0, 0, ID_UPD, i > 0);
+        mma_run<4>(lead, tmem + 128, y2, z, 128, 128, 0, 0, ID_UPD, i > 0);
+        mma_run<4>(lead, tmem + 128, lo, z, 128, 128, 0, 0, ID_UPD, 1);
+      } else {
+        mma_run<4>(lead, tmem, ROWS_Z ? z : y2, ROWS_Z ? y2 : z, 128, 128, 0, 0, ID_UPD, i > 0);
+        mma_run<4>(lead, tmem, ROWS_Z ? z : lo, ROWS_Z ? lo : z, 128, 128, 0, 0, ID_UPD, 1);
+      }
       commit(lead, y2_empty);
       commit(lead, &in_empty[i % KS]);
     }
@@ -1048,7 +1068,8 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
       ok = wait(&tab_full[i % kTabs], (i / kTabs) & 1, 97) && wait(&in_full[i % KS], (i / KS) & 1, 93) &&
            wait(y2_empty, (i & 1) ^ 1, 94);
       if (!ok) break;
-      const Factor f = factor(tab[(i % kTabs) * 64 + r]);
+      const float factor_r = tab[(i % kTabs) * 64 + r];
+      const Factor f = factor(factor_r);
       const uint32_t y2 = s::smem_u32(smem + CF::OFF_Y2);
       const uint32_t ya = s::smem_u32(smem + (i % KS) * 2 * kTile);
 #pragma unroll
@@ -1056,9 +1077,19 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
         const uint32_t off = (ch >> 3) * 8192 + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
         uint32_t x[4], hi[4], lo[4];
         s::ld_shared_v4(ya + off, x[0], x[1], x[2], x[3]);
+        if constexpr (FULL) {
+          uint32_t mid[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split_scaled(x[e], f, hi[e], lo[e]);
-        s::st_shared_v4(y2 + off, hi[0], hi[1], hi[2], hi[3]);
+          for (int e = 0; e < 4; ++e)
+            split3(__uint_as_float(x[e] << 16) * factor_r, __uint_as_float(x[e] & 0xffff0000u) * factor_r, hi[e], mid[e],
+                   lo[e]);
+          s::st_shared_v4(ya + off, hi[0], hi[1], hi[2], hi[3]);
+          s::st_shared_v4(y2 + off, mid[0], mid[1], mid[2], mid[3]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split_scaled(x[e], f, hi[e], lo[e]);
+          s::st_shared_v4(y2 + off, hi[0], hi[1], hi[2], hi[3]);
+        }
         s::st_shared_v4(y2 + kTile + off, lo[0], lo[1], lo[2], lo[3]);
       }
       s::fence_proxy_async();
@@ -1072,8 +1103,16 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
 #pragma unroll 1
       for (int c32 = 0; c32 < 4; ++c32) {
         uint32_t v[32];
-        s::tmem_ld32(tmem + c32 * 32 + (static_cast<uint32_t>(32 * (warp & 3)) << 16), v);
+        const uint32_t at = tmem + c32 * 32 + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+        s::tmem_ld32(at, v);
         s::tmem_ld_wait();
+        if constexpr (FULL) {
+          uint32_t u[32];
+          s::tmem_ld32(at + 128, u);
+          s::tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(u[e]));
+        }
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           dst[s::state_f4<128>(row, c32 * 8 + q)] =
@@ -1091,7 +1130,7 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
   __syncthreads();
   if (warp == 1) {
     s::tc_fence_after();
-    s::tmem_dealloc(tmem, 128);
+    s::tmem_dealloc(tmem, kCols);
   }
 }
 
@@ -1105,10 +1144,10 @@ struct Tile {
   Tile(const void* base, int64_t BH, int64_t N, int w_) : w(w_), ok(make_tmap_3d(&map, base, BH, N, w_, 64)) {}
 };
 
-template <bool SUFFIX, bool ROWS_Z>
+template <bool SUFFIX, bool ROWS_Z, bool FULL>
 inline cudaError_t launch_state_sm100(const Tile& y, const Tile& z, const TcStateParams& p, int64_t BH, cudaStream_t st) {
   if (!y.ok || !z.ok) return cudaErrorInvalidValue;
-  auto kern = gated_state_sm100_kernel<SUFFIX, ROWS_Z>;
+  auto kern = gated_state_sm100_kernel<SUFFIX, ROWS_Z, FULL>;
   static bool done[128];
   if (!smem_attribute_set(kern, StateCfg::SMEM, done)) return cudaErrorInvalidValue;
   return launch_pdl(kern, dim3((unsigned)(BH * p.count)), dim3(384), StateCfg::SMEM, st, y.map, z.map, p);

@@ -199,6 +199,25 @@ def test_state_behind_restarts(la2, chunk, dt, d, length, rate):  # noqa: F811
     assert by_head(pool, want) <= 1e-5
 
 
+@pytest.mark.parametrize("kind", ["soft", "weak", "strong", "restarts"])
+@pytest.mark.parametrize("B,H,N,d,dv,length", [(3, 4, 3001, 128, 128, 0), (1, 2, 512, 128, 128, 512),
+                                               (1, 3, 777, 64, 64, 0), (2, 2, 300, 64, 128, 128)])
+def test_pool_states_are_fp32(la2, chunk, B, H, N, d, dv, length, kind):  # noqa: F811
+    """A pool's state from bf16 keys and values holds fp32's digits, not those of a pair of bf16
+    values. Its products are exact to 2^-24. A tensor core's sum over 512 rows, the longest
+    piece here, adds 32 times, each cut off by at most 2^-23 and 2^-24 on average, of a sum
+    that grows like a root: 32 * 2/3 * 2^-24 = 1.3e-6; the smaller parts' sum and the gates'
+    exponentials (2^-22) add 2^-22 and 3 * 2^-24: 2e-6 in all, where pairs leave 4.5e-6."""
+    ins = make("bf16", B, H, N, d, dv, N, kind)
+    dev = [ins[n].cuda() for n in ("q", "k", "v", "gate", "do")]
+    chunk(length)
+    pool = torch.randn(B, H, d, dv, generator=torch.Generator().manual_seed(7)).cuda()
+    want = reference(*dev, state=pool)[5]
+    la2.kv_state_gated(*dev[1:4], pool)
+    la2.check()
+    assert by_head(pool, want) <= 2e-6
+
+
 @pytest.mark.parametrize("dt,d,length", [("bf16", 128, 0), ("bf16", 64, 64), ("bf16", 128, 128), ("f32", 40, 0),
                                          ("f32", 33, 64)])
 @pytest.mark.parametrize("at,n,up", [(0, 70, 0.25), (3, 30, 0.5), (70, 200, 0.5)])
