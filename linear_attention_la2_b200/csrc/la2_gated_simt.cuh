@@ -264,7 +264,7 @@ __device__ __forceinline__ void update_state(float* S, const float* a, const flo
         for (int i = 0; i < 4; ++i) {
           if (r + i >= d) break;
           float4* s = reinterpret_cast<float4*>(S + (r + i) * lb + c);
-          if (!fresh) {
+          if (!fresh && whole != 0.f) {  // (a restart drops the state, be it no number)
             const float4 x = *s;
             acc[i][0] = fmaf(whole, x.x, acc[i][0]);
             acc[i][1] = fmaf(whole, x.y, acc[i][1]);
@@ -313,6 +313,7 @@ __device__ __forceinline__ void load_state(float* S, const float* __restrict__ s
             if (c + e < sh.dv) x[e] = fmaf(f, src[e], x[e]);
         }
         if (j + 1 < n) f *= expf(static_cast<float>(tot[first + j * step]));
+        if (f == 0.f) break;
       }
     }
     if (sum && r < sh.d && c < sh.dv) store4(sum + (bh * sh.C + ch) * nel + r * sh.dv, c, sh.dv, x);
@@ -606,7 +607,7 @@ scan_kernel(float* __restrict__ s0, float* __restrict__ s1, const double* __rest
     for (int u = 0; u < U; ++u) {
       const int64_t ch = mode == 0 ? i0 + u : C - 1 - (i0 + u);
       if (i0 + u < C) p[ch * nel] = run;
-      run = fmaf(f[u], run, x[u]);
+      run = f[u] == 0.f ? x[u] : fmaf(f[u], run, x[u]);  // (a restart drops what may be no number)
     }
   }
 }

@@ -665,9 +665,14 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
       tmem_st8(tc + 8 * h, hi);
       if (PARTS == 2) tmem_st8(tc + 64 + 8 * h, lo);
       if (keep) {
-        const uint64_t ff = f2(f, f);
+        if (f == 0.f) {  // (a restart drops the state, be it no number)
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) unpack(mul2(f2(v[e], v[e + 1]), ff), v[e], v[e + 1]);
+          for (int e = 0; e < 16; ++e) v[e] = 0u;
+        } else {
+          const uint64_t ff = f2(f, f);
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) unpack(mul2(f2(v[e], v[e + 1]), ff), v[e], v[e + 1]);
+        }
         s::tmem_st16(ts + h * 16, v);
       }
     };
@@ -705,6 +710,7 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
               x[4 * q + 3] = fmaf(f, y.w, x[4 * q + 3]);
             }
             if (j + 1 < pieces) f *= expf(static_cast<float>(prm.tot[at]));
+            if (f == 0.f) break;  // (what a restart has dropped may be no number)
           }
           if (GRAD && prm.sum) {
             float4* dst = reinterpret_cast<float4*>(prm.sum + (bh * prm.C + ch) * 128 * 128);
@@ -889,11 +895,12 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 // 1 MMA, 2 the rows' factors, 4-11 scale rows (four threads a row), 4-7 write the
 // state out. Two CTAs an SM: one's scaling (about 1000 cycles a block) runs beside the
 // other's waits, loads and MMAs; one CTA with twice the buffers was 1.4 times slower.
+constexpr int kStateTab = 68;  // the rows' factors, and whether the block lies beyond a restart
 struct StateCfg {
   static constexpr int KS = 2;
   static constexpr int OFF_Y2 = KS * 2 * kTile;            // value and remainder (FULL: two remainders)
-  static constexpr int OFF_TAB = OFF_Y2 + 2 * kTile;       // rows' factors, kTabs blocks of 64
-  static constexpr int OFF_BAR = OFF_TAB + kTabs * 64 * 4;
+  static constexpr int OFF_TAB = OFF_Y2 + 2 * kTile;       // kTabs blocks' tables
+  static constexpr int OFF_BAR = OFF_TAB + kTabs * kStateTab * 4;
   static constexpr int NBAR = 2 * KS + 2 + 2 + kTabs;
   static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
   static_assert(SMEM <= 113 * 1024, "two CTAs an SM");
@@ -1001,6 +1008,11 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
       ok = wait(&in_full[i % KS], (i / KS) & 1, 91) && wait(y2_full, i & 1, 92);
       if (!ok) break;
       s::tc_fence_after();
+      if (tab[(i % kTabs) * kStateTab + 64] != 0.f) {  // beyond a restart: nothing to add, be it no number
+        commit(lead, y2_empty);
+        commit(lead, &in_empty[i % KS]);
+        continue;
+      }
       const uint64_t y2 = in_d + CF::OFF_Y2 / 16, y = in_d + (i % KS) * 2 * kTile / 16, z = y + kTile / 16;
       const uint64_t lo = y2 + kTile / 16;
       if constexpr (FULL) {
@@ -1051,7 +1063,9 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
             za = restart_behind(ex, ey, lane, 0);
             zb = restart_behind(ex, ey, lane, 1);
           }
-          reinterpret_cast<float2*>(tab + (i % kTabs) * 64)[lane] =
+          float* slot = tab + (i % kTabs) * kStateTab;
+          if (lane == 0) slot[64] = dead;
+          reinterpret_cast<float2*>(slot)[lane] =
               make_float2(dead || za ? 0.f : ex2(static_cast<float>(run + static_cast<double>(a))),
                           dead || zb ? 0.f : ex2(static_cast<float>(run + static_cast<double>(b))));
           run += static_cast<double>(all);
@@ -1068,7 +1082,7 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
       ok = wait(&tab_full[i % kTabs], (i / kTabs) & 1, 97) && wait(&in_full[i % KS], (i / KS) & 1, 93) &&
            wait(y2_empty, (i & 1) ^ 1, 94);
       if (!ok) break;
-      const float factor_r = tab[(i % kTabs) * 64 + r];
+      const float factor_r = tab[(i % kTabs) * kStateTab + r];
       const Factor f = factor(factor_r);
       const uint32_t y2 = s::smem_u32(smem + CF::OFF_Y2);
       const uint32_t ya = s::smem_u32(smem + (i % KS) * 2 * kTile);

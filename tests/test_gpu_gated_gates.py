@@ -261,6 +261,36 @@ def test_restart_with_growing_gates_hides_what_was_before(la2, chunk, dt, d, len
     assert bool(torch.isfinite(a[0].float()).all())
 
 
+@pytest.mark.parametrize("dt,d,length", [("bf16", 128, 0), ("bf16", 128, 1024), ("bf16", 128, 64), ("bf16", 64, 256),
+                                         ("f32", 32, 0), ("f32", 48, 1024)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_no_numbers_end_at_a_restart(la2, chunk, dt, d, length, bad):  # noqa: F811
+    """A document whose values are no numbers leaves the others bit for bit, but for the
+    64-row blocks in which it begins and ends, and the gates' gradients of the document before it."""
+    N, begin, end = 1000, 200, 700  # blocks 3 and 10: rows 192-255 and 640-703
+    ins = {n: t.cuda() for n, t in make(dt, 1, 2, N, d, d, 15).items()}
+    ins["gate"][..., [begin, end]] = -torch.inf
+    chunk(length)
+
+    def calls():
+        q, k, v, gate, do = (ins[n] for n in ("q", "k", "v", "gate", "do"))
+        pool = torch.full((1, 2, d, d), 2.0, device="cuda")
+        la2.kv_state_gated(k, v, gate, pool)
+        return (la2.forward_gated(q, k, v, gate), *la2.backward_gated(q, k, v, gate, do), pool)
+
+    a = calls()
+    for n in ("q", "k", "v", "do"):
+        ins[n][:, :, 300:310] = bad
+    b = calls()
+    la2.check()
+    assert not torch.isfinite(b[0][:, :, 300:310].float()).any()
+    for x, y, name in zip(a, b, ("o", "dq", "dk", "dv", "dgate")):
+        assert torch.equal(x[:, :, 704:], y[:, :, 704:]), name
+        if name != "dgate":
+            assert torch.equal(x[:, :, :192], y[:, :, :192]), name
+    assert torch.equal(a[5], b[5])
+
+
 @pytest.mark.parametrize("low", [-105.0, -150.0, -9000.0])
 @pytest.mark.parametrize("dt,d", [("bf16", 128), ("f32", 32)])
 def test_gates_that_are_zero_in_fp32_are_restarts(la2, dt, d, low):  # noqa: F811
