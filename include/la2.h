@@ -216,8 +216,10 @@ LA2_API la2_status la2_backward_decay(const void *q, const void *k, const void *
  * s <= t, 0 above. `gate` [B,H,N] holds LOG gates in `dt`: 0 is la2_forward's
  * causal op, a constant log(lambda) is la2_forward_decay's. A gate below -104, whose
  * exponential is 0 in fp32, -infinity included, is exactly 0: the state restarts at
- * that token (packed documents), whatever was before it as long as that is finite.
- * Gates above 0 follow the same formula. One K/V head per query head; q, k, v, o, dout,
+ * that token (packed documents), whatever was before it as long as that is finite. NaN
+ * and infinities of one document reach others only inside the 64-token blocks (counted
+ * from the sequence's first) in which it begins and ends, and in dgate also the document
+ * before it. Gates above 0 follow the same formula. One K/V head per query head; q, k, v, o, dout,
  * dq, dk, dvv as for la2_forward / la2_backward. dgate [B,H,N] receives the gradient by
  * the log gate,
  *   dgate_t = sum over i >= t > j of D[i][j] (q_i . k_j) (dout_i . v_j),

@@ -547,8 +547,7 @@ la2_status la2_decode_step_gated(const void* q, const void* k, const void* v, co
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   LaunchTimer t(K_GATED_DECODE, st);
   // Four columns per lane under the conditions of la2_decode_step's.
-  const bool v4 = dv % 4 == 0 && d <= kDecodeWarps * kRows && is_aligned(state, 16) && is_aligned(v, 4 * es) &&
-                  is_aligned(o, es);
+  const bool v4 = dv % 4 == 0 && d <= kDecodeWarps * kRows && is_aligned(state, 16) && is_aligned(v, 4 * es);
   const dim3 grid((unsigned)BH, (unsigned)(v4 ? (dv + 127) / 128 : (dv + 31) / 32)), block(32 * kDecodeWarps);
   auto launch = [&](auto tag) {
     using T = decltype(tag);

@@ -29,13 +29,18 @@
 // update -> copy -> update; S of the next block is issued before it, and the second
 // buffers of far and P let the epilogue and the mask trail.
 //
-// What bounds it: shared-memory bandwidth. Tile loads, operand reads, the scaling, P
-// and the output tile take about 2200 cycles of 128 bytes a 64-row block (GRAD 2900),
-// against 2850 cycles that a block's share of HBM takes at 148 SMs; the state's copy
-// as an operand in shared memory took 500 (GRAD 1000) more.
+// What bounds it: no unit alone. A 64-row block takes about 3600 cycles (B1 H32 N16K: 120 us
+// for 64 blocks a CTA), its share of HBM 2850 at 148 SMs, shared memory about 2200 of 128
+// bytes by count (tile loads, operand reads, the scaling, P and the output tile; GRAD 2900;
+// the state's copy as an operand there took 500, GRAD 1000, more), the tensor pipe a third, the
+// issue slots half. What is left are the waits of the chain update -> copy -> update and
+// between the roles.
 //
 // Gate sums: c in base 2, fp32, at most 64 terms; a restart counts as 0 there and cuts the
 // weights made of them.
+//
+// NaN and infinities: a restart drops the state and what chunks start from; inside the 64
+// rows of a block the products mix all rows (0 times NaN).
 //
 // GRAD (dQ, dK) also returns the rows' dots q . dq and k . dk (fp32, from the
 // unrounded rows) for the gates' gradient, a running difference of them: their
@@ -47,7 +52,12 @@
 // Widths of 64 run as 128: the tensor maps end at the tensor's width, so that the tiles'
 // second 64 columns arrive as zeros and are not stored, and the chunk states' other rows
 // and columns are zeros. The blocks' time is that of 128, a third of the CUDA cores' at
-// 64 (B4 H4 N2K: forward 97 -> 31 us, gradients 245 -> 105 us).
+// 64 (B4 H4 N2K: forward 97 -> 31 us, gradients 245 -> 83 us).
+//
+// Roundings: P and, in O and dV, the state's copy are one bf16 value each, as in the plain
+// and decayed forms' kernels: with Y~ and the sums finer, an output is 2.35e-3 off
+// (relative Frobenius) where its own rounding alone is 1.66e-3. A second value of P
+// would be another product of 64 x 128 x 64 a block and 16 KB that are not there.
 //
 // The roles' inner loops stay rolled: five roles share each scheduler, and unrolled
 // over a block their instructions came from beyond its instruction cache.

@@ -778,7 +778,8 @@ static int tile_of(const Args& a, bool vec, int sms) {
   return static_cast<int>(t);
 }
 
-// CTAs of the backward: each leaves its sums of dw, so at most as many as run at once.
+// CTAs of the backward: each leaves its sums of dw, so a bounded number (8 an SM, of which
+// 4 run at once: 128 registers a thread), which take further tiles in turn.
 static int bwd_grid(const Args& a, int tile, int sms) {
   const int64_t tiles = (a.B * a.N + tile - 1) / tile;
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(tiles, 8 * (int64_t)sms)));
