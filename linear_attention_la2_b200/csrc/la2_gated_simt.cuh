@@ -264,8 +264,9 @@ __device__ __forceinline__ void update_state(float* S, const float* a, const flo
         for (int i = 0; i < 4; ++i) {
           if (r + i >= d) break;
           float4* s = reinterpret_cast<float4*>(S + (r + i) * lb + c);
-          if (!fresh && whole != 0.f) {  // (a restart drops the state, be it no number)
-            const float4 x = *s;
+          if (!fresh) {
+            float4 x = *s;
+            if (whole == 0.f) x = make_float4(0.f, 0.f, 0.f, 0.f);  // (a restart drops it, be it no number)
             acc[i][0] = fmaf(whole, x.x, acc[i][0]);
             acc[i][1] = fmaf(whole, x.y, acc[i][1]);
             acc[i][2] = fmaf(whole, x.z, acc[i][2]);
@@ -304,16 +305,18 @@ __device__ __forceinline__ void load_state(float* S, const float* __restrict__ s
 #pragma unroll 4
       for (int j = 0; j < n; ++j) {
         const float* src = states + (first + j * step) * nel + r * sh.dv + c;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
         if (sh.dv % 4 == 0) {
-          const float4 v = *reinterpret_cast<const float4*>(src);
-          x[0] = fmaf(f, v.x, x[0]); x[1] = fmaf(f, v.y, x[1]); x[2] = fmaf(f, v.z, x[2]); x[3] = fmaf(f, v.w, x[3]);
+          const float4 u = *reinterpret_cast<const float4*>(src);
+          v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (c + e < sh.dv) x[e] = fmaf(f, src[e], x[e]);
+            if (c + e < sh.dv) v[e] = src[e];
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = f == 0.f ? x[e] : fmaf(f, v[e], x[e]);  // (dropped, be it no number)
         if (j + 1 < n) f *= expf(static_cast<float>(tot[first + j * step]));
-        if (f == 0.f) break;
       }
     }
     if (sum && r < sh.d && c < sh.dv) store4(sum + (bh * sh.C + ch) * nel + r * sh.dv, c, sh.dv, x);
