@@ -287,7 +287,7 @@ LA2_API la2_status la2_qk_norm_rope_backward(const void *dq_out, const void *dk_
                                              la2_stream_t stream);
 
 /*
- * Synchronises `stream`, then reports and clears the device-side error word
+ * Synchronises `stream`, then reports and clears the current device's error word
  * that kernels set when a bounded wait gives up (LA2_ERR_TIMEOUT) or a slot
  * index read on the device is refused (LA2_ERR_INVALID_ARG), or LA2_ERR_CUDA if
  * the stream holds a CUDA error. LA2_OK otherwise.

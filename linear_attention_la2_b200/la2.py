@@ -183,6 +183,8 @@ def _raise(code: int):
 
 # ------------------------------------------------------------ torch helpers
 
+_HERE = contextlib.nullcontext()
+
 
 def _dtype_code(t):
     import torch
@@ -453,7 +455,11 @@ def decode_step(q, k, v, state, out=None, stream=None):
 
 
 def check(stream=None):
-    _raise(la2_check(_stream_handle(stream)))
+    """Raises what the kernels of the stream's device have reported since the last call."""
+    import torch
+
+    with torch.cuda.device(stream.device) if stream is not None else _HERE:
+        _raise(la2_check(_stream_handle(stream)))
 
 
 def _states_arg(states, q):
@@ -564,9 +570,6 @@ def _width(t):
     if t.dim() == 0:
         raise La2Error(LA2_ERR_INVALID_ARG)
     return t.shape[-1]
-
-
-_HERE = contextlib.nullcontext()
 
 
 def _call_on(device, stream):
