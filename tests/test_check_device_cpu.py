@@ -20,8 +20,10 @@ def test_check_asks_the_streams_device(monkeypatch):
     @contextlib.contextmanager
     def device(d):
         before, current[0] = current[0], d.index
-        yield
-        current[0] = before
+        try:
+            yield
+        finally:
+            current[0] = before
 
     def la2_check(stream):
         asked.append((current[0], stream.value))
