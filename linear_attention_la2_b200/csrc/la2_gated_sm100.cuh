@@ -900,9 +900,9 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
 // pool's, after a prefill). Its Y~ is fp32's 24 bits as three bf16 values, the first over Y,
 // and the other two have a sum of their own, so that the first's loses no digits to as
 // many small addends again (B3 H16 N3001: 7e-7 off, as la2_kv_state's exact products are, in 33 us;
-// with value and remainder 4.5e-6 in 28.5 us). Bound by HBM, where K and V are read once, and, FULL,
+// with value and remainder 4.5e-6 in 28 us). Bound by HBM, where K and V are read once, and, FULL,
 // by shared memory (192 KB a block: 1500 cycles against 1350 of HBM). Warps: 0 loads,
-// 1 MMA, 2 the rows' factors, 4-11 scale rows (four threads a row), 4-7 write the
+// 1 MMA, 2 the rows' factors, 4-11 scale rows (four threads a row) and write the
 // state out. Two CTAs an SM: one's scaling (about 1000 cycles a block) runs beside the
 // other's waits, loads and MMAs; one CTA with twice the buffers was 1.4 times slower.
 constexpr int kStateTab = 68;  // the rows' factors, and whether the block lies beyond a restart
@@ -928,13 +928,13 @@ struct TcStateParams {
   int32_t beside;  // the launch before is independent: see begin_grid
 };
 
-// x as three bf16 values.
-__device__ __forceinline__ void split3(float x, float y, uint32_t& a, uint32_t& b, uint32_t& c) {
-  a = s::pack_bf16x2(x, y);
-  x -= __uint_as_float(a << 16);
-  y -= __uint_as_float(a & 0xffff0000u);
-  b = s::pack_bf16x2(x, y);
-  c = s::pack_bf16x2(x - __uint_as_float(b << 16), y - __uint_as_float(b & 0xffff0000u));
+// A pair as three bf16 values each.
+__device__ __forceinline__ void split3(uint64_t x, uint32_t& a, uint32_t& b, uint32_t& c) {
+  const uint64_t minus = f2(-1.f, -1.f);
+  a = pack2(x);
+  x = fma2(f2(a << 16, a & 0xffff0000u), minus, x);
+  b = pack2(x);
+  c = pack2(fma2(f2(b << 16, b & 0xffff0000u), minus, x));
 }
 
 // ROWS_Z: the state's rows are z's columns (what O and dV start from), else y's.
@@ -1105,8 +1105,7 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
           uint32_t mid[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            split3(__uint_as_float(x[e] << 16) * factor_r, __uint_as_float(x[e] & 0xffff0000u) * factor_r, hi[e], mid[e],
-                   lo[e]);
+            split3(mul2(f2(x[e] << 16, x[e] & 0xffff0000u), f2(factor_r, factor_r)), hi[e], mid[e], lo[e]);
           s::st_shared_v4(ya + off, hi[0], hi[1], hi[2], hi[3]);
           s::st_shared_v4(y2 + off, mid[0], mid[1], mid[2], mid[3]);
         } else {
@@ -1119,13 +1118,13 @@ gated_state_sm100_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_
       s::fence_proxy_async();
       s::mbar_arrive(y2_full);
     }
-    if (ok && warp < 8 && wait(done, 0, 95)) {
+    if (ok && wait(done, 0, 95)) {  // warps 4-7 the first 64 columns, 8-11 the others
       s::tc_fence_after();
       const int row = 32 * (warp & 3) + lane;
       float4* dst = reinterpret_cast<float4*>(prm.out + (bh * prm.K + ch) * 128 * 128);
       float* dst_t = prm.out_t ? prm.out_t + (bh * prm.K + ch) * 128 * 128 + (row >> 2) * 512 + (row & 3) : nullptr;
 #pragma unroll 1
-      for (int c32 = 0; c32 < 4; ++c32) {
+      for (int c32 = warp < 8 ? 0 : 2; c32 < (warp < 8 ? 2 : 4); ++c32) {
         uint32_t v[32];
         const uint32_t at = tmem + c32 * 32 + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         s::tmem_ld32(at, v);
