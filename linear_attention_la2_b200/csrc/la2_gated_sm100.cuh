@@ -526,11 +526,12 @@ gated_sm100_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         n, lane,
         [&](int i, int r) {
           const int64_t t = row_of(i) + r;
-          const __nv_bfloat16 x = i < n && t < t1 ? g[t] : __float2bfloat16(0.f);
-          // (nothing comes before the first token for its gate to pass on: 0, unless NaN)
-          return t > 0 || __hisnan(x) ? x : __float2bfloat16(0.f);
+          return i < n && t < t1 ? g[t] : __float2bfloat16(0.f);
         },
         [&](int i, __nv_bfloat16 gx, __nv_bfloat16 gy) {
+          // nothing comes before the first token for its gate to pass on: 0, unless NaN (not where it
+          // is loaded: four blocks ahead, the warp would wait for it there)
+          if (lane == 0 && row_of(i) == 0 && !__hisnan(gx)) gx = __float2bfloat16(0.f);
           const bool cx = is_restart(gx), cy = is_restart(gy);
           const uint32_t ex = __ballot_sync(0xffffffffu, cx), ey = __ballot_sync(0xffffffffu, cy);
           float a, b;
